@@ -1,15 +1,18 @@
 """Thin ctypes binding of libssscan.so (C ABI declared in include/ss_scan.h,
-include/ss_conv.h and include/ss_ssd.h).
+include/ss_conv.h, include/ss_ssd.h, include/ss_norm.h, include/ss_linear.h and
+include/ss_ckpt.h).
 
 The functions named like the C entry points (ss_scan_fwd, ss_scan_fwd_noalloc, ss_scan_fwd_dir,
 ss_scan_fwd_complex, ss_scan_fwd_complex_ws, ss_scan_bwd, ss_scan_step, ss_scan_step_complex, ss_scan_workspace_bytes, ss_scan_strerror, ss_scan_version,
 ss_conv1d_fwd, ss_conv1d_bwd, ss_conv1d_step, ss_conv1d_workspace_bytes, ss_ssd_fwd,
-ss_ssd_fwd_state, ss_ssd_step) only
+ss_ssd_fwd_state, ss_ssd_step, ss_layernorm_fwd, ss_layernorm_bwd, ss_layernorm_workspace_bytes,
+ss_linear_fwd, ss_linear_bwd, ss_linear_bwd_ckpt, ss_linear_workspace_bytes, ss_ckpt_pack,
+ss_ckpt_unpack) only
 marshal arguments: torch tensors become device pointers, None becomes NULL and
 the stream defaults to torch's current HIP stream.  Every step runs in the HIP
 kernels; there is no fallback.  The convenience wrappers scan_fwd, scan_bwd,
-scan_bidir, scan_fwd_complex, scan_step, scan_step_complex, conv1d_fwd, conv1d_bwd, conv1d_step, ssd_fwd and ssd_step additionally allocate
-outputs and workspace with torch.
+scan_bidir, scan_fwd_complex, scan_step, scan_step_complex, conv1d_fwd, conv1d_bwd, conv1d_step, ssd_fwd, ssd_step, layernorm_fwd, layernorm_bwd, linear_fwd, linear_bwd, ckpt_pack
+and ckpt_unpack additionally allocate outputs and workspace with torch.
 """
 from __future__ import annotations
 
@@ -30,6 +33,11 @@ SS_OP_FWD, SS_OP_BWD, SS_OP_FWD_COMPLEX = 0, 1, 2
 SS_DIR_FORWARD, SS_DIR_REVERSE = 0, 1
 
 _DTYPE = {torch.float32: SS_F32, torch.bfloat16: SS_BF16}
+SS_ACT_NONE, SS_ACT_SILU, SS_ACT_GELU, SS_ACT_SOFTPLUS = 0, 1, 2, 3
+SS_LINEAR_FWD, SS_LINEAR_BWD, SS_LINEAR_BWD_CKPT = 0, 1, 2
+SS_CKPT_BLOCK = 32
+_ACT = {"none": SS_ACT_NONE, "silu": SS_ACT_SILU, "gelu": SS_ACT_GELU,
+        "softplus": SS_ACT_SOFTPLUS}
 _DISC = {"zoh": SS_ZOH, "euler": SS_EULER}
 
 
@@ -51,6 +59,25 @@ class ss_ssd_desc_t(ctypes.Structure):
                 ("headdim", ctypes.c_int64), ("dstate", ctypes.c_int64),
                 ("ngroups", ctypes.c_int64), ("in_dtype", ctypes.c_int32),
                 ("out_dtype", ctypes.c_int32), ("dt_softplus", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
+class ss_norm_desc_t(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("dim", ctypes.c_int64), ("x_stride", ctypes.c_int64),
+                ("in_dtype", ctypes.c_int32), ("res_dtype", ctypes.c_int32),
+                ("out_dtype", ctypes.c_int32), ("eps", ctypes.c_float)]
+
+
+class ss_ckpt_desc_t(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("dim", ctypes.c_int64), ("x_stride", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class ss_linear_desc_t(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("in_dim", ctypes.c_int64), ("out_dim", ctypes.c_int64),
+                ("x_stride", ctypes.c_int64), ("in_dtype", ctypes.c_int32),
+                ("out_dtype", ctypes.c_int32), ("res_dtype", ctypes.c_int32),
+                ("grad_dtype", ctypes.c_int32), ("act", ctypes.c_int32),
                 ("reserved", ctypes.c_int32)]
 
 
@@ -106,6 +133,27 @@ def load_library():
         lib.ss_ssd_fwd_state.restype = I
         lib.ss_ssd_step.argtypes = [ctypes.POINTER(ss_ssd_desc_t)] + [P] * 9 + [P]
         lib.ss_ssd_step.restype = I
+        NM = ctypes.POINTER(ss_norm_desc_t)
+        lib.ss_layernorm_fwd.argtypes = [NM] + [P] * 8 + [P]
+        lib.ss_layernorm_fwd.restype = I
+        lib.ss_layernorm_workspace_bytes.argtypes = [NM]
+        lib.ss_layernorm_workspace_bytes.restype = SZ
+        lib.ss_layernorm_bwd.argtypes = [NM] + [P] * 9 + [P, SZ, P]
+        lib.ss_layernorm_bwd.restype = I
+        LN = ctypes.POINTER(ss_linear_desc_t)
+        lib.ss_linear_workspace_bytes.argtypes = [LN, I]
+        lib.ss_linear_workspace_bytes.restype = SZ
+        lib.ss_linear_fwd.argtypes = [LN] + [P] * 6 + [P, SZ, P]
+        lib.ss_linear_fwd.restype = I
+        lib.ss_linear_bwd.argtypes = [LN] + [P] * 7 + [P, SZ, P]
+        lib.ss_linear_bwd.restype = I
+        lib.ss_linear_bwd_ckpt.argtypes = [LN] + [P] * 8 + [P, SZ, P]
+        lib.ss_linear_bwd_ckpt.restype = I
+        CK = ctypes.POINTER(ss_ckpt_desc_t)
+        lib.ss_ckpt_pack.argtypes = [CK] + [P] * 3 + [P]
+        lib.ss_ckpt_pack.restype = I
+        lib.ss_ckpt_unpack.argtypes = [CK] + [P] * 3 + [P]
+        lib.ss_ckpt_unpack.restype = I
         lib.ss_scan_strerror.argtypes = [I]
         lib.ss_scan_strerror.restype = ctypes.c_char_p
         lib.ss_scan_version.argtypes = []
@@ -261,6 +309,71 @@ def ss_ssd_fwd_state(desc, x, dt, A, Bm, Cm, D, dt_bias, h0, y, h_last, stream=N
 def ss_ssd_step(desc, h, x, dt, A, Bm, Cm, D, dt_bias, y, stream=None) -> int:
     return load_library().ss_ssd_step(ctypes.byref(desc), _p(h), _p(x), _p(dt), _p(A), _p(Bm),
                                        _p(Cm), _p(D), _p(dt_bias), _p(y), _stream(stream))
+
+
+def make_norm_desc(rows, dim, x_stride=0, in_dtype=SS_BF16, res_dtype=SS_F32, out_dtype=SS_BF16,
+                   eps=1e-5) -> ss_norm_desc_t:
+    return ss_norm_desc_t(int(rows), int(dim), int(x_stride), int(in_dtype), int(res_dtype),
+                          int(out_dtype), float(eps))
+
+
+def ss_layernorm_fwd(desc, x, residual, weight, bias, y, sum, mean, rstd, stream=None) -> int:
+    return load_library().ss_layernorm_fwd(ctypes.byref(desc), _p(x), _p(residual), _p(weight),
+                                           _p(bias), _p(y), _p(sum), _p(mean), _p(rstd),
+                                           _stream(stream))
+
+
+def ss_layernorm_workspace_bytes(desc: ss_norm_desc_t) -> int:
+    return int(load_library().ss_layernorm_workspace_bytes(ctypes.byref(desc)))
+
+
+def ss_layernorm_bwd(desc, s, weight, mean, rstd, dy, dsum, dx, dweight, dbias, workspace,
+                     ws_bytes, stream=None) -> int:
+    return load_library().ss_layernorm_bwd(ctypes.byref(desc), _p(s), _p(weight), _p(mean),
+                                           _p(rstd), _p(dy), _p(dsum), _p(dx), _p(dweight),
+                                           _p(dbias), _p(workspace), int(ws_bytes),
+                                           _stream(stream))
+
+
+def make_linear_desc(rows, in_dim, out_dim, x_stride=0, in_dtype=SS_BF16, out_dtype=SS_BF16,
+                     res_dtype=SS_BF16, grad_dtype=SS_BF16, act=SS_ACT_NONE) -> ss_linear_desc_t:
+    return ss_linear_desc_t(int(rows), int(in_dim), int(out_dim), int(x_stride), int(in_dtype),
+                            int(out_dtype), int(res_dtype), int(grad_dtype), int(act), 0)
+
+
+def ss_linear_workspace_bytes(desc: ss_linear_desc_t, op: int) -> int:
+    return int(load_library().ss_linear_workspace_bytes(ctypes.byref(desc), int(op)))
+
+
+def ss_linear_fwd(desc, x, w, bias, residual, y, pre, workspace, ws_bytes, stream=None) -> int:
+    return load_library().ss_linear_fwd(ctypes.byref(desc), _p(x), _p(w), _p(bias), _p(residual),
+                                        _p(y), _p(pre), _p(workspace), int(ws_bytes),
+                                        _stream(stream))
+
+
+def ss_linear_bwd(desc, x, w, pre, dy, dx, dw, dbias, workspace, ws_bytes, stream=None) -> int:
+    return load_library().ss_linear_bwd(ctypes.byref(desc), _p(x), _p(w), _p(pre), _p(dy), _p(dx),
+                                        _p(dw), _p(dbias), _p(workspace), int(ws_bytes),
+                                        _stream(stream))
+
+
+def ss_linear_bwd_ckpt(desc, q, e, w, pre, dy, dx, dw, dbias, workspace, ws_bytes,
+                       stream=None) -> int:
+    return load_library().ss_linear_bwd_ckpt(ctypes.byref(desc), _p(q), _p(e), _p(w), _p(pre),
+                                             _p(dy), _p(dx), _p(dw), _p(dbias), _p(workspace),
+                                             int(ws_bytes), _stream(stream))
+
+
+def make_ckpt_desc(rows, dim, x_stride=0, dtype=SS_BF16) -> ss_ckpt_desc_t:
+    return ss_ckpt_desc_t(int(rows), int(dim), int(x_stride), int(dtype), 0)
+
+
+def ss_ckpt_pack(desc, x, q, e, stream=None) -> int:
+    return load_library().ss_ckpt_pack(ctypes.byref(desc), _p(x), _p(q), _p(e), _stream(stream))
+
+
+def ss_ckpt_unpack(desc, q, e, x, stream=None) -> int:
+    return load_library().ss_ckpt_unpack(ctypes.byref(desc), _p(q), _p(e), _p(x), _stream(stream))
 
 
 def _check(rc, where):
@@ -501,3 +614,241 @@ def ssd_step(h, x, dt, A, B, C, D=None, dt_bias=None, softplus=True, out_dtype=t
     y = torch.empty(x.shape, dtype=out_dtype, device=x.device)
     _check(ss_ssd_step(desc, h, x, dt, A, B, C, D, dt_bias, y, stream), "ss_ssd_step")
     return y
+
+
+# ------------------------------------------- the operators around the scan in a block
+def _dt(t, name):
+    if t not in _DTYPE:
+        raise ValueError("%s must be float32 or bfloat16 (got %s)" % (name, t))
+    return _DTYPE[t]
+
+
+def _f32(**tensors):
+    for name, t in tensors.items():
+        if t is not None and t.dtype != torch.float32:
+            raise ValueError("%s must be float32 (got %s)" % (name, t.dtype))
+
+
+def _shape(name, t, shape):
+    if t is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError("%s must have shape %s (got %s)" % (name, tuple(shape), tuple(t.shape)))
+
+
+def _x_stride(x, name):
+    """x_stride of rows read in place: 0 for dense rows at a 16-byte aligned
+    address, else the elements from one row to the next.  Rows that overlap (an
+    expanded axis) are refused."""
+    dim = x.shape[-1]
+    if x.is_contiguous():
+        return 0 if x.data_ptr() % 16 == 0 else dim
+    s = _row_stride(x, name)
+    if s < dim:
+        raise ValueError("%s: rows overlap (row stride below the row's length)" % name)
+    return s
+
+
+def _on_device(fn, stream, tensors):
+    """fn() with the tensors' GPU and the stream current, so that its outputs and
+    workspace are allocated for the stream the kernels run on.  stream: None (the
+    device's current one), a torch stream or a raw hipStream_t; memory of the
+    tensors is kept from reuse until a stream other than their own is done."""
+    dev = None
+    for t in tensors:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError("all tensors must be on the GPU")
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError("all tensors must be on one GPU")
+    if stream is None:
+        if dev.index == torch.cuda.current_device():
+            return fn()
+        with torch.cuda.device(dev):
+            return fn()
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=dev)
+    if stream.device != dev:
+        raise ValueError("the stream belongs to another GPU than the tensors")
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
+    with torch.cuda.stream(stream):
+        return fn()
+
+
+def layernorm_fwd(x, weight=None, bias=None, residual=None, eps=1e-5, out_dtype=None,
+                  save_stats=False, stream=None):
+    """Layer norm over the last axis of s = x + residual.  x may have a row
+    stride (a column range of a wider tensor); weight and bias are float32.
+    Returns a dict: y (out_dtype, default x's), sum (s in residual's dtype, the
+    new residual stream; None without a residual), mean and rstd (float32, None
+    unless save_stats)."""
+    def run():
+        _dense(weight=weight, bias=bias, residual=residual)
+        _f32(weight=weight, bias=bias)
+        dim = x.shape[-1]
+        _shape("weight", weight, (dim,))
+        _shape("bias", bias, (dim,))
+        _shape("residual", residual, x.shape)
+        odt = x.dtype if out_dtype is None else out_dtype
+        lead = x.shape[:-1]
+        desc = make_norm_desc(x.numel() // dim if dim else 0, dim, _x_stride(x, "x"),
+                              _dt(x.dtype, "x"),
+                              _dt(x.dtype if residual is None else residual.dtype, "residual"),
+                              _dt(odt, "out_dtype"), eps)
+        y = torch.empty(x.shape, dtype=odt, device=x.device)
+        s = None if residual is None else torch.empty_like(residual)
+        mean = rstd = None
+        if save_stats:
+            mean = torch.empty(lead, dtype=torch.float32, device=x.device)
+            rstd = torch.empty(lead, dtype=torch.float32, device=x.device)
+        _check(ss_layernorm_fwd(desc, x, residual, weight, bias, y, s, mean, rstd),
+               "ss_layernorm_fwd")
+        return {"y": y, "sum": s, "mean": mean, "rstd": rstd}
+    return _on_device(run, stream, (x, weight, bias, residual))
+
+
+def layernorm_bwd(s, dy, mean, rstd, weight=None, dsum=None, dx_dtype=None, stream=None):
+    """Backward of layernorm_fwd: s is what was normalised (x, or the returned
+    sum; a row stride is taken), dsum the gradient that reaches s from elsewhere.
+    Returns a dict: dx (dx_dtype, default dsum's dtype or float32; the gradient
+    of x and of the residual alike), dweight and dbias (float32)."""
+    def run():
+        _dense(weight=weight, mean=mean, rstd=rstd, dy=dy, dsum=dsum)
+        _f32(weight=weight, mean=mean, rstd=rstd)
+        dim = s.shape[-1]
+        _shape("weight", weight, (dim,))
+        _shape("mean", mean, s.shape[:-1])
+        _shape("rstd", rstd, s.shape[:-1])
+        _shape("dy", dy, s.shape)
+        _shape("dsum", dsum, s.shape)
+        rdt = dx_dtype
+        if rdt is None:
+            rdt = torch.float32 if dsum is None else dsum.dtype
+        if dsum is not None and dsum.dtype != rdt:
+            raise ValueError("dx_dtype must be dsum's dtype")
+        desc = make_norm_desc(s.numel() // dim if dim else 0, dim, _x_stride(s, "s"),
+                              _dt(s.dtype, "s"), _dt(rdt, "dx_dtype"), _dt(dy.dtype, "dy"))
+        dx = torch.empty(s.shape, dtype=rdt, device=s.device)
+        dw = torch.empty(dim, dtype=torch.float32, device=s.device)
+        db = torch.empty(dim, dtype=torch.float32, device=s.device)
+        nb = ss_layernorm_workspace_bytes(desc)
+        ws = workspace(nb, s.device)
+        _check(ss_layernorm_bwd(desc, s, weight, mean, rstd, dy, dsum, dx, dw, db, ws, nb),
+               "ss_layernorm_bwd")
+        return {"dx": dx, "dweight": dw, "dbias": db}
+    return _on_device(run, stream, (s, dy, mean, rstd, weight, dsum))
+
+
+def linear_fwd(x, w, bias=None, residual=None, act="none", out_dtype=None, save_pre=False,
+               stream=None):
+    """act(x w^T + bias) + residual for x (..., K) and w (N, K) of one dtype; x
+    may have a row stride.  bias is float32, residual (..., N) float32 or
+    bfloat16, act one of "none", "silu", "gelu", "softplus".  Returns y (..., N)
+    in out_dtype (default x's), and with save_pre the pre-activation values in
+    x's dtype as well."""
+    def run():
+        _dense(w=w, bias=bias, residual=residual)
+        _f32(bias=bias)
+        n, k = w.shape
+        oshape = (*x.shape[:-1], n)
+        _shape("x", x, (*x.shape[:-1], k))
+        _shape("bias", bias, (n,))
+        _shape("residual", residual, oshape)
+        if x.dtype != w.dtype:
+            raise ValueError("x and w must have one dtype")
+        odt = x.dtype if out_dtype is None else out_dtype
+        desc = make_linear_desc(x.numel() // k if k else 0, k, n, _x_stride(x, "x"),
+                                _dt(x.dtype, "x"), _dt(odt, "out_dtype"),
+                                _dt(odt if residual is None else residual.dtype, "residual"),
+                                SS_F32, _ACT[act])
+        y = torch.empty(oshape, dtype=odt, device=x.device)
+        pre = torch.empty(oshape, dtype=x.dtype, device=x.device) if save_pre else None
+        nb = ss_linear_workspace_bytes(desc, SS_LINEAR_FWD)
+        ws = workspace(nb, x.device)
+        _check(ss_linear_fwd(desc, x, w, bias, residual, y, pre, ws, nb), "ss_linear_fwd")
+        return (y, pre) if save_pre else y
+    return _on_device(run, stream, (x, w, bias, residual))
+
+
+def linear_bwd(x, w, dy, pre=None, act="none", bias=False, grad_dtype=None, need_dx=True,
+               need_dw=True, stream=None):
+    """Backward of linear_fwd given dy (..., N).  x: the forward's input, or its
+    8-bit checkpoint (q, e) from ckpt_pack (None when need_dw is false).  pre:
+    the forward's pre-activation values, with an activation.  Returns a dict: dx
+    (..., K) and dw (N, K) in grad_dtype (default w's), dbias (N) float32 when
+    bias is true; what is not asked for is None."""
+    packed = isinstance(x, tuple)
+    q, e = x if packed else (None, None)
+
+    def run():
+        _dense(w=w, dy=dy, pre=pre, q=q, e=e)
+        n, k = w.shape
+        lead = dy.shape[:-1]
+        rows = dy.numel() // n if n else 0
+        _shape("dy", dy, (*lead, n))
+        _shape("pre", pre, dy.shape)
+        if pre is not None and pre.dtype != w.dtype:
+            raise ValueError("pre must have w's dtype")
+        if need_dw and x is None:
+            raise ValueError("dw needs x")
+        xs = 0
+        if packed:
+            _shape("q", q, (*lead, k))
+            _shape("e", e, (*lead, -(-k // SS_CKPT_BLOCK)))
+            if q.dtype != torch.int8 or e.dtype != torch.uint8:
+                raise ValueError("a checkpoint is int8 values and uint8 exponents")
+        elif x is not None:
+            _shape("x", x, (*lead, k))
+            if x.dtype != w.dtype:
+                raise ValueError("x and w must have one dtype")
+            xs = _x_stride(x, "x")
+        gdt = w.dtype if grad_dtype is None else grad_dtype
+        desc = make_linear_desc(rows, k, n, xs, _dt(w.dtype, "w"), _dt(dy.dtype, "dy"),
+                                SS_F32, _dt(gdt, "grad_dtype"), _ACT[act])
+        dev = w.device
+        dx = torch.empty((*lead, k), dtype=gdt, device=dev) if need_dx else None
+        dw = torch.empty((n, k), dtype=gdt, device=dev) if need_dw else None
+        db = torch.empty(n, dtype=torch.float32, device=dev) if bias else None
+        op = SS_LINEAR_BWD_CKPT if packed else SS_LINEAR_BWD
+        nb = ss_linear_workspace_bytes(desc, op)
+        ws = workspace(nb, dev)
+        if packed:
+            _check(ss_linear_bwd_ckpt(desc, q, e, w, pre, dy, dx, dw, db, ws, nb),
+                   "ss_linear_bwd_ckpt")
+        else:
+            _check(ss_linear_bwd(desc, x, w, pre, dy, dx, dw, db, ws, nb), "ss_linear_bwd")
+        return {"dx": dx, "dw": dw, "dbias": db}
+    return _on_device(run, stream, (None if packed else x, q, e, w, dy, pre))
+
+
+def ckpt_pack(x, stream=None):
+    """8-bit checkpoint of x (..., D): (q, e), int8 values and one uint8 exponent
+    per 32 channels.  x may have a row stride."""
+    def run():
+        dim = x.shape[-1]
+        desc = make_ckpt_desc(x.numel() // dim if dim else 0, dim, _x_stride(x, "x"),
+                              _dt(x.dtype, "x"))
+        q = torch.empty(x.shape, dtype=torch.int8, device=x.device)
+        e = torch.empty((*x.shape[:-1], -(-dim // SS_CKPT_BLOCK)), dtype=torch.uint8,
+                        device=x.device)
+        _check(ss_ckpt_pack(desc, x, q, e), "ss_ckpt_pack")
+        return q, e
+    return _on_device(run, stream, (x,))
+
+
+def ckpt_unpack(q, e, dtype=torch.bfloat16, stream=None):
+    """The values of a checkpoint (q, e), in dtype."""
+    def run():
+        _dense(q=q, e=e)
+        dim = q.shape[-1]
+        _shape("e", e, (*q.shape[:-1], -(-dim // SS_CKPT_BLOCK)))
+        if q.dtype != torch.int8 or e.dtype != torch.uint8:
+            raise ValueError("a checkpoint is int8 values and uint8 exponents")
+        desc = make_ckpt_desc(q.numel() // dim if dim else 0, dim, 0, _dt(dtype, "dtype"))
+        x = torch.empty(q.shape, dtype=dtype, device=q.device)
+        _check(ss_ckpt_unpack(desc, q, e, x), "ss_ckpt_unpack")
+        return x
+    return _on_device(run, stream, (q, e))

@@ -13,15 +13,9 @@
 namespace ss {
 namespace {
 
-constexpr size_t kAlign = 256;     // workspace alignment
-constexpr size_t kPtrAlign = 16;   // every tensor pointer (rows are read with 16-byte loads)
 constexpr int64_t kBwdChunk = 32;   // backward time chunk (8 blocks of 4 steps)
 
 size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
-
-bool valid_dtype(int32_t t) { return t == SS_F32 || t == SS_BF16; }
-
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 // Sizes must be positive and B*L*D, B*L*N must stay far below 2^62 bytes.
 int check_desc(const ss_desc_t* d, bool need_len) {
@@ -324,7 +318,7 @@ int fwd_call(const ss_desc_t* desc, int direction, int accumulate, const void* u
 
 extern "C" {
 
-int ss_scan_version(void) { return 20000; }
+int ss_scan_version(void) { return 20100; }
 
 int ss_scan_arch_supported(const char* arch_name) {
   if (!arch_name) return SS_ERR_INVALID_ARG;

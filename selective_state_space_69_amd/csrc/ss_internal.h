@@ -6,7 +6,10 @@
 #include <cstddef>
 #include <cstdint>
 
+#include "ss_ckpt.h"
 #include "ss_conv.h"
+#include "ss_linear.h"
+#include "ss_norm.h"
 #include "ss_ssd.h"
 #include "ss_scan.h"
 
@@ -16,6 +19,12 @@ constexpr int kWave = 64;      // lanes per wavefront on CDNA
 constexpr int kMaxState = 16;  // states held per lane
 constexpr int kHalfWaveSplit = 8;
 constexpr int kOneStateSplit = 16;
+
+// Argument checks shared by the entry points.
+constexpr size_t kAlign = 256;     // workspace alignment
+constexpr size_t kPtrAlign = 16;   // every tensor pointer (rows are read with 16-byte loads)
+inline bool valid_dtype(int32_t t) { return t == SS_F32 || t == SS_BF16; }
+inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 // How a forward (or the forward recompute inside the backward) is split.
 // nsplit : waves per (b, 64-channel block), each holding 16 / nsplit states;
@@ -197,5 +206,48 @@ int launch_ssd_fwd(const ss_ssd_desc_t& d, const void* x, const void* dt, const 
 int launch_ssd_step(const ss_ssd_desc_t& d, float* h, const void* x, const void* dt,
                     const float* A, const void* Bm, const void* Cm, const float* D,
                     const float* dt_bias, void* y, void* stream);
+
+
+// Layer norm (ss_norm.hip): nwaves waves per row with vpt vectors of 8 channels
+// per thread.  Backward workspace: nparts partial rows (D) of dweight and of
+// dbias, fp32, 256-byte aligned.
+struct NormPlan {
+  int nwaves = 1, vpt = 1;
+  int64_t blocks = 1;
+  int nparts = 1;
+  size_t off_w = 0, off_b = 0, bytes = 0;
+};
+NormPlan plan_norm(const ss_norm_desc_t& d);
+int launch_norm_fwd(const ss_norm_desc_t& d, const void* x, const void* residual,
+                    const float* weight, const float* bias, void* y, void* sum, float* mean,
+                    float* rstd, void* stream);
+int launch_norm_bwd(const ss_norm_desc_t& d, const NormPlan& pl, const void* s,
+                    const float* weight, const float* mean, const float* rstd, const void* dy,
+                    const void* dsum, void* dx, float* dweight, float* dbias, char* ws,
+                    void* stream);
+
+// 8-bit checkpoints (ss_ckpt.hip).
+int launch_ckpt_pack(const ss_ckpt_desc_t& d, const void* x, int8_t* q, uint8_t* e, void* stream);
+int launch_ckpt_unpack(const ss_ckpt_desc_t& d, const int8_t* q, const uint8_t* e, void* x,
+                       void* stream);
+
+// Linear projections (ss_linear.hip).  Workspace, 256-byte aligned arrays:
+//   dpre : (M, N) in_dtype, dy act'(pre) (only with an activation, or a dy of
+//          another type than the operands)
+//   x    : (M, K) in_dtype, the checkpoint's values (SS_LINEAR_BWD_CKPT)
+//   sums : (chunks, N) fp32, dbias sums of chunk_rows rows
+//   part : fp32 partial products of a split contraction (the larger of dx's, dw's)
+struct LinearPlan {
+  bool need_dpre = false;
+  int64_t chunk_rows = 1, chunks = 1;
+  size_t off_dpre = 0, off_x = 0, off_sums = 0, off_part = 0, bytes = 0;
+};
+LinearPlan plan_linear(const ss_linear_desc_t& d, int op);
+int launch_linear_fwd(const ss_linear_desc_t& d, const void* x, const void* w, const float* bias,
+                      const void* residual, void* y, void* pre, char* ws, void* stream);
+// x or its checkpoint (q, e)
+int launch_linear_bwd(const ss_linear_desc_t& d, const LinearPlan& pl, const void* x,
+                      const int8_t* q, const uint8_t* e, const void* w, const void* pre,
+                      const void* dy, void* dx, void* dw, float* dbias, char* ws, void* stream);
 
 }  // namespace ss

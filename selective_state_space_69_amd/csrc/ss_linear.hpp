@@ -1,0 +1,144 @@
+// What the matrix-product kernels of the linear projections share: the problem
+// as each of the three products states it, and the epilogue.
+//
+// Every product is written O[r][s] = sum_t R(r, t) S(s, t), O row-major with s
+// contiguous:
+//   forward  y  (M, N): R = x    (t = k contiguous)   S = w  (t = k contiguous)
+//   backward dx (M, K): R = dpre (t = n contiguous)   S = w  (s = k contiguous)
+//            dw (N, K): R = dpre (r = n contiguous)   S = x  (s = k contiguous)
+// S feeds the A side of the MFMA and R the B side, so that a lane's four
+// accumulator registers are four neighbours of one output row.
+#pragma once
+
+#include "ss_device.hpp"
+
+namespace ss {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+struct MmParams {
+  const void* R;
+  const void* S;
+  int64_t ldr, lds;      // elements from one row of the operand's storage to the next
+  int64_t nR;            // output rows
+  int32_t nS;            // output columns
+  int64_t nT;            // contraction length
+  int64_t t_split;       // contraction length of one split (a multiple of the tile's)
+  int32_t splits;
+  int32_t tiles_r, tiles_s;
+  bool vec_r, vec_s;     // operand rows are 16-byte aligned
+  // epilogue
+  const float* bias;     // (nS) or null
+  const void* res;       // (nR, nS) or null
+  void* out;
+  void* pre;             // (nR, nS) or null
+  float* part;           // (splits, nR, nS) when splits > 1
+  int32_t act, out_bf16, res_bf16, pre_bf16;
+};
+
+__device__ __forceinline__ float apply_act(int act, float v) {
+  switch (act) {
+    case SS_ACT_SILU: return silu(v);
+    case SS_ACT_GELU: return 0.5f * v * (1.0f + erff(v * 0.70710678118654752f));
+    case SS_ACT_SOFTPLUS:   // max(v, 0) + log(1 + e^-|v|): the largest v pass through
+      return __builtin_fmaxf(v, 0.0f) + softplus_log2(-__builtin_fabsf(v) * kLog2e) * kLn2;
+    default: return v;
+  }
+}
+__device__ __forceinline__ float act_grad(int act, float v) {
+  switch (act) {
+    case SS_ACT_SILU: {
+      const float s = hw_rcp(1.0f + hw_exp2(-v * kLog2e));
+      return s * __builtin_fmaf(v, 1.0f - s, 1.0f);
+    }
+    case SS_ACT_GELU:
+      return 0.5f * (1.0f + erff(v * 0.70710678118654752f)) +
+             v * 0.39894228040143268f * hw_exp2(v * v * (-0.5f * kLog2e));
+    case SS_ACT_SOFTPLUS: return hw_rcp(1.0f + hw_exp2(-v * kLog2e));
+    default: return 1.0f;
+  }
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  return uint32_t(f32_to_bf16(lo)) | (uint32_t(f32_to_bf16(hi)) << 16);
+}
+__device__ __forceinline__ void store4(void* base, int64_t i, int bf16, const float (&v)[4]) {
+  if (bf16)
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(base) + i) =
+        make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+  else
+    *reinterpret_cast<float4*>(static_cast<float*>(base) + i) =
+        make_float4(v[0], v[1], v[2], v[3]);
+}
+
+// Four neighbours s..s+3 of output row r: bias, activation, residual, stores.
+// Rows keep 4-element alignment only where nS is a multiple of 4.
+__device__ __forceinline__ void epilogue4(const MmParams& p, int64_t r, int32_t s, float (&v)[4]) {
+  if (r >= p.nR || s >= p.nS) return;
+  const int64_t o = r * p.nS + s;
+  if ((p.nS & 3) == 0) {
+    if (p.bias) {
+      const float4 b = *reinterpret_cast<const float4*>(p.bias + s);
+      v[0] += b.x; v[1] += b.y; v[2] += b.z; v[3] += b.w;
+    }
+    if (p.pre) store4(p.pre, o, p.pre_bf16, v);
+    if (p.act != SS_ACT_NONE) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = apply_act(p.act, v[j]);
+    }
+    if (p.res) {
+      const float4 f = p.res_bf16 ? unpack4(load_raw4(static_cast<const uint16_t*>(p.res) + o))
+                                  : load_raw4(static_cast<const float*>(p.res) + o);
+      v[0] += f.x; v[1] += f.y; v[2] += f.z; v[3] += f.w;
+    }
+    store4(p.out, o, p.out_bf16, v);
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (s + j >= p.nS) break;
+    float f = v[j];
+    if (p.bias) f += p.bias[s + j];
+    if (p.pre) {
+      if (p.pre_bf16) static_cast<uint16_t*>(p.pre)[o + j] = f32_to_bf16(f);
+      else static_cast<float*>(p.pre)[o + j] = f;
+    }
+    f = apply_act(p.act, f);
+    if (p.res)
+      f += p.res_bf16 ? to_f32(static_cast<const uint16_t*>(p.res)[o + j])
+                      : static_cast<const float*>(p.res)[o + j];
+    if (p.out_bf16) static_cast<uint16_t*>(p.out)[o + j] = f32_to_bf16(f);
+    else static_cast<float*>(p.out)[o + j] = f;
+  }
+}
+
+// A split's partial sums, in fp32, for the kernel that joins them.
+__device__ __forceinline__ void store_partial4(const MmParams& p, int split, int64_t r, int32_t s,
+                                               const float (&v)[4]) {
+  if (r >= p.nR || s >= p.nS) return;
+  float* dst = p.part + (int64_t(split) * p.nR + r) * p.nS + s;
+  if ((p.nS & 3) == 0) {
+    *reinterpret_cast<float4*>(dst) = make_float4(v[0], v[1], v[2], v[3]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (s + j < p.nS) dst[j] = v[j];
+  }
+}
+
+// Output tile of work item `id`.  Neighbouring items (one XCD's) share operand
+// rows in its L2: tiles run down columns of a band of up to 8 tile rows.
+__device__ __forceinline__ void tile_of(const MmParams& p, int64_t id, int64_t* tr, int* ts) {
+  constexpr int kBand = 8;
+  const int64_t per_band = int64_t(kBand) * p.tiles_s;
+  const int64_t band = id / per_band;
+  const int64_t in = id - band * per_band;
+  const int64_t left = p.tiles_r - band * kBand;
+  const int64_t h = left < kBand ? left : kBand;
+  *tr = band * kBand + in % h;
+  *ts = int(in / h);
+}
+
+}  // namespace ss

@@ -1,0 +1,333 @@
+"""CPU-side checks of the operators around the scan: descriptors match the
+headers, invalid arguments are refused before any HIP call, and the binding
+refuses what the library would read wrongly."""
+import ctypes
+import os
+import re
+import subprocess
+
+import numpy as np
+import pytest
+import torch
+
+from selective_state_space_69_amd import binding as B
+import block_ref as ref
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+F = 1 << 20          # an aligned non-null "device pointer"; never dereferenced
+BF, F32 = B.SS_BF16, B.SS_F32
+INV, UNS, WSP = B.SS_ERR_INVALID_ARG, B.SS_ERR_UNSUPPORTED, B.SS_ERR_WORKSPACE
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    if not os.path.exists(B.LIB_PATH):
+        from selective_state_space_69_amd import build
+        build.build(verbose=False)
+    return B.load_library()
+
+
+def at(i):
+    return F + (i << 24)
+
+
+def norm_desc(**kw):
+    return B.make_norm_desc(**{**dict(rows=4, dim=64), **kw})
+
+
+def norm_fwd(d, **kw):
+    a = {**dict(x=at(0), residual=None, weight=None, bias=None, y=at(1), sum=None, mean=None,
+                rstd=None), **kw}
+    return B.ss_layernorm_fwd(d, *a.values(), stream=0)
+
+
+def norm_bwd(d, **kw):
+    a = {**dict(s=at(0), weight=at(1), mean=at(2), rstd=at(3), dy=at(4), dsum=None, dx=at(5),
+                dweight=at(6), dbias=at(7), workspace=at(8), ws_bytes=1 << 40), **kw}
+    return B.ss_layernorm_bwd(d, *a.values(), stream=0)
+
+
+def linear_desc(**kw):
+    return B.make_linear_desc(**{**dict(rows=64, in_dim=64, out_dim=64), **kw})
+
+
+def linear_fwd(d, **kw):
+    a = {**dict(x=at(0), w=at(1), bias=None, residual=None, y=at(2), pre=None, workspace=at(3),
+                ws_bytes=1 << 40), **kw}
+    return B.ss_linear_fwd(d, *a.values(), stream=0)
+
+
+def linear_bwd(d, **kw):
+    a = {**dict(x=at(0), w=at(1), pre=None, dy=at(2), dx=at(3), dw=at(4), dbias=None,
+                workspace=at(5), ws_bytes=1 << 40), **kw}
+    return B.ss_linear_bwd(d, *a.values(), stream=0)
+
+
+def linear_bwd_ckpt(d, **kw):
+    a = {**dict(q=at(0), e=at(6), w=at(1), pre=None, dy=at(2), dx=at(3), dw=at(4), dbias=None,
+                workspace=at(5), ws_bytes=1 << 40), **kw}
+    return B.ss_linear_bwd_ckpt(d, *a.values(), stream=0)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(rows=0), INV), (dict(rows=1 << 31), INV), (dict(dim=0), INV), (dict(dim=32769), UNS),
+    (dict(x_stride=63), INV), (dict(x_stride=(1 << 24) + 1), INV), (dict(in_dtype=2), UNS),
+    (dict(res_dtype=-1), UNS), (dict(out_dtype=9), UNS), (dict(eps=0.0), INV),
+    (dict(eps=float("nan")), INV), (dict(eps=float("inf")), INV), (dict(eps=-1e-5), INV),
+])
+def test_norm_descriptor(kw, code):
+    assert norm_fwd(norm_desc(**kw)) == code
+    if "eps" not in kw:
+        assert norm_bwd(norm_desc(**kw)) == code
+        assert B.ss_layernorm_workspace_bytes(norm_desc(**kw)) == 0
+
+
+@pytest.mark.parametrize("kw", [
+    dict(x=None), dict(y=None), dict(mean=at(5)), dict(rstd=at(5)), dict(y=at(0)),
+    dict(residual=at(1)), dict(sum=at(0)), dict(sum=at(1)), dict(mean=at(0), rstd=at(6)),
+    dict(mean=at(6), rstd=at(6)), dict(x=at(0) + 2), dict(y=at(1) + 8), dict(weight=at(5) + 4),
+    dict(residual=at(5) + 4),
+])
+def test_norm_fwd_arguments(kw):
+    assert norm_fwd(norm_desc(), **kw) == INV
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(s=None), INV), (dict(mean=None), INV), (dict(rstd=None), INV), (dict(dy=None), INV),
+    (dict(dx=None), INV), (dict(dx=at(0)), INV), (dict(dx=at(4)), INV), (dict(dweight=at(7)), INV),
+    (dict(dweight=at(5)), INV), (dict(dbias=at(1)), INV), (dict(dsum=at(9) + 2), INV),
+    (dict(workspace=None), WSP), (dict(ws_bytes=16), WSP), (dict(workspace=at(8) + 16), WSP),
+])
+def test_norm_bwd_arguments(kw, code):
+    assert norm_bwd(norm_desc(), **kw) == code
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(rows=0), INV), (dict(rows=1 << 31), INV), (dict(in_dim=0), INV),
+    (dict(in_dim=(1 << 20) + 1), INV), (dict(out_dim=0), INV), (dict(out_dim=(1 << 20) + 1), INV),
+    (dict(rows=(1 << 31) - 1, in_dim=1 << 20), INV), (dict(x_stride=63), INV),
+    (dict(x_stride=(1 << 20) + 1), INV), (dict(in_dtype=5), UNS), (dict(out_dtype=5), UNS),
+    (dict(act=4), UNS), (dict(act=-1), UNS),
+])
+def test_linear_descriptor(kw, code):
+    d = linear_desc(**kw)
+    assert linear_fwd(d) == code
+    assert linear_bwd(d, pre=at(9) if "act" in kw else None) == code
+    for op in (0, 1):
+        assert B.ss_linear_workspace_bytes(d, op) == 0
+    d.reserved = 1
+    assert linear_fwd(d) != B.SS_OK
+
+
+def test_linear_descriptor_rest():
+    assert linear_fwd(linear_desc(res_dtype=7)) == UNS
+    assert linear_bwd(linear_desc(grad_dtype=7)) == UNS
+    assert linear_bwd_ckpt(linear_desc(x_stride=80)) == UNS
+    d = linear_desc()
+    d.reserved = 1
+    assert linear_fwd(d) == INV and linear_bwd(d) == INV
+    assert B.ss_linear_workspace_bytes(linear_desc(), 3) == 0
+
+
+@pytest.mark.parametrize("kw", [
+    dict(x=None), dict(w=None), dict(y=None), dict(y=at(0)), dict(y=at(1)), dict(pre=at(2)),
+    dict(pre=at(0)), dict(residual=at(9), pre=at(9)), dict(x=at(0) + 2), dict(w=at(1) + 2),
+    dict(bias=at(9) + 4), dict(y=at(2) + 8), dict(residual=at(9) + 2),
+])
+def test_linear_fwd_arguments(kw):
+    assert linear_fwd(linear_desc(), **kw) == INV
+
+
+def test_linear_fwd_in_place_types():
+    # y over the residual needs one type
+    assert linear_fwd(linear_desc(res_dtype=F32, out_dtype=BF), residual=at(2)) == INV
+
+
+def test_linear_workspace():
+    d = linear_desc(rows=64, in_dim=4096, out_dim=64)     # few tiles, a long contraction: split
+    need = B.ss_linear_workspace_bytes(d, B.SS_LINEAR_FWD)
+    assert need > 0
+    assert linear_fwd(d, workspace=None, ws_bytes=0) == WSP
+    assert linear_fwd(d, ws_bytes=need - 1) == WSP
+    assert linear_fwd(d, workspace=at(3) + 16, ws_bytes=need) == WSP
+    a = B.ss_linear_workspace_bytes(linear_desc(), B.SS_LINEAR_BWD)
+    b = B.ss_linear_workspace_bytes(linear_desc(), B.SS_LINEAR_BWD_CKPT)
+    assert b >= a + 64 * 64 * 2                           # the checkpoint's values
+    c = B.ss_linear_workspace_bytes(linear_desc(act=1), B.SS_LINEAR_BWD)
+    assert c >= a + 64 * 64 * 2                           # dpre
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(w=None), INV), (dict(dy=None), INV), (dict(dx=None, dw=None), INV), (dict(x=None), INV),
+    (dict(pre=at(9)), INV), (dict(dx=at(4)), INV), (dict(dx=at(1)), INV), (dict(dw=at(2)), INV),
+    (dict(dbias=at(2)), INV), (dict(dbias=at(3)), INV), (dict(dy=at(2) + 4), INV),
+    (dict(x=at(0) + 2), INV), (dict(workspace=None), WSP),
+])
+def test_linear_bwd_arguments(kw, code):
+    assert linear_bwd(linear_desc(), **kw) == code
+
+
+def test_linear_bwd_needs_pre():
+    assert linear_bwd(linear_desc(act=B.SS_ACT_SILU)) == INV
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(q=None), INV), (dict(e=None), INV), (dict(q=at(0) + 8), INV), (dict(dw=at(0)), INV),
+    (dict(dx=at(6)), INV), (dict(workspace=None), WSP),
+])
+def test_linear_bwd_ckpt_arguments(kw, code):
+    assert linear_bwd_ckpt(linear_desc(), **kw) == code
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(rows=0), INV), (dict(dim=0), INV), (dict(x_stride=31), INV), (dict(dtype=3), UNS),
+    (dict(rows=1 << 41, dim=1), INV),
+])
+def test_ckpt_descriptor(kw, code):
+    d = B.make_ckpt_desc(**{**dict(rows=4, dim=64), **kw})
+    assert B.ss_ckpt_pack(d, at(0), at(1), at(2), stream=0) == code
+    assert B.ss_ckpt_unpack(d, at(1), at(2), at(0), stream=0) == code
+
+
+@pytest.mark.parametrize("ptrs", [(None, at(1), at(2)), (at(0), None, at(2)), (at(0), at(1), None),
+                                  (at(0), at(0), at(2)), (at(0), at(1), at(0)),
+                                  (at(0) + 2, at(1), at(2)), (at(0), at(1) + 8, at(2)),
+                                  (at(0), at(1), at(2) + 1)])
+def test_ckpt_arguments(ptrs):
+    x, q, e = ptrs
+    d = B.make_ckpt_desc(4, 64)
+    assert B.ss_ckpt_pack(d, x, q, e, stream=0) == INV
+    assert B.ss_ckpt_unpack(d, q, e, x, stream=0) == INV
+
+
+def test_null_descriptor(lib):
+    n = None
+    assert lib.ss_layernorm_fwd(n, *[F] * 8, n) == INV
+    assert lib.ss_layernorm_bwd(n, *[F] * 10, 0, n) == INV
+    assert lib.ss_linear_fwd(n, *[F] * 7, 0, n) == INV
+    assert lib.ss_linear_bwd(n, *[F] * 8, 0, n) == INV
+    assert lib.ss_linear_bwd_ckpt(n, *[F] * 9, 0, n) == INV
+    assert lib.ss_ckpt_pack(n, F, F, F, n) == INV
+    assert lib.ss_linear_workspace_bytes(n, 0) == 0
+    assert lib.ss_layernorm_workspace_bytes(n) == 0
+
+
+def test_descriptors_match_the_headers(tmp_path):
+    """Size and field offsets of the C structs against the ctypes ones."""
+    src = ['#include <stdio.h>', '#include "ss_norm.h"', '#include "ss_linear.h"',
+           'int main(void) {']
+    for t in (B.ss_norm_desc_t, B.ss_linear_desc_t, B.ss_ckpt_desc_t):
+        n = t.__name__
+        src.append('printf("%s %%zu\\n", sizeof(%s));' % (n, n))
+        for f, _ in t._fields_:
+            src.append('printf("%s.%s %%zu\\n", offsetof(%s, %s));' % (n, f, n, f))
+    src.append('return 0; }')
+    c = tmp_path / "d.c"
+    c.write_text("\n".join(src))
+    exe = str(tmp_path / "d")
+    subprocess.run(["gcc", "-I", os.path.join(ROOT, "include"), str(c), "-o", exe], check=True)
+    got = dict(line.split() for line in subprocess.run([exe], capture_output=True, text=True,
+                                                       check=True).stdout.splitlines())
+    for t in (B.ss_norm_desc_t, B.ss_linear_desc_t, B.ss_ckpt_desc_t):
+        assert int(got[t.__name__]) == ctypes.sizeof(t)
+        for f, _ in t._fields_:
+            assert int(got["%s.%s" % (t.__name__, f)]) == getattr(t, f).offset
+
+
+def test_binding_refuses_host_tensors():
+    x, w = torch.zeros(4, 8), torch.zeros(3, 8)
+    for call in (lambda: B.layernorm_fwd(x), lambda: B.linear_fwd(x, w), lambda: B.ckpt_pack(x),
+                 lambda: B.linear_bwd(x, w, torch.zeros(4, 3)),
+                 lambda: B.layernorm_bwd(x, x, torch.zeros(4), torch.zeros(4)),
+                 lambda: B.ckpt_unpack(x.to(torch.int8), x[:, :1].to(torch.uint8))):
+        with pytest.raises(ValueError, match="on the GPU"):
+            call()
+
+
+def test_binding_row_stride():
+    wide = torch.zeros(6, 12)
+    assert B._x_stride(wide[:, :8], "x") == 12
+    assert B._x_stride(wide, "x") == 0
+    with pytest.raises(ValueError, match="overlap"):
+        B._x_stride(torch.zeros(1, 8).expand(6, 8), "x")
+    with pytest.raises(ValueError, match="unit stride"):
+        B._x_stride(wide.t(), "x")
+    with pytest.raises(ValueError, match="evenly spaced"):
+        B._x_stride(torch.zeros(3, 4, 8)[:, :2], "x")
+
+
+# ------------------------------------------------ the 64-bit forms against differences
+@pytest.mark.parametrize("name", ["silu", "gelu", "softplus", "none"])
+def test_reference_linear_gradients(name):
+    g = torch.Generator().manual_seed(3)
+    x, w, dy = (torch.randn(s, generator=g, dtype=torch.float64) for s in ((5, 4), (3, 4), (5, 3)))
+    b = torch.randn(3, generator=g, dtype=torch.float64)
+
+    def loss(x, w, b):
+        return float((ref.act(name, x @ w.t() + b) * dy).sum())
+    dx, dw, db = ref.linear_bwd(x.float(), w.float(), dy, None, "none")[:3]
+    pre = x @ w.t() + b
+    d = dy * ref.act_grad(name, pre)
+    dx, dw, db = d @ w, d.t() @ x, d.sum(0)
+    h = 1e-6
+    for t, grad in ((x, dx), (w, dw), (b, db)):
+        for i in range(t.numel()):
+            old = float(t.view(-1)[i])
+            t.view(-1)[i] = old + h
+            up = loss(x, w, b)
+            t.view(-1)[i] = old - h
+            dn = loss(x, w, b)
+            t.view(-1)[i] = old
+            assert abs((up - dn) / (2 * h) - float(grad.view(-1)[i])) < 1e-7
+
+
+def test_reference_norm_gradients():
+    g = torch.Generator().manual_seed(4)
+    s, dy, dsum = (torch.randn(4, 6, generator=g, dtype=torch.float64) for _ in range(3))
+    w = torch.randn(6, generator=g, dtype=torch.float64)
+    b = torch.randn(6, generator=g, dtype=torch.float64)
+
+    def loss():
+        y = ref.norm_fwd(s, None, w, b, 1e-5)[0]
+        return float((y * dy).sum() + (s * dsum).sum())
+    _, _, mean, rstd = ref.norm_fwd(s, None, w, b, 1e-5)[:4]
+    dx, dw, db = ref.norm_bwd(s, dy, mean, rstd, w, dsum)[:3]
+    h = 1e-6
+    for t, grad in ((s, dx), (w, dw), (b, db)):
+        for i in range(t.numel()):
+            old = float(t.view(-1)[i])
+            t.view(-1)[i] = old + h
+            up = loss()
+            t.view(-1)[i] = old - h
+            dn = loss()
+            t.view(-1)[i] = old
+            assert abs((up - dn) / (2 * h) - float(grad.view(-1)[i])) < 1e-7
+
+
+def test_reference_checkpoint():
+    rng = np.random.default_rng(5)
+    x = (rng.standard_normal((7, 70)) * np.exp(rng.standard_normal((7, 70)))).astype(np.float32)
+    x[0, :32] = 0.0
+    x[1, 3] = np.inf
+    x[2, 40] = np.nan
+    q, e = ref.ckpt_pack(x)
+    y = ref.ckpt_unpack(q, e)
+    assert np.all(y[0, :32] == 0) and np.all(np.isnan(y[1, :32])) and np.all(np.isnan(y[2, 32:64]))
+    unit = np.repeat(np.exp2(e.astype(np.float64) - 127), 32, axis=1)[:, :70]
+    ok = np.isfinite(y)
+    err = np.abs(y - x)[ok]
+    lim = np.where(np.abs(q) == 127, 1.0, 0.5) * unit
+    assert np.all(err <= lim[ok])
+    top = np.abs(q[3:].astype(int))[:, :64].reshape(4, 2, 32).max(axis=2)
+    assert np.all((top >= 64) & (top <= 127))
+
+
+def test_headers_name_every_constant():
+    text = "".join(open(os.path.join(ROOT, "include", h)).read()
+                   for h in ("ss_linear.h", "ss_ckpt.h"))
+    for name in ("SS_LINEAR_FWD", "SS_LINEAR_BWD", "SS_LINEAR_BWD_CKPT", "SS_CKPT_BLOCK"):
+        m = re.search(r"#define %s (\d+)" % name, text)
+        assert m and int(m.group(1)) == getattr(B, name)
+    for name in ("SS_ACT_NONE", "SS_ACT_SILU", "SS_ACT_GELU", "SS_ACT_SOFTPLUS"):
+        m = re.search(r"%s = (\d+)" % name, text)
+        assert m and int(m.group(1)) == getattr(B, name)
