@@ -7,7 +7,7 @@
 // multiplied by v_mfma_f32_16x16x32_bf16 or v_mfma_f32_16x16x4_f32.  A lane
 // supplies 16 bytes of t at a time to either; the four fp32 products of those 16
 // bytes number t as 4 g + i (g = lane / 16) on both sides alike.
-#include "ss_linear.hpp"
+#include "ss_linear_mm.hpp"
 
 namespace ss {
 namespace {
@@ -238,8 +238,8 @@ __global__ __launch_bounds__(kThreads) void column_sum_kernel(const float* src, 
 size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 bool ptr16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
-// Splits of the contraction: enough work items for two rounds of the 256 CUs,
-// each at least 4 stages long.
+// Splits of the contraction over 128 x 128 tiles: enough work items for two
+// rounds of the 256 CUs, each at least 4 stages long.
 void plan_splits(int64_t nR, int64_t nS, int64_t nT, int step, int32_t* splits, int64_t* t_split) {
   const int64_t tiles = ((nR + kTile - 1) / kTile) * ((nS + kTile - 1) / kTile);
   int64_t k = tiles >= 256 ? 1 : (512 + tiles - 1) / tiles;
@@ -275,8 +275,21 @@ void run_mm(MmParams p, int32_t in_dtype, hipStream_t st) {
   p.vec_s = ptr16(p.S) && p.lds % e == 0;
   const int64_t items = int64_t(p.tiles_r) * p.tiles_s * p.splits;
   const unsigned blocks = unsigned(items < kMaxBlocks ? items : kMaxBlocks);
-  if (in_dtype == SS_BF16) mm_kernel<uint16_t, RT, ST><<<blocks, kThreads, 0, st>>>(p);
-  else mm_kernel<float, RT, ST><<<blocks, kThreads, 0, st>>>(p);
+  if (in_dtype == SS_BF16 && items <= kMaxBlocks &&
+      mm_operand_ok(p.R, p.ldr, RT ? p.nT : p.nR) && mm_operand_ok(p.S, p.lds, ST ? p.nT : p.nS)) {
+    const int64_t tiles = (p.nR + 255) / 256 * ((p.nS + 255) / 256);
+    const bool big = tiles >= 128;
+    if (big) {
+      p.tiles_r = int32_t((p.nR + 255) / 256);
+      p.tiles_s = (p.nS + 255) / 256;
+      p.splits = 1;
+    }
+    launch_mm(p, big, RT, ST, st);
+  } else if (in_dtype == SS_BF16) {
+    mm_kernel<uint16_t, RT, ST><<<blocks, kThreads, 0, st>>>(p);
+  } else {
+    mm_kernel<float, RT, ST><<<blocks, kThreads, 0, st>>>(p);
+  }
   if (p.splits > 1) {
     const int64_t n = (p.nR * ((p.nS + 3) / 4) + kThreads - 1) / kThreads;
     join_kernel<<<unsigned(n < kMaxBlocks ? n : kMaxBlocks), kThreads, 0, st>>>(p);

@@ -1,0 +1,515 @@
+// The linear projections' large bf16 products for gfx950: 256 x 256 output tiles
+// on the matrix cores.
+//
+// A workgroup is 8 waves, one workgroup to a CU; a wave owns 128 (s) x 64 (r) of
+// the tile as 8 x 4 accumulators of v_mfma_f32_16x16x32_bf16 (128 registers).  A
+// stage is 64 of the contraction: R 256 x 64 and S 256 x 64 bf16, copied from
+// global memory straight into LDS (16 bytes per lane), two stages deep.
+//
+// Schedule.  The waves of a SIMD form two groups that run half a step apart: while
+// one group multiplies, the other reads its next fragments from LDS and issues
+// copies, and a barrier swaps the roles.  A stage takes four such turns; a turn
+// multiplies 4 S fragments with 4 R fragments (16 MFMAs):
+//     turn 0: S rows lo, t 0..31     turn 1: S lo, t 32..63
+//     turn 2: S rows hi, t 0..31     turn 3: S hi, t 32..63
+// R fragments of both t halves stay in registers from turns 0 and 1 on, so R and
+// S lo of a buffer are free after turn 1 and are refilled (stage k + 2) in turns 2
+// and 3; S hi (stage k + 1) is refilled in turns 0 and 1.  Every copy thus has a
+// whole stage of time to land, and a wave waits for the copies of the next turn
+// pair with the later ones still in flight (8 instructions).  Stages past the end
+// are issued as well, out of the buffer's range (no memory is read), so that the
+// counts hold to the last stage.
+//
+// LDS layouts, permuted at the copy's source addresses (its destination is linear)
+// so that fragment reads touch all banks evenly (no conflicts by the counters):
+//   t contiguous:   128-byte rows of t, 16-byte unit c of row i at c ^ (i & 7);
+//                   a fragment is one 16-byte read per lane;
+//   t strided:      rows of t hold the operand's 256 (R) or 128 (S half) columns,
+//                   32-byte unit u of row t at u ^ f(t), f = t & 3 | (t & 8) / 2;
+//                   a fragment is two transposing 8-byte reads per lane
+//                   (ds_read_b64_tr_b16: 16 lanes read 4 rows of 16 and each
+//                   receives one column).
+// The transposing reads are written in assembly, with their wait in the same
+// block: before the builtin the compiler waits for every copy in flight.
+#include "ss_linear_mm.hpp"
+
+namespace ss {
+
+namespace {
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) void* lds_ptr;
+
+constexpr int kTile = 256;
+constexpr int kStep = 64;                          // t per stage
+constexpr int kThreads = 512;
+constexpr int kOffR = 0, kOffLo = 65536, kOffHi = 98304, kOffEpi = 131072;
+constexpr int kLds = 163840;
+
+#if defined(__HIP_DEVICE_COMPILE__)
+
+template <int N>
+__device__ __forceinline__ void wait_copies() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+// End of a turn: this wave's LDS reads have landed, then the barrier.  Nothing
+// moves across it.
+__device__ __forceinline__ void turn_end() {
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
+
+__device__ __forceinline__ bf16x8 join8(s16x4 x, s16x4 y) {
+  struct P { s16x4 x, y; };
+  return __builtin_bit_cast(bf16x8, P{x, y});
+}
+// Four transposed fragments at LDS addresses a[0..3] (+ OFF; the second half of
+// t, four rows on, at + HALF), and their wait.
+template <int OFF, int HALF>
+__device__ __forceinline__ void read_tr4(const uint32_t (&a)[4], bf16x8 (&f)[4]) {
+  s16x4 x0, x1, x2, x3, y0, y1, y2, y3;
+  asm volatile(
+      "ds_read_b64_tr_b16 %0, %8 offset:%12\n"
+      "ds_read_b64_tr_b16 %1, %8 offset:%13\n"
+      "ds_read_b64_tr_b16 %2, %9 offset:%12\n"
+      "ds_read_b64_tr_b16 %3, %9 offset:%13\n"
+      "ds_read_b64_tr_b16 %4, %10 offset:%12\n"
+      "ds_read_b64_tr_b16 %5, %10 offset:%13\n"
+      "ds_read_b64_tr_b16 %6, %11 offset:%12\n"
+      "ds_read_b64_tr_b16 %7, %11 offset:%13\n"
+      "s_waitcnt lgkmcnt(0)"
+      : "=&v"(x0), "=&v"(y0), "=&v"(x1), "=&v"(y1), "=&v"(x2), "=&v"(y2), "=&v"(x3), "=&v"(y3)
+      : "v"(a[0]), "v"(a[1]), "v"(a[2]), "v"(a[3]), "n"(OFF), "n"(OFF + HALF)
+      : "memory");
+  f[0] = join8(x0, y0);
+  f[1] = join8(x1, y1);
+  f[2] = join8(x2, y2);
+  f[3] = join8(x3, y3);
+}
+// The same for two sets of four.
+template <int OFFA, int HALFA, int OFFB, int HALFB>
+__device__ __forceinline__ void read_tr8(const uint32_t (&a)[4], bf16x8 (&fa)[4],
+                                         const uint32_t (&b)[4], bf16x8 (&fb)[4]) {
+  s16x4 x0, x1, x2, x3, y0, y1, y2, y3, u0, u1, u2, u3, v0, v1, v2, v3;
+  asm volatile(
+      "ds_read_b64_tr_b16 %0, %16 offset:%24\n"
+      "ds_read_b64_tr_b16 %1, %16 offset:%25\n"
+      "ds_read_b64_tr_b16 %2, %17 offset:%24\n"
+      "ds_read_b64_tr_b16 %3, %17 offset:%25\n"
+      "ds_read_b64_tr_b16 %4, %18 offset:%24\n"
+      "ds_read_b64_tr_b16 %5, %18 offset:%25\n"
+      "ds_read_b64_tr_b16 %6, %19 offset:%24\n"
+      "ds_read_b64_tr_b16 %7, %19 offset:%25\n"
+      "ds_read_b64_tr_b16 %8, %20 offset:%26\n"
+      "ds_read_b64_tr_b16 %9, %20 offset:%27\n"
+      "ds_read_b64_tr_b16 %10, %21 offset:%26\n"
+      "ds_read_b64_tr_b16 %11, %21 offset:%27\n"
+      "ds_read_b64_tr_b16 %12, %22 offset:%26\n"
+      "ds_read_b64_tr_b16 %13, %22 offset:%27\n"
+      "ds_read_b64_tr_b16 %14, %23 offset:%26\n"
+      "ds_read_b64_tr_b16 %15, %23 offset:%27\n"
+      "s_waitcnt lgkmcnt(0)"
+      : "=&v"(x0), "=&v"(y0), "=&v"(x1), "=&v"(y1), "=&v"(x2), "=&v"(y2), "=&v"(x3), "=&v"(y3),
+        "=&v"(u0), "=&v"(v0), "=&v"(u1), "=&v"(v1), "=&v"(u2), "=&v"(v2), "=&v"(u3), "=&v"(v3)
+      : "v"(a[0]), "v"(a[1]), "v"(a[2]), "v"(a[3]), "v"(b[0]), "v"(b[1]), "v"(b[2]), "v"(b[3]),
+        "n"(OFFA), "n"(OFFA + HALFA), "n"(OFFB), "n"(OFFB + HALFB)
+      : "memory");
+  fa[0] = join8(x0, y0);
+  fa[1] = join8(x1, y1);
+  fa[2] = join8(x2, y2);
+  fa[3] = join8(x3, y3);
+  fb[0] = join8(u0, v0);
+  fb[1] = join8(u1, v1);
+  fb[2] = join8(u2, v2);
+  fb[3] = join8(u3, v3);
+}
+
+// Byte offsets of one wave-wide copy instruction (unit ids id = (j 8 + wave) 64 +
+// lane of the stage) from the tile's origin; kOutOfRange outside the operand.
+// TC: rows of t.  W: columns of the stage; HALF: they are columns 0..63 and
+// 128..191 of the tile (an S half).  tpos: the unit's first t.
+template <bool TC, int W, bool HALF>
+__device__ __forceinline__ uint32_t copy_offset(int id, int64_t ld, int64_t i0, int64_t n,
+                                                int* tpos) {
+  if constexpr (TC) {
+    const int q = id / 8, c = (id & 7) ^ (q & 7);
+    const int row = HALF ? (q & 63) + (q >> 6) * 128 : q;
+    *tpos = c * 8;
+    return i0 + row < n ? uint32_t(row * ld * 2 + c * 16) : kOutOfRange;
+  } else {
+    constexpr int per = W / 8;
+    const int t = id / per, c1 = id % per;
+    const int f = (t & 3) | (((t >> 3) & 1) << 2);
+    const int c = (((c1 >> 1) ^ f) << 1) | (c1 & 1);
+    const int col = HALF ? (c * 8 & 63) + (c >> 3) * 128 : c * 8;
+    *tpos = t;
+    return i0 + col < n ? uint32_t(t * ld * 2 + col * 2) : kOutOfRange;
+  }
+}
+
+// Epilogue of 16 rows x 64 columns of a wave: the accumulators (lane: row lane &
+// 15, four neighbours of each 16-column piece q[i]) are turned through 4 KB of
+// LDS into whole rows, 8 columns per lane.  The loops are rolled: unrolled, the
+// epilogue outgrew the instruction cache and cost 20 us a tile.
+template <int ACT>
+__device__ __forceinline__ void rows_out(const MmParams& p, char* sl, const f32x4 (&q)[4],
+                                         int64_t r, int32_t s, int split) {
+  const int lane = threadIdx.x & 63, m = lane & 15, g = lane >> 4;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    *reinterpret_cast<f32x4*>(sl + m * 256 + (((4 * i + g) ^ m) << 4)) = q[i];
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  if ((p.nS & 7) == 0) {
+#pragma nounroll
+    for (int h = 0; h < 2; ++h) {
+      const int row = h * 8 + lane / 8, u = (lane & 7) * 2;
+      const f32x4 x = *reinterpret_cast<const f32x4*>(sl + row * 256 + ((u ^ row) << 4));
+      const f32x4 y = *reinterpret_cast<const f32x4*>(sl + row * 256 + (((u + 1) ^ row) << 4));
+      float v[8] = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
+      epilogue8<ACT>(p, r + row, s + u * 4, v, split);
+    }
+  } else {
+#pragma nounroll
+    for (int row = 0; row < 16; ++row) {
+      const float v = *reinterpret_cast<const float*>(sl + row * 256 + (((lane / 4) ^ row) << 4) +
+                                                      (lane & 3) * 4);
+      epilogue1<ACT>(p, r + row, s + lane, v, split);
+    }
+  }
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+}
+
+template <bool RT, bool ST, int ACT>
+__device__ __forceinline__ void mm256_tile(const MmParams& p, char* lds, int64_t tr, int ts) {
+  const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int m = lane & 15, g = lane >> 4;
+  const int64_t r0 = tr * kTile, s0 = int64_t(ts) * kTile;
+  uint32_t vr[4], vlo[2], vhi[2];
+  int tpr[4], tps[2];
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    vr[j] = copy_offset<RT, 256, false>((j * 8 + wv) * 64 + lane, p.ldr, r0, p.nR, &tpr[j]);
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int id = (j * 8 + wv) * 64 + lane;
+    vlo[j] = copy_offset<ST, 128, true>(id, p.lds, s0, p.nS, &tps[j]);
+    vhi[j] = copy_offset<ST, 128, true>(id, p.lds, s0 + 64, p.nS, &tps[j]);
+  }
+  const char* pr = static_cast<const char*>(p.R) + (RT ? r0 * p.ldr : r0) * 2;
+  const char* ps = static_cast<const char*>(p.S) + (ST ? s0 * p.lds : s0) * 2;
+  const char* psh = ps + (ST ? 64 * p.lds : 64) * 2;
+  const int64_t dr = RT ? kStep * 2 : p.ldr * kStep * 2;
+  const int64_t ds = ST ? kStep * 2 : p.lds * kStep * 2;
+  const int nk = int((p.nT + kStep - 1) / kStep);
+  const int rem = int(p.nT - int64_t(nk - 1) * kStep);      // t of the last stage, 1..64
+
+  // resource of stage k; past the last one no byte is in range
+  auto rsrc = [&](const char* base, int64_t step, int k) {
+    return __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<char*>(base + (k < nk ? k : nk - 1) * step), short(0),
+        k < nk ? 0x7fffffff : 0, 0x00020000);
+  };
+  auto copy = [&](Rsrc src, int dst, uint32_t off) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(src, (lds_ptr)(lds + dst), 16, off, 0, 0, 0);
+  };
+  // a partial last stage: units past the contraction's end read as zero
+  auto mask_r = [&](int k) {
+    if (k == nk - 1 && rem < kStep) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) vr[j] = tpr[j] < rem ? vr[j] : kOutOfRange;
+    }
+  };
+  auto mask_s = [&](int k, uint32_t (&v)[2]) {
+    if (k == nk - 1 && rem < kStep) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) v[j] = tps[j] < rem ? v[j] : kOutOfRange;
+    }
+  };
+  auto copy_r = [&](int k, int j) {
+    copy(rsrc(pr, dr, k), kOffR + (k & 1) * 32768 + (j * 8 + wv) * 1024, vr[j]);
+  };
+  auto copy_lo = [&](int k, int j) {
+    copy(rsrc(ps, ds, k), kOffLo + (k & 1) * 16384 + (j * 8 + wv) * 1024, vlo[j]);
+  };
+  auto copy_hi = [&](int k, int j) {
+    copy(rsrc(psh, ds, k), kOffHi + (k & 1) * 16384 + (j * 8 + wv) * 1024, vhi[j]);
+  };
+
+  const int wr = (wv >> 1) * 64, wsn = (wv & 1) * 128;      // the wave's corner
+  // fragment addresses in buffer 0; the other buffer is a constant away
+  uint32_t ar[4], as[4];
+  const uint32_t l0 = uint32_t(reinterpret_cast<uintptr_t>((lds_ptr)lds));
+  const int f = (m >> 2) | ((g & 1) << 2);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    // t contiguous: unit g of row (h 4 + g ^ lane & 7), h by XOR of 64 bytes
+    ar[i] = l0 + kOffR +
+            (RT ? uint32_t((wr + i * 16 + m) * 128 + ((g ^ (lane & 7)) << 4))
+                : uint32_t((g * 8 + (m >> 2)) * 512 + (((wr / 16 + i) ^ f) << 5) + (m & 3) * 8));
+    as[i] = l0 + kOffLo +
+            (ST ? uint32_t((wsn / 2 + i * 16 + m) * 128 + ((g ^ (lane & 7)) << 4))
+                : uint32_t((g * 8 + (m >> 2)) * 256 + (((wsn / 32 + i) ^ f) << 5) + (m & 3) * 8));
+  }
+  auto at = [&](uint32_t a) {
+    return *(const __attribute__((address_space(3))) bf16x8*)(uintptr_t(a));
+  };
+
+  f32x4 acc[8][4];
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+
+  mask_r(0);
+  mask_s(0, vlo);
+  mask_s(0, vhi);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) copy_r(0, j);
+#pragma unroll
+  for (int j = 0; j < 2; ++j) copy_lo(0, j);
+#pragma unroll
+  for (int j = 0; j < 2; ++j) copy_hi(0, j);
+  mask_r(1);
+  mask_s(1, vlo);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) copy_r(1, j);
+#pragma unroll
+  for (int j = 0; j < 2; ++j) copy_lo(1, j);
+  wait_copies<6>();
+  turn_end();
+  if (wv >= 4) turn_end();            // the second group runs one turn behind
+
+  bf16x8 b[2][4], a[4];
+  auto mma = [&](int i0, int h) {
+    __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        acc[i0 + i][j] =
+            __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[i], b[h][j], acc[i0 + i][j], 0, 0, 0);
+    __builtin_amdgcn_s_setprio(0);
+  };
+  // fragments of turn (half of S, t half): the S part, and R's with S lo
+  auto read = [&](auto hi_c, auto h_c) {
+    constexpr int hi = decltype(hi_c)::value, h = decltype(h_c)::value;
+    constexpr int so = hi * (kOffHi - kOffLo) + (ST ? 0 : h * 32 * 256);
+    constexpr int ro = RT ? 0 : h * 32 * 512;
+    if constexpr (hi == 0 && RT) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) b[h][j] = at(ar[j] ^ (h * 64));
+    }
+    if constexpr (ST) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) a[i] = at((as[i] ^ (h * 64)) + so);
+    }
+    if constexpr (hi == 0 && !RT && !ST) read_tr8<ro, 2048, so, 1024>(ar, b[h], as, a);
+    else if constexpr (!ST) read_tr4<so, 1024>(as, a);
+    else if constexpr (hi == 0 && !RT) read_tr4<ro, 2048>(ar, b[h]);
+  };
+  using I0 = std::integral_constant<int, 0>;
+  using I1 = std::integral_constant<int, 1>;
+  for (int k = 0; k < nk; ++k) {
+    mask_s(k + 1, vhi);
+    copy_hi(k + 1, 0);
+    read(I0{}, I0{});
+    turn_end();
+    mma(0, 0);
+    turn_end();
+    copy_hi(k + 1, 1);
+    read(I0{}, I1{});
+    wait_copies<8>();
+    turn_end();
+    mma(0, 1);
+    turn_end();
+    mask_r(k + 2);
+    mask_s(k + 2, vlo);
+    copy_r(k + 2, 0);
+    copy_r(k + 2, 1);
+    copy_lo(k + 2, 0);
+    read(I1{}, I0{});
+    turn_end();
+    mma(4, 0);
+    turn_end();
+    copy_r(k + 2, 2);
+    copy_r(k + 2, 3);
+    copy_lo(k + 2, 1);
+    read(I1{}, I1{});
+    wait_copies<8>();
+    turn_end();
+    mma(4, 1);
+    turn_end();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      ar[i] ^= 32768;
+      as[i] ^= 16384;
+    }
+  }
+  if (wv < 4) turn_end();
+  wait_copies<0>();
+
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const f32x4 q[4] = {acc[4 * c][j], acc[4 * c + 1][j], acc[4 * c + 2][j], acc[4 * c + 3][j]};
+      rows_out<ACT>(p, lds + kOffEpi + wv * 4096, q, r0 + wr + 16 * j,
+                    int32_t(s0) + wsn + 64 * c, 0);
+    }
+}
+#endif
+
+template <bool RT, bool ST, int ACT>
+__global__ __launch_bounds__(kThreads, 2) void mm256_kernel(MmParams p) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  __shared__ __attribute__((aligned(1024))) char lds[kLds];
+  const int64_t tiles = int64_t(p.tiles_r) * p.tiles_s;
+  int64_t tr;
+  int ts;
+  tile_of(p, xcd_contiguous(blockIdx.x, tiles), &tr, &ts);
+  mm256_tile<RT, ST, ACT>(p, lds, tr, ts);
+#endif
+}
+
+// 128 x 128 tiles for problems too small to fill the GPU with 256 x 256 ones: 4
+// waves of 64 x 64, the same stages and layouts, two buffers (64 KB, so two
+// workgroups share a CU and hide each other's barriers); the contraction may be
+// split.
+constexpr int kSmall = 128;
+constexpr int kSmallThreads = 256;
+
+template <bool RT, bool ST, int ACT>
+__global__ __launch_bounds__(kSmallThreads, 2) void mm128_kernel(MmParams p) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  __shared__ __attribute__((aligned(1024))) char lds[65536];
+  const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int m = lane & 15, g = lane >> 4;
+  const int64_t tiles = int64_t(p.tiles_r) * p.tiles_s;
+  const int split = int(int64_t(blockIdx.x) / tiles);
+  int64_t tr;
+  int ts;
+  tile_of(p, xcd_contiguous(int64_t(blockIdx.x) - split * tiles, tiles), &tr, &ts);
+  const int64_t r0 = tr * kSmall, s0 = int64_t(ts) * kSmall;
+  const int64_t t0 = split * p.t_split;
+  const int64_t t1 = t0 + p.t_split < p.nT ? t0 + p.t_split : p.nT;
+  uint32_t vr[4], vs[4];
+  int tpr[4], tps[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int id = (j * 4 + wv) * 64 + lane;
+    vr[j] = copy_offset<RT, 128, false>(id, p.ldr, r0, p.nR, &tpr[j]);
+    vs[j] = copy_offset<ST, 128, false>(id, p.lds, s0, p.nS, &tps[j]);
+  }
+  const char* pr = static_cast<const char*>(p.R) + (RT ? r0 * p.ldr + t0 : t0 * p.ldr + r0) * 2;
+  const char* ps = static_cast<const char*>(p.S) + (ST ? s0 * p.lds + t0 : t0 * p.lds + s0) * 2;
+  const int64_t dr = RT ? kStep * 2 : p.ldr * kStep * 2;
+  const int64_t ds = ST ? kStep * 2 : p.lds * kStep * 2;
+  const int nk = int((t1 - t0 + kStep - 1) / kStep);
+  const int rem = int(t1 - t0 - int64_t(nk - 1) * kStep);
+  auto copy = [&](int k) {
+    if (k == nk - 1 && rem < kStep) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        vr[j] = tpr[j] < rem ? vr[j] : kOutOfRange;
+        vs[j] = tps[j] < rem ? vs[j] : kOutOfRange;
+      }
+    }
+    const Rsrc a = make_rsrc(pr + k * dr), b = make_rsrc(ps + k * ds);
+    char* d = lds + (k & 1) * 32768 + wv * 1024;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(a, (lds_ptr)(d + j * 4096), 16, vr[j], 0, 0, 0);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(b, (lds_ptr)(d + 16384 + j * 4096), 16, vs[j], 0, 0,
+                                               0);
+  };
+  const int wr = (wv >> 1) * 64, wsn = (wv & 1) * 64;
+  uint32_t ar[4], as[4];
+  const uint32_t l0 = uint32_t(reinterpret_cast<uintptr_t>((lds_ptr)lds));
+  const int f = (m >> 2) | ((g & 1) << 2);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    ar[i] = l0 + (RT ? uint32_t((wr + i * 16 + m) * 128 + ((g ^ (lane & 7)) << 4))
+                     : uint32_t((g * 8 + (m >> 2)) * 256 + (((wr / 16 + i) ^ f) << 5) + (m & 3) * 8));
+    as[i] = l0 + 16384 +
+            (ST ? uint32_t((wsn + i * 16 + m) * 128 + ((g ^ (lane & 7)) << 4))
+                : uint32_t((g * 8 + (m >> 2)) * 256 + (((wsn / 16 + i) ^ f) << 5) + (m & 3) * 8));
+  }
+  auto at = [&](uint32_t a) {
+    return *(const __attribute__((address_space(3))) bf16x8*)(uintptr_t(a));
+  };
+  f32x4 acc[4][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+  auto part = [&](auto h_c) {
+    constexpr int h = decltype(h_c)::value;
+    bf16x8 a[4], b[4];
+    if constexpr (RT) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) b[j] = at(ar[j] ^ (h * 64));
+    }
+    if constexpr (ST) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) a[i] = at(as[i] ^ (h * 64));
+    }
+    if constexpr (!RT && !ST) read_tr8<h * 8192, 1024, h * 8192, 1024>(ar, b, as, a);
+    else if constexpr (!ST) read_tr4<h * 8192, 1024>(as, a);
+    else if constexpr (!RT) read_tr4<h * 8192, 1024>(ar, b);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[i], b[j], acc[i][j], 0, 0, 0);
+  };
+  copy(0);
+  for (int k = 0; k < nk; ++k) {
+    wait_copies<0>();
+    turn_end();       // stage k is whole, and stage k - 1 has been read by every wave
+    if (k + 1 < nk) copy(k + 1);
+    part(std::integral_constant<int, 0>{});
+    part(std::integral_constant<int, 1>{});
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      ar[i] ^= 32768;
+      as[i] ^= 32768;
+    }
+  }
+  turn_end();
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const f32x4 q[4] = {acc[0][j], acc[1][j], acc[2][j], acc[3][j]};
+    rows_out<ACT>(p, lds + wv * 4096, q, r0 + wr + 16 * j, int32_t(s0) + wsn, split);
+  }
+#endif
+}
+
+template <bool RT, bool ST, int ACT>
+void run(const MmParams& p, bool big, hipStream_t stream) {
+  const unsigned blocks = unsigned(p.tiles_r) * unsigned(p.tiles_s) * unsigned(p.splits);
+  if (big) mm256_kernel<RT, ST, ACT><<<blocks, kThreads, 0, stream>>>(p);
+  else mm128_kernel<RT, ST, ACT><<<blocks, kSmallThreads, 0, stream>>>(p);
+}
+
+}  // namespace
+
+void launch_mm(const MmParams& p, bool big, bool rt, bool st, hipStream_t stream) {
+  if (rt && st) {
+    // splits keep the activation for the join
+    switch (p.splits > 1 ? SS_ACT_NONE : p.act) {
+      case SS_ACT_SILU: return run<true, true, SS_ACT_SILU>(p, big, stream);
+      case SS_ACT_GELU: return run<true, true, SS_ACT_GELU>(p, big, stream);
+      case SS_ACT_SOFTPLUS: return run<true, true, SS_ACT_SOFTPLUS>(p, big, stream);
+      default: return run<true, true, SS_ACT_NONE>(p, big, stream);
+    }
+  }
+  if (rt) run<true, false, SS_ACT_NONE>(p, big, stream);
+  else run<false, false, SS_ACT_NONE>(p, big, stream);
+}
+
+}  // namespace ss
