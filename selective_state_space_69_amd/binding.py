@@ -617,21 +617,33 @@ def ssd_step(h, x, dt, A, B, C, D=None, dt_bias=None, softplus=True, out_dtype=t
 
 
 # ------------------------------------------- the operators around the scan in a block
+# Decode calls of these take a few microseconds on the GPU, so their wrappers keep
+# to plain integers (devices, streams, pointers) on the way to the library.
 def _dt(t, name):
-    if t not in _DTYPE:
+    d = _DTYPE.get(t)
+    if d is None:
         raise ValueError("%s must be float32 or bfloat16 (got %s)" % (name, t))
-    return _DTYPE[t]
+    return d
 
 
-def _f32(**tensors):
-    for name, t in tensors.items():
-        if t is not None and t.dtype != torch.float32:
-            raise ValueError("%s must be float32 (got %s)" % (name, t.dtype))
+def _f32(t, name):
+    if t is not None and t.dtype is not torch.float32:
+        raise ValueError("%s must be float32 (got %s)" % (name, t.dtype))
 
 
-def _shape(name, t, shape):
-    if t is not None and tuple(t.shape) != tuple(shape):
+def _arg(t, name, shape):
+    """Device pointer of a dense tensor of this shape (None: no tensor)."""
+    if t is None:
+        return None
+    if t.shape != shape:
         raise ValueError("%s must have shape %s (got %s)" % (name, tuple(shape), tuple(t.shape)))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous (got strides %s)" % (name, tuple(t.stride())))
+    return t.data_ptr()
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
 
 
 def _x_stride(x, name):
@@ -647,35 +659,38 @@ def _x_stride(x, name):
     return s
 
 
-def _on_device(fn, stream, tensors):
-    """fn() with the tensors' GPU and the stream current, so that its outputs and
-    workspace are allocated for the stream the kernels run on.  stream: None (the
-    device's current one), a torch stream or a raw hipStream_t; memory of the
-    tensors is kept from reuse until a stream other than their own is done."""
-    dev = None
+def _on_device(fn, stream, tensors, *args):
+    """fn(raw stream, *args) with the tensors' GPU and the stream current, so that
+    its outputs and workspace are allocated for the stream the kernels run on.
+    stream: None (the device's current one), a torch stream or a raw hipStream_t;
+    memory of the tensors is kept from reuse until a stream other than their own
+    is done."""
+    dev = -1
     for t in tensors:
         if t is None:
             continue
-        if not t.is_cuda:
+        d = t.get_device()
+        if d < 0:
             raise ValueError("all tensors must be on the GPU")
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
+        if dev < 0:
+            dev = d
+        elif d != dev:
             raise ValueError("all tensors must be on one GPU")
     if stream is None:
-        if dev.index == torch.cuda.current_device():
-            return fn()
+        raw = torch._C._cuda_getCurrentRawStream(dev)
+        if dev == torch._C._cuda_getDevice():
+            return fn(raw, *args)
         with torch.cuda.device(dev):
-            return fn()
+            return fn(raw, *args)
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream, device=dev)
-    if stream.device != dev:
+    if stream.device.index != dev:
         raise ValueError("the stream belongs to another GPU than the tensors")
     for t in tensors:
         if t is not None:
             t.record_stream(stream)
     with torch.cuda.stream(stream):
-        return fn()
+        return fn(stream.cuda_stream, *args)
 
 
 def layernorm_fwd(x, weight=None, bias=None, residual=None, eps=1e-5, out_dtype=None,
@@ -685,29 +700,31 @@ def layernorm_fwd(x, weight=None, bias=None, residual=None, eps=1e-5, out_dtype=
     Returns a dict: y (out_dtype, default x's), sum (s in residual's dtype, the
     new residual stream; None without a residual), mean and rstd (float32, None
     unless save_stats)."""
-    def run():
-        _dense(weight=weight, bias=bias, residual=residual)
-        _f32(weight=weight, bias=bias)
-        dim = x.shape[-1]
-        _shape("weight", weight, (dim,))
-        _shape("bias", bias, (dim,))
-        _shape("residual", residual, x.shape)
-        odt = x.dtype if out_dtype is None else out_dtype
-        lead = x.shape[:-1]
-        desc = make_norm_desc(x.numel() // dim if dim else 0, dim, _x_stride(x, "x"),
-                              _dt(x.dtype, "x"),
-                              _dt(x.dtype if residual is None else residual.dtype, "residual"),
-                              _dt(odt, "out_dtype"), eps)
-        y = torch.empty(x.shape, dtype=odt, device=x.device)
-        s = None if residual is None else torch.empty_like(residual)
-        mean = rstd = None
-        if save_stats:
-            mean = torch.empty(lead, dtype=torch.float32, device=x.device)
-            rstd = torch.empty(lead, dtype=torch.float32, device=x.device)
-        _check(ss_layernorm_fwd(desc, x, residual, weight, bias, y, s, mean, rstd),
-               "ss_layernorm_fwd")
-        return {"y": y, "sum": s, "mean": mean, "rstd": rstd}
-    return _on_device(run, stream, (x, weight, bias, residual))
+    return _on_device(_layernorm_fwd, stream, (x, weight, bias, residual), x, weight, bias,
+                      residual, eps, x.dtype if out_dtype is None else out_dtype, save_stats)
+
+
+def _layernorm_fwd(raw, x, weight, bias, residual, eps, odt, save_stats):
+    shape = x.shape
+    dim = shape[-1]
+    _f32(weight, "weight")
+    _f32(bias, "bias")
+    dt = _dt(x.dtype, "x")
+    desc = ss_norm_desc_t(x.numel() // dim if dim else 0, dim, _x_stride(x, "x"), dt,
+                          dt if residual is None else _dt(residual.dtype, "residual"),
+                          _dt(odt, "out_dtype"), eps)
+    wp, bp = _arg(weight, "weight", (dim,)), _arg(bias, "bias", (dim,))
+    rp = _arg(residual, "residual", shape)
+    y = x.new_empty(shape, dtype=odt)
+    s = None if residual is None else residual.new_empty(shape)
+    mean = rstd = None
+    if save_stats:
+        mean = x.new_empty(shape[:-1], dtype=torch.float32)
+        rstd = x.new_empty(shape[:-1], dtype=torch.float32)
+    _check(load_library().ss_layernorm_fwd(ctypes.byref(desc), x.data_ptr(), rp, wp, bp,
+                                           y.data_ptr(), _ptr(s), _ptr(mean), _ptr(rstd), raw),
+           "ss_layernorm_fwd")
+    return {"y": y, "sum": s, "mean": mean, "rstd": rstd}
 
 
 def layernorm_bwd(s, dy, mean, rstd, weight=None, dsum=None, dx_dtype=None, stream=None):
@@ -715,31 +732,35 @@ def layernorm_bwd(s, dy, mean, rstd, weight=None, dsum=None, dx_dtype=None, stre
     sum; a row stride is taken), dsum the gradient that reaches s from elsewhere.
     Returns a dict: dx (dx_dtype, default dsum's dtype or float32; the gradient
     of x and of the residual alike), dweight and dbias (float32)."""
-    def run():
-        _dense(weight=weight, mean=mean, rstd=rstd, dy=dy, dsum=dsum)
-        _f32(weight=weight, mean=mean, rstd=rstd)
-        dim = s.shape[-1]
-        _shape("weight", weight, (dim,))
-        _shape("mean", mean, s.shape[:-1])
-        _shape("rstd", rstd, s.shape[:-1])
-        _shape("dy", dy, s.shape)
-        _shape("dsum", dsum, s.shape)
-        rdt = dx_dtype
-        if rdt is None:
-            rdt = torch.float32 if dsum is None else dsum.dtype
-        if dsum is not None and dsum.dtype != rdt:
-            raise ValueError("dx_dtype must be dsum's dtype")
-        desc = make_norm_desc(s.numel() // dim if dim else 0, dim, _x_stride(s, "s"),
-                              _dt(s.dtype, "s"), _dt(rdt, "dx_dtype"), _dt(dy.dtype, "dy"))
-        dx = torch.empty(s.shape, dtype=rdt, device=s.device)
-        dw = torch.empty(dim, dtype=torch.float32, device=s.device)
-        db = torch.empty(dim, dtype=torch.float32, device=s.device)
-        nb = ss_layernorm_workspace_bytes(desc)
-        ws = workspace(nb, s.device)
-        _check(ss_layernorm_bwd(desc, s, weight, mean, rstd, dy, dsum, dx, dw, db, ws, nb),
-               "ss_layernorm_bwd")
-        return {"dx": dx, "dweight": dw, "dbias": db}
-    return _on_device(run, stream, (s, dy, mean, rstd, weight, dsum))
+    if dx_dtype is None:
+        dx_dtype = torch.float32 if dsum is None else dsum.dtype
+    return _on_device(_layernorm_bwd, stream, (s, dy, mean, rstd, weight, dsum), s, dy, mean, rstd,
+                      weight, dsum, dx_dtype)
+
+
+def _layernorm_bwd(raw, s, dy, mean, rstd, weight, dsum, rdt):
+    shape = s.shape
+    dim = shape[-1]
+    _f32(weight, "weight")
+    _f32(mean, "mean")
+    _f32(rstd, "rstd")
+    if dsum is not None and dsum.dtype != rdt:
+        raise ValueError("dx_dtype must be dsum's dtype")
+    desc = ss_norm_desc_t(s.numel() // dim if dim else 0, dim, _x_stride(s, "s"),
+                          _dt(s.dtype, "s"), _dt(rdt, "dx_dtype"), _dt(dy.dtype, "dy"), 1.0)
+    wp, mp = _arg(weight, "weight", (dim,)), _arg(mean, "mean", shape[:-1])
+    rp, dyp = _arg(rstd, "rstd", shape[:-1]), _arg(dy, "dy", shape)
+    dsp = _arg(dsum, "dsum", shape)
+    dx = s.new_empty(shape, dtype=rdt)
+    dw = s.new_empty((dim,), dtype=torch.float32)
+    db = s.new_empty((dim,), dtype=torch.float32)
+    lib = load_library()
+    nb = lib.ss_layernorm_workspace_bytes(ctypes.byref(desc))
+    ws = workspace(nb, s.device)
+    _check(lib.ss_layernorm_bwd(ctypes.byref(desc), s.data_ptr(), wp, mp, rp, dyp, dsp,
+                                dx.data_ptr(), dw.data_ptr(), db.data_ptr(), _ptr(ws), nb, raw),
+           "ss_layernorm_bwd")
+    return {"dx": dx, "dweight": dw, "dbias": db}
 
 
 def linear_fwd(x, w, bias=None, residual=None, act="none", out_dtype=None, save_pre=False,
@@ -749,28 +770,32 @@ def linear_fwd(x, w, bias=None, residual=None, act="none", out_dtype=None, save_
     bfloat16, act one of "none", "silu", "gelu", "softplus".  Returns y (..., N)
     in out_dtype (default x's), and with save_pre the pre-activation values in
     x's dtype as well."""
-    def run():
-        _dense(w=w, bias=bias, residual=residual)
-        _f32(bias=bias)
-        n, k = w.shape
-        oshape = (*x.shape[:-1], n)
-        _shape("x", x, (*x.shape[:-1], k))
-        _shape("bias", bias, (n,))
-        _shape("residual", residual, oshape)
-        if x.dtype != w.dtype:
-            raise ValueError("x and w must have one dtype")
-        odt = x.dtype if out_dtype is None else out_dtype
-        desc = make_linear_desc(x.numel() // k if k else 0, k, n, _x_stride(x, "x"),
-                                _dt(x.dtype, "x"), _dt(odt, "out_dtype"),
-                                _dt(odt if residual is None else residual.dtype, "residual"),
-                                SS_F32, _ACT[act])
-        y = torch.empty(oshape, dtype=odt, device=x.device)
-        pre = torch.empty(oshape, dtype=x.dtype, device=x.device) if save_pre else None
-        nb = ss_linear_workspace_bytes(desc, SS_LINEAR_FWD)
-        ws = workspace(nb, x.device)
-        _check(ss_linear_fwd(desc, x, w, bias, residual, y, pre, ws, nb), "ss_linear_fwd")
-        return (y, pre) if save_pre else y
-    return _on_device(run, stream, (x, w, bias, residual))
+    return _on_device(_linear_fwd, stream, (x, w, bias, residual), x, w, bias, residual, _ACT[act],
+                      x.dtype if out_dtype is None else out_dtype, save_pre)
+
+
+def _linear_fwd(raw, x, w, bias, residual, act, odt, save_pre):
+    n, k = w.shape
+    oshape = (*x.shape[:-1], n)
+    if x.shape[-1] != k:
+        raise ValueError("x must have %d columns (got %d)" % (k, x.shape[-1]))
+    if x.dtype != w.dtype:
+        raise ValueError("x and w must have one dtype")
+    _f32(bias, "bias")
+    od = _dt(odt, "out_dtype")
+    desc = ss_linear_desc_t(x.numel() // k if k else 0, k, n, _x_stride(x, "x"),
+                            _dt(x.dtype, "x"), od,
+                            od if residual is None else _dt(residual.dtype, "residual"), SS_F32,
+                            act, 0)
+    wp, bp, rp = _arg(w, "w", (n, k)), _arg(bias, "bias", (n,)), _arg(residual, "residual", oshape)
+    y = x.new_empty(oshape, dtype=odt)
+    pre = x.new_empty(oshape) if save_pre else None
+    lib = load_library()
+    nb = lib.ss_linear_workspace_bytes(ctypes.byref(desc), SS_LINEAR_FWD)
+    ws = workspace(nb, x.device)
+    _check(lib.ss_linear_fwd(ctypes.byref(desc), x.data_ptr(), wp, bp, rp, y.data_ptr(), _ptr(pre),
+                             _ptr(ws), nb, raw), "ss_linear_fwd")
+    return (y, pre) if save_pre else y
 
 
 def linear_bwd(x, w, dy, pre=None, act="none", bias=False, grad_dtype=None, need_dx=True,
@@ -780,75 +805,79 @@ def linear_bwd(x, w, dy, pre=None, act="none", bias=False, grad_dtype=None, need
     the forward's pre-activation values, with an activation.  Returns a dict: dx
     (..., K) and dw (N, K) in grad_dtype (default w's), dbias (N) float32 when
     bias is true; what is not asked for is None."""
-    packed = isinstance(x, tuple)
-    q, e = x if packed else (None, None)
+    q, e = x if isinstance(x, tuple) else (None, None)
+    x = None if isinstance(x, tuple) else x
+    return _on_device(_linear_bwd, stream, (w, dy, x, q, e, pre), x, q, e, w, dy, pre, _ACT[act],
+                      bias, w.dtype if grad_dtype is None else grad_dtype, need_dx, need_dw)
 
-    def run():
-        _dense(w=w, dy=dy, pre=pre, q=q, e=e)
-        n, k = w.shape
-        lead = dy.shape[:-1]
-        rows = dy.numel() // n if n else 0
-        _shape("dy", dy, (*lead, n))
-        _shape("pre", pre, dy.shape)
-        if pre is not None and pre.dtype != w.dtype:
-            raise ValueError("pre must have w's dtype")
-        if need_dw and x is None:
-            raise ValueError("dw needs x")
-        xs = 0
-        if packed:
-            _shape("q", q, (*lead, k))
-            _shape("e", e, (*lead, -(-k // SS_CKPT_BLOCK)))
-            if q.dtype != torch.int8 or e.dtype != torch.uint8:
-                raise ValueError("a checkpoint is int8 values and uint8 exponents")
-        elif x is not None:
-            _shape("x", x, (*lead, k))
-            if x.dtype != w.dtype:
-                raise ValueError("x and w must have one dtype")
-            xs = _x_stride(x, "x")
-        gdt = w.dtype if grad_dtype is None else grad_dtype
-        desc = make_linear_desc(rows, k, n, xs, _dt(w.dtype, "w"), _dt(dy.dtype, "dy"),
-                                SS_F32, _dt(gdt, "grad_dtype"), _ACT[act])
-        dev = w.device
-        dx = torch.empty((*lead, k), dtype=gdt, device=dev) if need_dx else None
-        dw = torch.empty((n, k), dtype=gdt, device=dev) if need_dw else None
-        db = torch.empty(n, dtype=torch.float32, device=dev) if bias else None
-        op = SS_LINEAR_BWD_CKPT if packed else SS_LINEAR_BWD
-        nb = ss_linear_workspace_bytes(desc, op)
-        ws = workspace(nb, dev)
-        if packed:
-            _check(ss_linear_bwd_ckpt(desc, q, e, w, pre, dy, dx, dw, db, ws, nb),
-                   "ss_linear_bwd_ckpt")
-        else:
-            _check(ss_linear_bwd(desc, x, w, pre, dy, dx, dw, db, ws, nb), "ss_linear_bwd")
-        return {"dx": dx, "dw": dw, "dbias": db}
-    return _on_device(run, stream, (None if packed else x, q, e, w, dy, pre))
+
+def _linear_bwd(raw, x, q, e, w, dy, pre, act, bias, gdt, need_dx, need_dw):
+    n, k = w.shape
+    lead = dy.shape[:-1]
+    if pre is not None and pre.dtype != w.dtype:
+        raise ValueError("pre must have w's dtype")
+    if need_dw and x is None and q is None:
+        raise ValueError("dw needs x")
+    dyp, prep, wp = _arg(dy, "dy", (*lead, n)), _arg(pre, "pre", (*lead, n)), _arg(w, "w", (n, k))
+    xs = 0
+    if q is not None:
+        qp, ep = _ckpt_args(q, e, (*lead, k))
+    elif x is not None:
+        if x.shape != (*lead, k):
+            raise ValueError("x must have shape %s (got %s)" % ((*lead, k), tuple(x.shape)))
+        if x.dtype != w.dtype:
+            raise ValueError("x and w must have one dtype")
+        xs = _x_stride(x, "x")
+    desc = ss_linear_desc_t(dy.numel() // n if n else 0, k, n, xs, _dt(w.dtype, "w"),
+                            _dt(dy.dtype, "dy"), SS_F32, _dt(gdt, "grad_dtype"), act, 0)
+    dx = w.new_empty((*lead, k), dtype=gdt) if need_dx else None
+    dw = w.new_empty((n, k), dtype=gdt) if need_dw else None
+    db = w.new_empty((n,), dtype=torch.float32) if bias else None
+    lib = load_library()
+    nb = lib.ss_linear_workspace_bytes(ctypes.byref(desc),
+                                       SS_LINEAR_BWD if q is None else SS_LINEAR_BWD_CKPT)
+    ws = workspace(nb, w.device)
+    rest = (wp, prep, dyp, _ptr(dx), _ptr(dw), _ptr(db), _ptr(ws), nb, raw)
+    if q is None:
+        _check(lib.ss_linear_bwd(ctypes.byref(desc), _ptr(x), *rest), "ss_linear_bwd")
+    else:
+        _check(lib.ss_linear_bwd_ckpt(ctypes.byref(desc), qp, ep, *rest), "ss_linear_bwd_ckpt")
+    return {"dx": dx, "dw": dw, "dbias": db}
+
+
+def _ckpt_args(q, e, shape):
+    if q.dtype != torch.int8 or e.dtype != torch.uint8:
+        raise ValueError("a checkpoint is int8 values and uint8 exponents")
+    return _arg(q, "q", shape), _arg(e, "e", (*shape[:-1], -(-shape[-1] // SS_CKPT_BLOCK)))
 
 
 def ckpt_pack(x, stream=None):
     """8-bit checkpoint of x (..., D): (q, e), int8 values and one uint8 exponent
     per 32 channels.  x may have a row stride."""
-    def run():
-        dim = x.shape[-1]
-        desc = make_ckpt_desc(x.numel() // dim if dim else 0, dim, _x_stride(x, "x"),
-                              _dt(x.dtype, "x"))
-        q = torch.empty(x.shape, dtype=torch.int8, device=x.device)
-        e = torch.empty((*x.shape[:-1], -(-dim // SS_CKPT_BLOCK)), dtype=torch.uint8,
-                        device=x.device)
-        _check(ss_ckpt_pack(desc, x, q, e), "ss_ckpt_pack")
-        return q, e
-    return _on_device(run, stream, (x,))
+    return _on_device(_ckpt_pack, stream, (x,), x)
+
+
+def _ckpt_pack(raw, x):
+    dim = x.shape[-1]
+    desc = ss_ckpt_desc_t(x.numel() // dim if dim else 0, dim, _x_stride(x, "x"),
+                          _dt(x.dtype, "x"), 0)
+    q = x.new_empty(x.shape, dtype=torch.int8)
+    e = x.new_empty((*x.shape[:-1], -(-dim // SS_CKPT_BLOCK)), dtype=torch.uint8)
+    _check(load_library().ss_ckpt_pack(ctypes.byref(desc), x.data_ptr(), q.data_ptr(),
+                                       e.data_ptr(), raw), "ss_ckpt_pack")
+    return q, e
 
 
 def ckpt_unpack(q, e, dtype=torch.bfloat16, stream=None):
     """The values of a checkpoint (q, e), in dtype."""
-    def run():
-        _dense(q=q, e=e)
-        dim = q.shape[-1]
-        _shape("e", e, (*q.shape[:-1], -(-dim // SS_CKPT_BLOCK)))
-        if q.dtype != torch.int8 or e.dtype != torch.uint8:
-            raise ValueError("a checkpoint is int8 values and uint8 exponents")
-        desc = make_ckpt_desc(q.numel() // dim if dim else 0, dim, 0, _dt(dtype, "dtype"))
-        x = torch.empty(q.shape, dtype=dtype, device=q.device)
-        _check(ss_ckpt_unpack(desc, q, e, x), "ss_ckpt_unpack")
-        return x
-    return _on_device(run, stream, (q, e))
+    return _on_device(_ckpt_unpack, stream, (q, e), q, e, dtype)
+
+
+def _ckpt_unpack(raw, q, e, dtype):
+    dim = q.shape[-1]
+    qp, ep = _ckpt_args(q, e, q.shape)
+    desc = ss_ckpt_desc_t(q.numel() // dim if dim else 0, dim, 0, _dt(dtype, "dtype"), 0)
+    x = q.new_empty(q.shape, dtype=dtype)
+    _check(load_library().ss_ckpt_unpack(ctypes.byref(desc), qp, ep, x.data_ptr(), raw),
+           "ss_ckpt_unpack")
+    return x

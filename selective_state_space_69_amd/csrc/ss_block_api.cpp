@@ -15,6 +15,7 @@ constexpr int64_t kMaxElems = int64_t(1) << 40;
 constexpr int64_t kMaxRows = INT32_MAX;
 constexpr int64_t kMaxStride = int64_t(1) << 24;
 constexpr int64_t kMaxLinear = int64_t(1) << 20;
+constexpr int64_t kMaxLinearRows = int64_t(1) << 30;   // 32-bit grids
 constexpr int64_t kMaxNormDim = 32768;
 
 size_t elem(int32_t dtype) { return dtype == SS_BF16 ? 2 : 4; }
@@ -68,7 +69,7 @@ int check_linear(const ss_linear_desc_t* d, int op) {
   if (!d) return SS_ERR_INVALID_ARG;
   if (op != SS_LINEAR_FWD && op != SS_LINEAR_BWD && op != SS_LINEAR_BWD_CKPT)
     return SS_ERR_INVALID_ARG;
-  if (d->rows < 1 || d->rows > kMaxRows || d->in_dim < 1 || d->out_dim < 1 ||
+  if (d->rows < 1 || d->rows > kMaxLinearRows || d->in_dim < 1 || d->out_dim < 1 ||
       d->in_dim > kMaxLinear || d->out_dim > kMaxLinear)
     return SS_ERR_INVALID_ARG;
   if (d->rows > kMaxElems / d->in_dim || d->rows > kMaxElems / d->out_dim ||

@@ -232,15 +232,16 @@ int launch_ckpt_unpack(const ss_ckpt_desc_t& d, const int8_t* q, const uint8_t* 
                        void* stream);
 
 // Linear projections (ss_linear.hip).  Workspace, 256-byte aligned arrays:
-//   dpre : (M, N) in_dtype, dy act'(pre) (only with an activation, or a dy of
-//          another type than the operands)
-//   x    : (M, K) in_dtype, the checkpoint's values (SS_LINEAR_BWD_CKPT)
+//   dpre : (M, N) in_dtype, dy act'(pre) (only with an activation, a dy of another
+//          type than the operands, or rows of dy that 16-byte loads cannot read)
+//   x, w : (M, K), (N, K) in_dtype, rows copied to a 16-byte aligned stride where
+//          they cannot be read in place; x: also the checkpoint's values
 //   sums : (chunks, N) fp32, dbias sums of chunk_rows rows
 //   part : fp32 partial products of a split contraction (the larger of dx's, dw's)
 struct LinearPlan {
   bool need_dpre = false;
   int64_t chunk_rows = 1, chunks = 1;
-  size_t off_dpre = 0, off_x = 0, off_sums = 0, off_part = 0, bytes = 0;
+  size_t off_dpre = 0, off_x = 0, off_w = 0, off_sums = 0, off_part = 0, bytes = 0;
 };
 LinearPlan plan_linear(const ss_linear_desc_t& d, int op);
 int launch_linear_fwd(const ss_linear_desc_t& d, const void* x, const void* w, const float* bias,

@@ -28,7 +28,6 @@ struct MmParams {
   int64_t t_split;       // contraction length of one split (a multiple of the tile's)
   int32_t splits;
   int32_t tiles_r, tiles_s;
-  bool vec_r, vec_s;     // operand rows are 16-byte aligned
   // epilogue
   const float* bias;     // (nS) or null
   const void* res;       // (nR, nS) or null
@@ -111,20 +110,6 @@ __device__ __forceinline__ void epilogue4(const MmParams& p, int64_t r, int32_t 
                       : static_cast<const float*>(p.res)[o + j];
     if (p.out_bf16) static_cast<uint16_t*>(p.out)[o + j] = f32_to_bf16(f);
     else static_cast<float*>(p.out)[o + j] = f;
-  }
-}
-
-// A split's partial sums, in fp32, for the kernel that joins them.
-__device__ __forceinline__ void store_partial4(const MmParams& p, int split, int64_t r, int32_t s,
-                                               const float (&v)[4]) {
-  if (r >= p.nR || s >= p.nS) return;
-  float* dst = p.part + (int64_t(split) * p.nR + r) * p.nS + s;
-  if ((p.nS & 3) == 0) {
-    *reinterpret_cast<float4*>(dst) = make_float4(v[0], v[1], v[2], v[3]);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (s + j < p.nS) dst[j] = v[j];
   }
 }
 

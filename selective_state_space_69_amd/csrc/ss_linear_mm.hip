@@ -1,7 +1,7 @@
-// The linear projections' large bf16 products for gfx950: 256 x 256 output tiles
-// on the matrix cores.
+// The linear projections' products for gfx950, on the matrix cores: 256 x 256
+// output tiles for large bf16 problems, 128 x 128 ones for the rest and for fp32.
 //
-// A workgroup is 8 waves, one workgroup to a CU; a wave owns 128 (s) x 64 (r) of
+// 256 x 256.  A workgroup is 8 waves, one workgroup to a CU; a wave owns 128 (s) x 64 (r) of
 // the tile as 8 x 4 accumulators of v_mfma_f32_16x16x32_bf16 (128 registers).  A
 // stage is 64 of the contraction: R 256 x 64 and S 256 x 64 bf16, copied from
 // global memory straight into LDS (16 bytes per lane), two stages deep.
@@ -127,26 +127,32 @@ __device__ __forceinline__ void read_tr8(const uint32_t (&a)[4], bf16x8 (&fa)[4]
   fb[3] = join8(u3, v3);
 }
 
-// Byte offsets of one wave-wide copy instruction (unit ids id = (j 8 + wave) 64 +
-// lane of the stage) from the tile's origin; kOutOfRange outside the operand.
-// TC: rows of t.  W: columns of the stage; HALF: they are columns 0..63 and
-// 128..191 of the tile (an S half).  tpos: the unit's first t.
-template <bool TC, int W, bool HALF>
+// Byte offsets of one wave-wide copy instruction (16-byte units id = (j waves +
+// wave) 64 + lane of the stage) from the tile's origin; kOutOfRange outside the
+// operand.  TC: rows of t (128 bytes).  W: columns of the stage; HALF: they are
+// columns 0..63 and 128..191 of the tile (an S half).  tpos: the unit's first t.
+template <typename T, bool TC, int W, bool HALF>
 __device__ __forceinline__ uint32_t copy_offset(int id, int64_t ld, int64_t i0, int64_t n,
                                                 int* tpos) {
+  constexpr int E = 16 / int(sizeof(T));
   if constexpr (TC) {
     const int q = id / 8, c = (id & 7) ^ (q & 7);
     const int row = HALF ? (q & 63) + (q >> 6) * 128 : q;
-    *tpos = c * 8;
-    return i0 + row < n ? uint32_t(row * ld * 2 + c * 16) : kOutOfRange;
+    *tpos = c * E;
+    return i0 + row < n ? uint32_t(row * ld * int(sizeof(T)) + c * 16) : kOutOfRange;
   } else {
-    constexpr int per = W / 8;
+    constexpr int per = W / E;
     const int t = id / per, c1 = id % per;
-    const int f = (t & 3) | (((t >> 3) & 1) << 2);
-    const int c = (((c1 >> 1) ^ f) << 1) | (c1 & 1);
-    const int col = HALF ? (c * 8 & 63) + (c >> 3) * 128 : c * 8;
+    int c;
+    if constexpr (sizeof(T) == 2) {
+      const int f = (t & 3) | (((t >> 3) & 1) << 2);
+      c = (((c1 >> 1) ^ f) << 1) | (c1 & 1);
+    } else {
+      c = c1 ^ (((t >> 2) & 3) << 2);
+    }
+    const int col = HALF ? (c * E & 63) + (c * E >> 6) * 128 : c * E;
     *tpos = t;
-    return i0 + col < n ? uint32_t(t * ld * 2 + col * 2) : kOutOfRange;
+    return i0 + col < n ? uint32_t((t * ld + col) * int(sizeof(T))) : kOutOfRange;
   }
 }
 
@@ -191,12 +197,12 @@ __device__ __forceinline__ void mm256_tile(const MmParams& p, char* lds, int64_t
   int tpr[4], tps[2];
 #pragma unroll
   for (int j = 0; j < 4; ++j)
-    vr[j] = copy_offset<RT, 256, false>((j * 8 + wv) * 64 + lane, p.ldr, r0, p.nR, &tpr[j]);
+    vr[j] = copy_offset<uint16_t, RT, 256, false>((j * 8 + wv) * 64 + lane, p.ldr, r0, p.nR, &tpr[j]);
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
     const int id = (j * 8 + wv) * 64 + lane;
-    vlo[j] = copy_offset<ST, 128, true>(id, p.lds, s0, p.nS, &tps[j]);
-    vhi[j] = copy_offset<ST, 128, true>(id, p.lds, s0 + 64, p.nS, &tps[j]);
+    vlo[j] = copy_offset<uint16_t, ST, 128, true>(id, p.lds, s0, p.nS, &tps[j]);
+    vhi[j] = copy_offset<uint16_t, ST, 128, true>(id, p.lds, s0 + 64, p.nS, &tps[j]);
   }
   const char* pr = static_cast<const char*>(p.R) + (RT ? r0 * p.ldr : r0) * 2;
   const char* ps = static_cast<const char*>(p.S) + (ST ? s0 * p.lds : s0) * 2;
@@ -374,17 +380,37 @@ __global__ __launch_bounds__(kThreads, 2) void mm256_kernel(MmParams p) {
 #endif
 }
 
-// 128 x 128 tiles for problems too small to fill the GPU with 256 x 256 ones: 4
-// waves of 64 x 64, the same stages and layouts, two buffers (64 KB, so two
-// workgroups share a CU and hide each other's barriers); the contraction may be
-// split.
+// 128 x 128 tiles for problems too small to fill the GPU with 256 x 256 ones, and
+// for fp32: 4 waves of 64 x 64, stages of 128 bytes of t (64 bf16, 32 fp32), two
+// buffers (64 KB, so two workgroups share a CU and hide each other's barriers);
+// the contraction may be split.  A lane supplies 16 bytes of t at a time to the
+// MFMAs of either type; the four fp32 products (v_mfma_f32_16x16x4_f32) of those
+// number t as 4 g + i on both sides.  A t-strided fp32 stage has rows of 128
+// columns, 64-byte blocks u of row t at u ^ (t / 4 & 3), read one element at a time.
 constexpr int kSmall = 128;
 constexpr int kSmallThreads = 256;
 
-template <bool RT, bool ST, int ACT>
+#if defined(__HIP_DEVICE_COMPILE__)
+template <typename T>
+__device__ __forceinline__ f32x4 mma(u32x4 a, u32x4 b, f32x4 c) {
+  if constexpr (sizeof(T) == 2) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
+                                                   __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      c = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(a[i]), __uint_as_float(b[i]), c, 0,
+                                               0, 0);
+    return c;
+  }
+}
+#endif
+
+template <typename T, bool RT, bool ST, int ACT>
 __global__ __launch_bounds__(kSmallThreads, 2) void mm128_kernel(MmParams p) {
 #if defined(__HIP_DEVICE_COMPILE__)
   __shared__ __attribute__((aligned(1024))) char lds[65536];
+  constexpr int kSz = int(sizeof(T)), kT = 128 / kSz;
   const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int m = lane & 15, g = lane >> 4;
   const int64_t tiles = int64_t(p.tiles_r) * p.tiles_s;
@@ -400,17 +426,16 @@ __global__ __launch_bounds__(kSmallThreads, 2) void mm128_kernel(MmParams p) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const int id = (j * 4 + wv) * 64 + lane;
-    vr[j] = copy_offset<RT, 128, false>(id, p.ldr, r0, p.nR, &tpr[j]);
-    vs[j] = copy_offset<ST, 128, false>(id, p.lds, s0, p.nS, &tps[j]);
+    vr[j] = copy_offset<T, RT, 128, false>(id, p.ldr, r0, p.nR, &tpr[j]);
+    vs[j] = copy_offset<T, ST, 128, false>(id, p.lds, s0, p.nS, &tps[j]);
   }
-  const char* pr = static_cast<const char*>(p.R) + (RT ? r0 * p.ldr + t0 : t0 * p.ldr + r0) * 2;
-  const char* ps = static_cast<const char*>(p.S) + (ST ? s0 * p.lds + t0 : t0 * p.lds + s0) * 2;
-  const int64_t dr = RT ? kStep * 2 : p.ldr * kStep * 2;
-  const int64_t ds = ST ? kStep * 2 : p.lds * kStep * 2;
-  const int nk = int((t1 - t0 + kStep - 1) / kStep);
-  const int rem = int(t1 - t0 - int64_t(nk - 1) * kStep);
+  const char* pr = static_cast<const char*>(p.R) + (RT ? r0 * p.ldr + t0 : t0 * p.ldr + r0) * kSz;
+  const char* ps = static_cast<const char*>(p.S) + (ST ? s0 * p.lds + t0 : t0 * p.lds + s0) * kSz;
+  const int64_t dr = RT ? 128 : p.ldr * 128, ds = ST ? 128 : p.lds * 128;
+  const int nk = int((t1 - t0 + kT - 1) / kT);
+  const int rem = int(t1 - t0 - int64_t(nk - 1) * kT);
   auto copy = [&](int k) {
-    if (k == nk - 1 && rem < kStep) {
+    if (k == nk - 1 && rem < kT) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         vr[j] = tpr[j] < rem ? vr[j] : kOutOfRange;
@@ -428,44 +453,66 @@ __global__ __launch_bounds__(kSmallThreads, 2) void mm128_kernel(MmParams p) {
                                                0);
   };
   const int wr = (wv >> 1) * 64, wsn = (wv & 1) * 64;
+  // fragment addresses in buffer 0
   uint32_t ar[4], as[4];
   const uint32_t l0 = uint32_t(reinterpret_cast<uintptr_t>((lds_ptr)lds));
   const int f = (m >> 2) | ((g & 1) << 2);
+  auto address = [&](bool tc, int c0) -> uint32_t {      // c0: first row or column
+    if (tc) return uint32_t((c0 + m) * 128 + ((g ^ (lane & 7)) << 4));
+    if (kSz == 2) return uint32_t((g * 8 + (m >> 2)) * 256 + (((c0 / 16) ^ f) << 5) + (m & 3) * 8);
+    return uint32_t(4 * g * 512 + (((c0 / 16) ^ g) << 6) + m * 4);
+  };
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    ar[i] = l0 + (RT ? uint32_t((wr + i * 16 + m) * 128 + ((g ^ (lane & 7)) << 4))
-                     : uint32_t((g * 8 + (m >> 2)) * 256 + (((wr / 16 + i) ^ f) << 5) + (m & 3) * 8));
-    as[i] = l0 + 16384 +
-            (ST ? uint32_t((wsn + i * 16 + m) * 128 + ((g ^ (lane & 7)) << 4))
-                : uint32_t((g * 8 + (m >> 2)) * 256 + (((wsn / 16 + i) ^ f) << 5) + (m & 3) * 8));
+    ar[i] = l0 + address(RT, wr + i * 16);
+    as[i] = l0 + 16384 + address(ST, wsn + i * 16);
   }
-  auto at = [&](uint32_t a) {
-    return *(const __attribute__((address_space(3))) bf16x8*)(uintptr_t(a));
-  };
   f32x4 acc[4][4];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
-  auto part = [&](auto h_c) {
+  // four fragments of half h of the stage's t
+  auto read = [&](auto tc_c, auto h_c, const uint32_t (&a)[4], u32x4 (&d)[4]) {
+    constexpr bool tc = decltype(tc_c)::value;
     constexpr int h = decltype(h_c)::value;
-    bf16x8 a[4], b[4];
-    if constexpr (RT) {
+    if constexpr (tc) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) b[j] = at(ar[j] ^ (h * 64));
-    }
-    if constexpr (ST) {
+      for (int i = 0; i < 4; ++i)
+        d[i] = *(const __attribute__((address_space(3))) u32x4*)(uintptr_t(a[i] ^ (h * 64)));
+    } else if constexpr (kSz == 2) {
+      bf16x8 t[4];
+      read_tr4<h * 8192, 1024>(a, t);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) a[i] = at(as[i] ^ (h * 64));
+      for (int i = 0; i < 4; ++i) d[i] = __builtin_bit_cast(u32x4, t[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          d[i][e] = *(const __attribute__((address_space(3))) uint32_t*)(uintptr_t(
+              a[i] + h * 8192 + e * 512));
     }
-    if constexpr (!RT && !ST) read_tr8<h * 8192, 1024, h * 8192, 1024>(ar, b, as, a);
-    else if constexpr (!ST) read_tr4<h * 8192, 1024>(as, a);
-    else if constexpr (!RT) read_tr4<h * 8192, 1024>(ar, b);
+  };
+  auto part = [&](auto h_c) {
+    u32x4 a[4], b[4];
+    if constexpr (kSz == 2 && !RT && !ST) {
+      constexpr int h = decltype(h_c)::value;
+      bf16x8 ta[4], tb[4];
+      read_tr8<h * 8192, 1024, h * 8192, 1024>(ar, tb, as, ta);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        a[i] = __builtin_bit_cast(u32x4, ta[i]);
+        b[i] = __builtin_bit_cast(u32x4, tb[i]);
+      }
+    } else {
+      read(std::integral_constant<bool, RT>{}, h_c, ar, b);
+      read(std::integral_constant<bool, ST>{}, h_c, as, a);
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[i], b[j], acc[i][j], 0, 0, 0);
+      for (int j = 0; j < 4; ++j) acc[i][j] = mma<T>(a[i], b[j], acc[i][j]);
   };
   copy(0);
   for (int k = 0; k < nk; ++k) {
@@ -490,26 +537,33 @@ __global__ __launch_bounds__(kSmallThreads, 2) void mm128_kernel(MmParams p) {
 }
 
 template <bool RT, bool ST, int ACT>
-void run(const MmParams& p, bool big, hipStream_t stream) {
+void run(const MmParams& p, MmTile tile, hipStream_t stream) {
   const unsigned blocks = unsigned(p.tiles_r) * unsigned(p.tiles_s) * unsigned(p.splits);
-  if (big) mm256_kernel<RT, ST, ACT><<<blocks, kThreads, 0, stream>>>(p);
-  else mm128_kernel<RT, ST, ACT><<<blocks, kSmallThreads, 0, stream>>>(p);
+  switch (tile) {
+    case MmTile::kBig: mm256_kernel<RT, ST, ACT><<<blocks, kThreads, 0, stream>>>(p); break;
+    case MmTile::kSmall:
+      mm128_kernel<uint16_t, RT, ST, ACT><<<blocks, kSmallThreads, 0, stream>>>(p);
+      break;
+    case MmTile::kSmallF32:
+      mm128_kernel<float, RT, ST, ACT><<<blocks, kSmallThreads, 0, stream>>>(p);
+      break;
+  }
 }
 
 }  // namespace
 
-void launch_mm(const MmParams& p, bool big, bool rt, bool st, hipStream_t stream) {
+void launch_mm(const MmParams& p, MmTile tile, bool rt, bool st, hipStream_t stream) {
   if (rt && st) {
-    // splits keep the activation for the join
-    switch (p.splits > 1 ? SS_ACT_NONE : p.act) {
-      case SS_ACT_SILU: return run<true, true, SS_ACT_SILU>(p, big, stream);
-      case SS_ACT_GELU: return run<true, true, SS_ACT_GELU>(p, big, stream);
-      case SS_ACT_SOFTPLUS: return run<true, true, SS_ACT_SOFTPLUS>(p, big, stream);
-      default: return run<true, true, SS_ACT_NONE>(p, big, stream);
+    // splits leave the activation to the join
+    switch (p.splits > 1 ? int(SS_ACT_NONE) : p.act) {
+      case SS_ACT_SILU: return run<true, true, SS_ACT_SILU>(p, tile, stream);
+      case SS_ACT_GELU: return run<true, true, SS_ACT_GELU>(p, tile, stream);
+      case SS_ACT_SOFTPLUS: return run<true, true, SS_ACT_SOFTPLUS>(p, tile, stream);
+      default: return run<true, true, SS_ACT_NONE>(p, tile, stream);
     }
   }
-  if (rt) run<true, false, SS_ACT_NONE>(p, big, stream);
-  else run<false, false, SS_ACT_NONE>(p, big, stream);
+  if (rt) run<true, false, SS_ACT_NONE>(p, tile, stream);
+  else run<false, false, SS_ACT_NONE>(p, tile, stream);
 }
 
 }  // namespace ss

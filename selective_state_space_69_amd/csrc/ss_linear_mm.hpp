@@ -8,16 +8,20 @@
 
 namespace ss {
 
-// Whether the bf16 kernels can read an operand: 16-byte aligned rows, and the
-// contiguous axis a multiple of 8 (a 16-byte unit is inside it or outside).
-inline bool mm_operand_ok(const void* p, int64_t ld, int64_t contiguous) {
-  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % 8 == 0 && contiguous % 8 == 0;
-}
+// O = R S^T on 256 x 256 (bf16, one split) or 128 x 128 tiles, as p.tiles_r,
+// p.tiles_s and p.splits say; rt, st: whether t is the operand's contiguous axis
+// (rt or not st).  An activation only with rt and st.
+// Operands are read in 16-byte units: rows are 16-byte aligned, and a row's last
+// unit is inside its storage, with zeros past the contraction's end where t is the
+// contiguous axis.
+enum class MmTile { kBig, kSmall, kSmallF32 };
+void launch_mm(const MmParams& p, MmTile tile, bool rt, bool st, hipStream_t stream);
 
-// O = R S^T on 256 x 256 (big, one split) or 128 x 128 tiles, as p.tiles_r, p.tiles_s
-// and p.splits say; rt, st: whether t is the operand's contiguous axis (rt or not
-// st).  An activation only with rt and st.
-void launch_mm(const MmParams& p, bool big, bool rt, bool st, hipStream_t stream);
+// O = R S^T for at most kRowsMax rows of R (t contiguous in both), with the
+// epilogue; vec: both operands' rows are 16-byte aligned and nT is a whole number
+// of 16-byte units.  One launch, no splits.
+constexpr int64_t kRowsMax = 32;
+void launch_rows(const MmParams& p, bool bf16, bool vec, hipStream_t stream);
 
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));

@@ -172,6 +172,9 @@ LINEAR = [
     (16, 2560, 256, "bf16", "f32", "none", True, "f32", 0, 0),
     (17, 320, 48, "bf16", "bf16", "gelu", False, "f32", 8, 8),
     (31, 1537, 77, "f32", "bf16", "silu", False, "bf16", 0, 0),
+    (32, 1024, 300, "bf16", "f32", "gelu", True, "f32", 0, 0),
+    (32, 516, 129, "f32", "f32", "softplus", True, None, 4, 0),
+    (33, 136, 80, "bf16", "bf16", "silu", True, None, 0, 0),
     (64, 256, 256, "bf16", "bf16", "silu", True, "bf16", 0, 0),
     (100, 48, 1536, "bf16", "bf16", "softplus", True, None, 32, 0),
     (128, 127, 129, "bf16", "f32", "none", True, "f32", 0, 0),
