@@ -81,6 +81,14 @@ __device__ __forceinline__ uint16_t f32_to_bf16(float f) {
   return uint16_t(x >> 16);
 }
 
+// two fp32 -> two bf16 (low half first), to nearest even, NaN kept, in one
+// instruction of gfx950
+__device__ __forceinline__ uint32_t cvt_bf16x2(float lo, float hi) {
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{lo, hi}, bf16x2));
+}
+
 template <typename T> __device__ __forceinline__ void store_out(T* p, float v);
 template <> __device__ __forceinline__ void store_out<float>(float* p, float v) { *p = v; }
 template <> __device__ __forceinline__ void store_out<uint16_t>(uint16_t* p, float v) {

@@ -209,10 +209,10 @@ int launch_ssd_step(const ss_ssd_desc_t& d, float* h, const void* x, const void*
 
 
 // Layer norm (ss_norm.hip): nwaves waves per row with vpt vectors of 8 channels
-// per thread.  Backward workspace: nparts partial rows (D) of dweight and of
+// per thread, groups rows side by side in a block.  Backward workspace: nparts partial rows (D) of dweight and of
 // dbias, fp32, 256-byte aligned.
 struct NormPlan {
-  int nwaves = 1, vpt = 1;
+  int nwaves = 1, vpt = 1, groups = 1;
   int64_t blocks = 1;
   int nparts = 1;
   size_t off_w = 0, off_b = 0, bytes = 0;
@@ -225,6 +225,10 @@ int launch_norm_bwd(const ss_norm_desc_t& d, const NormPlan& pl, const void* s,
                     const float* weight, const float* mean, const float* rstd, const void* dy,
                     const void* dsum, void* dx, float* dweight, float* dbias, char* ws,
                     void* stream);
+// Column sums of nparts rows of N floats, in a fixed order, of one array or two
+// (src1, dst1 null: one); a null dst is skipped (ss_norm.hip).
+void launch_column_sums(const float* src0, float* dst0, const float* src1, float* dst1,
+                        int64_t nparts, int32_t N, void* stream);
 
 // 8-bit checkpoints (ss_ckpt.hip).
 int launch_ckpt_pack(const ss_ckpt_desc_t& d, const void* x, int8_t* q, uint8_t* e, void* stream);

@@ -131,22 +131,6 @@ __global__ __launch_bounds__(kThreads) void dpre_kernel(DpreParams p) {
   }
 }
 
-__global__ __launch_bounds__(kThreads) void column_sum_kernel(const float* src, float* dst,
-                                                              int64_t nparts, int32_t N) {
-  __shared__ float part[4][64];
-  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
-  const int64_t c = int64_t(blockIdx.x) * 64 + lane;
-  float acc = 0.0f;
-  if (c < N) {
-#pragma unroll 8
-    for (int64_t i = wv; i < nparts; i += 4) acc += src[i * N + c];
-  }
-  part[wv][lane] = acc;
-  __syncthreads();
-  if (wv == 0 && c < N)
-    dst[c] = (part[0][lane] + part[1][lane]) + (part[2][lane] + part[3][lane]);
-}
-
 size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 bool ptr16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 int unit_of(const ss_linear_desc_t& d) { return d.in_dtype == SS_BF16 ? 8 : 4; }
@@ -334,8 +318,7 @@ int launch_linear_bwd(const ss_linear_desc_t& d, const LinearPlan& pl, const voi
     if (v == 8) dpre_types<8>(d, p, grid, st);
     else dpre_types<1>(d, p, grid, st);
     if (dbias)
-      column_sum_kernel<<<unsigned((d.out_dim + 63) / 64), kThreads, 0, st>>>(
-          p.part, dbias, pl.chunks, int32_t(d.out_dim));
+      launch_column_sums(p.part, dbias, nullptr, nullptr, pl.chunks, int32_t(d.out_dim), stream);
   }
   MmParams p{};
   p.R = dpre ? static_cast<const void*>(ws + pl.off_dpre) : dy;

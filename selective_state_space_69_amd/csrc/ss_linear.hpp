@@ -60,13 +60,10 @@ __device__ __forceinline__ float act_grad(int act, float v) {
   }
 }
 
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  return uint32_t(f32_to_bf16(lo)) | (uint32_t(f32_to_bf16(hi)) << 16);
-}
 __device__ __forceinline__ void store4(void* base, int64_t i, int bf16, const float (&v)[4]) {
   if (bf16)
     *reinterpret_cast<uint2*>(static_cast<uint16_t*>(base) + i) =
-        make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+        make_uint2(cvt_bf16x2(v[0], v[1]), cvt_bf16x2(v[2], v[3]));
   else
     *reinterpret_cast<float4*>(static_cast<float*>(base) + i) =
         make_float4(v[0], v[1], v[2], v[3]);

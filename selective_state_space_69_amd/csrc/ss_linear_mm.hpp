@@ -23,13 +23,6 @@ void launch_mm(const MmParams& p, MmTile tile, bool rt, bool st, hipStream_t str
 constexpr int64_t kRowsMax = 32;
 void launch_rows(const MmParams& p, bool bf16, bool vec, hipStream_t stream);
 
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-typedef float f32x2 __attribute__((ext_vector_type(2)));
-
-// two fp32 -> two bf16, to nearest even, in one instruction
-__device__ __forceinline__ uint32_t cvt_bf16x2(float lo, float hi) {
-  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{lo, hi}, bf16x2));
-}
 __device__ __forceinline__ void store8(void* base, int64_t i, int bf16, const float (&v)[8]) {
   if (bf16) {
     *reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + i) =

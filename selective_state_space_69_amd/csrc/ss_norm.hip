@@ -19,6 +19,8 @@ namespace {
 
 constexpr int kVec = 8;           // channels per thread and vector
 constexpr int kMaxWaves = 16;
+constexpr int kGroupWaves = 8;    // a block takes several narrow rows, up to so many waves
+constexpr int64_t kCUs = 256;
 constexpr int64_t kMaxRowBlocks = int64_t(1) << 20;   // a grid's threads stay below 2^32
 
 // Sum over the wave's 64 lanes, in a fixed order, in every lane: row_shr 1, 2,
@@ -39,62 +41,75 @@ __device__ __forceinline__ float wave_sum(float v) {
   return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
 }
 
-// 8 channels of a row in fp32.  VEC: 8 neighbours from column c, by 16-byte
-// loads; else 8 columns c, c + step, ... of which only those below D exist.
-template <typename T, bool VEC>
-__device__ __forceinline__ void load8(const T* row, int c, int step, int D, float (&v)[kVec]) {
-  if constexpr (VEC) {
-    if (c < D) {
-      if constexpr (sizeof(T) == 2) {
-        const uint4 r = *reinterpret_cast<const uint4*>(row + c);
-        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+// 8 neighbouring channels of a row from column c, in fp32 (0 past D).  Rows need
+// only their element's alignment: 16-byte accesses at any element address are
+// ordinary ones here.  TAIL: D is not a multiple of 8, and one thread's vector ends
+// past the row: it goes element by element.
+struct __attribute__((packed, aligned(2))) Raw8h { uint32_t w[4]; };
+struct __attribute__((packed, aligned(4))) Raw8f { float v[8]; };
+
+template <typename T> struct Raw8;
+template <> struct Raw8<uint16_t> { using type = Raw8h; };
+template <> struct Raw8<float> { using type = Raw8f; };
+
+// loaded in the storage form, widened where it is used, so that a prefetch does
+// not make the wave wait
+template <bool TAIL, typename T>
+__device__ __forceinline__ typename Raw8<T>::type load_raw8(const T* row, int c, int D) {
+  using R = typename Raw8<T>::type;
+  R r{};
+  if (c + kVec <= D) {
+    r = *reinterpret_cast<const R*>(row + c);
+  } else if (TAIL && c < D) {
+    struct Elems { T e[kVec]; } v;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          v[2 * i] = __uint_as_float(w[i] << 16);
-          v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-        }
-      } else {
-        const float4 a = *reinterpret_cast<const float4*>(row + c);
-        const float4 b = *reinterpret_cast<const float4*>(row + c + 4);
-        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-      }
-    } else {
+    for (int j = 0; j < kVec; ++j) v.e[j] = c + j < D ? row[c + j] : T(0);
+    r = __builtin_bit_cast(R, v);
+  }
+  return r;
+}
+__device__ __forceinline__ void widen8(const Raw8h& r, float (&v)[kVec]) {
 #pragma unroll
-      for (int j = 0; j < kVec; ++j) v[j] = 0.0f;
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < kVec; ++j) v[j] = c + j * step < D ? to_f32(row[c + j * step]) : 0.0f;
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(r.w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(r.w[i] & 0xffff0000u);
   }
 }
-
-template <typename T, bool VEC>
-__device__ __forceinline__ void store8(T* row, int c, int step, int D, const float (&v)[kVec]) {
-  if constexpr (VEC) {
-    if (c < D) {
-      if constexpr (sizeof(T) == 2) {
-        uint32_t w[4];
+__device__ __forceinline__ void widen8(const Raw8f& r, float (&v)[kVec]) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          w[i] = uint32_t(f32_to_bf16(v[2 * i])) | (uint32_t(f32_to_bf16(v[2 * i + 1])) << 16);
-        *reinterpret_cast<uint4*>(row + c) = make_uint4(w[0], w[1], w[2], w[3]);
-      } else {
-        *reinterpret_cast<float4*>(row + c) = make_float4(v[0], v[1], v[2], v[3]);
-        *reinterpret_cast<float4*>(row + c + 4) = make_float4(v[4], v[5], v[6], v[7]);
-      }
+  for (int j = 0; j < kVec; ++j) v[j] = r.v[j];
+}
+template <bool TAIL, typename T>
+__device__ __forceinline__ void load8(const T* row, int c, int D, float (&v)[kVec]) {
+  widen8(load_raw8<TAIL>(row, c, D), v);
+}
+
+template <bool TAIL, typename T>
+__device__ __forceinline__ void store8(T* row, int c, int D, const float (&v)[kVec]) {
+  if (c + kVec <= D) {
+    if constexpr (sizeof(T) == 2) {
+      Raw8h r;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) r.w[i] = cvt_bf16x2(v[2 * i], v[2 * i + 1]);
+      *reinterpret_cast<Raw8h*>(row + c) = r;
+    } else {
+      Raw8f r;
+#pragma unroll
+      for (int j = 0; j < kVec; ++j) r.v[j] = v[j];
+      *reinterpret_cast<Raw8f*>(row + c) = r;
     }
-  } else {
+  } else if (TAIL) {
 #pragma unroll
     for (int j = 0; j < kVec; ++j)
-      if (c + j * step < D) store_out<T>(row + c + j * step, v[j]);
+      if (c + j < D) store_out<T>(row + c + j, v[j]);
   }
 }
 
 // A thread's place in its row: tpr threads per row, vector k of thread t starts
-// at column (k tpr + t) 8 (VEC) or t + k 8 tpr with steps of tpr.
+// at column (k tpr + t) 8.
 struct Place {
   int tid, tpr, wave, nwaves;
+  int sub, groups;    // the block's rows side by side
   int64_t row;        // first row
   int64_t row_step;
 };
@@ -102,36 +117,35 @@ __device__ __forceinline__ Place place(int nwaves) {
   Place a;
   a.nwaves = nwaves;
   a.tpr = nwaves * kWave;
-  const int sub = nwaves == 1 ? int(threadIdx.x) / kWave : 0;   // rows side by side in a block
-  a.tid = int(threadIdx.x) - sub * a.tpr;
+  a.groups = int(blockDim.x) / a.tpr;
+  a.sub = int(threadIdx.x) / a.tpr;
+  a.tid = int(threadIdx.x) - a.sub * a.tpr;
   a.wave = a.tid / kWave;
-  const int rows = nwaves == 1 ? int(blockDim.x) / kWave : 1;
-  a.row = int64_t(blockIdx.x) * rows + sub;
-  a.row_step = int64_t(gridDim.x) * rows;
+  a.row = int64_t(blockIdx.x) * a.groups + a.sub;
+  a.row_step = int64_t(gridDim.x) * a.groups;
   return a;
 }
-template <bool VEC>
-__device__ __forceinline__ int col0(const Place& a, int k) {
-  return VEC ? (k * a.tpr + a.tid) * kVec : k * kVec * a.tpr + a.tid;
-}
+__device__ __forceinline__ int col0(const Place& a, int k) { return (k * a.tpr + a.tid) * kVec; }
 
-// Sums of v[0..N) over a row's threads; every thread gets them.  buf: floats that
-// no wave still reads from an earlier use (callers alternate).
+// Sums of v[0..N) over a row's threads; every thread gets them.  Every thread of
+// the block calls it.  buf: floats that no wave still reads from an earlier use
+// (callers alternate).
 template <int N>
 __device__ __forceinline__ void row_sum(const Place& a, float (&v)[N], float (&buf)[N][kMaxWaves]) {
 #pragma unroll
   for (int n = 0; n < N; ++n) v[n] = wave_sum(v[n]);
   if (a.nwaves == 1) return;
+  const int w0 = a.sub * a.nwaves;
   if ((threadIdx.x & 63) == 0) {
 #pragma unroll
-    for (int n = 0; n < N; ++n) buf[n][a.wave] = v[n];
+    for (int n = 0; n < N; ++n) buf[n][w0 + a.wave] = v[n];
   }
   __syncthreads();
 #pragma unroll
   for (int n = 0; n < N; ++n) v[n] = 0.0f;
   for (int i = 0; i < a.nwaves; ++i)
 #pragma unroll
-    for (int n = 0; n < N; ++n) v[n] += buf[n][i];
+    for (int n = 0; n < N; ++n) v[n] += buf[n][w0 + i];
 }
 
 struct NormFwdParams {
@@ -148,24 +162,26 @@ struct NormFwdParams {
   float eps, inv_d;
 };
 
-template <typename In, typename Res, typename Out, bool VEC, int VPT>
+template <typename In, typename Res, typename Out, int VPT, bool TAIL>
 __global__ __launch_bounds__(1024) void norm_fwd_kernel(NormFwdParams p) {
   __shared__ float buf1[1][kMaxWaves], buf2[2][kMaxWaves];
   const Place a = place(p.nwaves);
-  // one row per block, or one per wave without barriers: a row is uniform over
-  // everything that meets at row_sum's barrier
-  for (int64_t row = a.row; row < p.rows; row += a.row_step) {
+  // the block's groups walk together (row_sum has a barrier); a group past the last
+  // row repeats it and stores nothing
+  for (int64_t first = a.row - a.sub; first < p.rows; first += a.row_step) {
+    const bool live = first + a.sub < p.rows;
+    const int64_t row = live ? first + a.sub : p.rows - 1;
     const int64_t o = row * p.D;
     float s[VPT][kVec];
     float t[1] = {0.0f};
 #pragma unroll
     for (int k = 0; k < VPT; ++k)
-      load8<In, VEC>(static_cast<const In*>(p.x) + row * p.xs, col0<VEC>(a, k), a.tpr, p.D, s[k]);
+      load8<TAIL>(static_cast<const In*>(p.x) + row * p.xs, col0(a, k), p.D, s[k]);
     if (p.res) {
 #pragma unroll
       for (int k = 0; k < VPT; ++k) {
         float r[kVec];
-        load8<Res, VEC>(static_cast<const Res*>(p.res) + o, col0<VEC>(a, k), a.tpr, p.D, r);
+        load8<TAIL>(static_cast<const Res*>(p.res) + o, col0(a, k), p.D, r);
 #pragma unroll
         for (int j = 0; j < kVec; ++j) s[k][j] += r[j];
       }
@@ -174,10 +190,10 @@ __global__ __launch_bounds__(1024) void norm_fwd_kernel(NormFwdParams p) {
     for (int k = 0; k < VPT; ++k)
 #pragma unroll
       for (int j = 0; j < kVec; ++j) t[0] += s[k][j];
-    if (p.sum) {
+    if (p.sum && live) {
 #pragma unroll
       for (int k = 0; k < VPT; ++k)
-        store8<Res, VEC>(static_cast<Res*>(p.sum) + o, col0<VEC>(a, k), a.tpr, p.D, s[k]);
+        store8<TAIL>(static_cast<Res*>(p.sum) + o, col0(a, k), p.D, s[k]);
     }
     row_sum(a, t, buf1);
     const float mean = t[0] * p.inv_d;
@@ -186,7 +202,7 @@ __global__ __launch_bounds__(1024) void norm_fwd_kernel(NormFwdParams p) {
     for (int k = 0; k < VPT; ++k)
 #pragma unroll
       for (int j = 0; j < kVec; ++j) {
-        const bool on = col0<VEC>(a, k) + (VEC ? 0 : j * a.tpr) < p.D;
+        const bool on = col0(a, k) + j < p.D;
         s[k][j] = on ? s[k][j] - mean : 0.0f;
         c[0] += s[k][j];
         c[1] = __builtin_fmaf(s[k][j], s[k][j], c[1]);
@@ -196,27 +212,28 @@ __global__ __launch_bounds__(1024) void norm_fwd_kernel(NormFwdParams p) {
     const float var = __builtin_fmaf(c[1], p.inv_d, -rest * rest);
     // var is never below 0 but for rounding; NaN passes
     const float rstd = 1.0f / __builtin_sqrtf((var < 0.0f ? 0.0f : var) + p.eps);
-    if (p.mean && a.tid == 0) {
+    if (p.mean && live && a.tid == 0) {
       p.mean[row] = mean + rest;
       p.rstd[row] = rstd;
     }
+    if (!live) continue;
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
-      const int col = col0<VEC>(a, k);
+      const int col = col0(a, k);
       float f[kVec];
 #pragma unroll
       for (int j = 0; j < kVec; ++j) s[k][j] = (s[k][j] - rest) * rstd;
       if (p.w) {
-        load8<float, VEC>(p.w, col, a.tpr, p.D, f);
+        load8<TAIL>(p.w, col, p.D, f);
 #pragma unroll
         for (int j = 0; j < kVec; ++j) s[k][j] *= f[j];
       }
       if (p.b) {
-        load8<float, VEC>(p.b, col, a.tpr, p.D, f);
+        load8<TAIL>(p.b, col, p.D, f);
 #pragma unroll
         for (int j = 0; j < kVec; ++j) s[k][j] += f[j];
       }
-      store8<Out, VEC>(static_cast<Out*>(p.y) + o, col, a.tpr, p.D, s[k]);
+      store8<TAIL>(static_cast<Out*>(p.y) + o, col, p.D, s[k]);
     }
   }
 }
@@ -236,11 +253,12 @@ struct NormBwdParams {
   float inv_d;
 };
 
-// ACC: also sum dy xh and dy over the block's rows, in registers, one partial
-// row per walker (block, or wave where a row is one wave's).
-template <typename In, typename Res, typename Out, bool VEC, int VPT, bool ACC>
+// ACC (one vector per thread): also sum dy xh and dy over the block's rows, in
+// registers, one partial row per block.
+template <typename In, typename Res, typename Out, int VPT, bool TAIL, bool ACC>
 __global__ __launch_bounds__(1024) void norm_bwd_kernel(NormBwdParams p) {
   __shared__ float buf[2][2][kMaxWaves];
+  __shared__ float acc_buf[ACC ? kGroupWaves * kWave * kVec : 1];
   const Place a = place(p.nwaves);
   float aw[ACC ? VPT : 1][kVec], ab[ACC ? VPT : 1][kVec];
   if constexpr (ACC) {
@@ -249,59 +267,107 @@ __global__ __launch_bounds__(1024) void norm_bwd_kernel(NormBwdParams p) {
 #pragma unroll
       for (int j = 0; j < kVec; ++j) aw[k][j] = ab[k][j] = 0.0f;
   }
-  int par = 0;
-  for (int64_t row = a.row; row < p.rows; row += a.row_step, par ^= 1) {
-    const int64_t o = row * p.D;
-    float xh[VPT][kVec], g[VPT][kVec];
-    const float mean = p.mean[row], rstd = p.rstd[row];
-    float t1 = 0.0f, t2 = 0.0f;
+  constexpr bool kAhead = VPT == 1;
+  // the next row's s, dy and dsum are on their way while this one is summed (with
+  // one vector per thread; four would spill)
+  typename Raw8<In>::type rs[VPT];
+  typename Raw8<Out>::type rg[VPT];
+  typename Raw8<Res>::type rd[kAhead ? VPT : 1];
+  float rm = 0.0f, rr = 0.0f;
+  auto fetch = [&](int64_t row) {
+    rm = p.mean[row];
+    rr = p.rstd[row];
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
-      const int c = col0<VEC>(a, k);
-      load8<In, VEC>(static_cast<const In*>(p.s) + row * p.xs, c, a.tpr, p.D, xh[k]);
-      load8<Out, VEC>(static_cast<const Out*>(p.dy) + o, c, a.tpr, p.D, g[k]);
+      const int c = col0(a, k);
+      rs[k] = load_raw8<TAIL>(static_cast<const In*>(p.s) + row * p.xs, c, p.D);
+      rg[k] = load_raw8<TAIL>(static_cast<const Out*>(p.dy) + row * p.D, c, p.D);
+      if (kAhead && p.dsum)
+        rd[k] = load_raw8<TAIL>(static_cast<const Res*>(p.dsum) + row * p.D, c, p.D);
     }
+  };
+  auto clear = [&]() {
+    rm = rr = 0.0f;
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+      rs[k] = {};
+      rg[k] = {};
+      if (kAhead) rd[k] = {};
+    }
+  };
+  if (kAhead && a.row < p.rows) fetch(a.row);
+  int par = 0;
+  // the block's groups walk together (row_sum has a barrier); a group past the last
+  // row carries zeros
+  for (int64_t first = a.row - a.sub; first < p.rows; first += a.row_step, par ^= 1) {
+    const int64_t row = first + a.sub;
+    const bool live = row < p.rows;
+    if (!live) clear();
+    else if (!kAhead) fetch(row);
+    float xh[VPT][kVec], g[VPT][kVec], d[kAhead ? VPT : 1][kVec];
+    const float mean = rm, rstd = rr;
+    float t[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+      widen8(rs[k], xh[k]);
+      widen8(rg[k], g[k]);
+      if (kAhead && p.dsum) widen8(rd[k], d[k]);
+    }
+    if (kAhead && row + a.row_step < p.rows) fetch(row + a.row_step);
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
       float w[kVec];
-      if (p.w) load8<float, VEC>(p.w, col0<VEC>(a, k), a.tpr, p.D, w);
+      if (p.w) load8<TAIL>(p.w, col0(a, k), p.D, w);
 #pragma unroll
       for (int j = 0; j < kVec; ++j) {
-        const bool on = col0<VEC>(a, k) + (VEC ? 0 : j * a.tpr) < p.D;
+        const bool on = col0(a, k) + j < p.D;
         xh[k][j] = on ? (xh[k][j] - mean) * rstd : 0.0f;
         if constexpr (ACC) {
           aw[k][j] = __builtin_fmaf(g[k][j], xh[k][j], aw[k][j]);
           ab[k][j] += g[k][j];
         }
         if (p.w) g[k][j] *= w[j];
-        t1 += g[k][j];
-        t2 = __builtin_fmaf(g[k][j], xh[k][j], t2);
+        t[0] += g[k][j];
+        t[1] = __builtin_fmaf(g[k][j], xh[k][j], t[1]);
       }
     }
-    float t[2] = {t1, t2};
     row_sum(a, t, buf[par]);
     const float m1 = t[0] * p.inv_d, m2 = t[1] * p.inv_d;
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
-      const int c = col0<VEC>(a, k);
+      if (!kAhead && p.dsum && live)
+        load8<TAIL>(static_cast<const Res*>(p.dsum) + row * p.D, col0(a, k), p.D, d[0]);
 #pragma unroll
-      for (int j = 0; j < kVec; ++j) g[k][j] = rstd * (g[k][j] - m1 - xh[k][j] * m2);
-      if (p.dsum) {
-        float r[kVec];
-        load8<Res, VEC>(static_cast<const Res*>(p.dsum) + o, c, a.tpr, p.D, r);
-#pragma unroll
-        for (int j = 0; j < kVec; ++j) g[k][j] += r[j];
+      for (int j = 0; j < kVec; ++j) {
+        g[k][j] = rstd * (g[k][j] - m1 - xh[k][j] * m2);
+        if (p.dsum) g[k][j] += d[kAhead ? k : 0][j];
       }
-      store8<Res, VEC>(static_cast<Res*>(p.dx) + o, c, a.tpr, p.D, g[k]);
+      if (live) store8<TAIL>(static_cast<Res*>(p.dx) + row * p.D, col0(a, k), p.D, g[k]);
     }
   }
   if constexpr (ACC) {
-    // a.row numbers the walkers 0 .. a.row_step - 1: each writes its partial row
+    // the groups' sums are added in group order through LDS: one partial row per block
+    if (a.groups > 1) {
+      auto add = [&](float (&v)[kVec]) {
+        __syncthreads();
+        float* mine = acc_buf + (a.sub * a.tpr + a.tid) * kVec;
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) mine[j] = v[j];
+        __syncthreads();
+        if (a.sub == 0) {
+          for (int i = 1; i < a.groups; ++i)
+#pragma unroll
+            for (int j = 0; j < kVec; ++j) v[j] += acc_buf[(i * a.tpr + a.tid) * kVec + j];
+        }
+      };
+      add(aw[0]);
+      add(ab[0]);
+      if (a.sub != 0) return;
+    }
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
-      const int c = col0<VEC>(a, k);
-      store8<float, VEC>(p.pw + a.row * p.D, c, a.tpr, p.D, aw[k]);
-      store8<float, VEC>(p.pb + a.row * p.D, c, a.tpr, p.D, ab[k]);
+      store8<TAIL>(p.pw + int64_t(blockIdx.x) * p.D, col0(a, k), p.D, aw[k]);
+      store8<TAIL>(p.pb + int64_t(blockIdx.x) * p.D, col0(a, k), p.D, ab[k]);
     }
   }
 }
@@ -323,25 +389,35 @@ __global__ __launch_bounds__(256) void norm_wgrad_kernel(NormBwdParams p) {
   p.pb[int64_t(blockIdx.y) * p.D + c] = ab;
 }
 
-// dweight, dbias from the partial rows: 64 columns per block, 4 waves take every
-// fourth partial row each, their sums are added in wave order.
-__global__ __launch_bounds__(256) void norm_reduce_kernel(const float* pw, const float* pb,
-                                                          float* dw, float* db, int nparts,
-                                                          int D) {
-  __shared__ float part[4][64];
-  const float* src = blockIdx.y == 0 ? pw : pb;
-  float* dst = blockIdx.y == 0 ? dw : db;
+// Column sums of partial rows: 64 columns per block, 16 waves take every 16th row
+// each, their sums are added in wave order.  blockIdx.y picks one of two arrays.
+constexpr int kSumWaves = 16;
+struct SumParams {
+  const float* src[2];
+  float* dst[2];
+  int64_t nparts;
+  int32_t N;
+};
+__global__ __launch_bounds__(kSumWaves * kWave) void column_sum_kernel(SumParams p) {
+  __shared__ float part[kSumWaves][64];
+  const float* src = p.src[blockIdx.y];
+  float* dst = p.dst[blockIdx.y];
   if (!dst) return;
   const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
   const int c = int(blockIdx.x) * 64 + lane;
   float acc = 0.0f;
-  if (c < D) {
+  if (c < p.N) {
 #pragma unroll 8
-    for (int i = wv; i < nparts; i += 4) acc += src[int64_t(i) * D + c];
+    for (int64_t i = wv; i < p.nparts; i += kSumWaves) acc += src[i * p.N + c];
   }
   part[wv][lane] = acc;
   __syncthreads();
-  if (wv == 0 && c < D) dst[c] = (part[0][lane] + part[1][lane]) + (part[2][lane] + part[3][lane]);
+  if (wv == 0 && c < p.N) {
+    float t = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kSumWaves; ++i) t += part[i][lane];
+    dst[c] = t;
+  }
 }
 
 // waves per row and vectors per thread
@@ -350,36 +426,26 @@ void row_shape(int64_t D, int* nwaves, int* vpt) {
   *vpt = vecs <= kMaxWaves * kWave ? 1 : 4;
   *nwaves = int((vecs + *vpt * kWave - 1) / (*vpt * kWave));
 }
+int row_groups(int nwaves) { return nwaves < kGroupWaves ? kGroupWaves / nwaves : 1; }
 
-bool vec_ok(const ss_norm_desc_t& d, const void* x) {
-  const int64_t xs = d.x_stride ? d.x_stride : d.dim;
-  return d.dim % kVec == 0 && xs % kVec == 0 && reinterpret_cast<uintptr_t>(x) % 16 == 0;
+template <typename In, typename Res, typename Out>
+void fwd_types(const NormFwdParams& p, int vpt, int threads, int64_t blocks, hipStream_t st) {
+  const dim3 g{unsigned(blocks)}, b{unsigned(threads)};
+  const bool tail = p.D % kVec != 0;
+  if (vpt == 1 && !tail) norm_fwd_kernel<In, Res, Out, 1, false><<<g, b, 0, st>>>(p);
+  else if (vpt == 1) norm_fwd_kernel<In, Res, Out, 1, true><<<g, b, 0, st>>>(p);
+  else norm_fwd_kernel<In, Res, Out, 4, true><<<g, b, 0, st>>>(p);
 }
 
 template <typename In, typename Res, typename Out>
-void fwd_types(const NormFwdParams& p, bool vec, int vpt, int threads, int64_t blocks,
+void bwd_types(const NormBwdParams& p, int vpt, bool acc, int threads, int64_t blocks,
                hipStream_t st) {
   const dim3 g{unsigned(blocks)}, b{unsigned(threads)};
-  if (vec && vpt == 1) norm_fwd_kernel<In, Res, Out, true, 1><<<g, b, 0, st>>>(p);
-  else if (vec) norm_fwd_kernel<In, Res, Out, true, 4><<<g, b, 0, st>>>(p);
-  else if (vpt == 1) norm_fwd_kernel<In, Res, Out, false, 1><<<g, b, 0, st>>>(p);
-  else norm_fwd_kernel<In, Res, Out, false, 4><<<g, b, 0, st>>>(p);
-}
-
-template <typename In, typename Res, typename Out>
-void bwd_types(const NormBwdParams& p, bool vec, int vpt, bool acc, int threads, int64_t blocks,
-               hipStream_t st) {
-  const dim3 g{unsigned(blocks)}, b{unsigned(threads)};
-  if (vpt == 1) {
-    if (vec && acc) norm_bwd_kernel<In, Res, Out, true, 1, true><<<g, b, 0, st>>>(p);
-    else if (vec) norm_bwd_kernel<In, Res, Out, true, 1, false><<<g, b, 0, st>>>(p);
-    else if (acc) norm_bwd_kernel<In, Res, Out, false, 1, true><<<g, b, 0, st>>>(p);
-    else norm_bwd_kernel<In, Res, Out, false, 1, false><<<g, b, 0, st>>>(p);
-  } else if (vec) {
-    norm_bwd_kernel<In, Res, Out, true, 4, false><<<g, b, 0, st>>>(p);
-  } else {
-    norm_bwd_kernel<In, Res, Out, false, 4, false><<<g, b, 0, st>>>(p);
-  }
+  const bool tail = p.D % kVec != 0;
+  if (vpt != 1) norm_bwd_kernel<In, Res, Out, 4, true, false><<<g, b, 0, st>>>(p);
+  else if (!acc) norm_bwd_kernel<In, Res, Out, 1, true, false><<<g, b, 0, st>>>(p);
+  else if (tail) norm_bwd_kernel<In, Res, Out, 1, true, true><<<g, b, 0, st>>>(p);
+  else norm_bwd_kernel<In, Res, Out, 1, false, true><<<g, b, 0, st>>>(p);
 }
 
 // f(In, Res, Out) with the element types of three dtypes
@@ -399,18 +465,23 @@ void by_types(int32_t in, int32_t res, int32_t out, F&& f) {
 
 }  // namespace
 
+void launch_column_sums(const float* src0, float* dst0, const float* src1, float* dst1,
+                        int64_t nparts, int32_t N, void* stream) {
+  const SumParams p{{src0, src1}, {dst0, dst1}, nparts, N};
+  column_sum_kernel<<<dim3(unsigned((N + 63) / 64), dst1 ? 2 : 1), kSumWaves * kWave, 0,
+                      static_cast<hipStream_t>(stream)>>>(p);
+}
+
 NormPlan plan_norm(const ss_norm_desc_t& d) {
   NormPlan pl;
   row_shape(d.dim, &pl.nwaves, &pl.vpt);
-  const int64_t rows_per_block = pl.nwaves == 1 ? 4 : 1;
-  const int64_t row_blocks = (d.rows + rows_per_block - 1) / rows_per_block;
-  if (pl.vpt == 1) {
-    pl.blocks = row_blocks < 1024 ? row_blocks : 1024;
-    pl.nparts = int(pl.blocks * rows_per_block);
-  } else {
-    pl.blocks = row_blocks < 1024 ? row_blocks : 1024;
-    pl.nparts = int(d.rows < 64 ? d.rows : 64);
-  }
+  pl.groups = row_groups(pl.nwaves);
+  const int64_t row_blocks = (d.rows + pl.groups - 1) / pl.groups;
+  // The backward's blocks walk the rows, two to a CU: with the next row prefetched
+  // that keeps memory busy, and each block writes one partial row (16384 x 2560: 152
+  // us with one block per CU, 115 with two, 137 with three, 141 with four).
+  pl.blocks = row_blocks < 2 * kCUs ? row_blocks : 2 * kCUs;
+  pl.nparts = int(pl.vpt == 1 ? pl.blocks : (d.rows < 64 ? d.rows : 64));
   const size_t part = (size_t(pl.nparts) * size_t(d.dim) * 4 + 255) / 256 * 256;
   pl.off_w = 0;
   pl.off_b = part;
@@ -422,15 +493,14 @@ int launch_norm_fwd(const ss_norm_desc_t& d, const void* x, const void* residual
                     const float* weight, const float* bias, void* y, void* sum, float* mean,
                     float* rstd, void* stream) {
   const NormPlan pl = plan_norm(d);
-  const int rpb = pl.nwaves == 1 ? 4 : 1;
   NormFwdParams p{x, residual, weight, bias, y, sum, mean, rstd, d.rows,
                   d.x_stride ? d.x_stride : d.dim, int(d.dim), pl.nwaves, d.eps,
                   1.0f / float(d.dim)};
-  const int threads = rpb * pl.nwaves * kWave;
-  int64_t blocks = (d.rows + rpb - 1) / rpb;
+  const int threads = pl.groups * pl.nwaves * kWave;
+  int64_t blocks = (d.rows + pl.groups - 1) / pl.groups;
   if (blocks > kMaxRowBlocks) blocks = kMaxRowBlocks;
   by_types(d.in_dtype, d.res_dtype, d.out_dtype, [&](auto a, auto b, auto c) {
-    fwd_types<decltype(a), decltype(b), decltype(c)>(p, vec_ok(d, x), pl.vpt, threads, blocks,
+    fwd_types<decltype(a), decltype(b), decltype(c)>(p, pl.vpt, threads, blocks,
                                                      static_cast<hipStream_t>(stream));
   });
   return int(hipGetLastError());
@@ -441,24 +511,21 @@ int launch_norm_bwd(const ss_norm_desc_t& d, const NormPlan& pl, const void* s,
                     const void* dsum, void* dx, float* dweight, float* dbias, char* ws,
                     void* stream) {
   hipStream_t st = static_cast<hipStream_t>(stream);
-  const int rpb = pl.nwaves == 1 ? 4 : 1;
   const bool grads = dweight || dbias;
   NormBwdParams p{s, weight, mean, rstd, dy, dsum, dx,
                   grads ? reinterpret_cast<float*>(ws + pl.off_w) : nullptr,
                   grads ? reinterpret_cast<float*>(ws + pl.off_b) : nullptr, d.rows,
                   d.x_stride ? d.x_stride : d.dim, int(d.dim), pl.nwaves, 1.0f / float(d.dim)};
-  const int threads = rpb * pl.nwaves * kWave;
+  const int threads = pl.groups * pl.nwaves * kWave;
   const bool acc = grads && pl.vpt == 1;
   by_types(d.in_dtype, d.res_dtype, d.out_dtype, [&](auto a, auto b, auto c) {
-    bwd_types<decltype(a), decltype(b), decltype(c)>(p, vec_ok(d, s), pl.vpt, acc, threads,
+    bwd_types<decltype(a), decltype(b), decltype(c)>(p, pl.vpt, acc, threads,
                                                      pl.blocks, st);
     if (grads && !acc)
       norm_wgrad_kernel<decltype(a), decltype(c)>
           <<<dim3(unsigned((d.dim + 255) / 256), unsigned(pl.nparts)), 256, 0, st>>>(p);
   });
-  if (grads)
-    norm_reduce_kernel<<<dim3(unsigned((d.dim + 63) / 64), 2), 256, 0, st>>>(
-        p.pw, p.pb, dweight, dbias, pl.nparts, int(d.dim));
+  if (grads) launch_column_sums(p.pw, dweight, p.pb, dbias, pl.nparts, int32_t(d.dim), stream);
   return int(hipGetLastError());
 }
 
