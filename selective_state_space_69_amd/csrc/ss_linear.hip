@@ -1,6 +1,7 @@
 // Linear projections for gfx950: the plan, what prepares the products' operands
 // (aligned copies of rows that 16-byte loads cannot read in place, the backward's
 // pre-activation gradient), the join of split contractions, and the launchers.
+#include <cstdlib>
 #include "ss_linear_mm.hpp"
 
 namespace ss {
@@ -11,25 +12,25 @@ constexpr int64_t kMaxBlocks = int64_t(1) << 22;    // a grid's threads stay bel
 
 // Sum of the splits' partials, in order, and the epilogue.
 __global__ __launch_bounds__(kThreads) void join_kernel(MmParams p) {
-  const int64_t quads = (p.nS + 3) / 4;
-  const int64_t total = p.nR * quads;
+  const int64_t units = (p.nS + 7) / 8;
+  const int64_t total = p.nR * units;
   for (int64_t i = int64_t(blockIdx.x) * kThreads + threadIdx.x; i < total;
        i += int64_t(gridDim.x) * kThreads) {
-    const int64_t r = i / quads;
-    const int32_t s = int32_t(i - r * quads) * 4;
-    float v[4] = {0, 0, 0, 0};
-    for (int k = 0; k < p.splits; ++k) {
-      const float* src = p.part + (int64_t(k) * p.nR + r) * p.nS + s;
-      if ((p.nS & 3) == 0) {
-        const float4 f = *reinterpret_cast<const float4*>(src);
-        v[0] += f.x; v[1] += f.y; v[2] += f.z; v[3] += f.w;
-      } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (s + j < p.nS) v[j] += src[j];
+    const int64_t r = i / units;
+    const int32_t s = int32_t(i - r * units) * 8;
+    const float* src = p.part + r * p.nS + s;
+    const int64_t step = p.nR * p.nS;
+    if (s + 8 <= p.nS) {
+      float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+      for (int k = 0; k < p.splits; ++k) add8(src, k * step, 0, v);
+      epilogue8<kActOf>(p, r, s, v);
+    } else {
+      for (int j = 0; s + j < p.nS; ++j) {
+        float v = 0.0f;
+        for (int k = 0; k < p.splits; ++k) v += src[k * step + j];
+        epilogue1(p, p.act, r, s + j, v);
       }
     }
-    epilogue4(p, r, s, v);
   }
 }
 
@@ -50,9 +51,13 @@ __global__ __launch_bounds__(kThreads) void pad_kernel(PadParams p) {
     const int64_t r = total <= INT32_MAX ? int64_t(uint32_t(i) / uint32_t(p.units)) : i / p.units;
     const int c = int(i - r * p.units) * E;
     const T* src = static_cast<const T*>(p.src) + r * p.ld_src + c;
-    struct Elems { T e[E]; } v;
+    struct __attribute__((packed, aligned(sizeof(T)))) Elems { T e[E]; } v;
+    if (c + E <= p.cols) {
+      v = *reinterpret_cast<const Elems*>(src);      // 16 bytes at any element address
+    } else {
 #pragma unroll
-    for (int j = 0; j < E; ++j) v.e[j] = c + j < p.cols ? src[j] : T(0);
+      for (int j = 0; j < E; ++j) v.e[j] = c + j < p.cols ? src[j] : T(0);
+    }
     reinterpret_cast<u32x4*>(p.dst)[i] = __builtin_bit_cast(u32x4, v);
   }
 }
@@ -139,9 +144,10 @@ int64_t pad_to_unit(const ss_linear_desc_t& d, int64_t n) {
   return (n + e - 1) / e * e;
 }
 
-// How a product is tiled.  256 x 256 tiles (bf16) where they fill the GPU's 256
-// CUs at least half; else 128 x 128, with the contraction split until there are
-// about 512 work items (two to a CU) of at least 4 stages.
+// How a product is tiled.  bf16: 256 x 256 tiles where they fill the GPU's 256 CUs
+// at least half, else 128 x 128, of which two fit on a CU.  fp32: 64 x 64, of which
+// four or five fit.  With fewer tiles than fit, the contraction is split as often as
+// they still fit at once, into parts of at least 4 stages.
 struct Tiling {
   MmTile tile;
   int32_t tiles_r, tiles_s, splits;
@@ -152,18 +158,18 @@ Tiling tiling(const ss_linear_desc_t& d, int64_t nR, int64_t nS, int64_t nT) {
   t.splits = 1;
   t.t_split = nT;
   const int64_t r256 = (nR + 255) / 256, s256 = (nS + 255) / 256;
-  if (d.in_dtype == SS_BF16 && r256 * s256 >= 128) {
+  if (d.in_dtype == SS_BF16 && r256 * s256 >= (getenv("SMALL") ? 1<<30 : 128)) {
     t.tile = MmTile::kBig;
     t.tiles_r = int32_t(r256);
     t.tiles_s = int32_t(s256);
     return t;
   }
-  t.tile = d.in_dtype == SS_BF16 ? MmTile::kSmall : MmTile::kSmallF32;
-  t.tiles_r = int32_t((nR + 127) / 128);
-  t.tiles_s = int32_t((nS + 127) / 128);
-  const int64_t step = d.in_dtype == SS_BF16 ? 64 : 32;
-  const int64_t tiles = int64_t(t.tiles_r) * t.tiles_s;
-  int64_t k = tiles >= 256 ? 1 : (512 + tiles - 1) / tiles;
+  const bool bf16 = d.in_dtype == SS_BF16;
+  const int64_t side = bf16 ? 128 : 64, step = bf16 ? 64 : 32, fit = bf16 ? 512 : 1024;
+  t.tile = bf16 ? MmTile::kSmall : MmTile::kSmallF32;
+  t.tiles_r = int32_t((nR + side - 1) / side);
+  t.tiles_s = int32_t((nS + side - 1) / side);
+  int64_t k = fit / (int64_t(t.tiles_r) * t.tiles_s);
   const int64_t most = nT / (4 * step);
   if (k > most) k = most;
   if (k > 64) k = 64;
@@ -188,7 +194,7 @@ void run_mm(const ss_linear_desc_t& d, MmParams p, bool rt, bool st, hipStream_t
   p.t_split = t.t_split;
   launch_mm(p, t.tile, rt, st, stream);
   if (p.splits > 1) {
-    const int64_t n = (p.nR * ((p.nS + 3) / 4) + kThreads - 1) / kThreads;
+    const int64_t n = (p.nR * ((p.nS + 7) / 8) + kThreads - 1) / kThreads;
     join_kernel<<<unsigned(n < kMaxBlocks ? n : kMaxBlocks), kThreads, 0, stream>>>(p);
   }
 }

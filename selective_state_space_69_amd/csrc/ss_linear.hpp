@@ -60,56 +60,6 @@ __device__ __forceinline__ float act_grad(int act, float v) {
   }
 }
 
-__device__ __forceinline__ void store4(void* base, int64_t i, int bf16, const float (&v)[4]) {
-  if (bf16)
-    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(base) + i) =
-        make_uint2(cvt_bf16x2(v[0], v[1]), cvt_bf16x2(v[2], v[3]));
-  else
-    *reinterpret_cast<float4*>(static_cast<float*>(base) + i) =
-        make_float4(v[0], v[1], v[2], v[3]);
-}
-
-// Four neighbours s..s+3 of output row r: bias, activation, residual, stores.
-// Rows keep 4-element alignment only where nS is a multiple of 4.
-__device__ __forceinline__ void epilogue4(const MmParams& p, int64_t r, int32_t s, float (&v)[4]) {
-  if (r >= p.nR || s >= p.nS) return;
-  const int64_t o = r * p.nS + s;
-  if ((p.nS & 3) == 0) {
-    if (p.bias) {
-      const float4 b = *reinterpret_cast<const float4*>(p.bias + s);
-      v[0] += b.x; v[1] += b.y; v[2] += b.z; v[3] += b.w;
-    }
-    if (p.pre) store4(p.pre, o, p.pre_bf16, v);
-    if (p.act != SS_ACT_NONE) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] = apply_act(p.act, v[j]);
-    }
-    if (p.res) {
-      const float4 f = p.res_bf16 ? unpack4(load_raw4(static_cast<const uint16_t*>(p.res) + o))
-                                  : load_raw4(static_cast<const float*>(p.res) + o);
-      v[0] += f.x; v[1] += f.y; v[2] += f.z; v[3] += f.w;
-    }
-    store4(p.out, o, p.out_bf16, v);
-    return;
-  }
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    if (s + j >= p.nS) break;
-    float f = v[j];
-    if (p.bias) f += p.bias[s + j];
-    if (p.pre) {
-      if (p.pre_bf16) static_cast<uint16_t*>(p.pre)[o + j] = f32_to_bf16(f);
-      else static_cast<float*>(p.pre)[o + j] = f;
-    }
-    f = apply_act(p.act, f);
-    if (p.res)
-      f += p.res_bf16 ? to_f32(static_cast<const uint16_t*>(p.res)[o + j])
-                      : static_cast<const float*>(p.res)[o + j];
-    if (p.out_bf16) static_cast<uint16_t*>(p.out)[o + j] = f32_to_bf16(f);
-    else static_cast<float*>(p.out)[o + j] = f;
-  }
-}
-
 // Output tile of work item `id`.  Neighbouring items (one XCD's) share operand
 // rows in its L2: tiles run down columns of a band of up to 8 tile rows.
 __device__ __forceinline__ void tile_of(const MmParams& p, int64_t id, int64_t* tr, int* ts) {

@@ -6,19 +6,19 @@
 // stage is 64 of the contraction: R 256 x 64 and S 256 x 64 bf16, copied from
 // global memory straight into LDS (16 bytes per lane), two stages deep.
 //
-// Schedule.  The waves of a SIMD form two groups that run half a step apart: while
+// Schedule.  The waves of a SIMD form two groups that run half a turn apart: while
 // one group multiplies, the other reads its next fragments from LDS and issues
-// copies, and a barrier swaps the roles.  A stage takes four such turns; a turn
-// multiplies 4 S fragments with 4 R fragments (16 MFMAs):
+// copies, and a barrier swaps the roles.  A stage takes four turns of a read half
+// and a multiply half (4 S by 4 R fragments, 16 MFMAs):
 //     turn 0: S rows lo, t 0..31     turn 1: S lo, t 32..63
 //     turn 2: S rows hi, t 0..31     turn 3: S hi, t 32..63
 // R fragments of both t halves stay in registers from turns 0 and 1 on, so R and
 // S lo of a buffer are free after turn 1 and are refilled (stage k + 2) in turns 2
 // and 3; S hi (stage k + 1) is refilled in turns 0 and 1.  Every copy thus has a
-// whole stage of time to land, and a wave waits for the copies of the next turn
-// pair with the later ones still in flight (8 instructions).  Stages past the end
-// are issued as well, out of the buffer's range (no memory is read), so that the
-// counts hold to the last stage.
+// whole stage of time to land, and a wave waits for the copies of the next two
+// turns with the 8 younger ones still in flight.  Stages past the end are issued as
+// well, out of the buffer's range (no memory is read), so that the counts hold to
+// the last stage.  (Copies issued in the multiply halves instead cost 4%.)
 //
 // LDS layouts, permuted at the copy's source addresses (its destination is linear)
 // so that fragment reads touch all banks evenly (no conflicts by the counters):
@@ -43,6 +43,7 @@ typedef __attribute__((address_space(3))) void* lds_ptr;
 constexpr int kTile = 256;
 constexpr int kStep = 64;                          // t per stage
 constexpr int kThreads = 512;
+constexpr unsigned kCUs = 256;
 constexpr int kOffR = 0, kOffLo = 65536, kOffHi = 98304, kOffEpi = 131072;
 constexpr int kLds = 163840;
 
@@ -156,67 +157,89 @@ __device__ __forceinline__ uint32_t copy_offset(int id, int64_t ld, int64_t i0, 
   }
 }
 
-// Epilogue of 16 rows x 64 columns of a wave: the accumulators (lane: row lane &
+// Epilogue of 16 rows x 16 F columns of a wave: the accumulators (lane: row lane &
 // 15, four neighbours of each 16-column piece q[i]) are turned through 4 KB of
-// LDS into whole rows, 8 columns per lane.  The loops are rolled: unrolled, the
-// epilogue outgrew the instruction cache and cost 20 us a tile.
-template <int ACT>
-__device__ __forceinline__ void rows_out(const MmParams& p, char* sl, const f32x4 (&q)[4],
-                                         int64_t r, int32_t s, int split) {
+// LDS into whole rows, 8 columns per lane.  SPLIT: to a split's partial sums
+// instead.  The loops are rolled: unrolled, the epilogue outgrew the instruction
+// cache and cost 20 us a tile.
+template <int ACT, bool SPLIT, int F>
+__device__ __forceinline__ void rows_out(const MmParams& p, char* sl, const f32x4 (&q)[F],
+                                         int64_t r0, int32_t s0, int split) {
   const int lane = threadIdx.x & 63, m = lane & 15, g = lane >> 4;
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < F; ++i)
     *reinterpret_cast<f32x4*>(sl + m * 256 + (((4 * i + g) ^ m) << 4)) = q[i];
   asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-  if ((p.nS & 7) == 0) {
 #pragma nounroll
-    for (int h = 0; h < 2; ++h) {
-      const int row = h * 8 + lane / 8, u = (lane & 7) * 2;
+  for (int h = 0; h < F / 2; ++h) {
+    constexpr int per = 2 * F;          // lanes of a row
+    const int row = h * (64 / per) + lane / per, u = (lane % per) * 2;
+    const int64_t r = r0 + row;
+    const int32_t s = s0 + u * 4;
+    if (r >= p.nR || s >= p.nS) continue;
+    if (s + 8 <= p.nS) {
       const f32x4 x = *reinterpret_cast<const f32x4*>(sl + row * 256 + ((u ^ row) << 4));
       const f32x4 y = *reinterpret_cast<const f32x4*>(sl + row * 256 + (((u + 1) ^ row) << 4));
       float v[8] = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
-      epilogue8<ACT>(p, r + row, s + u * 4, v, split);
-    }
-  } else {
+      if constexpr (SPLIT) store8(p.part, (split * p.nR + r) * p.nS + s, 0, v);
+      else epilogue8<ACT>(p, r, s, v);
+    } else {
 #pragma nounroll
-    for (int row = 0; row < 16; ++row) {
-      const float v = *reinterpret_cast<const float*>(sl + row * 256 + (((lane / 4) ^ row) << 4) +
-                                                      (lane & 3) * 4);
-      epilogue1<ACT>(p, r + row, s + lane, v, split);
+      for (int j = 0; s + j < p.nS; ++j) {
+        const float v = *reinterpret_cast<const float*>(sl + row * 256 +
+                                                        (((u + j / 4) ^ row) << 4) + (j & 3) * 4);
+        if constexpr (SPLIT) p.part[(split * p.nR + r) * p.nS + s + j] = v;
+        else epilogue1(p, ACT, r, s + j, v);
+      }
     }
   }
   asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
 }
 
+// Workgroup b of the grid takes a tile of every round of gridDim.x tiles; the tiles
+// of a round lie together on an XCD.  Returns false past the last tile.
+__device__ __forceinline__ bool round_tile(const MmParams& p, int64_t round, int64_t* tr, int* ts) {
+  const int64_t tiles = int64_t(p.tiles_r) * p.tiles_s, first = round * gridDim.x;
+  const int64_t n = tiles - first < gridDim.x ? tiles - first : gridDim.x;
+  if (int64_t(blockIdx.x) >= n) return false;
+  tile_of(p, first + xcd_contiguous(blockIdx.x, n), tr, ts);
+  return true;
+}
+
 template <bool RT, bool ST, int ACT>
-__device__ __forceinline__ void mm256_tile(const MmParams& p, char* lds, int64_t tr, int ts) {
+__device__ __forceinline__ void mm256_body(const MmParams& p, char* lds) {
   const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int m = lane & 15, g = lane >> 4;
-  const int64_t r0 = tr * kTile, s0 = int64_t(ts) * kTile;
+  int64_t r0, s0;
   uint32_t vr[4], vlo[2], vhi[2];
   int tpr[4], tps[2];
+  const char *pr, *ps, *psh;
+  auto place = [&](int64_t tr, int ts) {
+    r0 = tr * kTile;
+    s0 = int64_t(ts) * kTile;
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
-    vr[j] = copy_offset<uint16_t, RT, 256, false>((j * 8 + wv) * 64 + lane, p.ldr, r0, p.nR, &tpr[j]);
+    for (int j = 0; j < 4; ++j)
+      vr[j] = copy_offset<uint16_t, RT, 256, false>((j * 8 + wv) * 64 + lane, p.ldr, r0, p.nR,
+                                                    &tpr[j]);
 #pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    const int id = (j * 8 + wv) * 64 + lane;
-    vlo[j] = copy_offset<uint16_t, ST, 128, true>(id, p.lds, s0, p.nS, &tps[j]);
-    vhi[j] = copy_offset<uint16_t, ST, 128, true>(id, p.lds, s0 + 64, p.nS, &tps[j]);
-  }
-  const char* pr = static_cast<const char*>(p.R) + (RT ? r0 * p.ldr : r0) * 2;
-  const char* ps = static_cast<const char*>(p.S) + (ST ? s0 * p.lds : s0) * 2;
-  const char* psh = ps + (ST ? 64 * p.lds : 64) * 2;
+    for (int j = 0; j < 2; ++j) {
+      const int id = (j * 8 + wv) * 64 + lane;
+      vlo[j] = copy_offset<uint16_t, ST, 128, true>(id, p.lds, s0, p.nS, &tps[j]);
+      vhi[j] = copy_offset<uint16_t, ST, 128, true>(id, p.lds, s0 + 64, p.nS, &tps[j]);
+    }
+    pr = static_cast<const char*>(p.R) + (RT ? r0 * p.ldr : r0) * 2;
+    ps = static_cast<const char*>(p.S) + (ST ? s0 * p.lds : s0) * 2;
+    psh = ps + (ST ? 64 * p.lds : 64) * 2;
+  };
   const int64_t dr = RT ? kStep * 2 : p.ldr * kStep * 2;
   const int64_t ds = ST ? kStep * 2 : p.lds * kStep * 2;
   const int nk = int((p.nT + kStep - 1) / kStep);
   const int rem = int(p.nT - int64_t(nk - 1) * kStep);      // t of the last stage, 1..64
 
-  // resource of stage k; past the last one no byte is in range
-  auto rsrc = [&](const char* base, int64_t step, int k) {
-    return __builtin_amdgcn_make_buffer_rsrc(
-        const_cast<char*>(base + (k < nk ? k : nk - 1) * step), short(0),
-        k < nk ? 0x7fffffff : 0, 0x00020000);
+  // resource of a stage k that starts at base; past the last one no byte is in range
+  auto rsrc = [&](const char* base, int k) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(base), short(0),
+                                             k < nk ? 0x7fffffff : 0, 0x00020000);
   };
   auto copy = [&](Rsrc src, int dst, uint32_t off) {
     __builtin_amdgcn_raw_ptr_buffer_load_lds(src, (lds_ptr)(lds + dst), 16, off, 0, 0, 0);
@@ -234,14 +257,15 @@ __device__ __forceinline__ void mm256_tile(const MmParams& p, char* lds, int64_t
       for (int j = 0; j < 2; ++j) v[j] = tps[j] < rem ? v[j] : kOutOfRange;
     }
   };
+  // pr, ps, psh: where the next stage to copy of R, S lo, S hi starts
   auto copy_r = [&](int k, int j) {
-    copy(rsrc(pr, dr, k), kOffR + (k & 1) * 32768 + (j * 8 + wv) * 1024, vr[j]);
+    copy(rsrc(pr, k), kOffR + (k & 1) * 32768 + (j * 8 + wv) * 1024, vr[j]);
   };
   auto copy_lo = [&](int k, int j) {
-    copy(rsrc(ps, ds, k), kOffLo + (k & 1) * 16384 + (j * 8 + wv) * 1024, vlo[j]);
+    copy(rsrc(ps, k), kOffLo + (k & 1) * 16384 + (j * 8 + wv) * 1024, vlo[j]);
   };
   auto copy_hi = [&](int k, int j) {
-    copy(rsrc(psh, ds, k), kOffHi + (k & 1) * 16384 + (j * 8 + wv) * 1024, vhi[j]);
+    copy(rsrc(psh, k), kOffHi + (k & 1) * 16384 + (j * 8 + wv) * 1024, vhi[j]);
   };
 
   const int wr = (wv >> 1) * 64, wsn = (wv & 1) * 128;      // the wave's corner
@@ -263,31 +287,31 @@ __device__ __forceinline__ void mm256_tile(const MmParams& p, char* lds, int64_t
     return *(const __attribute__((address_space(3))) bf16x8*)(uintptr_t(a));
   };
 
+  // the first copies of a tile: stage 0, and R and S lo of stage 1
+  auto begin = [&]() {
+    mask_r(0);
+    mask_s(0, vlo);
+    mask_s(0, vhi);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) copy_r(0, j);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) copy_lo(0, j);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) copy_hi(0, j);
+    pr += dr;
+    ps += ds;
+    psh += ds;
+    mask_r(1);
+    mask_s(1, vlo);
+    mask_s(1, vhi);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) copy_r(1, j);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) copy_lo(1, j);
+    pr += dr;
+    ps += ds;
+  };
   f32x4 acc[8][4];
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
-
-  mask_r(0);
-  mask_s(0, vlo);
-  mask_s(0, vhi);
-#pragma unroll
-  for (int j = 0; j < 4; ++j) copy_r(0, j);
-#pragma unroll
-  for (int j = 0; j < 2; ++j) copy_lo(0, j);
-#pragma unroll
-  for (int j = 0; j < 2; ++j) copy_hi(0, j);
-  mask_r(1);
-  mask_s(1, vlo);
-#pragma unroll
-  for (int j = 0; j < 4; ++j) copy_r(1, j);
-#pragma unroll
-  for (int j = 0; j < 2; ++j) copy_lo(1, j);
-  wait_copies<6>();
-  turn_end();
-  if (wv >= 4) turn_end();            // the second group runs one turn behind
-
   bf16x8 b[2][4], a[4];
   auto mma = [&](int i0, int h) {
     __builtin_amdgcn_s_setprio(1);
@@ -316,55 +340,97 @@ __device__ __forceinline__ void mm256_tile(const MmParams& p, char* lds, int64_t
     else if constexpr (!ST) read_tr4<so, 1024>(as, a);
     else if constexpr (hi == 0 && !RT) read_tr4<ro, 2048>(ar, b[h]);
   };
+  // plain reads are waited for at the end of the half-turn, so copies go after them;
+  // the transposing ones wait by themselves
+  constexpr bool kReadFirst = ST;
   using I0 = std::integral_constant<int, 0>;
   using I1 = std::integral_constant<int, 1>;
-  for (int k = 0; k < nk; ++k) {
-    mask_s(k + 1, vhi);
-    copy_hi(k + 1, 0);
-    read(I0{}, I0{});
-    turn_end();
-    mma(0, 0);
-    turn_end();
-    copy_hi(k + 1, 1);
-    read(I0{}, I1{});
-    wait_copies<8>();
-    turn_end();
-    mma(0, 1);
-    turn_end();
-    mask_r(k + 2);
-    mask_s(k + 2, vlo);
-    copy_r(k + 2, 0);
-    copy_r(k + 2, 1);
-    copy_lo(k + 2, 0);
-    read(I1{}, I0{});
-    turn_end();
-    mma(4, 0);
-    turn_end();
-    copy_r(k + 2, 2);
-    copy_r(k + 2, 3);
-    copy_lo(k + 2, 1);
-    read(I1{}, I1{});
-    wait_copies<8>();
-    turn_end();
-    mma(4, 1);
-    turn_end();
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      ar[i] ^= 32768;
-      as[i] ^= 16384;
-    }
-  }
-  if (wv < 4) turn_end();
-  wait_copies<0>();
 
+  int64_t tr;
+  int ts;
+  if (!round_tile(p, 0, &tr, &ts)) return;
+  place(tr, ts);
+  begin();
+  for (int64_t round = 0;; ++round) {
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
+    for (int i = 0; i < 8; ++i)
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const f32x4 q[4] = {acc[4 * c][j], acc[4 * c + 1][j], acc[4 * c + 2][j], acc[4 * c + 3][j]};
-      rows_out<ACT>(p, lds + kOffEpi + wv * 4096, q, r0 + wr + 16 * j,
-                    int32_t(s0) + wsn + 64 * c, 0);
+      for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+    // the tile's first copies, and the last tile's stores
+    wait_copies<0>();
+    turn_end();
+    if (wv >= 4) turn_end();            // the second group runs one turn behind
+    for (int k = 0; k < nk; ++k) {
+      if (!kReadFirst) copy_hi(k + 1, 0);
+      read(I0{}, I0{});
+      if (kReadFirst) copy_hi(k + 1, 0);
+      turn_end();
+      mma(0, 0);
+      turn_end();
+      if (!kReadFirst) copy_hi(k + 1, 1);
+      read(I0{}, I1{});
+      if (kReadFirst) copy_hi(k + 1, 1);
+      wait_copies<8>();
+      turn_end();
+      psh += ds;
+      mask_r(k + 2);
+      mask_s(k + 2, vlo);
+      mask_s(k + 2, vhi);
+      mma(0, 1);
+      turn_end();
+      auto half = [&](int j) {
+        copy_r(k + 2, 2 * j);
+        copy_r(k + 2, 2 * j + 1);
+        copy_lo(k + 2, j);
+      };
+      if (!kReadFirst) half(0);
+      read(I1{}, I0{});
+      if (kReadFirst) half(0);
+      turn_end();
+      mma(4, 0);
+      turn_end();
+      if (!kReadFirst) half(1);
+      read(I1{}, I1{});
+      if (kReadFirst) half(1);
+      wait_copies<8>();
+      turn_end();
+      pr += dr;
+      ps += ds;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        ar[i] ^= 32768;
+        as[i] ^= 16384;
+      }
+      mma(4, 1);
+      turn_end();
     }
+    if (wv < 4) turn_end();
+    wait_copies<0>();
+    if (nk & 1) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {     // back to buffer 0
+        ar[i] ^= 32768;
+        as[i] ^= 16384;
+      }
+    }
+    // the next tile's first copies run under this one's epilogue
+    const int64_t r = r0 + wr;
+    const int32_t c0 = int32_t(s0) + wsn;
+    const bool more = round_tile(p, round + 1, &tr, &ts);
+    if (more) {
+      place(tr, ts);
+      begin();
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const f32x4 q[4] = {acc[4 * c][j], acc[4 * c + 1][j], acc[4 * c + 2][j],
+                            acc[4 * c + 3][j]};
+        rows_out<ACT, false>(p, lds + kOffEpi + wv * 4096, q, r + 16 * j, c0 + 64 * c, 0);
+      }
+    if (!more) return;
+  }
 }
 #endif
 
@@ -372,23 +438,20 @@ template <bool RT, bool ST, int ACT>
 __global__ __launch_bounds__(kThreads, 2) void mm256_kernel(MmParams p) {
 #if defined(__HIP_DEVICE_COMPILE__)
   __shared__ __attribute__((aligned(1024))) char lds[kLds];
-  const int64_t tiles = int64_t(p.tiles_r) * p.tiles_s;
-  int64_t tr;
-  int ts;
-  tile_of(p, xcd_contiguous(blockIdx.x, tiles), &tr, &ts);
-  mm256_tile<RT, ST, ACT>(p, lds, tr, ts);
+  mm256_body<RT, ST, ACT>(p, lds);
 #endif
 }
 
-// 128 x 128 tiles for problems too small to fill the GPU with 256 x 256 ones, and
-// for fp32: 4 waves of 64 x 64, stages of 128 bytes of t (64 bf16, 32 fp32), two
-// buffers (64 KB, so two workgroups share a CU and hide each other's barriers);
-// the contraction may be split.  A lane supplies 16 bytes of t at a time to the
-// MFMAs of either type; the four fp32 products (v_mfma_f32_16x16x4_f32) of those
-// number t as 4 g + i on both sides.  A t-strided fp32 stage has rows of 128
-// columns, 64-byte blocks u of row t at u ^ (t / 4 & 3), read one element at a time.
-constexpr int kSmall = 128;
+// Square tiles of 128 (bf16 problems too small to fill the GPU with 256 x 256 ones)
+// or 64 (fp32): 4 waves of a quarter tile each, stages of 128 bytes of t (64 bf16,
+// 32 fp32) in the same layouts, two buffers, so that two (bf16) or five (fp32)
+// workgroups share a CU and hide each other's barriers; the contraction may be
+// split.  A lane supplies 16 bytes of t at a time to the MFMAs of either type; the
+// four fp32 products (v_mfma_f32_16x16x4_f32) of those number t as 4 g + i on both
+// sides.  A t-strided fp32 stage has rows of 64 columns, 64-byte blocks u of row t
+// at u ^ (t / 4 & 3), read one element at a time.
 constexpr int kSmallThreads = 256;
+template <typename T> constexpr int kSmallTile = sizeof(T) == 2 ? 128 : 64;
 
 #if defined(__HIP_DEVICE_COMPILE__)
 template <typename T>
@@ -407,10 +470,13 @@ __device__ __forceinline__ f32x4 mma(u32x4 a, u32x4 b, f32x4 c) {
 #endif
 
 template <typename T, bool RT, bool ST, int ACT>
-__global__ __launch_bounds__(kSmallThreads, 2) void mm128_kernel(MmParams p) {
+__global__ __launch_bounds__(kSmallThreads, 2) void mm_small_kernel(MmParams p) {
 #if defined(__HIP_DEVICE_COMPILE__)
-  __shared__ __attribute__((aligned(1024))) char lds[65536];
   constexpr int kSz = int(sizeof(T)), kT = 128 / kSz;
+  constexpr int kTileS = kSmallTile<T>, kF = kTileS / 32;   // fragments of a wave per side
+  constexpr int kOp = kTileS * 128;                         // bytes of an operand's stage
+  constexpr int kCols = kTileS * kSz;                       // bytes of a t-strided row
+  __shared__ __attribute__((aligned(1024))) char lds[4 * kOp];
   const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int m = lane & 15, g = lane >> 4;
   const int64_t tiles = int64_t(p.tiles_r) * p.tiles_s;
@@ -418,16 +484,16 @@ __global__ __launch_bounds__(kSmallThreads, 2) void mm128_kernel(MmParams p) {
   int64_t tr;
   int ts;
   tile_of(p, xcd_contiguous(int64_t(blockIdx.x) - split * tiles, tiles), &tr, &ts);
-  const int64_t r0 = tr * kSmall, s0 = int64_t(ts) * kSmall;
+  const int64_t r0 = tr * kTileS, s0 = int64_t(ts) * kTileS;
   const int64_t t0 = split * p.t_split;
   const int64_t t1 = t0 + p.t_split < p.nT ? t0 + p.t_split : p.nT;
-  uint32_t vr[4], vs[4];
-  int tpr[4], tps[4];
+  uint32_t vr[kF], vs[kF];
+  int tpr[kF], tps[kF];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
+  for (int j = 0; j < kF; ++j) {
     const int id = (j * 4 + wv) * 64 + lane;
-    vr[j] = copy_offset<T, RT, 128, false>(id, p.ldr, r0, p.nR, &tpr[j]);
-    vs[j] = copy_offset<T, ST, 128, false>(id, p.lds, s0, p.nS, &tps[j]);
+    vr[j] = copy_offset<T, RT, kTileS, false>(id, p.ldr, r0, p.nR, &tpr[j]);
+    vs[j] = copy_offset<T, ST, kTileS, false>(id, p.lds, s0, p.nS, &tps[j]);
   }
   const char* pr = static_cast<const char*>(p.R) + (RT ? r0 * p.ldr + t0 : t0 * p.ldr + r0) * kSz;
   const char* ps = static_cast<const char*>(p.S) + (ST ? s0 * p.lds + t0 : t0 * p.lds + s0) * kSz;
@@ -437,48 +503,48 @@ __global__ __launch_bounds__(kSmallThreads, 2) void mm128_kernel(MmParams p) {
   auto copy = [&](int k) {
     if (k == nk - 1 && rem < kT) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < kF; ++j) {
         vr[j] = tpr[j] < rem ? vr[j] : kOutOfRange;
         vs[j] = tps[j] < rem ? vs[j] : kOutOfRange;
       }
     }
     const Rsrc a = make_rsrc(pr + k * dr), b = make_rsrc(ps + k * ds);
-    char* d = lds + (k & 1) * 32768 + wv * 1024;
+    char* d = lds + (k & 1) * 2 * kOp + wv * 1024;
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < kF; ++j)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(a, (lds_ptr)(d + j * 4096), 16, vr[j], 0, 0, 0);
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(b, (lds_ptr)(d + 16384 + j * 4096), 16, vs[j], 0, 0,
+    for (int j = 0; j < kF; ++j)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(b, (lds_ptr)(d + kOp + j * 4096), 16, vs[j], 0, 0,
                                                0);
   };
-  const int wr = (wv >> 1) * 64, wsn = (wv & 1) * 64;
+  const int wr = (wv >> 1) * (kTileS / 2), wsn = (wv & 1) * (kTileS / 2);
   // fragment addresses in buffer 0
-  uint32_t ar[4], as[4];
+  uint32_t ar[kF], as[kF];
   const uint32_t l0 = uint32_t(reinterpret_cast<uintptr_t>((lds_ptr)lds));
   const int f = (m >> 2) | ((g & 1) << 2);
   auto address = [&](bool tc, int c0) -> uint32_t {      // c0: first row or column
     if (tc) return uint32_t((c0 + m) * 128 + ((g ^ (lane & 7)) << 4));
-    if (kSz == 2) return uint32_t((g * 8 + (m >> 2)) * 256 + (((c0 / 16) ^ f) << 5) + (m & 3) * 8);
-    return uint32_t(4 * g * 512 + (((c0 / 16) ^ g) << 6) + m * 4);
+    if (kSz == 2) return uint32_t((g * 8 + (m >> 2)) * kCols + (((c0 / 16) ^ f) << 5) + (m & 3) * 8);
+    return uint32_t(4 * g * kCols + (((c0 / 16) ^ g) << 6) + m * 4);
   };
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < kF; ++i) {
     ar[i] = l0 + address(RT, wr + i * 16);
-    as[i] = l0 + 16384 + address(ST, wsn + i * 16);
+    as[i] = l0 + kOp + address(ST, wsn + i * 16);
   }
-  f32x4 acc[4][4];
+  f32x4 acc[kF][kF];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < kF; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+    for (int j = 0; j < kF; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
   // four fragments of half h of the stage's t
-  auto read = [&](auto tc_c, auto h_c, const uint32_t (&a)[4], u32x4 (&d)[4]) {
+  auto read = [&](auto tc_c, auto h_c, const uint32_t (&a)[kF], u32x4 (&d)[kF]) {
     constexpr bool tc = decltype(tc_c)::value;
     constexpr int h = decltype(h_c)::value;
     if constexpr (tc) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < kF; ++i)
         d[i] = *(const __attribute__((address_space(3))) u32x4*)(uintptr_t(a[i] ^ (h * 64)));
     } else if constexpr (kSz == 2) {
       bf16x8 t[4];
@@ -487,15 +553,15 @@ __global__ __launch_bounds__(kSmallThreads, 2) void mm128_kernel(MmParams p) {
       for (int i = 0; i < 4; ++i) d[i] = __builtin_bit_cast(u32x4, t[i]);
     } else {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < kF; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           d[i][e] = *(const __attribute__((address_space(3))) uint32_t*)(uintptr_t(
-              a[i] + h * 8192 + e * 512));
+              a[i] + h * 16 * kCols + e * kCols));
     }
   };
   auto part = [&](auto h_c) {
-    u32x4 a[4], b[4];
+    u32x4 a[kF], b[kF];
     if constexpr (kSz == 2 && !RT && !ST) {
       constexpr int h = decltype(h_c)::value;
       bf16x8 ta[4], tb[4];
@@ -510,9 +576,9 @@ __global__ __launch_bounds__(kSmallThreads, 2) void mm128_kernel(MmParams p) {
       read(std::integral_constant<bool, ST>{}, h_c, as, a);
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < kF; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) acc[i][j] = mma<T>(a[i], b[j], acc[i][j]);
+      for (int j = 0; j < kF; ++j) acc[i][j] = mma<T>(a[i], b[j], acc[i][j]);
   };
   copy(0);
   for (int k = 0; k < nk; ++k) {
@@ -522,16 +588,21 @@ __global__ __launch_bounds__(kSmallThreads, 2) void mm128_kernel(MmParams p) {
     part(std::integral_constant<int, 0>{});
     part(std::integral_constant<int, 1>{});
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      ar[i] ^= 32768;
-      as[i] ^= 32768;
+    for (int i = 0; i < kF; ++i) {
+      ar[i] ^= 2 * kOp;
+      as[i] ^= 2 * kOp;
     }
   }
   turn_end();
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const f32x4 q[4] = {acc[0][j], acc[1][j], acc[2][j], acc[3][j]};
-    rows_out<ACT>(p, lds + wv * 4096, q, r0 + wr + 16 * j, int32_t(s0) + wsn, split);
+  for (int j = 0; j < kF; ++j) {
+    f32x4 q[kF];
+#pragma unroll
+    for (int i = 0; i < kF; ++i) q[i] = acc[i][j];
+    if (p.splits > 1)
+      rows_out<ACT, true>(p, lds + wv * 4096, q, r0 + wr + 16 * j, int32_t(s0) + wsn, split);
+    else
+      rows_out<ACT, false>(p, lds + wv * 4096, q, r0 + wr + 16 * j, int32_t(s0) + wsn, split);
   }
 #endif
 }
@@ -540,12 +611,15 @@ template <bool RT, bool ST, int ACT>
 void run(const MmParams& p, MmTile tile, hipStream_t stream) {
   const unsigned blocks = unsigned(p.tiles_r) * unsigned(p.tiles_s) * unsigned(p.splits);
   switch (tile) {
-    case MmTile::kBig: mm256_kernel<RT, ST, ACT><<<blocks, kThreads, 0, stream>>>(p); break;
+    case MmTile::kBig:
+      mm256_kernel<RT, ST, ACT>
+          <<<blocks < kCUs ? blocks : kCUs, kThreads, 0, stream>>>(p);
+      break;
     case MmTile::kSmall:
-      mm128_kernel<uint16_t, RT, ST, ACT><<<blocks, kSmallThreads, 0, stream>>>(p);
+      mm_small_kernel<uint16_t, RT, ST, ACT><<<blocks, kSmallThreads, 0, stream>>>(p);
       break;
     case MmTile::kSmallF32:
-      mm128_kernel<float, RT, ST, ACT><<<blocks, kSmallThreads, 0, stream>>>(p);
+      mm_small_kernel<float, RT, ST, ACT><<<blocks, kSmallThreads, 0, stream>>>(p);
       break;
   }
 }

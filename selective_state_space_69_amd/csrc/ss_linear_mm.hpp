@@ -8,8 +8,8 @@
 
 namespace ss {
 
-// O = R S^T on 256 x 256 (bf16, one split) or 128 x 128 tiles, as p.tiles_r,
-// p.tiles_s and p.splits say; rt, st: whether t is the operand's contiguous axis
+// O = R S^T on 256 x 256 (bf16, one split), 128 x 128 (bf16) or 64 x 64 (fp32) tiles,
+// as p.tiles_r, p.tiles_s and p.splits say; rt, st: whether t is the operand's contiguous axis
 // (rt or not st).  An activation only with rt and st.
 // Operands are read in 16-byte units: rows are 16-byte aligned, and a row's last
 // unit is inside its storage, with zeros past the contraction's end where t is the
@@ -23,78 +23,65 @@ void launch_mm(const MmParams& p, MmTile tile, bool rt, bool st, hipStream_t str
 constexpr int64_t kRowsMax = 32;
 void launch_rows(const MmParams& p, bool bf16, bool vec, hipStream_t stream);
 
+// Eight neighbours at any element address (16-byte accesses need no alignment).
+struct __attribute__((packed, aligned(2))) Halves8 { uint32_t w[4]; };
+struct __attribute__((packed, aligned(4))) Floats8 { float v[8]; };
 __device__ __forceinline__ void store8(void* base, int64_t i, int bf16, const float (&v)[8]) {
   if (bf16) {
-    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + i) =
-        make_uint4(cvt_bf16x2(v[0], v[1]), cvt_bf16x2(v[2], v[3]), cvt_bf16x2(v[4], v[5]),
-                   cvt_bf16x2(v[6], v[7]));
+    *reinterpret_cast<Halves8*>(static_cast<uint16_t*>(base) + i) =
+        Halves8{{cvt_bf16x2(v[0], v[1]), cvt_bf16x2(v[2], v[3]), cvt_bf16x2(v[4], v[5]),
+                 cvt_bf16x2(v[6], v[7])}};
   } else {
-    float4* d = reinterpret_cast<float4*>(static_cast<float*>(base) + i);
-    d[0] = make_float4(v[0], v[1], v[2], v[3]);
-    d[1] = make_float4(v[4], v[5], v[6], v[7]);
+    *reinterpret_cast<Floats8*>(static_cast<float*>(base) + i) =
+        Floats8{{v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7]}};
   }
 }
+__device__ __forceinline__ void add8(const void* base, int64_t i, int bf16, float (&v)[8]) {
+  if (bf16) {
+    const Halves8 h = *reinterpret_cast<const Halves8*>(static_cast<const uint16_t*>(base) + i);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[2 * j] += __uint_as_float(h.w[j] << 16);
+      v[2 * j + 1] += __uint_as_float(h.w[j] & 0xffff0000u);
+    }
+  } else {
+    const Floats8 f = *reinterpret_cast<const Floats8*>(static_cast<const float*>(base) + i);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] += f.v[j];
+  }
+}
+__device__ __forceinline__ void store1(void* base, int64_t i, int bf16, float v) {
+  if (bf16) static_cast<uint16_t*>(base)[i] = f32_to_bf16(v);
+  else static_cast<float*>(base)[i] = v;
+}
 
-// One element of the output, or of a split's partial sums.
-template <int ACT>
-__device__ __forceinline__ void epilogue1(const MmParams& p, int64_t r, int32_t s, float v,
-                                          int split) {
-  if (r >= p.nR || s >= p.nS) return;
+// One element of the output: bias, activation, residual, stores.
+__device__ __forceinline__ void epilogue1(const MmParams& p, int act, int64_t r, int32_t s,
+                                          float v) {
   const int64_t o = r * p.nS + s;
-  if (p.splits > 1) {
-    p.part[split * p.nR * p.nS + o] = v;
-    return;
-  }
   if (p.bias) v += p.bias[s];
-  if (p.pre) {
-    if (p.pre_bf16) static_cast<uint16_t*>(p.pre)[o] = f32_to_bf16(v);
-    else static_cast<float*>(p.pre)[o] = v;
-  }
-  v = apply_act(ACT, v);
+  if (p.pre) store1(p.pre, o, p.pre_bf16, v);
+  v = apply_act(act, v);
   if (p.res)
     v += p.res_bf16 ? to_f32(static_cast<const uint16_t*>(p.res)[o])
                     : static_cast<const float*>(p.res)[o];
-  if (p.out_bf16) static_cast<uint16_t*>(p.out)[o] = f32_to_bf16(v);
-  else static_cast<float*>(p.out)[o] = v;
+  store1(p.out, o, p.out_bf16, v);
 }
 
-// Eight neighbours s..s+7 of output row r; nS and s are multiples of 8.
+// Eight neighbours s..s+7 of output row r, all inside it.  ACT: the activation, or
+// kActOf for p.act.
+constexpr int kActOf = -1;
 template <int ACT>
-__device__ __forceinline__ void epilogue8(const MmParams& p, int64_t r, int32_t s, float (&v)[8],
-                                          int split) {
-  if (r >= p.nR || s >= p.nS) return;
+__device__ __forceinline__ void epilogue8(const MmParams& p, int64_t r, int32_t s, float (&v)[8]) {
+  const int act = ACT == kActOf ? p.act : ACT;
   const int64_t o = r * p.nS + s;
-  if (p.splits > 1) {
-    store8(p.part, split * p.nR * p.nS + o, 0, v);
-    return;
-  }
-  if (p.bias) {
-    const float4 b0 = *reinterpret_cast<const float4*>(p.bias + s);
-    const float4 b1 = *reinterpret_cast<const float4*>(p.bias + s + 4);
-    v[0] += b0.x; v[1] += b0.y; v[2] += b0.z; v[3] += b0.w;
-    v[4] += b1.x; v[5] += b1.y; v[6] += b1.z; v[7] += b1.w;
-  }
+  if (p.bias) add8(p.bias, s, 0, v);
   if (p.pre) store8(p.pre, o, p.pre_bf16, v);
-  if constexpr (ACT != SS_ACT_NONE) {
+  if (act != SS_ACT_NONE) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = apply_act(ACT, v[j]);
+    for (int j = 0; j < 8; ++j) v[j] = apply_act(act, v[j]);
   }
-  if (p.res) {
-    if (p.res_bf16) {
-      const uint4 w = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.res) + o);
-      const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        v[2 * j] += __uint_as_float(u[j] << 16);
-        v[2 * j + 1] += __uint_as_float(u[j] & 0xffff0000u);
-      }
-    } else {
-      const float4* f = reinterpret_cast<const float4*>(static_cast<const float*>(p.res) + o);
-      const float4 b0 = f[0], b1 = f[1];
-      v[0] += b0.x; v[1] += b0.y; v[2] += b0.z; v[3] += b0.w;
-      v[4] += b1.x; v[5] += b1.y; v[6] += b1.z; v[7] += b1.w;
-    }
-  }
+  if (p.res) add8(p.res, o, p.res_bf16, v);
   store8(p.out, o, p.out_bf16, v);
 }
 
