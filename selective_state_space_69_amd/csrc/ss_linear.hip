@@ -21,9 +21,11 @@ __global__ __launch_bounds__(kThreads) void join_kernel(MmParams p) {
     const float* src = p.part + r * p.nS + s;
     const int64_t step = p.nR * p.nS;
     if (s + 8 <= p.nS) {
-      float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-      for (int k = 0; k < p.splits; ++k) add8(src, k * step, 0, v);
-      epilogue8<kActOf>(p, r, s, v);
+      float v[8] = {0, 0, 0, 0, 0, 0, 0, 0}, bias[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+      const Res8 res = fetch_res8(p, r, s);
+      if (p.bias) add8(p.bias + s, bias);
+      for (int k = 0; k < p.splits; ++k) add8(src + k * step, v);
+      epilogue8<kActOf>(p, r, s, v, bias, res);
     } else {
       for (int j = 0; s + j < p.nS; ++j) {
         float v = 0.0f;

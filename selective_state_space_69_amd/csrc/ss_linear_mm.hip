@@ -157,41 +157,68 @@ __device__ __forceinline__ uint32_t copy_offset(int id, int64_t ld, int64_t i0, 
   }
 }
 
-// Epilogue of 16 rows x 16 F columns of a wave: the accumulators (lane: row lane &
-// 15, four neighbours of each 16-column piece q[i]) are turned through 4 KB of
-// LDS into whole rows, 8 columns per lane.  SPLIT: to a split's partial sums
-// instead.  The loops are rolled: unrolled, the epilogue outgrew the instruction
-// cache and cost 20 us a tile.
+// The epilogue of a wave's 16 F-column pieces.  The accumulators (lane: row lane &
+// 15, four neighbours of each 16-column piece) are turned through 4 KB of LDS into
+// whole rows, 8 columns per lane, 2 F lanes to a row.  Bias is fetched once per
+// column, a piece's residual before the stores of the piece in front of it: a wave's
+// loads wait for its older stores.  The loop over rows is rolled: unrolled, the
+// epilogue outgrew the instruction cache and cost 20 us a tile.
+template <int F>
+struct Piece {
+  static constexpr int kPer = 2 * F;                // lanes of a row
+  static constexpr int kRows = 64 / kPer;           // rows of one pass
+  static constexpr int kPasses = 16 / kRows;
+  int64_t r;      // this lane's row in the first pass
+  int32_t s;      // its first column
+  Res8 res[kPasses];
+  __device__ __forceinline__ void fetch(const MmParams& p, int64_t r0, int32_t s0) {
+    const int lane = threadIdx.x & 63;
+    r = r0 + lane / kPer;
+    s = s0 + (lane % kPer) * 8;
+#pragma unroll
+    for (int h = 0; h < kPasses; ++h) res[h] = fetch_res8(p, r + h * kRows, s);
+  }
+};
+__device__ __forceinline__ void fetch_bias(const MmParams& p, int32_t s, float (&bias)[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) bias[j] = 0.0f;
+  if (p.bias && s + 8 <= p.nS) add8(p.bias + s, bias);
+}
+
+// One piece of 16 rows x 16 F columns; SPLIT: to a split's partial sums instead.
 template <int ACT, bool SPLIT, int F>
-__device__ __forceinline__ void rows_out(const MmParams& p, char* sl, const f32x4 (&q)[F],
-                                         int64_t r0, int32_t s0, int split) {
+__device__ __forceinline__ void piece_out(const MmParams& p, char* sl, const f32x4 (&q)[F],
+                                          const Piece<F>& at, const float (&bias)[8], int split) {
   const int lane = threadIdx.x & 63, m = lane & 15, g = lane >> 4;
 #pragma unroll
   for (int i = 0; i < F; ++i)
     *reinterpret_cast<f32x4*>(sl + m * 256 + (((4 * i + g) ^ m) << 4)) = q[i];
   asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  const int u = (lane % Piece<F>::kPer) * 2;
+  Res8 res = at.res[0];
 #pragma nounroll
-  for (int h = 0; h < F / 2; ++h) {
-    constexpr int per = 2 * F;          // lanes of a row
-    const int row = h * (64 / per) + lane / per, u = (lane % per) * 2;
-    const int64_t r = r0 + row;
-    const int32_t s = s0 + u * 4;
-    if (r >= p.nR || s >= p.nS) continue;
-    if (s + 8 <= p.nS) {
-      const f32x4 x = *reinterpret_cast<const f32x4*>(sl + row * 256 + ((u ^ row) << 4));
-      const f32x4 y = *reinterpret_cast<const f32x4*>(sl + row * 256 + (((u + 1) ^ row) << 4));
-      float v[8] = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
-      if constexpr (SPLIT) store8(p.part, (split * p.nR + r) * p.nS + s, 0, v);
-      else epilogue8<ACT>(p, r, s, v);
-    } else {
+  for (int h = 0; h < Piece<F>::kPasses; ++h) {
+    const int row = h * Piece<F>::kRows + lane / Piece<F>::kPer;
+    const int64_t r = at.r + h * Piece<F>::kRows;
+    const int32_t s = at.s;
+    if (r < p.nR && s < p.nS) {
+      if (s + 8 <= p.nS) {
+        const f32x4 x = *reinterpret_cast<const f32x4*>(sl + row * 256 + ((u ^ row) << 4));
+        const f32x4 y = *reinterpret_cast<const f32x4*>(sl + row * 256 + (((u + 1) ^ row) << 4));
+        float v[8] = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
+        if constexpr (SPLIT) store8(p.part, (split * p.nR + r) * p.nS + s, 0, v);
+        else epilogue8<ACT>(p, r, s, v, bias, res);
+      } else {
 #pragma nounroll
-      for (int j = 0; s + j < p.nS; ++j) {
-        const float v = *reinterpret_cast<const float*>(sl + row * 256 +
-                                                        (((u + j / 4) ^ row) << 4) + (j & 3) * 4);
-        if constexpr (SPLIT) p.part[(split * p.nR + r) * p.nS + s + j] = v;
-        else epilogue1(p, ACT, r, s + j, v);
+        for (int j = 0; s + j < p.nS; ++j) {
+          const float v = *reinterpret_cast<const float*>(
+              sl + row * 256 + (((u + j / 4) ^ row) << 4) + (j & 3) * 4);
+          if constexpr (SPLIT) p.part[(split * p.nR + r) * p.nS + s + j] = v;
+          else epilogue1(p, ACT, r, s + j, v);
+        }
       }
     }
+    if constexpr (Piece<F>::kPasses > 1) res = at.res[Piece<F>::kPasses - 1];
   }
   asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
 }
@@ -206,15 +233,29 @@ __device__ __forceinline__ bool round_tile(const MmParams& p, int64_t round, int
   return true;
 }
 
+// The kernel's parameters, read again where they are used from here on: held in
+// scalar registers through the main loop they would crowd it.
+__device__ __forceinline__ MmParams reread_params() {
+  constexpr int kWords = int(sizeof(MmParams) / 8);
+  static_assert(sizeof(MmParams) % 8 == 0, "read in 8-byte words");
+  uint64_t a = uint64_t(__builtin_amdgcn_kernarg_segment_ptr());   // the only parameter
+  asm volatile("" : "+s"(a));
+  struct Words { uint64_t w[kWords]; } v;
+#pragma unroll
+  for (int i = 0; i < kWords; ++i)
+    v.w[i] = ((const __attribute__((address_space(4))) uint64_t*)a)[i];
+  return __builtin_bit_cast(MmParams, v);
+}
+
 template <bool RT, bool ST, int ACT>
-__device__ __forceinline__ void mm256_body(const MmParams& p, char* lds) {
+__device__ __forceinline__ void mm256_body(const MmParams& p0, char* lds) {
   const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int m = lane & 15, g = lane >> 4;
   int64_t r0, s0;
   uint32_t vr[4], vlo[2], vhi[2];
   int tpr[4], tps[2];
   const char *pr, *ps, *psh;
-  auto place = [&](int64_t tr, int ts) {
+  auto place = [&](const MmParams& p, int64_t tr, int ts) {
     r0 = tr * kTile;
     s0 = int64_t(ts) * kTile;
 #pragma unroll
@@ -231,10 +272,10 @@ __device__ __forceinline__ void mm256_body(const MmParams& p, char* lds) {
     ps = static_cast<const char*>(p.S) + (ST ? s0 * p.lds : s0) * 2;
     psh = ps + (ST ? 64 * p.lds : 64) * 2;
   };
-  const int64_t dr = RT ? kStep * 2 : p.ldr * kStep * 2;
-  const int64_t ds = ST ? kStep * 2 : p.lds * kStep * 2;
-  const int nk = int((p.nT + kStep - 1) / kStep);
-  const int rem = int(p.nT - int64_t(nk - 1) * kStep);      // t of the last stage, 1..64
+  const int64_t dr = RT ? kStep * 2 : p0.ldr * kStep * 2;
+  const int64_t ds = ST ? kStep * 2 : p0.lds * kStep * 2;
+  const int nk = int((p0.nT + kStep - 1) / kStep);
+  const int rem = int(p0.nT - int64_t(nk - 1) * kStep);      // t of the last stage, 1..64
 
   // resource of a stage k that starts at base; past the last one no byte is in range
   auto rsrc = [&](const char* base, int k) {
@@ -244,17 +285,19 @@ __device__ __forceinline__ void mm256_body(const MmParams& p, char* lds) {
   auto copy = [&](Rsrc src, int dst, uint32_t off) {
     __builtin_amdgcn_raw_ptr_buffer_load_lds(src, (lds_ptr)(lds + dst), 16, off, 0, 0, 0);
   };
-  // a partial last stage: units past the contraction's end read as zero
-  auto mask_r = [&](int k) {
-    if (k == nk - 1 && rem < kStep) {
+  // a partial last stage: units past the contraction's end read as zero (the empty
+  // asm keeps this a branch, taken once: as selects it cost each stage 12 of them)
+  const bool partial = rem < kStep;
+  auto mask_all = [&](int k) {
+    if (partial && k == nk - 1) {
+      asm volatile("");
 #pragma unroll
       for (int j = 0; j < 4; ++j) vr[j] = tpr[j] < rem ? vr[j] : kOutOfRange;
-    }
-  };
-  auto mask_s = [&](int k, uint32_t (&v)[2]) {
-    if (k == nk - 1 && rem < kStep) {
 #pragma unroll
-      for (int j = 0; j < 2; ++j) v[j] = tps[j] < rem ? v[j] : kOutOfRange;
+      for (int j = 0; j < 2; ++j) {
+        vlo[j] = tps[j] < rem ? vlo[j] : kOutOfRange;
+        vhi[j] = tps[j] < rem ? vhi[j] : kOutOfRange;
+      }
     }
   };
   // pr, ps, psh: where the next stage to copy of R, S lo, S hi starts
@@ -289,9 +332,7 @@ __device__ __forceinline__ void mm256_body(const MmParams& p, char* lds) {
 
   // the first copies of a tile: stage 0, and R and S lo of stage 1
   auto begin = [&]() {
-    mask_r(0);
-    mask_s(0, vlo);
-    mask_s(0, vhi);
+    mask_all(0);
 #pragma unroll
     for (int j = 0; j < 4; ++j) copy_r(0, j);
 #pragma unroll
@@ -301,9 +342,7 @@ __device__ __forceinline__ void mm256_body(const MmParams& p, char* lds) {
     pr += dr;
     ps += ds;
     psh += ds;
-    mask_r(1);
-    mask_s(1, vlo);
-    mask_s(1, vhi);
+    mask_all(1);
 #pragma unroll
     for (int j = 0; j < 4; ++j) copy_r(1, j);
 #pragma unroll
@@ -348,8 +387,8 @@ __device__ __forceinline__ void mm256_body(const MmParams& p, char* lds) {
 
   int64_t tr;
   int ts;
-  if (!round_tile(p, 0, &tr, &ts)) return;
-  place(tr, ts);
+  if (!round_tile(p0, 0, &tr, &ts)) return;
+  place(p0, tr, ts);
   begin();
   for (int64_t round = 0;; ++round) {
 #pragma unroll
@@ -373,9 +412,7 @@ __device__ __forceinline__ void mm256_body(const MmParams& p, char* lds) {
       wait_copies<8>();
       turn_end();
       psh += ds;
-      mask_r(k + 2);
-      mask_s(k + 2, vlo);
-      mask_s(k + 2, vhi);
+      mask_all(k + 2);
       mma(0, 1);
       turn_end();
       auto half = [&](int j) {
@@ -414,21 +451,27 @@ __device__ __forceinline__ void mm256_body(const MmParams& p, char* lds) {
       }
     }
     // the next tile's first copies run under this one's epilogue
+    const MmParams p = reread_params();
     const int64_t r = r0 + wr;
     const int32_t c0 = int32_t(s0) + wsn;
     const bool more = round_tile(p, round + 1, &tr, &ts);
     if (more) {
-      place(tr, ts);
+      place(p, tr, ts);
       begin();
     }
+    Piece<4> now, next;
+    float bias[2][8];
+    fetch_bias(p, c0 + (lane & 7) * 8, bias[0]);
+    fetch_bias(p, c0 + 64 + (lane & 7) * 8, bias[1]);
+    now.fetch(p, r, c0);
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const f32x4 q[4] = {acc[4 * c][j], acc[4 * c + 1][j], acc[4 * c + 2][j],
-                            acc[4 * c + 3][j]};
-        rows_out<ACT, false>(p, lds + kOffEpi + wv * 4096, q, r + 16 * j, c0 + 64 * c, 0);
-      }
+    for (int i = 0; i < 8; ++i) {       // rows 16 (i / 2), columns 64 (i & 1)
+      const int j = i / 2, c = i & 1;
+      if (i < 7) next.fetch(p, r + 16 * ((i + 1) / 2), c0 + 64 * ((i + 1) & 1));
+      const f32x4 q[4] = {acc[4 * c][j], acc[4 * c + 1][j], acc[4 * c + 2][j], acc[4 * c + 3][j]};
+      piece_out<ACT, false>(p, lds + kOffEpi + wv * 4096, q, now, bias[c], 0);
+      now = next;
+    }
     if (!more) return;
   }
 }
@@ -594,15 +637,26 @@ __global__ __launch_bounds__(kSmallThreads, 2) void mm_small_kernel(MmParams p) 
     }
   }
   turn_end();
+  const int64_t r = r0 + wr;
+  const int32_t c = int32_t(s0) + wsn;
+  Piece<kF> now, next;
+  float bias[8];
+  fetch_bias(p, c + (lane % Piece<kF>::kPer) * 8, bias);
+  if (p.splits == 1) now.fetch(p, r, c);
 #pragma unroll
   for (int j = 0; j < kF; ++j) {
     f32x4 q[kF];
 #pragma unroll
     for (int i = 0; i < kF; ++i) q[i] = acc[i][j];
-    if (p.splits > 1)
-      rows_out<ACT, true>(p, lds + wv * 4096, q, r0 + wr + 16 * j, int32_t(s0) + wsn, split);
-    else
-      rows_out<ACT, false>(p, lds + wv * 4096, q, r0 + wr + 16 * j, int32_t(s0) + wsn, split);
+    if (p.splits > 1) {
+      now.r = r + 16 * j + lane / Piece<kF>::kPer;
+      now.s = c + (lane % Piece<kF>::kPer) * 8;
+      piece_out<ACT, true>(p, lds + wv * 4096, q, now, bias, split);
+    } else {
+      if (j + 1 < kF) next.fetch(p, r + 16 * (j + 1), c);
+      piece_out<ACT, false>(p, lds + wv * 4096, q, now, bias, 0);
+      now = next;
+    }
   }
 #endif
 }

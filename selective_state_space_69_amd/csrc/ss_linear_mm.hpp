@@ -36,19 +36,10 @@ __device__ __forceinline__ void store8(void* base, int64_t i, int bf16, const fl
         Floats8{{v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7]}};
   }
 }
-__device__ __forceinline__ void add8(const void* base, int64_t i, int bf16, float (&v)[8]) {
-  if (bf16) {
-    const Halves8 h = *reinterpret_cast<const Halves8*>(static_cast<const uint16_t*>(base) + i);
+__device__ __forceinline__ void add8(const float* src, float (&v)[8]) {
+  const Floats8 f = *reinterpret_cast<const Floats8*>(src);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      v[2 * j] += __uint_as_float(h.w[j] << 16);
-      v[2 * j + 1] += __uint_as_float(h.w[j] & 0xffff0000u);
-    }
-  } else {
-    const Floats8 f = *reinterpret_cast<const Floats8*>(static_cast<const float*>(base) + i);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] += f.v[j];
-  }
+  for (int j = 0; j < 8; ++j) v[j] += f.v[j];
 }
 __device__ __forceinline__ void store1(void* base, int64_t i, int bf16, float v) {
   if (bf16) static_cast<uint16_t*>(base)[i] = f32_to_bf16(v);
@@ -68,20 +59,52 @@ __device__ __forceinline__ void epilogue1(const MmParams& p, int act, int64_t r,
   store1(p.out, o, p.out_bf16, v);
 }
 
-// Eight neighbours s..s+7 of output row r, all inside it.  ACT: the activation, or
-// kActOf for p.act.
+// Eight neighbours of the residual, fetched ahead in their storage form.
+struct Res8 { uint32_t w[8]; };
+__device__ __forceinline__ Res8 fetch_res8(const MmParams& p, int64_t r, int32_t s) {
+  Res8 f{};
+  if (p.res && r < p.nR && s + 8 <= p.nS) {
+    const int64_t o = r * p.nS + s;
+    if (p.res_bf16) {
+      const Halves8 h = *reinterpret_cast<const Halves8*>(static_cast<const uint16_t*>(p.res) + o);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) f.w[j] = h.w[j];
+    } else {
+      const Floats8 v = *reinterpret_cast<const Floats8*>(static_cast<const float*>(p.res) + o);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f.w[j] = __float_as_uint(v.v[j]);
+    }
+  }
+  return f;
+}
+
+// Eight neighbours s..s+7 of output row r, all inside it; bias: theirs (0 without
+// one).  ACT: the activation, or kActOf for p.act.
 constexpr int kActOf = -1;
 template <int ACT>
-__device__ __forceinline__ void epilogue8(const MmParams& p, int64_t r, int32_t s, float (&v)[8]) {
+__device__ __forceinline__ void epilogue8(const MmParams& p, int64_t r, int32_t s, float (&v)[8],
+                                          const float (&bias)[8], const Res8& res) {
   const int act = ACT == kActOf ? p.act : ACT;
   const int64_t o = r * p.nS + s;
-  if (p.bias) add8(p.bias, s, 0, v);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] += bias[j];
   if (p.pre) store8(p.pre, o, p.pre_bf16, v);
   if (act != SS_ACT_NONE) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = apply_act(act, v[j]);
   }
-  if (p.res) add8(p.res, o, p.res_bf16, v);
+  if (p.res) {
+    if (p.res_bf16) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        v[2 * j] += __uint_as_float(res.w[j] << 16);
+        v[2 * j + 1] += __uint_as_float(res.w[j] & 0xffff0000u);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] += __uint_as_float(res.w[j]);
+    }
+  }
   store8(p.out, o, p.out_bf16, v);
 }
 
