@@ -1,7 +1,6 @@
 // Linear projections for gfx950: the plan, what prepares the products' operands
 // (aligned copies of rows that 16-byte loads cannot read in place, the backward's
 // pre-activation gradient), the join of split contractions, and the launchers.
-#include <cstdlib>
 #include "ss_linear_mm.hpp"
 
 namespace ss {
@@ -148,8 +147,15 @@ int64_t pad_to_unit(const ss_linear_desc_t& d, int64_t n) {
 
 // How a product is tiled.  bf16: 256 x 256 tiles where they fill the GPU's 256 CUs
 // at least half, else 128 x 128, of which two fit on a CU.  fp32: 64 x 64, of which
-// four or five fit.  With fewer tiles than fit, the contraction is split as often as
-// they still fit at once, into parts of at least 4 stages.
+// four fit.  Where the tiles of a long contraction leave CUs empty it is split, into
+// as many parts as the model below finds best: a stage of 128 bytes takes 0.7 us
+// with one workgroup on a CU and 0.9 us for two (fp32: 0.5 us for each, not below
+// 0.7), and a split product pays for the join kernel and for its partial sums'
+// way to memory and back.  Measured, 768 x 1536 over 5003 rows (72 tiles, 79 stages):
+// 50.9 us in one part, 30.5 in three (the model's choice), 28.7 in five, 36.6 in
+// eight; 5003 x 768 over 1536 (240 tiles, 24 stages): 22.2 us in one (the choice),
+// 28.2 in two; 1000 x 512 over 2560 (32 tiles, 40 stages): 29.0, 21.2 in two, 16.7
+// in five (the choice).
 struct Tiling {
   MmTile tile;
   int32_t tiles_r, tiles_s, splits;
@@ -160,7 +166,7 @@ Tiling tiling(const ss_linear_desc_t& d, int64_t nR, int64_t nS, int64_t nT) {
   t.splits = 1;
   t.t_split = nT;
   const int64_t r256 = (nR + 255) / 256, s256 = (nS + 255) / 256;
-  if (d.in_dtype == SS_BF16 && r256 * s256 >= (getenv("SMALL") ? 1<<30 : 128)) {
+  if (d.in_dtype == SS_BF16 && r256 * s256 >= 128) {
     t.tile = MmTile::kBig;
     t.tiles_r = int32_t(r256);
     t.tiles_s = int32_t(s256);
@@ -171,11 +177,19 @@ Tiling tiling(const ss_linear_desc_t& d, int64_t nR, int64_t nS, int64_t nT) {
   t.tile = bf16 ? MmTile::kSmall : MmTile::kSmallF32;
   t.tiles_r = int32_t((nR + side - 1) / side);
   t.tiles_s = int32_t((nS + side - 1) / side);
-  int64_t k = fit / (int64_t(t.tiles_r) * t.tiles_s);
-  const int64_t most = nT / (4 * step);
-  if (k > most) k = most;
-  if (k > 64) k = 64;
-  if (k < 1) k = 1;
+  const int64_t tiles = int64_t(t.tiles_r) * t.tiles_s, stages = (nT + step - 1) / step;
+  const double out_us = double(nR) * double(nS) * 8.0 / 4.0e6;    // one part there and back
+  int64_t k = 1;
+  double best = 0.0;
+  for (int64_t i = 1; i <= 64 && (i == 1 || (i * tiles <= fit && i * 2 <= stages)); ++i) {
+    const int64_t per_cu = (i * tiles + 255) / 256;
+    const double stage_us = bf16 ? (per_cu > 1 ? 0.9 : 0.7) : (per_cu > 1 ? 0.5 * per_cu : 0.7);
+    const double us = double((stages + i - 1) / i) * stage_us + (i > 1 ? 6.0 + i * out_us : 0.0);
+    if (i == 1 || us < best) {
+      best = us;
+      k = i;
+    }
+  }
   int64_t len = (nT + k - 1) / k;
   len = (len + step - 1) / step * step;
   t.t_split = len;
