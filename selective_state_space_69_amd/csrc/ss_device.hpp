@@ -108,12 +108,15 @@ template <> __device__ __forceinline__ void buf_store<uint16_t>(Rsrc r, uint32_t
 // r log2 e = e log2 e) and below 2^-24 of the result elsewhere, so 1/u1 is
 // replaced by 2 - u1 (relative error (u1 - 1)^2 / u1).  Small steps keep full
 // relative accuracy down to the smallest normal e.
-__device__ __forceinline__ float softplus_log2(float x2) {
-  const float e = hw_exp2(-__builtin_fabsf(x2));
+__device__ __forceinline__ float log2_1p_exp2(float nx2) {      // log2(1 + 2^nx2), nx2 <= 0
+  const float e = hw_exp2(nx2);
   const float u1 = 1.0f + e;
   const float r = e - (u1 - 1.0f);                               // exact rounding error of u1
   const float k = __builtin_fmaf(-u1, kLog2e, 2.0f * kLog2e);    // log2(e) (2 - u1)
-  return __builtin_fmaxf(x2, 0.0f) + __builtin_fmaf(r, k, hw_log2(u1));
+  return __builtin_fmaf(r, k, hw_log2(u1));
+}
+__device__ __forceinline__ float softplus_log2(float x2) {
+  return __builtin_fmaxf(x2, 0.0f) + log2_1p_exp2(-__builtin_fabsf(x2));
 }
 
 // Exact-ZOH input coefficient coef = (exp(x) - 1) / A with x = dt A ("Mamba: S4

@@ -22,8 +22,13 @@ __global__ __launch_bounds__(kThreads) void join_kernel(MmParams p) {
     if (s + 8 <= p.nS) {
       float v[8] = {0, 0, 0, 0, 0, 0, 0, 0}, bias[8] = {0, 0, 0, 0, 0, 0, 0, 0};
       const Res8 res = fetch_res8(p, r, s);
-      if (p.bias) add8(p.bias + s, bias);
-      for (int k = 0; k < p.splits; ++k) add8(src + k * step, v);
+      if (p.bias) load8(p.bias + s, bias);
+      for (int k = 0; k < p.splits; ++k) {
+        float f[8];
+        load8(src + k * step, f);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] += f[j];
+      }
       epilogue8<kActOf>(p, r, s, v, bias, res);
     } else {
       for (int j = 0; s + j < p.nS; ++j) {

@@ -182,7 +182,7 @@ struct Piece {
 __device__ __forceinline__ void fetch_bias(const MmParams& p, int32_t s, float (&bias)[8]) {
 #pragma unroll
   for (int j = 0; j < 8; ++j) bias[j] = 0.0f;
-  if (p.bias && s + 8 <= p.nS) add8(p.bias + s, bias);
+  if (p.bias && s + 8 <= p.nS) load8(p.bias + s, bias);
 }
 
 // One piece of 16 rows x 16 F columns; SPLIT: to a split's partial sums instead.
@@ -213,7 +213,7 @@ __device__ __forceinline__ void piece_out(const MmParams& p, char* sl, const f32
         for (int j = 0; s + j < p.nS; ++j) {
           const float v = *reinterpret_cast<const float*>(
               sl + row * 256 + (((u + j / 4) ^ row) << 4) + (j & 3) * 4);
-          if constexpr (SPLIT) p.part[(split * p.nR + r) * p.nS + s + j] = v;
+          if constexpr (SPLIT) store1(p.part, (split * p.nR + r) * p.nS + s + j, 0, v);
           else epilogue1(p, ACT, r, s + j, v);
         }
       }

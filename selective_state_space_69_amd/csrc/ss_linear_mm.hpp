@@ -23,39 +23,50 @@ void launch_mm(const MmParams& p, MmTile tile, bool rt, bool st, hipStream_t str
 constexpr int64_t kRowsMax = 32;
 void launch_rows(const MmParams& p, bool bf16, bool vec, hipStream_t stream);
 
-// Eight neighbours at any element address (16-byte accesses need no alignment).
-struct __attribute__((packed, aligned(2))) Halves8 { uint32_t w[4]; };
-struct __attribute__((packed, aligned(4))) Floats8 { float v[8]; };
+// Accesses of the epilogue: to global memory (said so, since the parameters may have
+// come back from memory as plain words), eight neighbours at any element address
+// (16-byte accesses need no alignment).
+template <typename T> using Global = __attribute__((address_space(1))) T;
+typedef uint32_t Halves8 __attribute__((ext_vector_type(4), aligned(2)));
+typedef float Floats4 __attribute__((ext_vector_type(4), aligned(4)));
+
 __device__ __forceinline__ void store8(void* base, int64_t i, int bf16, const float (&v)[8]) {
   if (bf16) {
-    *reinterpret_cast<Halves8*>(static_cast<uint16_t*>(base) + i) =
-        Halves8{{cvt_bf16x2(v[0], v[1]), cvt_bf16x2(v[2], v[3]), cvt_bf16x2(v[4], v[5]),
-                 cvt_bf16x2(v[6], v[7])}};
+    Global<uint16_t>* d = (Global<uint16_t>*)base + i;
+    *(Global<Halves8>*)d = Halves8{cvt_bf16x2(v[0], v[1]), cvt_bf16x2(v[2], v[3]),
+                                   cvt_bf16x2(v[4], v[5]), cvt_bf16x2(v[6], v[7])};
   } else {
-    *reinterpret_cast<Floats8*>(static_cast<float*>(base) + i) =
-        Floats8{{v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7]}};
+    Global<float>* d = (Global<float>*)base + i;
+    *(Global<Floats4>*)d = Floats4{v[0], v[1], v[2], v[3]};
+    *(Global<Floats4>*)(d + 4) = Floats4{v[4], v[5], v[6], v[7]};
   }
 }
-__device__ __forceinline__ void add8(const float* src, float (&v)[8]) {
-  const Floats8 f = *reinterpret_cast<const Floats8*>(src);
+__device__ __forceinline__ void load8(const float* src, float (&v)[8]) {
+  const Global<Floats4>* s = (const Global<Floats4>*)src;
+  const Floats4 a = *s, b = *(const Global<Floats4>*)((const Global<float>*)src + 4);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) v[j] += f.v[j];
+  for (int j = 0; j < 4; ++j) {
+    v[j] = a[j];
+    v[4 + j] = b[j];
+  }
 }
 __device__ __forceinline__ void store1(void* base, int64_t i, int bf16, float v) {
-  if (bf16) static_cast<uint16_t*>(base)[i] = f32_to_bf16(v);
-  else static_cast<float*>(base)[i] = v;
+  if (bf16) ((Global<uint16_t>*)base)[i] = f32_to_bf16(v);
+  else ((Global<float>*)base)[i] = v;
+}
+__device__ __forceinline__ float load1(const void* base, int64_t i, int bf16) {
+  return bf16 ? to_f32(uint16_t(((const Global<uint16_t>*)base)[i]))
+              : float(((const Global<float>*)base)[i]);
 }
 
 // One element of the output: bias, activation, residual, stores.
 __device__ __forceinline__ void epilogue1(const MmParams& p, int act, int64_t r, int32_t s,
                                           float v) {
   const int64_t o = r * p.nS + s;
-  if (p.bias) v += p.bias[s];
+  if (p.bias) v += load1(p.bias, s, 0);
   if (p.pre) store1(p.pre, o, p.pre_bf16, v);
   v = apply_act(act, v);
-  if (p.res)
-    v += p.res_bf16 ? to_f32(static_cast<const uint16_t*>(p.res)[o])
-                    : static_cast<const float*>(p.res)[o];
+  if (p.res) v += load1(p.res, o, p.res_bf16);
   store1(p.out, o, p.out_bf16, v);
 }
 
@@ -66,13 +77,14 @@ __device__ __forceinline__ Res8 fetch_res8(const MmParams& p, int64_t r, int32_t
   if (p.res && r < p.nR && s + 8 <= p.nS) {
     const int64_t o = r * p.nS + s;
     if (p.res_bf16) {
-      const Halves8 h = *reinterpret_cast<const Halves8*>(static_cast<const uint16_t*>(p.res) + o);
+      const Halves8 h = *(const Global<Halves8>*)((const Global<uint16_t>*)p.res + o);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) f.w[j] = h.w[j];
+      for (int j = 0; j < 4; ++j) f.w[j] = h[j];
     } else {
-      const Floats8 v = *reinterpret_cast<const Floats8*>(static_cast<const float*>(p.res) + o);
+      float v[8];
+      load8(static_cast<const float*>(p.res) + o, v);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) f.w[j] = __float_as_uint(v.v[j]);
+      for (int j = 0; j < 8; ++j) f.w[j] = __float_as_uint(v[j]);
     }
   }
   return f;

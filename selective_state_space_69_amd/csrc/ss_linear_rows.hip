@@ -90,18 +90,7 @@ __global__ __launch_bounds__(kWaves * kWave) void rows_kernel(MmParams p) {
     float f = 0.0f;
 #pragma unroll
     for (int k = 0; k < kWaves; ++k) f += part[k][b][row][s];
-    const int64_t o = r * p.nS + s0 + s;
-    if (p.bias) f += p.bias[s0 + s];
-    if (p.pre) {
-      if (p.pre_bf16) static_cast<uint16_t*>(p.pre)[o] = f32_to_bf16(f);
-      else static_cast<float*>(p.pre)[o] = f;
-    }
-    f = apply_act(p.act, f);
-    if (p.res)
-      f += p.res_bf16 ? to_f32(static_cast<const uint16_t*>(p.res)[o])
-                      : static_cast<const float*>(p.res)[o];
-    if (p.out_bf16) static_cast<uint16_t*>(p.out)[o] = f32_to_bf16(f);
-    else static_cast<float*>(p.out)[o] = f;
+    epilogue1(p, p.act, r, s0 + s, f);
   }
 }
 
