@@ -185,8 +185,9 @@ __device__ __forceinline__ void fetch_bias(const MmParams& p, int32_t s, float (
   if (p.bias && s + 8 <= p.nS) load8(p.bias + s, bias);
 }
 
-// One piece of 16 rows x 16 F columns; SPLIT: to a split's partial sums instead.
-template <int ACT, bool SPLIT, int F>
+// One piece of 16 rows x 16 F columns.  SPLIT: to a split's partial sums instead;
+// STREAM: past the caches.
+template <int ACT, bool SPLIT, bool STREAM, int F>
 __device__ __forceinline__ void piece_out(const MmParams& p, char* sl, const f32x4 (&q)[F],
                                           const Piece<F>& at, const float (&bias)[8], int split) {
   const int lane = threadIdx.x & 63, m = lane & 15, g = lane >> 4;
@@ -207,7 +208,7 @@ __device__ __forceinline__ void piece_out(const MmParams& p, char* sl, const f32
         const f32x4 y = *reinterpret_cast<const f32x4*>(sl + row * 256 + (((u + 1) ^ row) << 4));
         float v[8] = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
         if constexpr (SPLIT) store8(p.part, (split * p.nR + r) * p.nS + s, 0, v);
-        else epilogue8<ACT>(p, r, s, v, bias, res);
+        else epilogue8<ACT, STREAM>(p, r, s, v, bias, res);
       } else {
 #pragma nounroll
         for (int j = 0; s + j < p.nS; ++j) {
@@ -469,7 +470,7 @@ __device__ __forceinline__ void mm256_body(const MmParams& p0, char* lds) {
       const int j = i / 2, c = i & 1;
       if (i < 7) next.fetch(p, r + 16 * ((i + 1) / 2), c0 + 64 * ((i + 1) & 1));
       const f32x4 q[4] = {acc[4 * c][j], acc[4 * c + 1][j], acc[4 * c + 2][j], acc[4 * c + 3][j]};
-      piece_out<ACT, false>(p, lds + kOffEpi + wv * 4096, q, now, bias[c], 0);
+      piece_out<ACT, false, true>(p, lds + kOffEpi + wv * 4096, q, now, bias[c], 0);
       now = next;
     }
     if (!more) return;
@@ -651,10 +652,10 @@ __global__ __launch_bounds__(kSmallThreads, 2) void mm_small_kernel(MmParams p) 
     if (p.splits > 1) {
       now.r = r + 16 * j + lane / Piece<kF>::kPer;
       now.s = c + (lane % Piece<kF>::kPer) * 8;
-      piece_out<ACT, true>(p, lds + wv * 4096, q, now, bias, split);
+      piece_out<ACT, true, false>(p, lds + wv * 4096, q, now, bias, split);
     } else {
       if (j + 1 < kF) next.fetch(p, r + 16 * (j + 1), c);
-      piece_out<ACT, false>(p, lds + wv * 4096, q, now, bias, 0);
+      piece_out<ACT, false, false>(p, lds + wv * 4096, q, now, bias, 0);
       now = next;
     }
   }

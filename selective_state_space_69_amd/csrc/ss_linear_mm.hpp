@@ -30,11 +30,18 @@ template <typename T> using Global = __attribute__((address_space(1))) T;
 typedef uint32_t Halves8 __attribute__((ext_vector_type(4), aligned(2)));
 typedef float Floats4 __attribute__((ext_vector_type(4), aligned(4)));
 
+// STREAM: bf16 past the caches, for outputs larger than they are (16384 x 10240: 676
+// -> 662 us; they keep the operands instead).  fp32 goes through them: its two
+// 16-byte halves of a lane make whole lines only there (16384 x 5120: 370 us, 382
+// streamed).
+template <bool STREAM = false>
 __device__ __forceinline__ void store8(void* base, int64_t i, int bf16, const float (&v)[8]) {
   if (bf16) {
-    Global<uint16_t>* d = (Global<uint16_t>*)base + i;
-    *(Global<Halves8>*)d = Halves8{cvt_bf16x2(v[0], v[1]), cvt_bf16x2(v[2], v[3]),
-                                   cvt_bf16x2(v[4], v[5]), cvt_bf16x2(v[6], v[7])};
+    Global<Halves8>* d = (Global<Halves8>*)((Global<uint16_t>*)base + i);
+    const Halves8 x{cvt_bf16x2(v[0], v[1]), cvt_bf16x2(v[2], v[3]), cvt_bf16x2(v[4], v[5]),
+                    cvt_bf16x2(v[6], v[7])};
+    if constexpr (STREAM) __builtin_nontemporal_store(x, d);
+    else *d = x;
   } else {
     Global<float>* d = (Global<float>*)base + i;
     *(Global<Floats4>*)d = Floats4{v[0], v[1], v[2], v[3]};
@@ -93,14 +100,14 @@ __device__ __forceinline__ Res8 fetch_res8(const MmParams& p, int64_t r, int32_t
 // Eight neighbours s..s+7 of output row r, all inside it; bias: theirs (0 without
 // one).  ACT: the activation, or kActOf for p.act.
 constexpr int kActOf = -1;
-template <int ACT>
+template <int ACT, bool STREAM = false>
 __device__ __forceinline__ void epilogue8(const MmParams& p, int64_t r, int32_t s, float (&v)[8],
                                           const float (&bias)[8], const Res8& res) {
   const int act = ACT == kActOf ? p.act : ACT;
   const int64_t o = r * p.nS + s;
 #pragma unroll
   for (int j = 0; j < 8; ++j) v[j] += bias[j];
-  if (p.pre) store8(p.pre, o, p.pre_bf16, v);
+  if (p.pre) store8<STREAM>(p.pre, o, p.pre_bf16, v);
   if (act != SS_ACT_NONE) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = apply_act(act, v[j]);
@@ -117,7 +124,7 @@ __device__ __forceinline__ void epilogue8(const MmParams& p, int64_t r, int32_t 
       for (int j = 0; j < 8; ++j) v[j] += __uint_as_float(res.w[j]);
     }
   }
-  store8(p.out, o, p.out_bf16, v);
+  store8<STREAM>(p.out, o, p.out_bf16, v);
 }
 
 }  // namespace ss
