@@ -42,7 +42,8 @@ extern "C" {
 
 typedef enum { SS_ACT_NONE = 0, SS_ACT_SILU = 1, SS_ACT_GELU = 2, SS_ACT_SOFTPLUS = 3 } ss_act_t;
 
-/* 1 <= rows <= 2^30; 1 <= in_dim, out_dim <= 2^20; no operand beyond 2^40 elements. */
+/* 1 <= rows <= 2^28; 1 <= in_dim, out_dim <= 2^20; x, w and y of at most 2^35
+ * elements each. */
 typedef struct ss_linear_desc {
   int64_t rows;       /* M, tokens */
   int64_t in_dim;     /* K */

@@ -15,7 +15,9 @@ constexpr int64_t kMaxElems = int64_t(1) << 40;
 constexpr int64_t kMaxRows = INT32_MAX;
 constexpr int64_t kMaxStride = int64_t(1) << 24;
 constexpr int64_t kMaxLinear = int64_t(1) << 20;
-constexpr int64_t kMaxLinearRows = int64_t(1) << 30;   // 32-bit grids
+// 64 x 64 tiles of any product stay below 2^24, a grid's threads below 2^32
+constexpr int64_t kMaxLinearRows = int64_t(1) << 28;
+constexpr int64_t kMaxLinearElems = int64_t(1) << 35;
 constexpr int64_t kMaxNormDim = 32768;
 
 size_t elem(int32_t dtype) { return dtype == SS_BF16 ? 2 : 4; }
@@ -72,8 +74,8 @@ int check_linear(const ss_linear_desc_t* d, int op) {
   if (d->rows < 1 || d->rows > kMaxLinearRows || d->in_dim < 1 || d->out_dim < 1 ||
       d->in_dim > kMaxLinear || d->out_dim > kMaxLinear)
     return SS_ERR_INVALID_ARG;
-  if (d->rows > kMaxElems / d->in_dim || d->rows > kMaxElems / d->out_dim ||
-      d->out_dim > kMaxElems / d->in_dim)
+  if (d->rows > kMaxLinearElems / d->in_dim || d->rows > kMaxLinearElems / d->out_dim ||
+      d->out_dim > kMaxLinearElems / d->in_dim)
     return SS_ERR_INVALID_ARG;
   if (bad_stride(d->x_stride, d->in_dim, kMaxLinear)) return SS_ERR_INVALID_ARG;
   if (d->reserved != 0) return SS_ERR_INVALID_ARG;

@@ -103,9 +103,10 @@ def test_norm_bwd_arguments(kw, code):
 
 
 @pytest.mark.parametrize("kw,code", [
-    (dict(rows=0), INV), (dict(rows=(1 << 30) + 1), INV), (dict(in_dim=0), INV),
+    (dict(rows=0), INV), (dict(rows=(1 << 28) + 1), INV), (dict(in_dim=0), INV),
     (dict(in_dim=(1 << 20) + 1), INV), (dict(out_dim=0), INV), (dict(out_dim=(1 << 20) + 1), INV),
-    (dict(rows=1 << 30, in_dim=1 << 20), INV), (dict(x_stride=63), INV),
+    (dict(rows=1 << 28, in_dim=256), INV),
+    (dict(rows=1 << 28, out_dim=256), INV), (dict(in_dim=1 << 20, out_dim=1 << 16), INV), (dict(x_stride=63), INV),
     (dict(x_stride=(1 << 20) + 1), INV), (dict(in_dtype=5), UNS), (dict(out_dtype=5), UNS),
     (dict(act=4), UNS), (dict(act=-1), UNS),
 ])

@@ -269,6 +269,67 @@ def test_linear_bwd_ckpt(case):
             assert torch.equal(got[key], want[key]), key
 
 
+def random_linear(seed):
+    """One problem drawn over the supported ranges: sizes spread over their
+    logarithm, odd ones and multiples of 8 and 64 among them."""
+    rng = np.random.default_rng(seed)
+
+    def size(lo, hi):
+        v = int(round(float(np.exp(rng.uniform(np.log(lo), np.log(hi))))))
+        step = int(rng.choice([1, 1, 8, 64]))
+        return max(lo, v - v % step if v >= step else v)
+    m, k, n = size(1, 5000), size(1, 2500), size(1, 2500)
+    ti = str(rng.choice(["f32", "bf16", "bf16"]))
+    return (m, k, n, ti, str(rng.choice(["f32", "bf16"])),
+            str(rng.choice(["none", "silu", "gelu", "softplus"])), bool(rng.integers(2)),
+            [None, "f32", "bf16"][int(rng.integers(3))], *[(0, 0), (0, 0), (8, 8), (3, 1)][
+                int(rng.integers(4))])
+
+
+@pytest.mark.parametrize("seed", range(40))
+def test_linear_random(seed):
+    case = random_linear(7000 + seed)
+    log("linear random", case)
+    m, k, n, ti, to, name, hb = case[:7]
+    x, xin, w, b, r = linear_inputs(case, 8000 + 7 * seed)
+    y, pre = B.linear_fwd(xin, w, b, residual=r, act=name, out_dtype=DT[to], save_pre=True)
+    ry, rp, ty, tp = ref.linear_fwd(x, w, b, r, name)
+    check(y, ry, ty, "y")
+    check(pre, rp, tp, "pre")
+    dy = rand(9000 + seed, m, n, dtype=DT[to])
+    got = B.linear_bwd(xin, w, dy, pre=pre if name != "none" else None, act=name, bias=True,
+                       grad_dtype=torch.float32)
+    torch.cuda.synchronize()
+    dx, dw, db, tx, tw, tb = ref.linear_bwd(x, w, dy, pre, name)
+    check(got["dx"], dx, tx, "dx")
+    check(got["dw"], dw, tw, "dw")
+    check(got["dbias"], db, tb, "dbias")
+
+
+@pytest.mark.parametrize("seed", range(20))
+def test_norm_random(seed):
+    rng = np.random.default_rng(500 + seed)
+    rows = int(np.exp(rng.uniform(0, np.log(6000))))
+    dim = int(np.exp(rng.uniform(0, np.log(12000))))
+    ti, tr, to = (DT[str(rng.choice(["f32", "bf16"]))] for _ in range(3))
+    log("norm random", rows, dim, ti, tr, to)
+    x, r = rand(600 + seed, rows, dim, dtype=ti), rand(700 + seed, rows, dim, dtype=tr, offset=2.0)
+    w, b = rand(800 + seed, dim, offset=1.0), rand(900 + seed, dim)
+    got = B.layernorm_fwd(x, w, b, residual=r, eps=1e-3, out_dtype=to, save_stats=True)
+    y, s, mean, rstd, ty, tm, ts = ref.norm_fwd(x, r, w, b, float(np.float32(1e-3)))
+    check(got["y"], y, ty, "y")
+    check(got["sum"], s, U * s.abs(), "sum")
+    check(got["mean"], mean, tm + U * mean.abs(), "mean")
+    check(got["rstd"], rstd, ts, "rstd")
+    dy, ds = rand(1000 + seed, rows, dim, dtype=to), rand(1100 + seed, rows, dim, dtype=tr)
+    g = B.layernorm_bwd(got["sum"], dy, got["mean"], got["rstd"], w, dsum=ds)
+    torch.cuda.synchronize()
+    dx, dw, db, tx, tw, tb = ref.norm_bwd(got["sum"], dy, got["mean"], got["rstd"], w, ds)
+    check(g["dx"], dx, tx, "dx")
+    check(g["dweight"], dw, tw, "dweight")
+    check(g["dbias"], db, tb, "dbias")
+
+
 @pytest.mark.parametrize("m,k,n", [(4, 96, 64), (40, 200, 72), (300, 512, 256), (64, 4096, 128)])
 def test_linear_residual_in_place(m, k, n):
     x, w = rand(40, m, k, dtype=torch.bfloat16), rand(41, n, k, dtype=torch.bfloat16)
