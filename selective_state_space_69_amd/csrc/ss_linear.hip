@@ -40,17 +40,21 @@ __global__ __launch_bounds__(kThreads) void join_kernel(MmParams p) {
   }
 }
 
-// A tensor's rows at a 16-byte aligned stride, zero past their end: one 16-byte
-// unit of the copy per thread.
-struct PadParams {
+// Rows of one or two tensors (blockIdx.y) at a 16-byte aligned stride, zero past
+// their end: one 16-byte unit of the copy per thread.
+struct PadJob {
   const void* src;
   void* dst;
   int64_t ld_src, rows;
   int32_t cols, units;     // units of a row of the copy
 };
+struct PadParams {
+  PadJob job[2];
+};
 template <typename T>
-__global__ __launch_bounds__(kThreads) void pad_kernel(PadParams p) {
+__global__ __launch_bounds__(kThreads) void pad_kernel(PadParams q) {
   constexpr int E = 16 / int(sizeof(T));
+  const PadJob p = q.job[blockIdx.y];
   const int64_t total = p.rows * p.units;
   for (int64_t i = int64_t(blockIdx.x) * kThreads + threadIdx.x; i < total;
        i += int64_t(gridDim.x) * kThreads) {
@@ -220,20 +224,32 @@ void run_mm(const ss_linear_desc_t& d, MmParams p, bool rt, bool st, hipStream_t
   }
 }
 
-// rows x cols of src as an operand: in place where 16-byte units can read it, else
-// copied to dst with rows of pad_to_unit(cols) elements.
-const void* operand(const ss_linear_desc_t& d, const void* src, int64_t* ld, int64_t rows,
-                    int64_t cols, char* dst, hipStream_t st) {
-  const int e = unit_of(d);
-  if (ptr16(src) && *ld % e == 0 && cols % e == 0) return src;
-  PadParams p{src, dst, *ld, rows, int32_t(cols), int32_t(pad_to_unit(d, cols) / e)};
-  const int64_t n = (rows * p.units + kThreads - 1) / kThreads;
-  const unsigned blocks = unsigned(n < kMaxBlocks ? n : kMaxBlocks);
-  if (d.in_dtype == SS_BF16) pad_kernel<uint16_t><<<blocks, kThreads, 0, st>>>(p);
-  else pad_kernel<float><<<blocks, kThreads, 0, st>>>(p);
-  *ld = pad_to_unit(d, cols);
-  return dst;
-}
+// The operands of a call that 16-byte units cannot read in place, copied to rows of
+// pad_to_unit(cols) elements by one launch.
+struct Operands {
+  const ss_linear_desc_t& d;
+  PadParams pad{};
+  int n = 0;
+  // rows x cols of src, rows *ld elements apart: where the products read it
+  const void* take(const void* src, int64_t* ld, int64_t rows, int64_t cols, char* dst) {
+    const int e = unit_of(d);
+    if (ptr16(src) && *ld % e == 0 && cols % e == 0) return src;
+    pad.job[n++] = PadJob{src, dst, *ld, rows, int32_t(cols), int32_t(pad_to_unit(d, cols) / e)};
+    *ld = pad_to_unit(d, cols);
+    return dst;
+  }
+  void launch(hipStream_t st) {
+    if (n == 0) return;
+    int64_t blocks = 1;
+    for (int i = 0; i < n; ++i) {
+      const int64_t b = (pad.job[i].rows * pad.job[i].units + kThreads - 1) / kThreads;
+      if (b > blocks) blocks = b;
+    }
+    const dim3 grid(unsigned(blocks < kMaxBlocks ? blocks : kMaxBlocks), unsigned(n));
+    if (d.in_dtype == SS_BF16) pad_kernel<uint16_t><<<grid, kThreads, 0, st>>>(pad);
+    else pad_kernel<float><<<grid, kThreads, 0, st>>>(pad);
+  }
+};
 
 template <typename Dy, typename T, int V>
 void dpre_act(const DpreParams& p, dim3 grid, hipStream_t st) {
@@ -324,8 +340,10 @@ int launch_linear_fwd(const ss_linear_desc_t& d, const void* x, const void* w, c
     return int(hipGetLastError());
   }
   const LinearPlan pl = plan_linear(d, SS_LINEAR_FWD);
-  p.R = operand(d, x, &p.ldr, d.rows, d.in_dim, ws + pl.off_x, st);
-  p.S = operand(d, w, &p.lds, d.out_dim, d.in_dim, ws + pl.off_w, st);
+  Operands ops{d};
+  p.R = ops.take(x, &p.ldr, d.rows, d.in_dim, ws + pl.off_x);
+  p.S = ops.take(w, &p.lds, d.out_dim, d.in_dim, ws + pl.off_w);
+  ops.launch(st);
   p.part = reinterpret_cast<float*>(ws + pl.off_part);
   run_mm(d, p, true, true, st);
   return int(hipGetLastError());
@@ -354,9 +372,14 @@ int launch_linear_bwd(const ss_linear_desc_t& d, const LinearPlan& pl, const voi
   p.part = reinterpret_cast<float*>(ws + pl.off_part);
   p.act = SS_ACT_NONE;
   p.out_bf16 = d.grad_dtype == SS_BF16;
+  Operands ops{d};
+  int64_t ld_w = d.in_dim, ld_x = d.x_stride ? d.x_stride : d.in_dim;
+  if (dx) w = ops.take(w, &ld_w, d.out_dim, d.in_dim, ws + pl.off_w);
+  if (dw && x) x = ops.take(x, &ld_x, d.rows, d.in_dim, ws + pl.off_x);
+  ops.launch(st);
   if (dx) {
-    p.lds = d.in_dim;
-    p.S = operand(d, w, &p.lds, d.out_dim, d.in_dim, ws + pl.off_w, st);
+    p.S = w;
+    p.lds = ld_w;
     p.nR = d.rows;
     p.nT = d.out_dim;
     p.out = dx;
@@ -367,15 +390,14 @@ int launch_linear_bwd(const ss_linear_desc_t& d, const LinearPlan& pl, const voi
       ss_ckpt_desc_t c{};
       c.rows = d.rows;
       c.dim = d.in_dim;
-      c.x_stride = p.lds = pad_to_unit(d, d.in_dim);
+      c.x_stride = ld_x = pad_to_unit(d, d.in_dim);
       c.dtype = d.in_dtype;
       const int rc = launch_ckpt_unpack(c, q, e, ws + pl.off_x, stream);
       if (rc) return rc;
-      p.S = ws + pl.off_x;
-    } else {
-      p.lds = d.x_stride ? d.x_stride : d.in_dim;
-      p.S = operand(d, x, &p.lds, d.rows, d.in_dim, ws + pl.off_x, st);
+      x = ws + pl.off_x;
     }
+    p.S = x;
+    p.lds = ld_x;
     p.nR = d.out_dim;
     p.nT = d.rows;
     p.out = dw;
