@@ -155,16 +155,19 @@ int64_t pad_to_unit(const ss_linear_desc_t& d, int64_t n) {
 }
 
 // How a product is tiled.  bf16: 256 x 256 tiles where they fill the GPU's 256 CUs
-// at least half, else 128 x 128, of which two fit on a CU.  fp32: 64 x 64, of which
-// four fit.  Where the tiles of a long contraction leave CUs empty it is split, into
-// as many parts as the model below finds best: a stage of 128 bytes takes 0.7 us
-// with one workgroup on a CU and 0.9 us for two (fp32: 0.5 us for each, not below
-// 0.7), and a split product pays for the join kernel and for its partial sums'
-// way to memory and back.  Measured, 768 x 1536 over 5003 rows (72 tiles, 79 stages):
-// 50.9 us in one part, 30.5 in three (the model's choice), 28.7 in five, 36.6 in
-// eight; 5003 x 768 over 1536 (240 tiles, 24 stages): 22.2 us in one (the choice),
-// 28.2 in two; 1000 x 512 over 2560 (32 tiles, 40 stages): 29.0, 21.2 in two, 16.7
-// in five (the choice).
+// at least half, else 128 x 128, of which two fit on a CU, or one of two wave groups
+// that share its stages.  fp32: 64 x 64, of which five fit.  Where the tiles of a
+// long contraction leave CUs empty it is split.  The model below picks the groups
+// and the number of parts: a stage of 128 bytes takes 0.7 us with one group of waves
+// on a CU and 0.9 us for two (fp32: 0.5 us for each, not below 0.7), two groups meet
+// for 1 us, and a split product pays for the join kernel and for its partial sums'
+// way to memory and back.  Measured, one group and two:
+//   768 x 1536 over 5003 (72 tiles, 79 stages), three parts   31.3   28.7 us
+//     (one group in one part 50.9, two 34.6, five 28.7, eight 36.6)
+//   5003 x 768 over 1536 (240 tiles, 24 stages), one part     22.5   19.8
+//     (one group in two parts 28.2)
+//   2048 x 1536 over 768 (192 tiles, 12 stages), one part     13.9   11.3
+//   512 x 5120 over 2560 (160 tiles, 40 stages), one part     33.3   27.5
 struct Tiling {
   MmTile tile;
   int32_t tiles_r, tiles_s, splits;
@@ -193,10 +196,14 @@ Tiling tiling(const ss_linear_desc_t& d, int64_t nR, int64_t nS, int64_t nT) {
   for (int64_t i = 1; i <= 64 && (i == 1 || (i * tiles <= fit && i * 2 <= stages)); ++i) {
     const int64_t per_cu = (i * tiles + 255) / 256;
     const double stage_us = bf16 ? (per_cu > 1 ? 0.9 : 0.7) : (per_cu > 1 ? 0.5 * per_cu : 0.7);
-    const double us = double((stages + i - 1) / i) * stage_us + (i > 1 ? 6.0 + i * out_us : 0.0);
-    if (i == 1 || us < best) {
-      best = us;
+    const double join_us = i > 1 ? 6.0 + i * out_us : 0.0;
+    const double us = double((stages + i - 1) / i) * stage_us + join_us;
+    const double pair_us = double((stages + 2 * i - 1) / (2 * i)) * 0.9 + 1.0 + join_us;
+    const bool pair = bf16 && per_cu == 1 && pair_us < us;
+    if (i == 1 || (pair ? pair_us : us) < best) {
+      best = pair ? pair_us : us;
       k = i;
+      if (bf16) t.tile = pair ? MmTile::kSmallPair : MmTile::kSmall;
     }
   }
   int64_t len = (nT + k - 1) / k;

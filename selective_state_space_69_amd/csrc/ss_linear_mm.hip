@@ -513,15 +513,19 @@ __device__ __forceinline__ f32x4 mma(u32x4 a, u32x4 b, f32x4 c) {
 }
 #endif
 
-template <typename T, bool RT, bool ST, int ACT>
-__global__ __launch_bounds__(kSmallThreads, 2) void mm_small_kernel(MmParams p) {
+// G = 2 (bf16): two such groups of 4 waves in a workgroup, each with its own buffers
+// and half of the stages, for problems with at most one tile per CU; their sums meet
+// in LDS and each group stores half of the tile.
+template <typename T, bool RT, bool ST, int ACT, int G>
+__global__ __launch_bounds__(kSmallThreads * G, 2) void mm_small_kernel(MmParams p) {
 #if defined(__HIP_DEVICE_COMPILE__)
   constexpr int kSz = int(sizeof(T)), kT = 128 / kSz;
   constexpr int kTileS = kSmallTile<T>, kF = kTileS / 32;   // fragments of a wave per side
   constexpr int kOp = kTileS * 128;                         // bytes of an operand's stage
   constexpr int kCols = kTileS * kSz;                       // bytes of a t-strided row
-  __shared__ __attribute__((aligned(1024))) char lds[4 * kOp];
-  const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+  __shared__ __attribute__((aligned(1024))) char lds[4 * kOp * G];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wv8 = __builtin_amdgcn_readfirstlane(tid >> 6), wv = wv8 & 3, grp = wv8 >> 2;
   const int m = lane & 15, g = lane >> 4;
   const int64_t tiles = int64_t(p.tiles_r) * p.tiles_s;
   const int split = int(int64_t(blockIdx.x) / tiles);
@@ -539,21 +543,31 @@ __global__ __launch_bounds__(kSmallThreads, 2) void mm_small_kernel(MmParams p) 
     vr[j] = copy_offset<T, RT, kTileS, false>(id, p.ldr, r0, p.nR, &tpr[j]);
     vs[j] = copy_offset<T, ST, kTileS, false>(id, p.lds, s0, p.nS, &tps[j]);
   }
-  const char* pr = static_cast<const char*>(p.R) + (RT ? r0 * p.ldr + t0 : t0 * p.ldr + r0) * kSz;
-  const char* ps = static_cast<const char*>(p.S) + (ST ? s0 * p.lds + t0 : t0 * p.lds + s0) * kSz;
   const int64_t dr = RT ? 128 : p.ldr * 128, ds = ST ? 128 : p.lds * 128;
-  const int nk = int((t1 - t0 + kT - 1) / kT);
-  const int rem = int(t1 - t0 - int64_t(nk - 1) * kT);
+  const int stages = int((t1 - t0 + kT - 1) / kT);
+  const int rem = int(t1 - t0 - int64_t(stages - 1) * kT);
+  // the group's stages: nk of them (the walk's length, for both groups) from k0 on
+  const int nk = G == 1 ? stages : (stages + 1) / 2, k0 = grp * nk;
+  const char* pr = static_cast<const char*>(p.R) +
+                   (RT ? r0 * p.ldr + t0 : t0 * p.ldr + r0) * kSz + k0 * dr;
+  const char* ps = static_cast<const char*>(p.S) +
+                   (ST ? s0 * p.lds + t0 : t0 * p.lds + s0) * kSz + k0 * ds;
+  char* const mine = lds + grp * 4 * kOp;
   auto copy = [&](int k) {
-    if (k == nk - 1 && rem < kT) {
+    if (k0 + k == stages - 1 && rem < kT) {
 #pragma unroll
       for (int j = 0; j < kF; ++j) {
         vr[j] = tpr[j] < rem ? vr[j] : kOutOfRange;
         vs[j] = tps[j] < rem ? vs[j] : kOutOfRange;
       }
     }
-    const Rsrc a = make_rsrc(pr + k * dr), b = make_rsrc(ps + k * ds);
-    char* d = lds + (k & 1) * 2 * kOp + wv * 1024;
+    // past the last stage nothing is in range, and the buffer is cleared
+    const int range = k0 + k < stages ? 0x7fffffff : 0;
+    const Rsrc a = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(range ? pr + k * dr : pr),
+                                                     short(0), range, 0x00020000);
+    const Rsrc b = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(range ? ps + k * ds : ps),
+                                                     short(0), range, 0x00020000);
+    char* d = mine + (k & 1) * 2 * kOp + wv * 1024;
 #pragma unroll
     for (int j = 0; j < kF; ++j)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(a, (lds_ptr)(d + j * 4096), 16, vr[j], 0, 0, 0);
@@ -565,7 +579,7 @@ __global__ __launch_bounds__(kSmallThreads, 2) void mm_small_kernel(MmParams p) 
   const int wr = (wv >> 1) * (kTileS / 2), wsn = (wv & 1) * (kTileS / 2);
   // fragment addresses in buffer 0
   uint32_t ar[kF], as[kF];
-  const uint32_t l0 = uint32_t(reinterpret_cast<uintptr_t>((lds_ptr)lds));
+  const uint32_t l0 = uint32_t(reinterpret_cast<uintptr_t>((lds_ptr)mine));
   const int f = (m >> 2) | ((g & 1) << 2);
   auto address = [&](bool tc, int c0) -> uint32_t {      // c0: first row or column
     if (tc) return uint32_t((c0 + m) * 128 + ((g ^ (lane & 7)) << 4));
@@ -638,24 +652,48 @@ __global__ __launch_bounds__(kSmallThreads, 2) void mm_small_kernel(MmParams p) 
     }
   }
   turn_end();
-  const int64_t r = r0 + wr;
+  constexpr int kOut = kF / G;          // rows of pieces this group stores
+  f32x4 sum[kF][kOut];
+  if constexpr (G == 1) {
+#pragma unroll
+    for (int i = 0; i < kF; ++i)
+#pragma unroll
+      for (int j = 0; j < kOut; ++j) sum[i][j] = acc[i][j];
+  } else {
+    // each group hands the other its half: 256 threads x 16 bytes per accumulator
+    f32x4* box = reinterpret_cast<f32x4*>(lds) + (tid & 255);
+#pragma unroll
+    for (int i = 0; i < kF; ++i)
+#pragma unroll
+      for (int j = 0; j < kOut; ++j) {
+        sum[i][j] = grp == 0 ? acc[i][j] : acc[i][kOut + j];
+        box[((grp * kF + i) * kOut + j) * 256] = grp == 0 ? acc[i][kOut + j] : acc[i][j];
+      }
+    turn_end();
+#pragma unroll
+    for (int i = 0; i < kF; ++i)
+#pragma unroll
+      for (int j = 0; j < kOut; ++j) sum[i][j] += box[(((grp ^ 1) * kF + i) * kOut + j) * 256];
+  }
+  char* const sl = lds + (G == 1 ? 0 : 4 * kOp) + wv8 * 4096;
+  const int64_t r = r0 + wr + 16 * kOut * grp;
   const int32_t c = int32_t(s0) + wsn;
   Piece<kF> now, next;
   float bias[8];
   fetch_bias(p, c + (lane % Piece<kF>::kPer) * 8, bias);
   if (p.splits == 1) now.fetch(p, r, c);
 #pragma unroll
-  for (int j = 0; j < kF; ++j) {
+  for (int j = 0; j < kOut; ++j) {
     f32x4 q[kF];
 #pragma unroll
-    for (int i = 0; i < kF; ++i) q[i] = acc[i][j];
+    for (int i = 0; i < kF; ++i) q[i] = sum[i][j];
     if (p.splits > 1) {
       now.r = r + 16 * j + lane / Piece<kF>::kPer;
       now.s = c + (lane % Piece<kF>::kPer) * 8;
-      piece_out<ACT, true, false>(p, lds + wv * 4096, q, now, bias, split);
+      piece_out<ACT, true, false>(p, sl, q, now, bias, split);
     } else {
-      if (j + 1 < kF) next.fetch(p, r + 16 * (j + 1), c);
-      piece_out<ACT, false, false>(p, lds + wv * 4096, q, now, bias, 0);
+      if (j + 1 < kOut) next.fetch(p, r + 16 * (j + 1), c);
+      piece_out<ACT, false, false>(p, sl, q, now, bias, 0);
       now = next;
     }
   }
@@ -671,10 +709,13 @@ void run(const MmParams& p, MmTile tile, hipStream_t stream) {
           <<<blocks < kCUs ? blocks : kCUs, kThreads, 0, stream>>>(p);
       break;
     case MmTile::kSmall:
-      mm_small_kernel<uint16_t, RT, ST, ACT><<<blocks, kSmallThreads, 0, stream>>>(p);
+      mm_small_kernel<uint16_t, RT, ST, ACT, 1><<<blocks, kSmallThreads, 0, stream>>>(p);
+      break;
+    case MmTile::kSmallPair:
+      mm_small_kernel<uint16_t, RT, ST, ACT, 2><<<blocks, 2 * kSmallThreads, 0, stream>>>(p);
       break;
     case MmTile::kSmallF32:
-      mm_small_kernel<float, RT, ST, ACT><<<blocks, kSmallThreads, 0, stream>>>(p);
+      mm_small_kernel<float, RT, ST, ACT, 1><<<blocks, kSmallThreads, 0, stream>>>(p);
       break;
   }
 }

@@ -14,7 +14,8 @@ namespace ss {
 // Operands are read in 16-byte units: rows are 16-byte aligned, and a row's last
 // unit is inside its storage, with zeros past the contraction's end where t is the
 // contiguous axis.
-enum class MmTile { kBig, kSmall, kSmallF32 };
+// kSmallPair: 128 x 128 tiles by two groups of waves, at most one tile per CU.
+enum class MmTile { kBig, kSmall, kSmallPair, kSmallF32 };
 void launch_mm(const MmParams& p, MmTile tile, bool rt, bool st, hipStream_t stream);
 
 // O = R S^T for at most kRowsMax rows of R (t contiguous in both), with the
