@@ -154,9 +154,13 @@ int64_t pad_to_unit(const ss_linear_desc_t& d, int64_t n) {
   return (n + e - 1) / e * e;
 }
 
-// How a product is tiled.  bf16: 256 x 256 tiles where they fill the GPU's 256 CUs
-// at least half, else 128 x 128, of which two fit on a CU, or one of two wave groups
-// that share its stages.  fp32: 64 x 64, of which five fit.  Where the tiles of a
+// How a product is tiled.  bf16: 128 x 128 tiles while all of them fit on the 256 CUs
+// at once, two to a CU (or one, of two wave groups that share its stages); else 256 x
+// 256, unless they would be mostly empty: a stage of 128 bytes of 512 small tiles
+// takes 1.0 us, of 256 large ones 1.41, so large ones pay from 2.82 small tiles to a
+// large one.  Measured, small and large tiles, contraction 2560: 2048 x 4096 (512
+// small tiles) 45.9 and 53.6 us, 2560 x 4096 (640) 69.8 and 55.8, 4096 x 4096 89.4
+// and 68.0.  fp32: 64 x 64, of which five fit.  Where the tiles of a
 // long contraction leave CUs empty it is split.  The model below picks the groups
 // and the number of parts: a stage of 128 bytes takes 0.7 us with one group of waves
 // on a CU and 0.9 us for two (fp32: 0.5 us for each, not below 0.7), two groups meet
@@ -178,7 +182,8 @@ Tiling tiling(const ss_linear_desc_t& d, int64_t nR, int64_t nS, int64_t nT) {
   t.splits = 1;
   t.t_split = nT;
   const int64_t r256 = (nR + 255) / 256, s256 = (nS + 255) / 256;
-  if (d.in_dtype == SS_BF16 && r256 * s256 >= 128) {
+  const int64_t t128 = (nR + 127) / 128 * ((nS + 127) / 128);
+  if (d.in_dtype == SS_BF16 && t128 > 512 && t128 * 100 > 282 * r256 * s256) {
     t.tile = MmTile::kBig;
     t.tiles_r = int32_t(r256);
     t.tiles_s = int32_t(s256);

@@ -189,13 +189,15 @@ LINEAR = [
     (1500, 1536, 768, "bf16", "f32", "none", False, "f32", 0, 0),
     # enough 256 x 256 tiles for the large kernel: forward (contractions of one
     # partial, two and three stages, of many), dx, dw
-    (4096, 40, 2048, "bf16", "bf16", "gelu", True, None, 0, 0),
-    (4090, 128, 2050, "bf16", "f32", "none", True, "bf16", 0, 0),
-    (8190, 136, 1048, "bf16", "bf16", "silu", True, "f32", 8, 8),
+    (4096, 40, 2560, "bf16", "bf16", "gelu", True, None, 0, 0),
+    (4090, 128, 2314, "bf16", "f32", "none", True, "bf16", 0, 0),
+    (8190, 136, 1400, "bf16", "bf16", "silu", True, "f32", 8, 8),
+    (70000, 64, 120, "bf16", "bf16", "none", True, None, 0, 0),
     (4099, 1536, 2056, "bf16", "bf16", "softplus", True, None, 0, 0),
-    (4100, 2056, 72, "bf16", "bf16", "none", False, None, 0, 0),
+    (4100, 2568, 72, "bf16", "bf16", "none", False, None, 0, 0),
     (72, 4104, 2056, "bf16", "bf16", "none", False, None, 0, 0),
     (2000, 2048, 4096, "bf16", "bf16", "none", True, None, 0, 0),
+    (2570, 2048, 4096, "bf16", "bf16", "none", True, "bf16", 0, 0),
 ]
 
 
