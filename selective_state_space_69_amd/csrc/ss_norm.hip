@@ -47,7 +47,9 @@ __device__ __forceinline__ float wave_sum(float v) {
 // 8 neighbouring channels of a row from column c, in fp32 (0 past D).  Rows need
 // only their element's alignment: 16-byte accesses at any element address are
 // ordinary ones here.  TAIL: D is not a multiple of 8, and one thread's vector ends
-// past the row: it goes element by element.
+// past the row: it is stored element by element, and loaded as the row's last eight,
+// shifted into place where it is widened (element by element the load would have to
+// be waited for on the spot, with everything prefetched behind it).
 struct __attribute__((packed, aligned(2))) Raw8h { uint32_t w[4]; };
 struct __attribute__((packed, aligned(4))) Raw8f { float v[8]; };
 
@@ -61,9 +63,10 @@ template <bool TAIL, typename T>
 __device__ __forceinline__ typename Raw8<T>::type load_raw8(const T* row, int c, int D) {
   using R = typename Raw8<T>::type;
   R r{};
-  if (c + kVec <= D) {
-    r = *reinterpret_cast<const R*>(row + c);
-  } else if (TAIL && c < D) {
+  if (!TAIL || D >= kVec) {
+    const int at = TAIL && c + kVec > D ? D - kVec : c;
+    if (c < D) r = *reinterpret_cast<const R*>(row + at);
+  } else {
     struct Elems { T e[kVec]; } v;
 #pragma unroll
     for (int j = 0; j < kVec; ++j) v.e[j] = c + j < D ? row[c + j] : T(0);
@@ -82,9 +85,21 @@ __device__ __forceinline__ void widen8(const Raw8f& r, float (&v)[kVec]) {
 #pragma unroll
   for (int j = 0; j < kVec; ++j) v[j] = r.v[j];
 }
+// the vector at column c, 0 past D
+template <bool TAIL, typename R>
+__device__ __forceinline__ void widen8(const R& r, int c, int D, float (&v)[kVec]) {
+  widen8(r, v);
+  if constexpr (TAIL) {
+    const int by = D >= kVec && c < D && c + kVec > D ? c + kVec - D : 0;
+#pragma unroll
+    for (int s = 4; s > 0; s /= 2)
+#pragma unroll
+      for (int j = 0; j < kVec; ++j) v[j] = by & s ? (j + s < kVec ? v[j + s] : 0.0f) : v[j];
+  }
+}
 template <bool TAIL, typename T>
 __device__ __forceinline__ void load8(const T* row, int c, int D, float (&v)[kVec]) {
-  widen8(load_raw8<TAIL>(row, c, D), v);
+  widen8<TAIL>(load_raw8<TAIL>(row, c, D), c, D, v);
 }
 
 template <bool TAIL, typename T>
@@ -312,9 +327,10 @@ __global__ __launch_bounds__(1024) void norm_bwd_kernel(NormBwdParams p) {
     float t[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
-      widen8(rs[k], xh[k]);
-      widen8(rg[k], g[k]);
-      if (kAhead && p.dsum) widen8(rd[k], d[k]);
+      const int c = col0(a, k);
+      widen8<TAIL>(rs[k], c, p.D, xh[k]);
+      widen8<TAIL>(rg[k], c, p.D, g[k]);
+      if (kAhead && p.dsum) widen8<TAIL>(rd[k], c, p.D, d[k]);
     }
     if (kAhead && row + a.row_step < p.rows) fetch(row + a.row_step);
 #pragma unroll
