@@ -312,7 +312,8 @@ int ss_scan_arch_supported(const char* arch_name);
 const char* ss_scan_strerror(int status);
 
 /* Library ABI version (major * 10000 + minor * 100 + patch).  2.0 added the
- * trailing bc_stride field of ss_desc_t (the struct grew by 8 bytes). */
+ * trailing bc_stride field of ss_desc_t (the struct grew by 8 bytes); 2.1 the
+ * entry points of ss_norm.h, ss_linear.h and ss_ckpt.h. */
 int ss_scan_version(void);
 
 #ifdef __cplusplus

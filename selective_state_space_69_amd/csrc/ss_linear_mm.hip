@@ -31,6 +31,10 @@
 //                   receives one column).
 // The transposing reads are written in assembly, with their wait in the same
 // block: before the builtin the compiler waits for every copy in flight.
+//
+// Measured, 16384 rows: 2560 -> 10240 forward 651 us (1320 TFLOP/s; the matrix cores
+// are busy 65% of the cycles, at the 1.9 GHz that power allows), dx of 5120 -> 2560 in
+// fp32 360 us, its dw 369 us (200 tiles on 256 CUs).
 #include "ss_linear_mm.hpp"
 
 namespace ss {

@@ -8,6 +8,10 @@
 // rows per fragment, rows past M repeat the last one and are not stored), so one
 // pass serves up to 32 tokens.  The waves' partial tiles are added in wave order
 // through LDS and the epilogue runs on the sums: one launch, no workspace.
+//
+// Bound by memory and a launch's ramp: 8 rows, 2560 -> 10240 bf16 take 13.6 us (3.9
+// TB/s of w; 15.4 us with w always out of cache).  4 or 16 waves, twice the loads in
+// flight, whole lines per wave or streamed loads were no faster (15.4 to 17.6).
 #include "ss_linear_mm.hpp"
 
 namespace ss {
