@@ -12,7 +12,7 @@
  *     pre = x w^T + bias           x : (M, K)   w : (N, K)   bias : (N)
  *     y   = act(pre) + residual    y, pre, residual : (M, N)
  *     act : none | silu v sigmoid(v) | gelu v Phi(v) (Phi: the normal
- *           distribution function, by erf) | softplus log(1 + e^v)
+ *           distribution function) | softplus log(1 + e^v)
  * and backward, with dpre = dy act'(pre),
  *     dx = dpre w (M, K)     dw = dpre^T x (N, K)     dbias = sum_rows dpre (N)
  * (the residual's gradient is dy itself).  A few rows (decoding) run in kernels

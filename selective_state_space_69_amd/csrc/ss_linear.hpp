@@ -48,10 +48,34 @@ __device__ __forceinline__ float max0(float v) {
   return v > 0.0f ? v : 0.0f;
 #endif
 }
+// Upper tail of the normal distribution, Q(z) = 1 - Phi(z) at z = |v|, and its
+// density's exponential g = e^(-z^2/2).  Q = g G(t) with t = 1 / (1 + 0.23 z): e^(z^2/2)
+// Q(z) is smooth in t on (0, 1], and G is the degree 8 polynomial of least relative
+// error (4.8e-8, fitted for z in [0, 14]), so both sides of the GELU keep their
+// relative accuracy.  No branch, two transcendentals: a third of the work of erff
+// (fp32 3001 x 770 x 1537 with GELU: 91 us with erff, 78 so).
+__device__ __forceinline__ float normal_tail(float v, float& g) {
+  const float t = hw_rcp(__builtin_fmaf(__builtin_fabsf(v), 0.23f, 1.0f));
+  float p = -0.07846643577207714f;
+  p = __builtin_fmaf(p, t, 0.2904092622834526f);
+  p = __builtin_fmaf(p, t, -0.27811700323595473f);
+  p = __builtin_fmaf(p, t, 0.30146138824941776f);
+  p = __builtin_fmaf(p, t, -0.032912219220029286f);
+  p = __builtin_fmaf(p, t, 0.11951057618200757f);
+  p = __builtin_fmaf(p, t, 0.08576384069547627f);
+  p = __builtin_fmaf(p, t, 0.0923783211191706f);
+  p = __builtin_fmaf(p, t, -2.7754017451191973e-05f);
+  g = hw_exp2(v * v * (-0.5f * kLog2e));
+  return p * g;
+}
 __device__ __forceinline__ float apply_act(int act, float v) {
   switch (act) {
     case SS_ACT_SILU: return silu(v);
-    case SS_ACT_GELU: return 0.5f * v * (1.0f + erff(v * 0.70710678118654752f));
+    case SS_ACT_GELU: {
+      float g;
+      const float q = normal_tail(v, g);
+      return v * (v > 0.0f ? 1.0f - q : q);
+    }
     case SS_ACT_SOFTPLUS:   // max(v, 0) + log(1 + e^-|v|): the largest v pass through
       return __builtin_fmaf(log2_1p_exp2(__builtin_fabsf(v) * -kLog2e), kLn2, max0(v));
     default: return v;
@@ -63,9 +87,11 @@ __device__ __forceinline__ float act_grad(int act, float v) {
       const float s = hw_rcp(1.0f + hw_exp2(-v * kLog2e));
       return s * __builtin_fmaf(v, 1.0f - s, 1.0f);
     }
-    case SS_ACT_GELU:
-      return 0.5f * (1.0f + erff(v * 0.70710678118654752f)) +
-             v * 0.39894228040143268f * hw_exp2(v * v * (-0.5f * kLog2e));
+    case SS_ACT_GELU: {
+      float g;
+      const float q = normal_tail(v, g);
+      return __builtin_fmaf(v * 0.39894228040143268f, g, v > 0.0f ? 1.0f - q : q);
+    }
     case SS_ACT_SOFTPLUS: return hw_rcp(1.0f + hw_exp2(-v * kLog2e));
     default: return 1.0f;
   }

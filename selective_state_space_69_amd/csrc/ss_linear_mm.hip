@@ -1,9 +1,9 @@
 // The linear projections' products for gfx950, on the matrix cores: 256 x 256
-// output tiles for large bf16 problems, 128 x 128 ones for the rest and for fp32.
+// output tiles for large bf16 problems, 128 x 128 for the rest, 64 x 64 for fp32.
 //
-// 256 x 256.  A workgroup is 8 waves, one workgroup to a CU; a wave owns 128 (s) x 64 (r) of
-// the tile as 8 x 4 accumulators of v_mfma_f32_16x16x32_bf16 (128 registers).  A
-// stage is 64 of the contraction: R 256 x 64 and S 256 x 64 bf16, copied from
+// 256 x 256.  A workgroup is 8 waves, one workgroup to a CU; a wave owns 128 (s) x 64
+// (r) of the tile as 8 x 4 accumulators of v_mfma_f32_16x16x32_bf16 (128 registers).
+// A stage is 64 of the contraction: R 256 x 64 and S 256 x 64 bf16, copied from
 // global memory straight into LDS (16 bytes per lane), two stages deep.
 //
 // Schedule.  The waves of a SIMD form two groups that run half a turn apart: while

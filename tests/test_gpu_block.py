@@ -370,6 +370,24 @@ def test_linear_saturated_activations():
         assert bool((g[:3].abs() <= 1e-30).all()), name
 
 
+def test_gelu_tails():
+    """v Phi(v) and its derivative keep their relative accuracy on both sides: the
+    exponential's argument v^2 / 2 carries two roundings, the rest about 20."""
+    v = torch.linspace(-12.0, 12.0, 4801, device="cuda").view(-1, 1)
+    v = v[v.abs().view(-1) > 1e-3]
+    w = torch.ones(1, 1, device="cuda")
+    ref64 = ref.act("gelu", v.double())
+    y = B.linear_fwd(v, w, act="gelu")
+    g = B.linear_bwd(None, w, torch.ones_like(v), pre=v, act="gelu", need_dw=False)["dx"]
+    torch.cuda.synchronize()
+    lim = U * (20 + 2 * v.double() ** 2)
+    assert bool(((y.double() - ref64).abs() <= lim * ref64.abs()).all())
+    # the derivative's two terms cancel for negative v: bound by their sizes
+    phi = torch.exp(-v.double() ** 2 / 2) / np.sqrt(2 * np.pi)
+    size = torch.special.ndtr(v.double()) + v.double().abs() * phi
+    assert bool(((g.double() - ref.act_grad("gelu", v.double())).abs() <= lim * size).all())
+
+
 # ------------------------------------------------------------------ checkpoints
 CKPT = [(1, 1, "f32", 0, 0), (3, 31, "bf16", 0, 0), (5, 32, "f32", 0, 0), (4, 33, "bf16", 0, 0),
         (7, 40, "bf16", 0, 0), (17, 100, "f32", 0, 0), (9, 104, "bf16", 24, 8),
