@@ -11,11 +11,17 @@ HALF = {torch.float32: 2.0 ** -24, torch.bfloat16: 2.0 ** -8}   # finfo(t).eps /
 DT = {"f32": torch.float32, "bf16": torch.bfloat16}
 
 
+def normal_cdf(v):
+    """Phi(v); by erfc, since torch.special.ndtr returns 0 in the far negative tail
+    on the GPU (Phi(-12) = 1.8e-33)."""
+    return 0.5 * torch.special.erfc(-v * math.sqrt(0.5))
+
+
 def act(name, v):
     if name == "silu":
         return v * torch.sigmoid(v)
     if name == "gelu":
-        return v * torch.special.ndtr(v)
+        return v * normal_cdf(v)
     if name == "softplus":
         return torch.logaddexp(v, torch.zeros((), dtype=v.dtype, device=v.device))
     return v
@@ -26,7 +32,7 @@ def act_grad(name, v):
         s = torch.sigmoid(v)
         return s + v * s * torch.sigmoid(-v)
     if name == "gelu":
-        return torch.special.ndtr(v) + v * torch.exp(-v * v / 2) / math.sqrt(2 * math.pi)
+        return normal_cdf(v) + v * torch.exp(-v * v / 2) / math.sqrt(2 * math.pi)
     if name == "softplus":
         return torch.sigmoid(v)
     return torch.ones_like(v)
