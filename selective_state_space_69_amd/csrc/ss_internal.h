@@ -241,11 +241,13 @@ int launch_ckpt_unpack(const ss_ckpt_desc_t& d, const int8_t* q, const uint8_t* 
 //   x, w : (M, K), (N, K) in_dtype, rows copied to a 16-byte aligned stride where
 //          they cannot be read in place; x: also the checkpoint's values
 //   sums : (chunks, N) fp32, dbias sums of chunk_rows rows
-//   part : fp32 partial products of a split contraction (the larger of dx's, dw's)
+//   part : fp32 partial products of split contractions (dx's and dw's in one place,
+//          or dw's off_part_dw bytes behind dx's where one launch computes both)
 struct LinearPlan {
   bool need_dpre = false;
   int64_t chunk_rows = 1, chunks = 1;
-  size_t off_dpre = 0, off_x = 0, off_w = 0, off_sums = 0, off_part = 0, bytes = 0;
+  size_t off_dpre = 0, off_x = 0, off_w = 0, off_sums = 0, off_part = 0,
+         off_part_dw = 0, bytes = 0;
 };
 LinearPlan plan_linear(const ss_linear_desc_t& d, int op);
 int launch_linear_fwd(const ss_linear_desc_t& d, const void* x, const void* w, const float* bias,

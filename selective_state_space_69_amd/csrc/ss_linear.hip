@@ -176,64 +176,108 @@ struct Tiling {
   MmTile tile;
   int32_t tiles_r, tiles_s, splits;
   int64_t t_split;
+  double us;       // the model's time
+};
+constexpr double kLaunchUs = 6.0;       // a product's launch, first copies and epilogue
+double stage_us(bool bf16, int64_t items) {
+  const int64_t per_cu = (items + 255) / 256;
+  return bf16 ? (per_cu > 1 ? 0.9 : 0.7) : (per_cu > 1 ? 0.5 * double(per_cu) : 0.7);
+}
+// the join of k parts, their sums written and read
+double join_us(int64_t nR, int64_t nS, int64_t k) {
+  return k > 1 ? 6.0 + double(k) * double(nR) * double(nS) * 8.0 / 4.0e6 : 0.0;
+}
+// What one product offers to choose from: its small tiles, its stages, how many
+// items fit on the GPU at once.
+struct Small {
+  bool bf16;
+  int64_t nR, nS, nT, step, tiles_r, tiles_s, tiles, stages, fit;
+  Small(const ss_linear_desc_t& d, int64_t r, int64_t s, int64_t t) : nR(r), nS(s), nT(t) {
+    bf16 = d.in_dtype == SS_BF16;
+    const int64_t side = bf16 ? 128 : 64;
+    step = bf16 ? 64 : 32;
+    fit = bf16 ? 512 : 1024;
+    tiles_r = (nR + side - 1) / side;
+    tiles_s = (nS + side - 1) / side;
+    tiles = tiles_r * tiles_s;
+    stages = (nT + step - 1) / step;
+  }
+  int64_t per_part(int64_t k) const { return (stages + k - 1) / k; }
+  // k parts; those that hold no stage are dropped
+  Tiling tiling(MmTile tile, int64_t k, double us) const {
+    const int64_t len = per_part(k) * step;
+    return Tiling{tile, int32_t(tiles_r), int32_t(tiles_s), int32_t((nT + len - 1) / len), len, us};
+  }
 };
 Tiling tiling(const ss_linear_desc_t& d, int64_t nR, int64_t nS, int64_t nT) {
-  Tiling t{};
-  t.splits = 1;
-  t.t_split = nT;
   const int64_t r256 = (nR + 255) / 256, s256 = (nS + 255) / 256;
-  const int64_t t128 = (nR + 127) / 128 * ((nS + 127) / 128);
-  if (d.in_dtype == SS_BF16 && t128 > 512 && t128 * 100 > 282 * r256 * s256) {
-    t.tile = MmTile::kBig;
-    t.tiles_r = int32_t(r256);
-    t.tiles_s = int32_t(s256);
-    return t;
+  const Small p(d, nR, nS, nT);
+  if (p.bf16 && p.tiles > 512 && p.tiles * 100 > 282 * r256 * s256) {
+    const int64_t rounds = (r256 * s256 + 255) / 256;
+    return Tiling{MmTile::kBig, int32_t(r256), int32_t(s256), 1, nT,
+                  kLaunchUs + 1.41 * double(rounds * p.stages)};
   }
-  const bool bf16 = d.in_dtype == SS_BF16;
-  const int64_t side = bf16 ? 128 : 64, step = bf16 ? 64 : 32, fit = bf16 ? 512 : 1024;
-  t.tile = bf16 ? MmTile::kSmall : MmTile::kSmallF32;
-  t.tiles_r = int32_t((nR + side - 1) / side);
-  t.tiles_s = int32_t((nS + side - 1) / side);
-  const int64_t tiles = int64_t(t.tiles_r) * t.tiles_s, stages = (nT + step - 1) / step;
-  const double out_us = double(nR) * double(nS) * 8.0 / 4.0e6;    // one part there and back
-  int64_t k = 1;
-  double best = 0.0;
-  for (int64_t i = 1; i <= 64 && (i == 1 || (i * tiles <= fit && i * 2 <= stages)); ++i) {
-    const int64_t per_cu = (i * tiles + 255) / 256;
-    const double stage_us = bf16 ? (per_cu > 1 ? 0.9 : 0.7) : (per_cu > 1 ? 0.5 * per_cu : 0.7);
-    const double join_us = i > 1 ? 6.0 + i * out_us : 0.0;
-    const double us = double((stages + i - 1) / i) * stage_us + join_us;
-    const double pair_us = double((stages + 2 * i - 1) / (2 * i)) * 0.9 + 1.0 + join_us;
-    const bool pair = bf16 && per_cu == 1 && pair_us < us;
-    if (i == 1 || (pair ? pair_us : us) < best) {
-      best = pair ? pair_us : us;
-      k = i;
-      if (bf16) t.tile = pair ? MmTile::kSmallPair : MmTile::kSmall;
+  Tiling best{};
+  for (int64_t k = 1; k <= 64 && (k == 1 || (k * p.tiles <= p.fit && k * 2 <= p.stages)); ++k) {
+    const double rest = kLaunchUs + join_us(nR, nS, k);
+    double us = double(p.per_part(k)) * stage_us(p.bf16, k * p.tiles) + rest;
+    MmTile tile = p.bf16 ? MmTile::kSmall : MmTile::kSmallF32;
+    if (p.bf16 && k * p.tiles <= 256) {
+      const double two = double(p.per_part(2 * k)) * 0.9 + 1.0 + rest;
+      if (two < us) {
+        us = two;
+        tile = MmTile::kSmallPair;
+      }
     }
+    if (k == 1 || us < best.us) best = p.tiling(tile, k, us);
   }
-  int64_t len = (nT + k - 1) / k;
-  len = (len + step - 1) / step * step;
-  t.t_split = len;
-  t.splits = int32_t((nT + len - 1) / len);
-  return t;
+  return best;
+}
+// dx and dw in one launch, where both fit on the GPU at once and the model finds that
+// faster than one after the other (bf16 5003 x 768 x 1536, whole call: 48 us, both 37).
+bool tiling_both(const ss_linear_desc_t& d, Tiling* dx, Tiling* dw) {
+  const Small a(d, d.rows, d.in_dim, d.out_dim), b(d, d.out_dim, d.in_dim, d.rows);
+  const MmTile tile = a.bf16 ? MmTile::kSmall : MmTile::kSmallF32;
+  double best = tiling(d, a.nR, a.nS, a.nT).us + tiling(d, b.nR, b.nS, b.nT).us;
+  bool found = false;
+  for (int64_t i = 1; i <= 16 && i * 2 <= a.stages + 1; ++i)
+    for (int64_t j = 1; j <= 64 && j * 2 <= b.stages + 1; ++j) {
+      const int64_t items = i * a.tiles + j * b.tiles;
+      if (items > a.fit) break;
+      const int64_t stages = a.per_part(i) > b.per_part(j) ? a.per_part(i) : b.per_part(j);
+      const double us = kLaunchUs + double(stages) * stage_us(a.bf16, items) +
+                        join_us(a.nR, a.nS, i) + join_us(b.nR, b.nS, j);
+      if (us < best) {
+        best = us;
+        found = true;
+        *dx = a.tiling(tile, i, us);
+        *dw = b.tiling(tile, j, us);
+      }
+    }
+  return found;
 }
 
-size_t part_bytes(const ss_linear_desc_t& d, int64_t nR, int64_t nS, int64_t nT) {
-  const Tiling t = tiling(d, nR, nS, nT);
+size_t part_bytes(const Tiling& t, int64_t nR, int64_t nS) {
   return t.splits > 1 ? align256(size_t(t.splits) * size_t(nR) * size_t(nS) * 4) : 0;
 }
 
-void run_mm(const ss_linear_desc_t& d, MmParams p, bool rt, bool st, hipStream_t stream) {
-  const Tiling t = tiling(d, p.nR, p.nS, p.nT);
+MmParams tiled(MmParams p, const Tiling& t, char* part) {
   p.tiles_r = t.tiles_r;
   p.tiles_s = t.tiles_s;
   p.splits = t.splits;
   p.t_split = t.t_split;
+  p.part = reinterpret_cast<float*>(part);
+  return p;
+}
+void join(const MmParams& p, hipStream_t stream) {
+  if (p.splits == 1) return;
+  const int64_t n = (p.nR * ((p.nS + 7) / 8) + kThreads - 1) / kThreads;
+  join_kernel<<<unsigned(n < kMaxBlocks ? n : kMaxBlocks), kThreads, 0, stream>>>(p);
+}
+void run_mm(MmParams p, const Tiling& t, bool rt, bool st, char* part, hipStream_t stream) {
+  p = tiled(p, t, part);
   launch_mm(p, t.tile, rt, st, stream);
-  if (p.splits > 1) {
-    const int64_t n = (p.nR * ((p.nS + 7) / 8) + kThreads - 1) / kThreads;
-    join_kernel<<<unsigned(n < kMaxBlocks ? n : kMaxBlocks), kThreads, 0, stream>>>(p);
-  }
+  join(p, stream);
 }
 
 // The operands of a call that 16-byte units cannot read in place, copied to rows of
@@ -303,7 +347,7 @@ LinearPlan plan_linear(const ss_linear_desc_t& d, int op) {
     if (d.rows <= kRowsMax) return pl;
     if (pad_x) pl.off_x = take(x_bytes);
     if (pad_k) pl.off_w = take(w_bytes);
-    pl.off_part = take(part_bytes(d, d.rows, d.out_dim, d.in_dim));
+    pl.off_part = take(part_bytes(tiling(d, d.rows, d.out_dim, d.in_dim), d.rows, d.out_dim));
     pl.bytes = off;
     return pl;
   }
@@ -320,9 +364,18 @@ LinearPlan plan_linear(const ss_linear_desc_t& d, int op) {
   if (op == SS_LINEAR_BWD_CKPT || pad_x) pl.off_x = take(x_bytes);
   if (pad_k) pl.off_w = take(w_bytes);
   pl.off_sums = take(align256(size_t(pl.chunks) * size_t(d.out_dim) * 4));
-  const size_t a = part_bytes(d, d.rows, d.in_dim, d.out_dim);
-  const size_t b = part_bytes(d, d.out_dim, d.in_dim, d.rows);
-  pl.off_part = take(a > b ? a : b);
+  // dx's and dw's parts: one after the other in one place, or side by side
+  const size_t a = part_bytes(tiling(d, d.rows, d.in_dim, d.out_dim), d.rows, d.in_dim);
+  const size_t b = part_bytes(tiling(d, d.out_dim, d.in_dim, d.rows), d.out_dim, d.in_dim);
+  size_t part = a > b ? a : b;
+  Tiling ta, tb;
+  if (tiling_both(d, &ta, &tb)) {
+    const size_t pa = part_bytes(ta, d.rows, d.in_dim);
+    const size_t both = pa + part_bytes(tb, d.out_dim, d.in_dim);
+    pl.off_part_dw = pa;
+    if (both > part) part = both;
+  }
+  pl.off_part = take(part);
   pl.bytes = off;
   return pl;
 }
@@ -356,8 +409,7 @@ int launch_linear_fwd(const ss_linear_desc_t& d, const void* x, const void* w, c
   p.R = ops.take(x, &p.ldr, d.rows, d.in_dim, ws + pl.off_x);
   p.S = ops.take(w, &p.lds, d.out_dim, d.in_dim, ws + pl.off_w);
   ops.launch(st);
-  p.part = reinterpret_cast<float*>(ws + pl.off_part);
-  run_mm(d, p, true, true, st);
+  run_mm(p, tiling(d, p.nR, p.nS, p.nT), true, true, ws + pl.off_part, st);
   return int(hipGetLastError());
 }
 
@@ -381,39 +433,56 @@ int launch_linear_bwd(const ss_linear_desc_t& d, const LinearPlan& pl, const voi
   p.R = dpre ? static_cast<const void*>(ws + pl.off_dpre) : dy;
   p.ldr = pl.need_dpre ? pad_to_unit(d, d.out_dim) : d.out_dim;
   p.nS = int32_t(d.in_dim);
-  p.part = reinterpret_cast<float*>(ws + pl.off_part);
   p.act = SS_ACT_NONE;
   p.out_bf16 = d.grad_dtype == SS_BF16;
   Operands ops{d};
-  int64_t ld_w = d.in_dim, ld_x = d.x_stride ? d.x_stride : d.in_dim;
-  if (dx) w = ops.take(w, &ld_w, d.out_dim, d.in_dim, ws + pl.off_w);
-  if (dw && x) x = ops.take(x, &ld_x, d.rows, d.in_dim, ws + pl.off_x);
-  ops.launch(st);
+  MmParams px = p, pw = p;
+  px.lds = d.in_dim;
+  pw.lds = d.x_stride ? d.x_stride : d.in_dim;
   if (dx) {
-    p.S = w;
-    p.lds = ld_w;
-    p.nR = d.rows;
-    p.nT = d.out_dim;
-    p.out = dx;
-    run_mm(d, p, true, false, st);
+    px.S = ops.take(w, &px.lds, d.out_dim, d.in_dim, ws + pl.off_w);
+    px.nR = d.rows;
+    px.nT = d.out_dim;
+    px.out = dx;
   }
   if (dw) {
     if (q) {
       ss_ckpt_desc_t c{};
       c.rows = d.rows;
       c.dim = d.in_dim;
-      c.x_stride = ld_x = pad_to_unit(d, d.in_dim);
+      c.x_stride = pw.lds = pad_to_unit(d, d.in_dim);
       c.dtype = d.in_dtype;
+      pw.S = ws + pl.off_x;
       const int rc = launch_ckpt_unpack(c, q, e, ws + pl.off_x, stream);
       if (rc) return rc;
-      x = ws + pl.off_x;
+    } else {
+      pw.S = ops.take(x, &pw.lds, d.rows, d.in_dim, ws + pl.off_x);
     }
-    p.S = x;
-    p.lds = ld_x;
-    p.nR = d.out_dim;
-    p.nT = d.rows;
-    p.out = dw;
-    run_mm(d, p, false, false, st);
+    pw.nR = d.out_dim;
+    pw.nT = d.rows;
+    pw.out = dw;
+  }
+  ops.launch(st);
+  char* const part = ws + pl.off_part;
+  // one gradient alone is computed as it is beside the other: the same sums
+  Tiling tx, tw;
+  char* part_dw = part;
+  const bool both = tiling_both(d, &tx, &tw);
+  if (both) {
+    part_dw += pl.off_part_dw;
+  } else {
+    tx = tiling(d, d.rows, d.in_dim, d.out_dim);
+    tw = tiling(d, d.out_dim, d.in_dim, d.rows);
+  }
+  if (both && dx && dw) {
+    px = tiled(px, tx, part);
+    pw = tiled(pw, tw, part_dw);
+    launch_mm_both(px, pw, d.in_dtype == SS_BF16, st);
+    join(px, st);
+    join(pw, st);
+  } else {
+    if (dx) run_mm(px, tx, true, false, part, st);
+    if (dw) run_mm(pw, tw, false, false, part_dw, st);
   }
   return int(hipGetLastError());
 }

@@ -319,7 +319,7 @@ __device__ __forceinline__ void mm256_body(const MmParams& p0, char* lds) {
   const int wr = (wv >> 1) * 64, wsn = (wv & 1) * 128;      // the wave's corner
   // fragment addresses in buffer 0; the other buffer is a constant away
   uint32_t ar[4], as[4];
-  const uint32_t l0 = uint32_t(reinterpret_cast<uintptr_t>((lds_ptr)lds));
+  const uint32_t l0 = uint32_t(reinterpret_cast<uintptr_t>((lds_ptr)lds));   // 0: the only array
   const int f = (m >> 2) | ((g & 1) << 2);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -519,23 +519,24 @@ __device__ __forceinline__ f32x4 mma(u32x4 a, u32x4 b, f32x4 c) {
 
 // G = 2 (bf16): two such groups of 4 waves in a workgroup, each with its own buffers
 // and half of the stages, for problems with at most one tile per CU; their sums meet
-// in LDS and each group stores half of the tile.
-template <typename T, bool RT, bool ST, int ACT, int G>
-__global__ __launch_bounds__(kSmallThreads * G, 2) void mm_small_kernel(MmParams p) {
+// in LDS and each group stores half of the tile.  lds: kSmallLds<T> bytes per group;
+// block: the work item, a tile of a split.
+template <typename T> constexpr int kSmallLds = 4 * kSmallTile<T> * 128;
 #if defined(__HIP_DEVICE_COMPILE__)
+template <typename T, bool RT, bool ST, int ACT, int G>
+__device__ __forceinline__ void mm_small_body(const MmParams& p, int64_t block, char* lds) {
   constexpr int kSz = int(sizeof(T)), kT = 128 / kSz;
   constexpr int kTileS = kSmallTile<T>, kF = kTileS / 32;   // fragments of a wave per side
   constexpr int kOp = kTileS * 128;                         // bytes of an operand's stage
   constexpr int kCols = kTileS * kSz;                       // bytes of a t-strided row
-  __shared__ __attribute__((aligned(1024))) char lds[4 * kOp * G];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wv8 = __builtin_amdgcn_readfirstlane(tid >> 6), wv = wv8 & 3, grp = wv8 >> 2;
   const int m = lane & 15, g = lane >> 4;
   const int64_t tiles = int64_t(p.tiles_r) * p.tiles_s;
-  const int split = int(int64_t(blockIdx.x) / tiles);
+  const int split = int(block / tiles);
   int64_t tr;
   int ts;
-  tile_of(p, xcd_contiguous(int64_t(blockIdx.x) - split * tiles, tiles), &tr, &ts);
+  tile_of(p, xcd_contiguous(block - split * tiles, tiles), &tr, &ts);
   const int64_t r0 = tr * kTileS, s0 = int64_t(ts) * kTileS;
   const int64_t t0 = split * p.t_split;
   const int64_t t1 = t0 + p.t_split < p.nT ? t0 + p.t_split : p.nT;
@@ -701,6 +702,28 @@ __global__ __launch_bounds__(kSmallThreads * G, 2) void mm_small_kernel(MmParams
       now = next;
     }
   }
+}
+#endif
+
+template <typename T, bool RT, bool ST, int ACT, int G>
+__global__ __launch_bounds__(kSmallThreads * G, 2) void mm_small_kernel(MmParams p) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  __shared__ __attribute__((aligned(1024))) char lds[kSmallLds<T> * G];
+  mm_small_body<T, RT, ST, ACT, G>(p, blockIdx.x, lds);
+#endif
+}
+
+// Both products of a backward pass, dx (R t contiguous) and dw (t strided), side by
+// side: each alone would leave half of the CUs' slots empty.
+template <typename T>
+__global__ __launch_bounds__(kSmallThreads, 2) void mm_both_kernel(MmParams dx, MmParams dw) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  __shared__ __attribute__((aligned(1024))) char lds[kSmallLds<T>];
+  const int64_t items = int64_t(dw.tiles_r) * dw.tiles_s * dw.splits;
+  if (int64_t(blockIdx.x) < items)
+    mm_small_body<T, false, false, SS_ACT_NONE, 1>(dw, blockIdx.x, lds);
+  else
+    mm_small_body<T, true, false, SS_ACT_NONE, 1>(dx, int64_t(blockIdx.x) - items, lds);
 #endif
 }
 
@@ -725,6 +748,13 @@ void run(const MmParams& p, MmTile tile, hipStream_t stream) {
 }
 
 }  // namespace
+
+void launch_mm_both(const MmParams& dx, const MmParams& dw, bool bf16, hipStream_t stream) {
+  const unsigned blocks = unsigned(dx.tiles_r) * unsigned(dx.tiles_s) * unsigned(dx.splits) +
+                          unsigned(dw.tiles_r) * unsigned(dw.tiles_s) * unsigned(dw.splits);
+  if (bf16) mm_both_kernel<uint16_t><<<blocks, kSmallThreads, 0, stream>>>(dx, dw);
+  else mm_both_kernel<float><<<blocks, kSmallThreads, 0, stream>>>(dx, dw);
+}
 
 void launch_mm(const MmParams& p, MmTile tile, bool rt, bool st, hipStream_t stream) {
   if (rt && st) {

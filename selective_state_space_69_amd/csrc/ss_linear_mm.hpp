@@ -17,6 +17,8 @@ namespace ss {
 // kSmallPair: 128 x 128 tiles by two groups of waves, at most one tile per CU.
 enum class MmTile { kBig, kSmall, kSmallPair, kSmallF32 };
 void launch_mm(const MmParams& p, MmTile tile, bool rt, bool st, hipStream_t stream);
+// dx (rt, not st) and dw (neither) on small tiles of one group, in one launch.
+void launch_mm_both(const MmParams& dx, const MmParams& dw, bool bf16, hipStream_t stream);
 
 // O = R S^T for at most kRowsMax rows of R (t contiguous in both), with the
 // epilogue; vec: both operands' rows are 16-byte aligned and nT is a whole number
