@@ -155,17 +155,22 @@ int64_t pad_to_unit(const ss_linear_desc_t& d, int64_t n) {
 }
 
 // How a product is tiled.  bf16: 128 x 128 tiles while all of them fit on the 256 CUs
-// at once, two to a CU (or one, of two wave groups that share its stages); else 256 x
-// 256, unless they would be mostly empty: a stage of 128 bytes of 512 small tiles
-// takes 1.0 us, of 256 large ones 1.41, so large ones pay from 2.82 small tiles to a
-// large one.  Measured, small and large tiles, contraction 2560: 2048 x 4096 (512
-// small tiles) 45.9 and 53.6 us, 2560 x 4096 (640) 69.8 and 55.8, 4096 x 4096 89.4
-// and 68.0.  fp32: 64 x 64, of which five fit.  Where the tiles of a
-// long contraction leave CUs empty it is split.  The model below picks the groups
-// and the number of parts: a stage of 128 bytes takes 0.7 us with one group of waves
-// on a CU and 0.9 us for two (fp32: 0.5 us for each, not below 0.7), two groups meet
-// for 1 us, and a split product pays for the join kernel and for its partial sums'
-// way to memory and back.  Measured, one group and two:
+// at once, two to a CU (or one, of two wave groups that share its stages), and where
+// 256 x 256 ones would be mostly empty.  Beyond that, 256 x 256 tiles against 128 x
+// 128 ones three to a CU with one buffer each, whichever ends first: a large tile
+// takes 1.25 us per stage of 128 bytes and 7 us around them with nothing beside it,
+// a small one 0.47 and 1 us of its CU, whose other tiles cover its waits.  Measured,
+// large and single-buffered tiles (bf16 out, us):
+//   contraction            160            320            640           1280
+//   16384 x 5120      68.5   64.9    73.7   75.7   106.0  124.2   174.7  214.5
+//   with softplus     83.4   72.9    91.8   89.3   125.3  139.0   194.3  228.4
+//   4096 x 5120       25.8   18.4    30.0   23.9    42.3   34.4    66.1   58.2
+// fp32: 64 x 64, of which five fit. Where the tiles of a long contraction leave CUs
+// empty it is split. The model below picks the groups and the number of parts: a
+// stage of 128 bytes takes 0.7 us with one group of waves on a CU and 0.9 us for two
+// (fp32: 0.5 us for each, not below 0.7), two groups meet for 1 us, and a split
+// product pays for the join kernel and for its partial sums' way to memory and back.
+// Measured, one group and two:
 //   768 x 1536 over 5003 (72 tiles, 79 stages), three parts   31.3   28.7 us
 //     (one group in one part 50.9, two 34.6, five 28.7, eight 36.6)
 //   5003 x 768 over 1536 (240 tiles, 24 stages), one part     22.5   19.8
@@ -213,9 +218,11 @@ Tiling tiling(const ss_linear_desc_t& d, int64_t nR, int64_t nS, int64_t nT) {
   const int64_t r256 = (nR + 255) / 256, s256 = (nS + 255) / 256;
   const Small p(d, nR, nS, nT);
   if (p.bf16 && p.tiles > 512 && p.tiles * 100 > 282 * r256 * s256) {
-    const int64_t rounds = (r256 * s256 + 255) / 256;
-    return Tiling{MmTile::kBig, int32_t(r256), int32_t(s256), 1, nT,
-                  kLaunchUs + 1.41 * double(rounds * p.stages)};
+    const int64_t rounds = (r256 * s256 + 255) / 256, per_cu = (p.tiles + 255) / 256;
+    const double big = kLaunchUs + double(rounds) * (1.25 * double(p.stages) + 7.0);
+    const double single = kLaunchUs + double(per_cu) * (0.47 * double(p.stages) + 1.0);
+    if (single < big) return p.tiling(MmTile::kSmallSingle, 1, single);
+    return Tiling{MmTile::kBig, int32_t(r256), int32_t(s256), 1, nT, big};
   }
   Tiling best{};
   for (int64_t k = 1; k <= 64 && (k == 1 || (k * p.tiles <= p.fit && k * 2 <= p.stages)); ++k) {

@@ -519,11 +519,15 @@ __device__ __forceinline__ f32x4 mma(u32x4 a, u32x4 b, f32x4 c) {
 
 // G = 2 (bf16): two such groups of 4 waves in a workgroup, each with its own buffers
 // and half of the stages, for problems with at most one tile per CU; their sums meet
-// in LDS and each group stores half of the tile.  lds: kSmallLds<T> bytes per group;
-// block: the work item, a tile of a split.
-template <typename T> constexpr int kSmallLds = 4 * kSmallTile<T> * 128;
+// in LDS and each group stores half of the tile.
+// NB = 1 (bf16): one buffer, so that three workgroups share a CU: while one waits for
+// its copies or runs its epilogue the others multiply, which pays where a tile has few
+// stages (16384 x 160 x 5120 with softplus: 83 us on 256 x 256 tiles, 73 on these, 95
+// with two buffers and two to a CU).
+// lds: kSmallLds<T, NB> bytes per group; block: the work item, a tile of a split.
+template <typename T, int NB> constexpr int kSmallLds = 2 * NB * kSmallTile<T> * 128;
 #if defined(__HIP_DEVICE_COMPILE__)
-template <typename T, bool RT, bool ST, int ACT, int G>
+template <typename T, bool RT, bool ST, int ACT, int G, int NB>
 __device__ __forceinline__ void mm_small_body(const MmParams& p, int64_t block, char* lds) {
   constexpr int kSz = int(sizeof(T)), kT = 128 / kSz;
   constexpr int kTileS = kSmallTile<T>, kF = kTileS / 32;   // fragments of a wave per side
@@ -572,7 +576,7 @@ __device__ __forceinline__ void mm_small_body(const MmParams& p, int64_t block, 
                                                      short(0), range, 0x00020000);
     const Rsrc b = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(range ? ps + k * ds : ps),
                                                      short(0), range, 0x00020000);
-    char* d = mine + (k & 1) * 2 * kOp + wv * 1024;
+    char* d = mine + (NB == 2 ? (k & 1) * 2 * kOp : 0) + wv * 1024;
 #pragma unroll
     for (int j = 0; j < kF; ++j)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(a, (lds_ptr)(d + j * 4096), 16, vr[j], 0, 0, 0);
@@ -647,16 +651,22 @@ __device__ __forceinline__ void mm_small_body(const MmParams& p, int64_t block, 
   for (int k = 0; k < nk; ++k) {
     wait_copies<0>();
     turn_end();       // stage k is whole, and stage k - 1 has been read by every wave
-    if (k + 1 < nk) copy(k + 1);
+    if (NB == 2 && k + 1 < nk) copy(k + 1);
     part(std::integral_constant<int, 0>{});
-    part(std::integral_constant<int, 1>{});
+    // the second half of the last stage may lie past the contraction's end
+    if (k0 + k < stages - 1 || rem > kT / 2) part(std::integral_constant<int, 1>{});
+    if constexpr (NB == 2) {
 #pragma unroll
-    for (int i = 0; i < kF; ++i) {
-      ar[i] ^= 2 * kOp;
-      as[i] ^= 2 * kOp;
+      for (int i = 0; i < kF; ++i) {
+        ar[i] ^= 2 * kOp;
+        as[i] ^= 2 * kOp;
+      }
+    } else {
+      turn_end();
+      if (k + 1 < nk) copy(k + 1);
     }
   }
-  turn_end();
+  if (NB == 2) turn_end();
   constexpr int kOut = kF / G;          // rows of pieces this group stores
   f32x4 sum[kF][kOut];
   if constexpr (G == 1) {
@@ -705,11 +715,11 @@ __device__ __forceinline__ void mm_small_body(const MmParams& p, int64_t block, 
 }
 #endif
 
-template <typename T, bool RT, bool ST, int ACT, int G>
-__global__ __launch_bounds__(kSmallThreads * G, 2) void mm_small_kernel(MmParams p) {
+template <typename T, bool RT, bool ST, int ACT, int G, int NB>
+__global__ __launch_bounds__(kSmallThreads * G, NB == 1 ? 3 : 2) void mm_small_kernel(MmParams p) {
 #if defined(__HIP_DEVICE_COMPILE__)
-  __shared__ __attribute__((aligned(1024))) char lds[kSmallLds<T> * G];
-  mm_small_body<T, RT, ST, ACT, G>(p, blockIdx.x, lds);
+  __shared__ __attribute__((aligned(1024))) char lds[kSmallLds<T, NB> * G];
+  mm_small_body<T, RT, ST, ACT, G, NB>(p, blockIdx.x, lds);
 #endif
 }
 
@@ -718,12 +728,12 @@ __global__ __launch_bounds__(kSmallThreads * G, 2) void mm_small_kernel(MmParams
 template <typename T>
 __global__ __launch_bounds__(kSmallThreads, 2) void mm_both_kernel(MmParams dx, MmParams dw) {
 #if defined(__HIP_DEVICE_COMPILE__)
-  __shared__ __attribute__((aligned(1024))) char lds[kSmallLds<T>];
+  __shared__ __attribute__((aligned(1024))) char lds[kSmallLds<T, 2>];
   const int64_t items = int64_t(dw.tiles_r) * dw.tiles_s * dw.splits;
   if (int64_t(blockIdx.x) < items)
-    mm_small_body<T, false, false, SS_ACT_NONE, 1>(dw, blockIdx.x, lds);
+    mm_small_body<T, false, false, SS_ACT_NONE, 1, 2>(dw, blockIdx.x, lds);
   else
-    mm_small_body<T, true, false, SS_ACT_NONE, 1>(dx, int64_t(blockIdx.x) - items, lds);
+    mm_small_body<T, true, false, SS_ACT_NONE, 1, 2>(dx, int64_t(blockIdx.x) - items, lds);
 #endif
 }
 
@@ -736,13 +746,16 @@ void run(const MmParams& p, MmTile tile, hipStream_t stream) {
           <<<blocks < kCUs ? blocks : kCUs, kThreads, 0, stream>>>(p);
       break;
     case MmTile::kSmall:
-      mm_small_kernel<uint16_t, RT, ST, ACT, 1><<<blocks, kSmallThreads, 0, stream>>>(p);
+      mm_small_kernel<uint16_t, RT, ST, ACT, 1, 2><<<blocks, kSmallThreads, 0, stream>>>(p);
+      break;
+    case MmTile::kSmallSingle:
+      mm_small_kernel<uint16_t, RT, ST, ACT, 1, 1><<<blocks, kSmallThreads, 0, stream>>>(p);
       break;
     case MmTile::kSmallPair:
-      mm_small_kernel<uint16_t, RT, ST, ACT, 2><<<blocks, 2 * kSmallThreads, 0, stream>>>(p);
+      mm_small_kernel<uint16_t, RT, ST, ACT, 2, 2><<<blocks, 2 * kSmallThreads, 0, stream>>>(p);
       break;
     case MmTile::kSmallF32:
-      mm_small_kernel<float, RT, ST, ACT, 1><<<blocks, kSmallThreads, 0, stream>>>(p);
+      mm_small_kernel<float, RT, ST, ACT, 1, 2><<<blocks, kSmallThreads, 0, stream>>>(p);
       break;
   }
 }

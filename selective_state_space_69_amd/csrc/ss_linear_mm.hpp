@@ -15,7 +15,8 @@ namespace ss {
 // unit is inside its storage, with zeros past the contraction's end where t is the
 // contiguous axis.
 // kSmallPair: 128 x 128 tiles by two groups of waves, at most one tile per CU.
-enum class MmTile { kBig, kSmall, kSmallPair, kSmallF32 };
+// kSmallSingle: 128 x 128 tiles, three to a CU, with one buffer each.
+enum class MmTile { kBig, kSmall, kSmallPair, kSmallSingle, kSmallF32 };
 void launch_mm(const MmParams& p, MmTile tile, bool rt, bool st, hipStream_t stream);
 // dx (rt, not st) and dw (neither) on small tiles of one group, in one launch.
 void launch_mm_both(const MmParams& dx, const MmParams& dw, bool bf16, hipStream_t stream);

@@ -198,6 +198,12 @@ LINEAR = [
     (72, 4104, 2056, "bf16", "bf16", "none", False, None, 0, 0),
     (2000, 2048, 4096, "bf16", "bf16", "none", True, None, 0, 0),
     (2570, 2048, 4096, "bf16", "bf16", "none", True, "bf16", 0, 0),
+    # 256 x 256 tiles of a few stages, the last a partial one: forward (one tile and
+    # two tiles to a workgroup), dx, dw
+    (4090, 344, 4010, "bf16", "bf16", "gelu", True, "f32", 8, 0),
+    (8190, 616, 4090, "bf16", "bf16", "softplus", True, None, 0, 0),
+    (4060, 4072, 520, "bf16", "bf16", "none", False, None, 0, 0),
+    (520, 4072, 4060, "bf16", "bf16", "none", False, None, 0, 0),
 ]
 
 
