@@ -522,8 +522,10 @@ __device__ __forceinline__ f32x4 mma(u32x4 a, u32x4 b, f32x4 c) {
 // in LDS and each group stores half of the tile.
 // NB = 1 (bf16): one buffer, so that three workgroups share a CU: while one waits for
 // its copies or runs its epilogue the others multiply, which pays where a tile has few
-// stages (16384 x 160 x 5120 with softplus: 83 us on 256 x 256 tiles, 73 on these, 95
-// with two buffers and two to a CU).
+// stages (16384 x 160 x 5120 with softplus: 89 us on 256 x 256 tiles, 81 on these, 95
+// with two buffers and two to a CU; 4096 rows: 33 and 21).  Its outputs are streamed
+// (4096 rows: 23 -> 21 us).  A stage of three tiles then runs at the rate of LDS: 32
+// KB in and 64 KB out of it per tile.
 // lds: kSmallLds<T, NB> bytes per group; block: the work item, a tile of a split.
 template <typename T, int NB> constexpr int kSmallLds = 2 * NB * kSmallTile<T> * 128;
 #if defined(__HIP_DEVICE_COMPILE__)
@@ -708,7 +710,7 @@ __device__ __forceinline__ void mm_small_body(const MmParams& p, int64_t block, 
       piece_out<ACT, true, false>(p, sl, q, now, bias, split);
     } else {
       if (j + 1 < kOut) next.fetch(p, r + 16 * (j + 1), c);
-      piece_out<ACT, false, false>(p, sl, q, now, bias, 0);
+      piece_out<ACT, false, NB == 1>(p, sl, q, now, bias, 0);
       now = next;
     }
   }
