@@ -244,21 +244,26 @@ Tiling tiling(const ss_linear_desc_t& d, int64_t nR, int64_t nS, int64_t nT) {
 // faster than one after the other (bf16 5003 x 768 x 1536, whole call: 48 us, both 37).
 bool tiling_both(const ss_linear_desc_t& d, Tiling* dx, Tiling* dw) {
   const Small a(d, d.rows, d.in_dim, d.out_dim), b(d, d.out_dim, d.in_dim, d.rows);
-  const MmTile tile = a.bf16 ? MmTile::kSmall : MmTile::kSmallF32;
+  const MmTile single = a.bf16 ? MmTile::kSmall : MmTile::kSmallF32;
+  auto longer = [](int64_t u, int64_t v) { return u > v ? u : v; };
   double best = tiling(d, a.nR, a.nS, a.nT).us + tiling(d, b.nR, b.nS, b.nT).us;
   bool found = false;
   for (int64_t i = 1; i <= 16 && i * 2 <= a.stages + 1; ++i)
     for (int64_t j = 1; j <= 64 && j * 2 <= b.stages + 1; ++j) {
       const int64_t items = i * a.tiles + j * b.tiles;
       if (items > a.fit) break;
-      const int64_t stages = a.per_part(i) > b.per_part(j) ? a.per_part(i) : b.per_part(j);
-      const double us = kLaunchUs + double(stages) * stage_us(a.bf16, items) +
-                        join_us(a.nR, a.nS, i) + join_us(b.nR, b.nS, j);
-      if (us < best) {
-        best = us;
+      const double rest = kLaunchUs + join_us(a.nR, a.nS, i) + join_us(b.nR, b.nS, j);
+      const int64_t one = longer(a.per_part(i), b.per_part(j));
+      const int64_t two = longer(a.per_part(2 * i), b.per_part(2 * j));
+      const double us[2] = {double(one) * stage_us(a.bf16, items) + rest,
+                            double(two) * 0.9 + 1.0 + rest};
+      const int pair = a.bf16 && items <= 256 && us[1] < us[0];
+      if (us[pair] < best) {
+        best = us[pair];
         found = true;
-        *dx = a.tiling(tile, i, us);
-        *dw = b.tiling(tile, j, us);
+        const MmTile tile = pair ? MmTile::kSmallPair : single;
+        *dx = a.tiling(tile, i, best);
+        *dw = b.tiling(tile, j, best);
       }
     }
   return found;
@@ -484,7 +489,7 @@ int launch_linear_bwd(const ss_linear_desc_t& d, const LinearPlan& pl, const voi
   if (both && dx && dw) {
     px = tiled(px, tx, part);
     pw = tiled(pw, tw, part_dw);
-    launch_mm_both(px, pw, d.in_dtype == SS_BF16, st);
+    launch_mm_both(px, pw, tx.tile, st);
     join(px, st);
     join(pw, st);
   } else {

@@ -655,9 +655,9 @@ __device__ __forceinline__ void mm_small_body(const MmParams& p, int64_t block, 
     turn_end();       // stage k is whole, and stage k - 1 has been read by every wave
     if (NB == 2 && k + 1 < nk) copy(k + 1);
     part(std::integral_constant<int, 0>{});
-    // the second half of the last stage may lie past the contraction's end (the branch
-    // keeps the halves apart, which long contractions pay for: fp32 89 -> 96 us)
-    if (NB == 2 || k + 1 < nk || rem > kT / 2) part(std::integral_constant<int, 1>{});
+    // the second half of the last stage may lie past the contraction's end (fp32 takes
+    // it all the same: the branch between its halves costs 89 -> 96 us)
+    if (kSz == 4 || k0 + k < stages - 1 || rem > kT / 2) part(std::integral_constant<int, 1>{});
     if constexpr (NB == 2) {
 #pragma unroll
       for (int i = 0; i < kF; ++i) {
@@ -728,15 +728,15 @@ __global__ __launch_bounds__(kSmallThreads * G, NB == 1 ? 3 : 2) void mm_small_k
 
 // Both products of a backward pass, dx (R t contiguous) and dw (t strided), side by
 // side: each alone would leave half of the CUs' slots empty.
-template <typename T>
-__global__ __launch_bounds__(kSmallThreads, 2) void mm_both_kernel(MmParams dx, MmParams dw) {
+template <typename T, int G>
+__global__ __launch_bounds__(kSmallThreads * G, 2) void mm_both_kernel(MmParams dx, MmParams dw) {
 #if defined(__HIP_DEVICE_COMPILE__)
-  __shared__ __attribute__((aligned(1024))) char lds[kSmallLds<T, 2>];
+  __shared__ __attribute__((aligned(1024))) char lds[kSmallLds<T, 2> * G];
   const int64_t items = int64_t(dw.tiles_r) * dw.tiles_s * dw.splits;
   if (int64_t(blockIdx.x) < items)
-    mm_small_body<T, false, false, SS_ACT_NONE, 1, 2>(dw, blockIdx.x, lds);
+    mm_small_body<T, false, false, SS_ACT_NONE, G, 2>(dw, blockIdx.x, lds);
   else
-    mm_small_body<T, true, false, SS_ACT_NONE, 1, 2>(dx, int64_t(blockIdx.x) - items, lds);
+    mm_small_body<T, true, false, SS_ACT_NONE, G, 2>(dx, int64_t(blockIdx.x) - items, lds);
 #endif
 }
 
@@ -765,11 +765,15 @@ void run(const MmParams& p, MmTile tile, hipStream_t stream) {
 
 }  // namespace
 
-void launch_mm_both(const MmParams& dx, const MmParams& dw, bool bf16, hipStream_t stream) {
+void launch_mm_both(const MmParams& dx, const MmParams& dw, MmTile tile, hipStream_t stream) {
   const unsigned blocks = unsigned(dx.tiles_r) * unsigned(dx.tiles_s) * unsigned(dx.splits) +
                           unsigned(dw.tiles_r) * unsigned(dw.tiles_s) * unsigned(dw.splits);
-  if (bf16) mm_both_kernel<uint16_t><<<blocks, kSmallThreads, 0, stream>>>(dx, dw);
-  else mm_both_kernel<float><<<blocks, kSmallThreads, 0, stream>>>(dx, dw);
+  if (tile == MmTile::kSmallPair)
+    mm_both_kernel<uint16_t, 2><<<blocks, 2 * kSmallThreads, 0, stream>>>(dx, dw);
+  else if (tile == MmTile::kSmall)
+    mm_both_kernel<uint16_t, 1><<<blocks, kSmallThreads, 0, stream>>>(dx, dw);
+  else
+    mm_both_kernel<float, 1><<<blocks, kSmallThreads, 0, stream>>>(dx, dw);
 }
 
 void launch_mm(const MmParams& p, MmTile tile, bool rt, bool st, hipStream_t stream) {
