@@ -188,6 +188,7 @@ double stage_us(bool bf16, int64_t items) {
   const int64_t per_cu = (items + 255) / 256;
   return bf16 ? (per_cu > 1 ? 0.9 : 0.7) : (per_cu > 1 ? 0.5 * double(per_cu) : 0.7);
 }
+double big_us(int64_t stages) { return 1.25 * double(stages) + 7.0; }
 // the join of k parts, their sums written and read
 double join_us(int64_t nR, int64_t nS, int64_t k) {
   return k > 1 ? 6.0 + double(k) * double(nR) * double(nS) * 8.0 / 4.0e6 : 0.0;
@@ -219,7 +220,7 @@ Tiling tiling(const ss_linear_desc_t& d, int64_t nR, int64_t nS, int64_t nT) {
   const Small p(d, nR, nS, nT);
   if (p.bf16 && p.tiles > 512 && p.tiles * 100 > 282 * r256 * s256) {
     const int64_t rounds = (r256 * s256 + 255) / 256, per_cu = (p.tiles + 255) / 256;
-    const double big = kLaunchUs + double(rounds) * (1.25 * double(p.stages) + 7.0);
+    const double big = kLaunchUs + double(rounds) * big_us(p.stages);
     const double single = kLaunchUs + double(per_cu) * (0.47 * double(p.stages) + 1.0);
     if (single < big) return p.tiling(MmTile::kSmallSingle, 1, single);
     return Tiling{MmTile::kBig, int32_t(r256), int32_t(s256), 1, nT, big};
@@ -240,14 +241,40 @@ Tiling tiling(const ss_linear_desc_t& d, int64_t nR, int64_t nS, int64_t nT) {
   }
   return best;
 }
-// dx and dw in one launch, where both fit on the GPU at once and the model finds that
-// faster than one after the other (bf16 5003 x 768 x 1536, whole call: 48 us, both 37).
-bool tiling_both(const ss_linear_desc_t& d, Tiling* dx, Tiling* dw) {
+// The tiles of a backward pass.  One launch computes dx and dw where the model finds
+// that faster than one after the other: small tiles that all fit on the GPU at once
+// (bf16 5003 x 768 x 1536, whole call: 48 us, both 37), or 256 x 256 ones, where the
+// workgroups that dw's last round does not reach go on with dx's tiles, the others
+// taking `few` of those each.
+struct Backward {
+  Tiling dx, dw;
+  bool both;
+  int behind, few;
+};
+Backward tilings_bwd(const ss_linear_desc_t& d) {
   const Small a(d, d.rows, d.in_dim, d.out_dim), b(d, d.out_dim, d.in_dim, d.rows);
-  const MmTile single = a.bf16 ? MmTile::kSmall : MmTile::kSmallF32;
+  Backward t{tiling(d, a.nR, a.nS, a.nT), tiling(d, b.nR, b.nS, b.nT), false, 0, 0};
+  double best = t.dx.us + t.dw.us;
   auto longer = [](int64_t u, int64_t v) { return u > v ? u : v; };
-  double best = tiling(d, a.nR, a.nS, a.nT).us + tiling(d, b.nR, b.nS, b.nT).us;
-  bool found = false;
+  if (t.dx.tile == MmTile::kBig && t.dw.tile == MmTile::kBig) {
+    const double ux = big_us(a.stages), uw = big_us(b.stages);
+    const int64_t nx = int64_t(t.dx.tiles_r) * t.dx.tiles_s;
+    const int64_t nw = int64_t(t.dw.tiles_r) * t.dw.tiles_s;
+    const int64_t behind = nw % 256, rest = 256 - behind;
+    for (int64_t few = 0; few <= nx / 256 && (few == 0 || behind); ++few) {
+      const int64_t most = few + (nx - few * 256 + rest - 1) / rest;
+      const double late = uw + double(few) * ux, early = double(most) * ux;
+      const double us = kLaunchUs + double(nw / 256) * uw +
+                        (behind && late > early ? late : early);
+      if (us < best) {
+        best = us;
+        t.both = true;
+        t.behind = int(behind);
+        t.few = int(few);
+      }
+    }
+    return t;
+  }
   for (int64_t i = 1; i <= 16 && i * 2 <= a.stages + 1; ++i)
     for (int64_t j = 1; j <= 64 && j * 2 <= b.stages + 1; ++j) {
       const int64_t items = i * a.tiles + j * b.tiles;
@@ -260,13 +287,14 @@ bool tiling_both(const ss_linear_desc_t& d, Tiling* dx, Tiling* dw) {
       const int pair = a.bf16 && items <= 256 && us[1] < us[0];
       if (us[pair] < best) {
         best = us[pair];
-        found = true;
-        const MmTile tile = pair ? MmTile::kSmallPair : single;
-        *dx = a.tiling(tile, i, best);
-        *dw = b.tiling(tile, j, best);
+        const MmTile tile = pair ? MmTile::kSmallPair
+                                 : a.bf16 ? MmTile::kSmall : MmTile::kSmallF32;
+        t.both = true;
+        t.dx = a.tiling(tile, i, best);
+        t.dw = b.tiling(tile, j, best);
       }
     }
-  return found;
+  return t;
 }
 
 size_t part_bytes(const Tiling& t, int64_t nR, int64_t nS) {
@@ -377,17 +405,10 @@ LinearPlan plan_linear(const ss_linear_desc_t& d, int op) {
   if (pad_k) pl.off_w = take(w_bytes);
   pl.off_sums = take(align256(size_t(pl.chunks) * size_t(d.out_dim) * 4));
   // dx's and dw's parts: one after the other in one place, or side by side
-  const size_t a = part_bytes(tiling(d, d.rows, d.in_dim, d.out_dim), d.rows, d.in_dim);
-  const size_t b = part_bytes(tiling(d, d.out_dim, d.in_dim, d.rows), d.out_dim, d.in_dim);
-  size_t part = a > b ? a : b;
-  Tiling ta, tb;
-  if (tiling_both(d, &ta, &tb)) {
-    const size_t pa = part_bytes(ta, d.rows, d.in_dim);
-    const size_t both = pa + part_bytes(tb, d.out_dim, d.in_dim);
-    pl.off_part_dw = pa;
-    if (both > part) part = both;
-  }
-  pl.off_part = take(part);
+  const Backward t = tilings_bwd(d);
+  const size_t a = part_bytes(t.dx, d.rows, d.in_dim), b = part_bytes(t.dw, d.out_dim, d.in_dim);
+  pl.off_part_dw = t.both ? a : 0;
+  pl.off_part = take(t.both ? a + b : a > b ? a : b);
   pl.bytes = off;
   return pl;
 }
@@ -477,24 +498,17 @@ int launch_linear_bwd(const ss_linear_desc_t& d, const LinearPlan& pl, const voi
   ops.launch(st);
   char* const part = ws + pl.off_part;
   // one gradient alone is computed as it is beside the other: the same sums
-  Tiling tx, tw;
-  char* part_dw = part;
-  const bool both = tiling_both(d, &tx, &tw);
-  if (both) {
-    part_dw += pl.off_part_dw;
-  } else {
-    tx = tiling(d, d.rows, d.in_dim, d.out_dim);
-    tw = tiling(d, d.out_dim, d.in_dim, d.rows);
-  }
-  if (both && dx && dw) {
-    px = tiled(px, tx, part);
-    pw = tiled(pw, tw, part_dw);
-    launch_mm_both(px, pw, tx.tile, st);
+  const Backward t = tilings_bwd(d);
+  char* const part_dw = part + pl.off_part_dw;
+  if (t.both && dx && dw) {
+    px = tiled(px, t.dx, part);
+    pw = tiled(pw, t.dw, part_dw);
+    launch_mm_both(px, pw, t.dx.tile, t.behind, t.few, st);
     join(px, st);
     join(pw, st);
   } else {
-    if (dx) run_mm(px, tx, true, false, part, st);
-    if (dw) run_mm(pw, tw, false, false, part_dw, st);
+    if (dx) run_mm(px, t.dx, true, false, part, st);
+    if (dw) run_mm(pw, t.dw, false, false, part_dw, st);
   }
   return int(hipGetLastError());
 }

@@ -48,6 +48,8 @@ constexpr int kTile = 256;
 constexpr int kStep = 64;                          // t per stage
 constexpr int kThreads = 512;
 constexpr unsigned kCUs = 256;
+// dx's tiles beside dw's: the workgroups below `behind` take `few` of them each
+struct Behind { int32_t behind, few; };
 constexpr int kOffR = 0, kOffLo = 65536, kOffHi = 98304, kOffEpi = 131072;
 constexpr int kLds = 163840;
 
@@ -228,32 +230,55 @@ __device__ __forceinline__ void piece_out(const MmParams& p, char* sl, const f32
   asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
 }
 
-// Workgroup b of the grid takes a tile of every round of gridDim.x tiles; the tiles
-// of a round lie together on an XCD.  Returns false past the last tile.
-__device__ __forceinline__ bool round_tile(const MmParams& p, int64_t round, int64_t* tr, int* ts) {
-  const int64_t tiles = int64_t(p.tiles_r) * p.tiles_s, first = round * gridDim.x;
-  const int64_t n = tiles - first < gridDim.x ? tiles - first : gridDim.x;
-  if (int64_t(blockIdx.x) >= n) return false;
-  tile_of(p, first + xcd_contiguous(blockIdx.x, n), tr, ts);
+// Which tile of a product a workgroup takes in its round'th turn (false: none is
+// left).  A turn's takers are `takers` workgroups, this one the i-th; their tiles
+// start at `first` and lie together on an XCD.
+__device__ __forceinline__ bool turn_tile(const MmParams& p, int64_t first, int64_t takers,
+                                          int64_t i, int64_t* tr, int* ts) {
+  const int64_t left = int64_t(p.tiles_r) * p.tiles_s - first;
+  const int64_t n = left < takers ? left : takers;
+  if (i >= n) return false;
+  tile_of(p, first + xcd_contiguous(i, n), tr, ts);
   return true;
 }
+// every workgroup takes a tile of every round
+struct EveryRound {
+  __device__ __forceinline__ bool operator()(const MmParams& p, int64_t round, int64_t* tr,
+                                             int* ts) const {
+    return turn_tile(p, round * gridDim.x, gridDim.x, blockIdx.x, tr, ts);
+  }
+};
+// the workgroups below `behind` come late and take only `few` tiles each
+struct BehindOthers {
+  Behind b;
+  __device__ __forceinline__ bool operator()(const MmParams& p, int64_t round, int64_t* tr,
+                                             int* ts) const {
+    const int64_t all = gridDim.x, rest = all - b.behind;
+    if (round < b.few) return turn_tile(p, round * all, all, blockIdx.x, tr, ts);
+    if (int(blockIdx.x) < b.behind) return false;
+    return turn_tile(p, b.few * all + (round - b.few) * rest, rest,
+                     blockIdx.x - b.behind, tr, ts);
+  }
+};
 
-// The kernel's parameters, read again where they are used from here on: held in
-// scalar registers through the main loop they would crowd it.
-__device__ __forceinline__ MmParams reread_params() {
-  constexpr int kWords = int(sizeof(MmParams) / 8);
-  static_assert(sizeof(MmParams) % 8 == 0, "read in 8-byte words");
-  uint64_t a = uint64_t(__builtin_amdgcn_kernarg_segment_ptr());   // the only parameter
+// Kernel parameters, read again where they are used from here on: held in scalar
+// registers through the main loop they would crowd it.  AT: where a T is among them.
+template <typename T, int AT>
+__device__ __forceinline__ T reread_params() {
+  constexpr int kWords = int(sizeof(T) / 8);
+  static_assert(sizeof(T) % 8 == 0 && AT % 8 == 0, "read in 8-byte words");
+  uint64_t a = uint64_t(__builtin_amdgcn_kernarg_segment_ptr()) + AT;
   asm volatile("" : "+s"(a));
   struct Words { uint64_t w[kWords]; } v;
 #pragma unroll
   for (int i = 0; i < kWords; ++i)
     v.w[i] = ((const __attribute__((address_space(4))) uint64_t*)a)[i];
-  return __builtin_bit_cast(MmParams, v);
+  return __builtin_bit_cast(T, v);
 }
 
-template <bool RT, bool ST, int ACT>
-__device__ __forceinline__ void mm256_body(const MmParams& p0, char* lds) {
+// AT: where p0 is among the kernel's parameters
+template <bool RT, bool ST, int ACT, int AT, typename Turns>
+__device__ __forceinline__ void mm256_body(const MmParams& p0, const Turns& turn, char* lds) {
   const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int m = lane & 15, g = lane >> 4;
   int64_t r0, s0;
@@ -392,7 +417,7 @@ __device__ __forceinline__ void mm256_body(const MmParams& p0, char* lds) {
 
   int64_t tr;
   int ts;
-  if (!round_tile(p0, 0, &tr, &ts)) return;
+  if (!turn(p0, 0, &tr, &ts)) return;
   place(p0, tr, ts);
   begin();
   for (int64_t round = 0;; ++round) {
@@ -456,10 +481,10 @@ __device__ __forceinline__ void mm256_body(const MmParams& p0, char* lds) {
       }
     }
     // the next tile's first copies run under this one's epilogue
-    const MmParams p = reread_params();
+    const MmParams p = reread_params<MmParams, AT>();
     const int64_t r = r0 + wr;
     const int32_t c0 = int32_t(s0) + wsn;
-    const bool more = round_tile(p, round + 1, &tr, &ts);
+    const bool more = turn(p, round + 1, &tr, &ts);
     if (more) {
       place(p, tr, ts);
       begin();
@@ -486,7 +511,21 @@ template <bool RT, bool ST, int ACT>
 __global__ __launch_bounds__(kThreads, 2) void mm256_kernel(MmParams p) {
 #if defined(__HIP_DEVICE_COMPILE__)
   __shared__ __attribute__((aligned(1024))) char lds[kLds];
-  mm256_body<RT, ST, ACT>(p, lds);
+  mm256_body<RT, ST, ACT, 0>(p, EveryRound{}, lds);
+#endif
+}
+
+// Both products of a backward pass: dw's tiles, of which the last round does not
+// reach every workgroup, then dx's (16384 rows, 5120 -> 2560: 750 us one after the
+// other, where dw's 200 tiles leave 56 CUs idle, 708 together; 2560 -> 5120 from a
+// checkpoint 757 and 686).
+__global__ __launch_bounds__(kThreads, 2) void mm256_both_kernel(MmParams dw, MmParams, Behind) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  __shared__ __attribute__((aligned(1024))) char lds[kLds];
+  constexpr int kDx = int(sizeof(MmParams)), kTurns = 2 * kDx;
+  mm256_body<false, false, SS_ACT_NONE, 0>(dw, EveryRound{}, lds);
+  const MmParams dx = reread_params<MmParams, kDx>();
+  mm256_body<true, false, SS_ACT_NONE, kDx>(dx, BehindOthers{reread_params<Behind, kTurns>()}, lds);
 #endif
 }
 
@@ -765,7 +804,12 @@ void run(const MmParams& p, MmTile tile, hipStream_t stream) {
 
 }  // namespace
 
-void launch_mm_both(const MmParams& dx, const MmParams& dw, MmTile tile, hipStream_t stream) {
+void launch_mm_both(const MmParams& dx, const MmParams& dw, MmTile tile, int behind, int few,
+                    hipStream_t stream) {
+  if (tile == MmTile::kBig) {
+    mm256_both_kernel<<<kCUs, kThreads, 0, stream>>>(dw, dx, Behind{behind, few});
+    return;
+  }
   const unsigned blocks = unsigned(dx.tiles_r) * unsigned(dx.tiles_s) * unsigned(dx.splits) +
                           unsigned(dw.tiles_r) * unsigned(dw.tiles_s) * unsigned(dw.splits);
   if (tile == MmTile::kSmallPair)

@@ -204,6 +204,10 @@ LINEAR = [
     (8190, 616, 4090, "bf16", "bf16", "softplus", True, None, 0, 0),
     (4060, 4072, 520, "bf16", "bf16", "none", False, None, 0, 0),
     (520, 4072, 4060, "bf16", "bf16", "none", False, None, 0, 0),
+    # dx's tiles behind dw's in one launch: a last round of dw that reaches some of the
+    # workgroups, and all of them
+    (9003, 2950, 2901, "bf16", "bf16", "silu", True, None, 0, 0),
+    (2600, 4090, 4080, "bf16", "bf16", "none", True, None, 0, 0),
 ]
 
 
