@@ -21,7 +21,7 @@ __global__ __launch_bounds__(kThreads) void join_kernel(MmParams p) {
     const int64_t step = p.nR * p.nS;
     if (s + 8 <= p.nS) {
       float v[8] = {0, 0, 0, 0, 0, 0, 0, 0}, bias[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-      const Res8 res = fetch_res8(p, r, s);
+      const Res8 res = fetch_res8(p, r * p.nS + s, true);
       if (p.bias) load8(p.bias + s, bias);
       for (int k = 0; k < p.splits; ++k) {
         float f[8];
@@ -29,7 +29,7 @@ __global__ __launch_bounds__(kThreads) void join_kernel(MmParams p) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] += f[j];
       }
-      epilogue8<kActOf>(p, r, s, v, bias, res);
+      epilogue8<kActOf>(p, r * p.nS + s, v, bias, res);
     } else {
       for (int j = 0; s + j < p.nS; ++j) {
         float v = 0.0f;

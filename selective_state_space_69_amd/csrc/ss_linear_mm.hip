@@ -176,13 +176,20 @@ struct Piece {
   static constexpr int kPasses = 16 / kRows;
   int64_t r;      // this lane's row in the first pass
   int32_t s;      // its first column
+  int64_t o;      // their element of the output
   Res8 res[kPasses];
-  __device__ __forceinline__ void fetch(const MmParams& p, int64_t r0, int32_t s0) {
+  __device__ __forceinline__ void place(const MmParams& p, int64_t r0, int32_t s0) {
     const int lane = threadIdx.x & 63;
     r = r0 + lane / kPer;
     s = s0 + (lane % kPer) * 8;
+    o = r * p.nS + s;
+  }
+  __device__ __forceinline__ void fetch(const MmParams& p, int64_t r0, int32_t s0) {
+    place(p, r0, s0);
+    if (!p.res) return;
 #pragma unroll
-    for (int h = 0; h < kPasses; ++h) res[h] = fetch_res8(p, r + h * kRows, s);
+    for (int h = 0; h < kPasses; ++h)
+      res[h] = fetch_res8(p, o + h * kRows * int64_t(p.nS), r + h * kRows < p.nR && s + 8 <= p.nS);
   }
 };
 __device__ __forceinline__ void fetch_bias(const MmParams& p, int32_t s, float (&bias)[8]) {
@@ -206,21 +213,21 @@ __device__ __forceinline__ void piece_out(const MmParams& p, char* sl, const f32
 #pragma nounroll
   for (int h = 0; h < Piece<F>::kPasses; ++h) {
     const int row = h * Piece<F>::kRows + lane / Piece<F>::kPer;
-    const int64_t r = at.r + h * Piece<F>::kRows;
+    const int64_t r = at.r + h * Piece<F>::kRows, o = at.o + h * Piece<F>::kRows * int64_t(p.nS);
     const int32_t s = at.s;
     if (r < p.nR && s < p.nS) {
       if (s + 8 <= p.nS) {
         const f32x4 x = *reinterpret_cast<const f32x4*>(sl + row * 256 + ((u ^ row) << 4));
         const f32x4 y = *reinterpret_cast<const f32x4*>(sl + row * 256 + (((u + 1) ^ row) << 4));
         float v[8] = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
-        if constexpr (SPLIT) store8(p.part, (split * p.nR + r) * p.nS + s, 0, v);
-        else epilogue8<ACT, STREAM>(p, r, s, v, bias, res);
+        if constexpr (SPLIT) store8(p.part, split * p.nR * p.nS + o, 0, v);
+        else epilogue8<ACT, STREAM>(p, o, v, bias, res);
       } else {
 #pragma nounroll
         for (int j = 0; s + j < p.nS; ++j) {
           const float v = *reinterpret_cast<const float*>(
               sl + row * 256 + (((u + j / 4) ^ row) << 4) + (j & 3) * 4);
-          if constexpr (SPLIT) store1(p.part, (split * p.nR + r) * p.nS + s + j, 0, v);
+          if constexpr (SPLIT) store1(p.part, split * p.nR * p.nS + o + j, 0, v);
           else epilogue1(p, ACT, r, s + j, v);
         }
       }
@@ -563,8 +570,7 @@ __device__ __forceinline__ f32x4 mma(u32x4 a, u32x4 b, f32x4 c) {
 // its copies or runs its epilogue the others multiply, which pays where a tile has few
 // stages (16384 x 160 x 5120 with softplus: 89 us on 256 x 256 tiles, 81 on these, 95
 // with two buffers and two to a CU; 4096 rows: 33 and 21).  Its outputs are streamed
-// (4096 rows: 23 -> 21 us).  A stage of three tiles then runs at the rate of LDS: 32
-// KB in and 64 KB out of it per tile.
+// (4096 rows: 23 -> 21 us).
 // lds: kSmallLds<T, NB> bytes per group; block: the work item, a tile of a split.
 template <typename T, int NB> constexpr int kSmallLds = 2 * NB * kSmallTile<T> * 128;
 #if defined(__HIP_DEVICE_COMPILE__)
@@ -745,8 +751,7 @@ __device__ __forceinline__ void mm_small_body(const MmParams& p, int64_t block, 
 #pragma unroll
     for (int i = 0; i < kF; ++i) q[i] = sum[i][j];
     if (p.splits > 1) {
-      now.r = r + 16 * j + lane / Piece<kF>::kPer;
-      now.s = c + (lane % Piece<kF>::kPer) * 8;
+      now.place(p, r + 16 * j, c);
       piece_out<ACT, true, false>(p, sl, q, now, bias, split);
     } else {
       if (j + 1 < kOut) next.fetch(p, r + 16 * (j + 1), c);

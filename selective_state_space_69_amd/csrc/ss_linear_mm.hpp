@@ -84,12 +84,13 @@ __device__ __forceinline__ void epilogue1(const MmParams& p, int act, int64_t r,
   store1(p.out, o, p.out_bf16, v);
 }
 
-// Eight neighbours of the residual, fetched ahead in their storage form.
+// Eight neighbours of the residual from element o on, fetched ahead in their storage
+// form; left unset where there is none (to clear it for nothing costs as much as the
+// rest of a piece's addresses).
 struct Res8 { uint32_t w[8]; };
-__device__ __forceinline__ Res8 fetch_res8(const MmParams& p, int64_t r, int32_t s) {
-  Res8 f{};
-  if (p.res && r < p.nR && s + 8 <= p.nS) {
-    const int64_t o = r * p.nS + s;
+__device__ __forceinline__ Res8 fetch_res8(const MmParams& p, int64_t o, bool inside) {
+  Res8 f;
+  if (p.res && inside) {
     if (p.res_bf16) {
       const Halves8 h = *(const Global<Halves8>*)((const Global<uint16_t>*)p.res + o);
 #pragma unroll
@@ -104,14 +105,13 @@ __device__ __forceinline__ Res8 fetch_res8(const MmParams& p, int64_t r, int32_t
   return f;
 }
 
-// Eight neighbours s..s+7 of output row r, all inside it; bias: theirs (0 without
-// one).  ACT: the activation, or kActOf for p.act.
+// Eight neighbours of an output row from element o on, all inside it; bias: theirs (0
+// without one).  ACT: the activation, or kActOf for p.act.
 constexpr int kActOf = -1;
 template <int ACT, bool STREAM = false>
-__device__ __forceinline__ void epilogue8(const MmParams& p, int64_t r, int32_t s, float (&v)[8],
+__device__ __forceinline__ void epilogue8(const MmParams& p, int64_t o, float (&v)[8],
                                           const float (&bias)[8], const Res8& res) {
   const int act = ACT == kActOf ? p.act : ACT;
-  const int64_t o = r * p.nS + s;
 #pragma unroll
   for (int j = 0; j < 8; ++j) v[j] += bias[j];
   if (p.pre) store8<STREAM>(p.pre, o, p.pre_bf16, v);
