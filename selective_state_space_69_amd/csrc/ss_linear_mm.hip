@@ -245,7 +245,7 @@ __device__ __forceinline__ bool turn_tile(const MmParams& p, int64_t first, int6
   const int64_t left = int64_t(p.tiles_r) * p.tiles_s - first;
   const int64_t n = left < takers ? left : takers;
   if (i >= n) return false;
-  tile_of(p, first + xcd_contiguous(i, n), tr, ts);
+  tile_of(p, uint32_t(first + xcd_contiguous(i, n)), tr, ts);
   return true;
 }
 // every workgroup takes a tile of every round
@@ -575,7 +575,7 @@ __device__ __forceinline__ f32x4 mma(u32x4 a, u32x4 b, f32x4 c) {
 template <typename T, int NB> constexpr int kSmallLds = 2 * NB * kSmallTile<T> * 128;
 #if defined(__HIP_DEVICE_COMPILE__)
 template <typename T, bool RT, bool ST, int ACT, int G, int NB>
-__device__ __forceinline__ void mm_small_body(const MmParams& p, int64_t block, char* lds) {
+__device__ __forceinline__ void mm_small_body(const MmParams& p, uint32_t block, char* lds) {
   constexpr int kSz = int(sizeof(T)), kT = 128 / kSz;
   constexpr int kTileS = kSmallTile<T>, kF = kTileS / 32;   // fragments of a wave per side
   constexpr int kOp = kTileS * 128;                         // bytes of an operand's stage
@@ -583,11 +583,11 @@ __device__ __forceinline__ void mm_small_body(const MmParams& p, int64_t block, 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wv8 = __builtin_amdgcn_readfirstlane(tid >> 6), wv = wv8 & 3, grp = wv8 >> 2;
   const int m = lane & 15, g = lane >> 4;
-  const int64_t tiles = int64_t(p.tiles_r) * p.tiles_s;
+  const uint32_t tiles = uint32_t(p.tiles_r) * uint32_t(p.tiles_s);
   const int split = int(block / tiles);
   int64_t tr;
   int ts;
-  tile_of(p, xcd_contiguous(block - split * tiles, tiles), &tr, &ts);
+  tile_of(p, uint32_t(xcd_contiguous(block - uint32_t(split) * tiles, tiles)), &tr, &ts);
   const int64_t r0 = tr * kTileS, s0 = int64_t(ts) * kTileS;
   const int64_t t0 = split * p.t_split;
   const int64_t t1 = t0 + p.t_split < p.nT ? t0 + p.t_split : p.nT;
@@ -776,11 +776,11 @@ template <typename T, int G>
 __global__ __launch_bounds__(kSmallThreads * G, 2) void mm_both_kernel(MmParams dx, MmParams dw) {
 #if defined(__HIP_DEVICE_COMPILE__)
   __shared__ __attribute__((aligned(1024))) char lds[kSmallLds<T, 2> * G];
-  const int64_t items = int64_t(dw.tiles_r) * dw.tiles_s * dw.splits;
-  if (int64_t(blockIdx.x) < items)
+  const uint32_t items = uint32_t(dw.tiles_r) * uint32_t(dw.tiles_s) * uint32_t(dw.splits);
+  if (blockIdx.x < items)
     mm_small_body<T, false, false, SS_ACT_NONE, G, 2>(dw, blockIdx.x, lds);
   else
-    mm_small_body<T, true, false, SS_ACT_NONE, G, 2>(dx, int64_t(blockIdx.x) - items, lds);
+    mm_small_body<T, true, false, SS_ACT_NONE, G, 2>(dx, blockIdx.x - items, lds);
 #endif
 }
 
