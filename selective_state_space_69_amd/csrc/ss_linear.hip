@@ -162,11 +162,13 @@ int64_t pad_to_unit(const ss_linear_desc_t& d, int64_t n) {
 // a small one 0.47 and 1 us of its CU, whose other tiles cover its waits.  Measured,
 // large and single-buffered tiles (bf16 out, us):
 //   contraction            160            320            640           1280
-//   16384 x 5120      68.5   64.9    73.7   75.7   106.0  124.2   174.7  214.5
-//   with softplus     83.4   72.9    91.8   89.3   125.3  139.0   194.3  228.4
-//   4096 x 5120       25.8   18.4    30.0   23.9    42.3   34.4    66.1   58.2
-// fp32: 64 x 64, of which five fit. Where the tiles of a long contraction leave CUs
-// empty it is split. The model below picks the groups and the number of parts: a
+//   16384 x 5120      66.8   64.8    77.0   79.5   111.5  127.4   185.0  217.6
+//   with softplus     85.0   70.8    96.0   89.2   128.4  130.9   198.5  226.8
+//   4096 x 5120       25.3   16.7    29.9   20.3    42.0   32.8    66.0   57.4
+// (small and double-buffered against large, contraction 2560: 2048 x 4096, 512 small
+// tiles, 45.9 and 53.6).
+// fp32: 64 x 64, of which five fit.  Where the tiles of a long contraction leave CUs
+// empty it is split.  The model below picks the groups and the number of parts: a
 // stage of 128 bytes takes 0.7 us with one group of waves on a CU and 0.9 us for two
 // (fp32: 0.5 us for each, not below 0.7), two groups meet for 1 us, and a split
 // product pays for the join kernel and for its partial sums' way to memory and back.

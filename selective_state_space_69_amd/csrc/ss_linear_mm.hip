@@ -33,8 +33,9 @@
 // block: before the builtin the compiler waits for every copy in flight.
 //
 // Measured, 16384 rows: 2560 -> 10240 forward 651 us (1320 TFLOP/s; the matrix cores
-// are busy 65% of the cycles, at the 1.9 GHz that power allows), dx of 5120 -> 2560 in
-// fp32 360 us, its dw 369 us (200 tiles on 256 CUs).
+// are busy 65% of the cycles, at the 1.9 GHz that power allows), dx and dw of 5120
+// -> 2560 in fp32 714 us together (1200; 360 and 369 us each alone, dw's 200 tiles on
+// 256 CUs).
 #include "ss_linear_mm.hpp"
 
 namespace ss {
@@ -568,8 +569,8 @@ __device__ __forceinline__ f32x4 mma(u32x4 a, u32x4 b, f32x4 c) {
 // in LDS and each group stores half of the tile.
 // NB = 1 (bf16): one buffer, so that three workgroups share a CU: while one waits for
 // its copies or runs its epilogue the others multiply, which pays where a tile has few
-// stages (16384 x 160 x 5120 with softplus: 89 us on 256 x 256 tiles, 81 on these, 95
-// with two buffers and two to a CU; 4096 rows: 33 and 21).  Its outputs are streamed
+// stages (16384 x 160 x 5120 with softplus: 85 us on 256 x 256 tiles, 71 on these, 95
+// with two buffers and two to a CU; 4096 rows: 33 and 20).  Its outputs are streamed
 // (4096 rows: 23 -> 21 us).
 // lds: kSmallLds<T, NB> bytes per group; block: the work item, a tile of a split.
 template <typename T, int NB> constexpr int kSmallLds = 2 * NB * kSmallTile<T> * 128;
