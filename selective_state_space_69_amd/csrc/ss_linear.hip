@@ -40,7 +40,7 @@ __global__ __launch_bounds__(kThreads) void join_kernel(MmParams p) {
   }
 }
 
-// Rows of one or two tensors (blockIdx.y) at a 16-byte aligned stride, zero past
+// bf16 rows of one or two tensors (blockIdx.y) at a 16-byte aligned stride, zero past
 // their end: one 16-byte unit of the copy per thread.
 struct PadJob {
   const void* src;
@@ -51,22 +51,21 @@ struct PadJob {
 struct PadParams {
   PadJob job[2];
 };
-template <typename T>
 __global__ __launch_bounds__(kThreads) void pad_kernel(PadParams q) {
-  constexpr int E = 16 / int(sizeof(T));
+  constexpr int E = 8;
   const PadJob p = q.job[blockIdx.y];
   const int64_t total = p.rows * p.units;
   for (int64_t i = int64_t(blockIdx.x) * kThreads + threadIdx.x; i < total;
        i += int64_t(gridDim.x) * kThreads) {
     const int64_t r = total <= INT32_MAX ? int64_t(uint32_t(i) / uint32_t(p.units)) : i / p.units;
     const int c = int(i - r * p.units) * E;
-    const T* src = static_cast<const T*>(p.src) + r * p.ld_src + c;
-    struct __attribute__((packed, aligned(sizeof(T)))) Elems { T e[E]; } v;
+    const uint16_t* src = static_cast<const uint16_t*>(p.src) + r * p.ld_src + c;
+    struct __attribute__((packed, aligned(2))) Elems { uint16_t e[E]; } v;
     if (c + E <= p.cols) {
       v = *reinterpret_cast<const Elems*>(src);      // 16 bytes at any element address
     } else {
 #pragma unroll
-      for (int j = 0; j < E; ++j) v.e[j] = c + j < p.cols ? src[j] : T(0);
+      for (int j = 0; j < E; ++j) v.e[j] = c + j < p.cols ? src[j] : uint16_t(0);
     }
     reinterpret_cast<u32x4*>(p.dst)[i] = __builtin_bit_cast(u32x4, v);
   }
@@ -322,20 +321,27 @@ void run_mm(MmParams p, const Tiling& t, bool rt, bool st, char* part, hipStream
   join(p, stream);
 }
 
-// The operands of a call that 16-byte units cannot read in place, copied to rows of
-// pad_to_unit(cols) elements by one launch.
+// The operands of a call that 16-byte units cannot read in place: bf16 ones are copied
+// to rows of pad_to_unit(cols) elements by one launch, for fp32 ones the products are
+// told to read single elements.
 struct Operands {
   const ss_linear_desc_t& d;
   PadParams pad{};
   int n = 0;
+  bool any = false;
   // rows x cols of src, rows *ld elements apart: where the products read it
   const void* take(const void* src, int64_t* ld, int64_t rows, int64_t cols, char* dst) {
     const int e = unit_of(d);
     if (ptr16(src) && *ld % e == 0 && cols % e == 0) return src;
+    if (d.in_dtype == SS_F32) {
+      any = true;
+      return src;
+    }
     pad.job[n++] = PadJob{src, dst, *ld, rows, int32_t(cols), int32_t(pad_to_unit(d, cols) / e)};
     *ld = pad_to_unit(d, cols);
     return dst;
   }
+  MmTile tile(MmTile t) const { return any && t == MmTile::kSmallF32 ? MmTile::kSmallF32Any : t; }
   void launch(hipStream_t st) {
     if (n == 0) return;
     int64_t blocks = 1;
@@ -344,8 +350,7 @@ struct Operands {
       if (b > blocks) blocks = b;
     }
     const dim3 grid(unsigned(blocks < kMaxBlocks ? blocks : kMaxBlocks), unsigned(n));
-    if (d.in_dtype == SS_BF16) pad_kernel<uint16_t><<<grid, kThreads, 0, st>>>(pad);
-    else pad_kernel<float><<<grid, kThreads, 0, st>>>(pad);
+    pad_kernel<<<grid, kThreads, 0, st>>>(pad);
   }
 };
 
@@ -378,7 +383,8 @@ LinearPlan plan_linear(const ss_linear_desc_t& d, int op) {
   const size_t x_bytes = align256(size_t(d.rows) * size_t(pad_to_unit(d, d.in_dim)) * esize);
   const size_t w_bytes = align256(size_t(d.out_dim) * size_t(pad_to_unit(d, d.in_dim)) * esize);
   // rows with a stride may start anywhere: reserve a copy
-  const bool pad_k = d.in_dim % unit_of(d) != 0, pad_x = pad_k || d.x_stride != 0;
+  const bool bf16 = d.in_dtype == SS_BF16;
+  const bool pad_k = bf16 && d.in_dim % 8 != 0, pad_x = pad_k || (bf16 && d.x_stride != 0);
   size_t off = 0;
   auto take = [&](size_t bytes) {
     const size_t at = off;
@@ -393,7 +399,8 @@ LinearPlan plan_linear(const ss_linear_desc_t& d, int op) {
     pl.bytes = off;
     return pl;
   }
-  pl.need_dpre = d.act != SS_ACT_NONE || d.out_dtype != d.in_dtype || d.out_dim % unit_of(d) != 0;
+  pl.need_dpre = d.act != SS_ACT_NONE || d.out_dtype != d.in_dtype ||
+                 (bf16 && d.out_dim % 8 != 0);
   // about 1024 blocks over the columns and row chunks, at least 16 rows each
   const int64_t span = 64 * dpre_vec(d), cols = (d.out_dim + span - 1) / span;
   int64_t chunks = (1024 + cols - 1) / cols;
@@ -444,7 +451,9 @@ int launch_linear_fwd(const ss_linear_desc_t& d, const void* x, const void* w, c
   p.R = ops.take(x, &p.ldr, d.rows, d.in_dim, ws + pl.off_x);
   p.S = ops.take(w, &p.lds, d.out_dim, d.in_dim, ws + pl.off_w);
   ops.launch(st);
-  run_mm(p, tiling(d, p.nR, p.nS, p.nT), true, true, ws + pl.off_part, st);
+  Tiling t = tiling(d, p.nR, p.nS, p.nT);
+  t.tile = ops.tile(t.tile);
+  run_mm(p, t, true, true, ws + pl.off_part, st);
   return int(hipGetLastError());
 }
 
@@ -500,7 +509,10 @@ int launch_linear_bwd(const ss_linear_desc_t& d, const LinearPlan& pl, const voi
   ops.launch(st);
   char* const part = ws + pl.off_part;
   // one gradient alone is computed as it is beside the other: the same sums
-  const Backward t = tilings_bwd(d);
+  if (!dpre && d.out_dim % unit_of(d) != 0) ops.any = true;     // dy in place (fp32)
+  Backward t = tilings_bwd(d);
+  t.dx.tile = ops.tile(t.dx.tile);
+  t.dw.tile = ops.tile(t.dw.tile);
   char* const part_dw = part + pl.off_part_dw;
   if (t.both && dx && dw) {
     px = tiled(px, t.dx, part);

@@ -135,19 +135,21 @@ __device__ __forceinline__ void read_tr8(const uint32_t (&a)[4], bf16x8 (&fa)[4]
   fb[3] = join8(u3, v3);
 }
 
-// Byte offsets of one wave-wide copy instruction (16-byte units id = (j waves +
-// wave) 64 + lane of the stage) from the tile's origin; kOutOfRange outside the
-// operand.  TC: rows of t (128 bytes).  W: columns of the stage; HALF: they are
-// columns 0..63 and 128..191 of the tile (an S half).  tpos: the unit's first t.
-template <typename T, bool TC, int W, bool HALF>
-__device__ __forceinline__ uint32_t copy_offset(int id, int64_t ld, int64_t i0, int64_t n,
+// Byte offsets of one wave-wide copy instruction (pieces (j waves + wave) 64 + lane of
+// the stage, BYTES each: 16-byte units, or their elements) from the tile's origin;
+// kOutOfRange outside the operand.  TC: rows of t (128 bytes).  W: columns of the
+// stage; HALF: they are columns 0..63 and 128..191 of the tile (an S half).  tpos: the
+// piece's first t.
+template <typename T, bool TC, int W, bool HALF, int BYTES = 16>
+__device__ __forceinline__ uint32_t copy_offset(int piece, int64_t ld, int64_t i0, int64_t n,
                                                 int* tpos) {
   constexpr int E = 16 / int(sizeof(T));
+  const int id = piece / (16 / BYTES), e = piece % (16 / BYTES);
   if constexpr (TC) {
     const int q = id / 8, c = (id & 7) ^ (q & 7);
     const int row = HALF ? (q & 63) + (q >> 6) * 128 : q;
-    *tpos = c * E;
-    return i0 + row < n ? uint32_t(row * ld * int(sizeof(T)) + c * 16) : kOutOfRange;
+    *tpos = c * E + e;
+    return i0 + row < n ? uint32_t((row * ld + c * E + e) * int(sizeof(T))) : kOutOfRange;
   } else {
     constexpr int per = W / E;
     const int t = id / per, c1 = id % per;
@@ -158,7 +160,7 @@ __device__ __forceinline__ uint32_t copy_offset(int id, int64_t ld, int64_t i0, 
     } else {
       c = c1 ^ (((t >> 2) & 3) << 2);
     }
-    const int col = HALF ? (c * E & 63) + (c * E >> 6) * 128 : c * E;
+    const int col = HALF ? (c * E & 63) + (c * E >> 6) * 128 : c * E + e;
     *tpos = t;
     return i0 + col < n ? uint32_t((t * ld + col) * int(sizeof(T))) : kOutOfRange;
   }
@@ -572,10 +574,14 @@ __device__ __forceinline__ f32x4 mma(u32x4 a, u32x4 b, f32x4 c) {
 // stages (16384 x 160 x 5120 with softplus: 85 us on 256 x 256 tiles, 71 on these, 95
 // with two buffers and two to a CU; 4096 rows: 33 and 20).  Its outputs are streamed
 // (4096 rows: 23 -> 21 us).
+// BYTES: of a lane's copy, 16, or 4 for fp32 operands that 16-byte units cannot read
+// (odd sizes, odd offsets): four times the instructions, beside fp32 MFMAs that leave
+// time for them, but no aligned copy first (3001 x 770 x 1537: 84 us with the copy, 78
+// so; 700 x 2561 x 513 34 and 28, its backward 55 and 45).
 // lds: kSmallLds<T, NB> bytes per group; block: the work item, a tile of a split.
 template <typename T, int NB> constexpr int kSmallLds = 2 * NB * kSmallTile<T> * 128;
 #if defined(__HIP_DEVICE_COMPILE__)
-template <typename T, bool RT, bool ST, int ACT, int G, int NB>
+template <typename T, bool RT, bool ST, int ACT, int G, int NB, int BYTES>
 __device__ __forceinline__ void mm_small_body(const MmParams& p, uint32_t block, char* lds) {
   constexpr int kSz = int(sizeof(T)), kT = 128 / kSz;
   constexpr int kTileS = kSmallTile<T>, kF = kTileS / 32;   // fragments of a wave per side
@@ -592,13 +598,14 @@ __device__ __forceinline__ void mm_small_body(const MmParams& p, uint32_t block,
   const int64_t r0 = tr * kTileS, s0 = int64_t(ts) * kTileS;
   const int64_t t0 = split * p.t_split;
   const int64_t t1 = t0 + p.t_split < p.nT ? t0 + p.t_split : p.nT;
-  uint32_t vr[kF], vs[kF];
-  int tpr[kF], tps[kF];
+  constexpr int kCopies = kOp / (256 * BYTES);              // of a wave, per operand
+  uint32_t vr[kCopies], vs[kCopies];
+  int tpr[kCopies], tps[kCopies];
 #pragma unroll
-  for (int j = 0; j < kF; ++j) {
+  for (int j = 0; j < kCopies; ++j) {
     const int id = (j * 4 + wv) * 64 + lane;
-    vr[j] = copy_offset<T, RT, kTileS, false>(id, p.ldr, r0, p.nR, &tpr[j]);
-    vs[j] = copy_offset<T, ST, kTileS, false>(id, p.lds, s0, p.nS, &tps[j]);
+    vr[j] = copy_offset<T, RT, kTileS, false, BYTES>(id, p.ldr, r0, p.nR, &tpr[j]);
+    vs[j] = copy_offset<T, ST, kTileS, false, BYTES>(id, p.lds, s0, p.nS, &tps[j]);
   }
   const int64_t dr = RT ? 128 : p.ldr * 128, ds = ST ? 128 : p.lds * 128;
   const int stages = int((t1 - t0 + kT - 1) / kT);
@@ -613,7 +620,7 @@ __device__ __forceinline__ void mm_small_body(const MmParams& p, uint32_t block,
   auto copy = [&](int k) {
     if (k0 + k == stages - 1 && rem < kT) {
 #pragma unroll
-      for (int j = 0; j < kF; ++j) {
+      for (int j = 0; j < kCopies; ++j) {
         vr[j] = tpr[j] < rem ? vr[j] : kOutOfRange;
         vs[j] = tps[j] < rem ? vs[j] : kOutOfRange;
       }
@@ -624,14 +631,15 @@ __device__ __forceinline__ void mm_small_body(const MmParams& p, uint32_t block,
                                                      short(0), range, 0x00020000);
     const Rsrc b = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(range ? ps + k * ds : ps),
                                                      short(0), range, 0x00020000);
-    char* d = mine + (NB == 2 ? (k & 1) * 2 * kOp : 0) + wv * 1024;
+    char* d = mine + (NB == 2 ? (k & 1) * 2 * kOp : 0) + wv * 64 * BYTES;
 #pragma unroll
-    for (int j = 0; j < kF; ++j)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(a, (lds_ptr)(d + j * 4096), 16, vr[j], 0, 0, 0);
+    for (int j = 0; j < kCopies; ++j)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(a, (lds_ptr)(d + j * 256 * BYTES), BYTES, vr[j], 0,
+                                               0, 0);
 #pragma unroll
-    for (int j = 0; j < kF; ++j)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(b, (lds_ptr)(d + kOp + j * 4096), 16, vs[j], 0, 0,
-                                               0);
+    for (int j = 0; j < kCopies; ++j)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(b, (lds_ptr)(d + kOp + j * 256 * BYTES), BYTES,
+                                               vs[j], 0, 0, 0);
   };
   const int wr = (wv >> 1) * (kTileS / 2), wsn = (wv & 1) * (kTileS / 2);
   // fragment addresses in buffer 0
@@ -763,25 +771,25 @@ __device__ __forceinline__ void mm_small_body(const MmParams& p, uint32_t block,
 }
 #endif
 
-template <typename T, bool RT, bool ST, int ACT, int G, int NB>
+template <typename T, bool RT, bool ST, int ACT, int G, int NB, int BYTES = 16>
 __global__ __launch_bounds__(kSmallThreads * G, NB == 1 ? 3 : 2) void mm_small_kernel(MmParams p) {
 #if defined(__HIP_DEVICE_COMPILE__)
   __shared__ __attribute__((aligned(1024))) char lds[kSmallLds<T, NB> * G];
-  mm_small_body<T, RT, ST, ACT, G, NB>(p, blockIdx.x, lds);
+  mm_small_body<T, RT, ST, ACT, G, NB, BYTES>(p, blockIdx.x, lds);
 #endif
 }
 
 // Both products of a backward pass, dx (R t contiguous) and dw (t strided), side by
 // side: each alone would leave half of the CUs' slots empty.
-template <typename T, int G>
+template <typename T, int G, int BYTES = 16>
 __global__ __launch_bounds__(kSmallThreads * G, 2) void mm_both_kernel(MmParams dx, MmParams dw) {
 #if defined(__HIP_DEVICE_COMPILE__)
   __shared__ __attribute__((aligned(1024))) char lds[kSmallLds<T, 2> * G];
   const uint32_t items = uint32_t(dw.tiles_r) * uint32_t(dw.tiles_s) * uint32_t(dw.splits);
   if (blockIdx.x < items)
-    mm_small_body<T, false, false, SS_ACT_NONE, G, 2>(dw, blockIdx.x, lds);
+    mm_small_body<T, false, false, SS_ACT_NONE, G, 2, BYTES>(dw, blockIdx.x, lds);
   else
-    mm_small_body<T, true, false, SS_ACT_NONE, G, 2>(dx, blockIdx.x - items, lds);
+    mm_small_body<T, true, false, SS_ACT_NONE, G, 2, BYTES>(dx, blockIdx.x - items, lds);
 #endif
 }
 
@@ -805,6 +813,9 @@ void run(const MmParams& p, MmTile tile, hipStream_t stream) {
     case MmTile::kSmallF32:
       mm_small_kernel<float, RT, ST, ACT, 1, 2><<<blocks, kSmallThreads, 0, stream>>>(p);
       break;
+    case MmTile::kSmallF32Any:
+      mm_small_kernel<float, RT, ST, ACT, 1, 2, 4><<<blocks, kSmallThreads, 0, stream>>>(p);
+      break;
   }
 }
 
@@ -822,8 +833,10 @@ void launch_mm_both(const MmParams& dx, const MmParams& dw, MmTile tile, int beh
     mm_both_kernel<uint16_t, 2><<<blocks, 2 * kSmallThreads, 0, stream>>>(dx, dw);
   else if (tile == MmTile::kSmall)
     mm_both_kernel<uint16_t, 1><<<blocks, kSmallThreads, 0, stream>>>(dx, dw);
-  else
+  else if (tile == MmTile::kSmallF32)
     mm_both_kernel<float, 1><<<blocks, kSmallThreads, 0, stream>>>(dx, dw);
+  else
+    mm_both_kernel<float, 1, 4><<<blocks, kSmallThreads, 0, stream>>>(dx, dw);
 }
 
 void launch_mm(const MmParams& p, MmTile tile, bool rt, bool st, hipStream_t stream) {

@@ -15,8 +15,10 @@ namespace ss {
 // unit is inside its storage, with zeros past the contraction's end where t is the
 // contiguous axis.
 // kSmallPair: 128 x 128 tiles by two groups of waves, at most one tile per CU.
+// kSmallF32Any: operands at any element address, of any row length; nothing past a row
+// is read.
 // kSmallSingle: 128 x 128 tiles, three to a CU, with one buffer each.
-enum class MmTile { kBig, kSmall, kSmallPair, kSmallSingle, kSmallF32 };
+enum class MmTile { kBig, kSmall, kSmallPair, kSmallSingle, kSmallF32, kSmallF32Any };
 void launch_mm(const MmParams& p, MmTile tile, bool rt, bool st, hipStream_t stream);
 // dx (rt, not st) and dw (neither) in one launch; not on kSmallSingle.  kBig: the
 // workgroups below `behind`, those that dw's last round reaches (0: it reaches all),
