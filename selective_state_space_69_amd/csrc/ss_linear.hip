@@ -156,9 +156,9 @@ int64_t pad_to_unit(const ss_linear_desc_t& d, int64_t n) {
 // How a product is tiled.  bf16: 128 x 128 tiles while all of them fit on the 256 CUs
 // at once, two to a CU (or one, of two wave groups that share its stages), and where
 // 256 x 256 ones would be mostly empty.  Beyond that, 256 x 256 tiles against 128 x
-// 128 ones three to a CU with one buffer each, whichever ends first: a large tile
+// 128 ones four to a CU with one buffer each, whichever ends first: a large tile
 // takes 1.25 us per stage of 128 bytes and 7 us around them with nothing beside it,
-// a small one 0.47 and 1 us of its CU, whose other tiles cover its waits.  Measured,
+// a small one 0.48 and 0.8 us of its CU, whose other tiles cover its waits.  Measured,
 // large and single-buffered tiles (bf16 out, us):
 //   contraction            160            320            640           1280
 //   16384 x 5120      66.8   64.8    77.0   79.5   111.5  127.4   185.0  217.6
@@ -222,7 +222,7 @@ Tiling tiling(const ss_linear_desc_t& d, int64_t nR, int64_t nS, int64_t nT) {
   if (p.bf16 && p.tiles > 512 && p.tiles * 100 > 282 * r256 * s256) {
     const int64_t rounds = (r256 * s256 + 255) / 256, per_cu = (p.tiles + 255) / 256;
     const double big = kLaunchUs + double(rounds) * big_us(p.stages);
-    const double single = kLaunchUs + double(per_cu) * (0.47 * double(p.stages) + 1.0);
+    const double single = kLaunchUs + double(per_cu) * (0.48 * double(p.stages) + 0.8);
     if (single < big) return p.tiling(MmTile::kSmallSingle, 1, single);
     return Tiling{MmTile::kBig, int32_t(r256), int32_t(s256), 1, nT, big};
   }

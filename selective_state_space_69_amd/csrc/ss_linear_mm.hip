@@ -202,8 +202,8 @@ __device__ __forceinline__ void fetch_bias(const MmParams& p, int32_t s, float (
 }
 
 // One piece of 16 rows x 16 F columns.  SPLIT: to a split's partial sums instead;
-// STREAM: past the caches.
-template <int ACT, bool SPLIT, bool STREAM, int F>
+// STREAM: past the caches; RES: with a residual perhaps.
+template <int ACT, bool SPLIT, bool STREAM, bool RES, int F>
 __device__ __forceinline__ void piece_out(const MmParams& p, char* sl, const f32x4 (&q)[F],
                                           const Piece<F>& at, const float (&bias)[8], int split) {
   const int lane = threadIdx.x & 63, m = lane & 15, g = lane >> 4;
@@ -212,7 +212,8 @@ __device__ __forceinline__ void piece_out(const MmParams& p, char* sl, const f32
     *reinterpret_cast<f32x4*>(sl + m * 256 + (((4 * i + g) ^ m) << 4)) = q[i];
   asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
   const int u = (lane % Piece<F>::kPer) * 2;
-  Res8 res = at.res[0];
+  Res8 res;
+  if constexpr (RES) res = at.res[0];
 #pragma nounroll
   for (int h = 0; h < Piece<F>::kPasses; ++h) {
     const int row = h * Piece<F>::kRows + lane / Piece<F>::kPer;
@@ -224,7 +225,7 @@ __device__ __forceinline__ void piece_out(const MmParams& p, char* sl, const f32
         const f32x4 y = *reinterpret_cast<const f32x4*>(sl + row * 256 + (((u + 1) ^ row) << 4));
         float v[8] = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
         if constexpr (SPLIT) store8(p.part, split * p.nR * p.nS + o, 0, v);
-        else epilogue8<ACT, STREAM>(p, o, v, bias, res);
+        else epilogue8<ACT, STREAM, RES>(p, o, v, bias, res);
       } else {
 #pragma nounroll
         for (int j = 0; s + j < p.nS; ++j) {
@@ -235,7 +236,7 @@ __device__ __forceinline__ void piece_out(const MmParams& p, char* sl, const f32
         }
       }
     }
-    if constexpr (Piece<F>::kPasses > 1) res = at.res[Piece<F>::kPasses - 1];
+    if constexpr (RES && Piece<F>::kPasses > 1) res = at.res[Piece<F>::kPasses - 1];
   }
   asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
 }
@@ -509,7 +510,7 @@ __device__ __forceinline__ void mm256_body(const MmParams& p0, const Turns& turn
       const int j = i / 2, c = i & 1;
       if (i < 7) next.fetch(p, r + 16 * ((i + 1) / 2), c0 + 64 * ((i + 1) & 1));
       const f32x4 q[4] = {acc[4 * c][j], acc[4 * c + 1][j], acc[4 * c + 2][j], acc[4 * c + 3][j]};
-      piece_out<ACT, false, true>(p, lds + kOffEpi + wv * 4096, q, now, bias[c], 0);
+      piece_out<ACT, false, true, true>(p, lds + kOffEpi + wv * 4096, q, now, bias[c], 0);
       now = next;
     }
     if (!more) return;
@@ -569,11 +570,14 @@ __device__ __forceinline__ f32x4 mma(u32x4 a, u32x4 b, f32x4 c) {
 // G = 2 (bf16): two such groups of 4 waves in a workgroup, each with its own buffers
 // and half of the stages, for problems with at most one tile per CU; their sums meet
 // in LDS and each group stores half of the tile.
-// NB = 1 (bf16): one buffer, so that three workgroups share a CU: while one waits for
+// NB = 1 (bf16): one buffer, so that four workgroups share a CU: while one waits for
 // its copies or runs its epilogue the others multiply, which pays where a tile has few
 // stages (16384 x 160 x 5120 with softplus: 85 us on 256 x 256 tiles, 71 on these, 95
 // with two buffers and two to a CU; 4096 rows: 33 and 20).  Its outputs are streamed
 // (4096 rows: 23 -> 21 us).
+// RES: with a residual perhaps; without, its registers leave room for a fourth
+// workgroup on a CU (the same with softplus 78 us with three and 73 with four, without
+// an activation 63 and 50).
 // BYTES: of a lane's copy, 16, or 4 for fp32 operands that 16-byte units cannot read
 // (odd sizes, odd offsets): four times the instructions, beside fp32 MFMAs that leave
 // time for them, but no aligned copy first (3001 x 770 x 1537: 84 us with the copy, 78
@@ -581,7 +585,7 @@ __device__ __forceinline__ f32x4 mma(u32x4 a, u32x4 b, f32x4 c) {
 // lds: kSmallLds<T, NB> bytes per group; block: the work item, a tile of a split.
 template <typename T, int NB> constexpr int kSmallLds = 2 * NB * kSmallTile<T> * 128;
 #if defined(__HIP_DEVICE_COMPILE__)
-template <typename T, bool RT, bool ST, int ACT, int G, int NB, int BYTES>
+template <typename T, bool RT, bool ST, int ACT, int G, int NB, int BYTES, bool RES>
 __device__ __forceinline__ void mm_small_body(const MmParams& p, uint32_t block, char* lds) {
   constexpr int kSz = int(sizeof(T)), kT = 128 / kSz;
   constexpr int kTileS = kSmallTile<T>, kF = kTileS / 32;   // fragments of a wave per side
@@ -753,7 +757,8 @@ __device__ __forceinline__ void mm_small_body(const MmParams& p, uint32_t block,
   Piece<kF> now, next;
   float bias[8];
   fetch_bias(p, c + (lane % Piece<kF>::kPer) * 8, bias);
-  if (p.splits == 1) now.fetch(p, r, c);
+  if (RES && p.splits == 1) now.fetch(p, r, c);
+  else now.place(p, r, c);
 #pragma unroll
   for (int j = 0; j < kOut; ++j) {
     f32x4 q[kF];
@@ -761,21 +766,26 @@ __device__ __forceinline__ void mm_small_body(const MmParams& p, uint32_t block,
     for (int i = 0; i < kF; ++i) q[i] = sum[i][j];
     if (p.splits > 1) {
       now.place(p, r + 16 * j, c);
-      piece_out<ACT, true, false>(p, sl, q, now, bias, split);
+      piece_out<ACT, true, false, true>(p, sl, q, now, bias, split);
     } else {
-      if (j + 1 < kOut) next.fetch(p, r + 16 * (j + 1), c);
-      piece_out<ACT, false, NB == 1>(p, sl, q, now, bias, 0);
+      if constexpr (RES) {
+        if (j + 1 < kOut) next.fetch(p, r + 16 * (j + 1), c);
+      } else {
+        next.place(p, r + 16 * (j + 1), c);
+      }
+      piece_out<ACT, false, NB == 1, RES>(p, sl, q, now, bias, 0);
       now = next;
     }
   }
 }
 #endif
 
-template <typename T, bool RT, bool ST, int ACT, int G, int NB, int BYTES = 16>
-__global__ __launch_bounds__(kSmallThreads * G, NB == 1 ? 3 : 2) void mm_small_kernel(MmParams p) {
+template <typename T, bool RT, bool ST, int ACT, int G, int NB, int BYTES = 16, bool RES = true>
+__global__ __launch_bounds__(kSmallThreads * G, NB == 1 ? (RES ? 3 : 4) : 2)
+void mm_small_kernel(MmParams p) {
 #if defined(__HIP_DEVICE_COMPILE__)
   __shared__ __attribute__((aligned(1024))) char lds[kSmallLds<T, NB> * G];
-  mm_small_body<T, RT, ST, ACT, G, NB, BYTES>(p, blockIdx.x, lds);
+  mm_small_body<T, RT, ST, ACT, G, NB, BYTES, RES>(p, blockIdx.x, lds);
 #endif
 }
 
@@ -787,9 +797,9 @@ __global__ __launch_bounds__(kSmallThreads * G, 2) void mm_both_kernel(MmParams 
   __shared__ __attribute__((aligned(1024))) char lds[kSmallLds<T, 2> * G];
   const uint32_t items = uint32_t(dw.tiles_r) * uint32_t(dw.tiles_s) * uint32_t(dw.splits);
   if (blockIdx.x < items)
-    mm_small_body<T, false, false, SS_ACT_NONE, G, 2, BYTES>(dw, blockIdx.x, lds);
+    mm_small_body<T, false, false, SS_ACT_NONE, G, 2, BYTES, false>(dw, blockIdx.x, lds);
   else
-    mm_small_body<T, true, false, SS_ACT_NONE, G, 2, BYTES>(dx, blockIdx.x - items, lds);
+    mm_small_body<T, true, false, SS_ACT_NONE, G, 2, BYTES, false>(dx, blockIdx.x - items, lds);
 #endif
 }
 
@@ -805,7 +815,11 @@ void run(const MmParams& p, MmTile tile, hipStream_t stream) {
       mm_small_kernel<uint16_t, RT, ST, ACT, 1, 2><<<blocks, kSmallThreads, 0, stream>>>(p);
       break;
     case MmTile::kSmallSingle:
-      mm_small_kernel<uint16_t, RT, ST, ACT, 1, 1><<<blocks, kSmallThreads, 0, stream>>>(p);
+      if (!p.res)
+        mm_small_kernel<uint16_t, RT, ST, ACT, 1, 1, 16, false>
+            <<<blocks, kSmallThreads, 0, stream>>>(p);
+      else if constexpr (RT && ST)
+        mm_small_kernel<uint16_t, RT, ST, ACT, 1, 1><<<blocks, kSmallThreads, 0, stream>>>(p);
       break;
     case MmTile::kSmallPair:
       mm_small_kernel<uint16_t, RT, ST, ACT, 2, 2><<<blocks, 2 * kSmallThreads, 0, stream>>>(p);

@@ -17,7 +17,7 @@ namespace ss {
 // kSmallPair: 128 x 128 tiles by two groups of waves, at most one tile per CU.
 // kSmallF32Any: operands at any element address, of any row length; nothing past a row
 // is read.
-// kSmallSingle: 128 x 128 tiles, three to a CU, with one buffer each.
+// kSmallSingle: 128 x 128 tiles, four to a CU (three with a residual), with one buffer each.
 enum class MmTile { kBig, kSmall, kSmallPair, kSmallSingle, kSmallF32, kSmallF32Any };
 void launch_mm(const MmParams& p, MmTile tile, bool rt, bool st, hipStream_t stream);
 // dx (rt, not st) and dw (neither) in one launch; not on kSmallSingle.  kBig: the
@@ -110,7 +110,7 @@ __device__ __forceinline__ Res8 fetch_res8(const MmParams& p, int64_t o, bool in
 // Eight neighbours of an output row from element o on, all inside it; bias: theirs (0
 // without one).  ACT: the activation, or kActOf for p.act.
 constexpr int kActOf = -1;
-template <int ACT, bool STREAM = false>
+template <int ACT, bool STREAM = false, bool RES = true>
 __device__ __forceinline__ void epilogue8(const MmParams& p, int64_t o, float (&v)[8],
                                           const float (&bias)[8], const Res8& res) {
   const int act = ACT == kActOf ? p.act : ACT;
@@ -121,7 +121,7 @@ __device__ __forceinline__ void epilogue8(const MmParams& p, int64_t o, float (&
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = apply_act(act, v[j]);
   }
-  if (p.res) {
+  if (RES && p.res) {
     if (p.res_bf16) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
