@@ -157,13 +157,14 @@ int64_t pad_to_unit(const ss_linear_desc_t& d, int64_t n) {
 // at once, two to a CU (or one, of two wave groups that share its stages), and where
 // 256 x 256 ones would be mostly empty.  Beyond that, 256 x 256 tiles against 128 x
 // 128 ones four to a CU with one buffer each, whichever ends first: a large tile
-// takes 1.25 us per stage of 128 bytes and 7 us around them with nothing beside it,
-// a small one 0.48 and 0.8 us of its CU, whose other tiles cover its waits.  Measured,
-// large and single-buffered tiles (bf16 out, us):
+// takes 0.75 to 1.45 us per stage of 128 bytes (the more CUs are busy the lower is the
+// clock) and 6.5 us around them with nothing beside it, a small one 0.46 and 0.9 us of
+// its CU, whose other tiles cover its waits.  Measured, large and single-buffered
+// tiles (bf16 out, us):
 //   contraction            160            320            640           1280
-//   16384 x 5120      66.8   64.8    77.0   79.5   111.5  127.4   185.0  217.6
-//   with softplus     85.0   70.8    96.0   89.2   128.4  130.9   198.5  226.8
-//   4096 x 5120       25.3   16.7    29.9   20.3    42.0   32.8    66.0   57.4
+//   16384 x 5120      67.6   51.8    80.7   72.3   116.1  115.4   188.0  203.6
+//   with softplus     85.8   62.1   100.7   83.9   137.3  127.0   207.7  217.4
+//   4096 x 5120       25.6   16.0    30.0   22.5    42.9   35.1    67.8   60.0
 // (small and double-buffered against large, contraction 2560: 2048 x 4096, 512 small
 // tiles, 45.9 and 53.6).
 // fp32: 64 x 64, of which five fit.  Where the tiles of a long contraction leave CUs
@@ -189,7 +190,8 @@ double stage_us(bool bf16, int64_t items) {
   const int64_t per_cu = (items + 255) / 256;
   return bf16 ? (per_cu > 1 ? 0.9 : 0.7) : (per_cu > 1 ? 0.5 * double(per_cu) : 0.7);
 }
-double big_us(int64_t stages) { return 1.25 * double(stages) + 7.0; }
+// a large tile, of a launch that fills the GPU
+double big_us(int64_t stages) { return 1.45 * double(stages) + 6.5; }
 // the join of k parts, their sums written and read
 double join_us(int64_t nR, int64_t nS, int64_t k) {
   return k > 1 ? 6.0 + double(k) * double(nR) * double(nS) * 8.0 / 4.0e6 : 0.0;
@@ -221,8 +223,9 @@ Tiling tiling(const ss_linear_desc_t& d, int64_t nR, int64_t nS, int64_t nT) {
   const Small p(d, nR, nS, nT);
   if (p.bf16 && p.tiles > 512 && p.tiles * 100 > 282 * r256 * s256) {
     const int64_t rounds = (r256 * s256 + 255) / 256, per_cu = (p.tiles + 255) / 256;
-    const double big = kLaunchUs + double(rounds) * big_us(p.stages);
-    const double single = kLaunchUs + double(per_cu) * (0.48 * double(p.stages) + 0.8);
+    const double fill = double(r256 * s256) / double(256 * rounds);
+    const double big = kLaunchUs + double(rounds) * ((0.75 + 0.7 * fill) * double(p.stages) + 6.5);
+    const double single = kLaunchUs + double(per_cu) * (0.46 * double(p.stages) + 0.9);
     if (single < big) return p.tiling(MmTile::kSmallSingle, 1, single);
     return Tiling{MmTile::kBig, int32_t(r256), int32_t(s256), 1, nT, big};
   }
@@ -255,13 +258,13 @@ struct Backward {
 Backward tilings_bwd(const ss_linear_desc_t& d) {
   const Small a(d, d.rows, d.in_dim, d.out_dim), b(d, d.out_dim, d.in_dim, d.rows);
   Backward t{tiling(d, a.nR, a.nS, a.nT), tiling(d, b.nR, b.nS, b.nT), false, 0, 0};
-  double best = t.dx.us + t.dw.us;
   auto longer = [](int64_t u, int64_t v) { return u > v ? u : v; };
   if (t.dx.tile == MmTile::kBig && t.dw.tile == MmTile::kBig) {
     const double ux = big_us(a.stages), uw = big_us(b.stages);
     const int64_t nx = int64_t(t.dx.tiles_r) * t.dx.tiles_s;
     const int64_t nw = int64_t(t.dw.tiles_r) * t.dw.tiles_s;
     const int64_t behind = nw % 256, rest = 256 - behind;
+    double best = 2.0 * kLaunchUs + double((nx + 255) / 256) * ux + double((nw + 255) / 256) * uw;
     for (int64_t few = 0; few <= nx / 256 && (few == 0 || behind); ++few) {
       const int64_t most = few + (nx - few * 256 + rest - 1) / rest;
       const double late = uw + double(few) * ux, early = double(most) * ux;
@@ -276,6 +279,7 @@ Backward tilings_bwd(const ss_linear_desc_t& d) {
     }
     return t;
   }
+  double best = t.dx.us + t.dw.us;
   for (int64_t i = 1; i <= 16 && i * 2 <= a.stages + 1; ++i)
     for (int64_t j = 1; j <= 64 && j * 2 <= b.stages + 1; ++j) {
       const int64_t items = i * a.tiles + j * b.tiles;

@@ -572,7 +572,7 @@ __device__ __forceinline__ f32x4 mma(u32x4 a, u32x4 b, f32x4 c) {
 // in LDS and each group stores half of the tile.
 // NB = 1 (bf16): one buffer, so that four workgroups share a CU: while one waits for
 // its copies or runs its epilogue the others multiply, which pays where a tile has few
-// stages (16384 x 160 x 5120 with softplus: 85 us on 256 x 256 tiles, 71 on these, 95
+// stages (16384 x 160 x 5120 with softplus: 86 us on 256 x 256 tiles, 62 on these, 95
 // with two buffers and two to a CU; 4096 rows: 33 and 20).  Its outputs are streamed
 // (4096 rows: 23 -> 21 us).
 // RES: with a residual perhaps; without, its registers leave room for a fourth

@@ -208,6 +208,7 @@ LINEAR = [
     # workgroups, and all of them
     (9003, 2950, 2901, "bf16", "bf16", "silu", True, None, 0, 0),
     (2600, 4090, 4080, "bf16", "bf16", "none", True, None, 0, 0),
+    (4090, 728, 4010, "bf16", "bf16", "gelu", True, "f32", 8, 0),
 ]
 
 
