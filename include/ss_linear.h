@@ -82,9 +82,11 @@ int ss_linear_fwd(const ss_linear_desc_t* desc, const void* x, const void* w, co
 /*
  * Backward.  w and dy required; pre required iff act is not SS_ACT_NONE (in
  * in_dtype); outputs dx, dw (grad_dtype) and dbias (float32) optional, at least
- * one, all overwritten; x required iff dw is asked for.  With bf16 operands,
- * dpre enters both products as bf16: exact for a bf16 dy without activation,
- * else rounded once (dbias is summed before that rounding).  No output may
+ * one, all overwritten; x required iff dw is asked for.  With bf16 operands a
+ * bf16 dy without activation enters both products as it is.  Any other dpre is
+ * float32, and grad_dtype says what the products see of it: bf16 gradients, its
+ * value rounded to bf16; float32 ones, the sum of two bf16 values (2^-16 of it),
+ * for twice the work.  dbias is summed before either rounding.  No output may
  * alias another argument.
  */
 int ss_linear_bwd(const ss_linear_desc_t* desc, const void* x, const void* w, const void* pre,

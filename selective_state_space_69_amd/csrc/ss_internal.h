@@ -237,14 +237,16 @@ int launch_ckpt_unpack(const ss_ckpt_desc_t& d, const int8_t* q, const uint8_t* 
 
 // Linear projections (ss_linear.hip).  Workspace, 256-byte aligned arrays:
 //   dpre : (M, N) in_dtype, dy act'(pre) (only with an activation, a dy of another
-//          type than the operands, or bf16 rows of dy that 16-byte loads cannot read)
+//          type than the operands, or bf16 rows of dy that 16-byte loads cannot read);
+//          sum2: as the sum of two bf16, 2 elements per value, where one cannot hold it
 //   x, w : (M, K), (N, K) bf16, rows copied to a 16-byte aligned stride where they
 //          cannot be read in place (fp32 always is); x: also the checkpoint's values
 //   sums : (chunks, N) fp32, dbias sums of chunk_rows rows
 //   part : fp32 partial products of split contractions (dx's and dw's in one place,
 //          or dw's off_part_dw bytes behind dx's where one launch computes both)
 struct LinearPlan {
-  bool need_dpre = false;
+  bool need_dpre = false, sum2 = false;
+  int64_t ld_dpre = 0;                 // elements from one row of dpre to the next
   int64_t chunk_rows = 1, chunks = 1;
   size_t off_dpre = 0, off_x = 0, off_w = 0, off_sums = 0, off_part = 0,
          off_part_dw = 0, bytes = 0;

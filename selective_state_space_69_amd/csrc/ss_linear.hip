@@ -76,14 +76,25 @@ __global__ __launch_bounds__(kThreads) void pad_kernel(PadParams q) {
 // 64 V columns (V neighbours per lane; 8 where every row of dy and pre is 16-byte
 // aligned) and a chunk of rows, a wave every fourth row of it, four at a time; the
 // waves' sums are added in order into one partial row per block.
+// What bf16 operands see of a dpre that is not bf16 goes by the gradients' type.  bf16
+// gradients: bf16(dpre), a second half step beside their own (errors of 2.3e-3 instead
+// of 1.7e-3 of a gradient, 2-norms).  fp32 gradients: sum2, each value as hi = bf16(v)
+// and lo = bf16(v - hi), 8 hi, then their 8 lo, exact to 2^-16 (2.5e-6; 1.7e-3 with hi
+// alone) for twice the products' MFMAs (bf16 4096 x 768 x 1536 with fp32 dy: 41 -> 60
+// us, 16384 x 2560 x 5120 768 -> 1434).
 struct DpreParams {
   const void* dy;
   const void* pre;
   void* d;            // or null
   float* part;        // (gridDim.y, N) or null
   int64_t M, rows;    // rows per block
-  int32_t N, ld, act;
+  int32_t N, ld, act, sum2;
 };
+// what bf16(v) leaves of v (0, not infinity less infinity, of what it makes infinite)
+__device__ __forceinline__ float rest_of(float v) {
+  const uint32_t hi = cvt_bf16x2(0.0f, v) & 0xffff0000u;
+  return (hi & 0x7f800000u) == 0x7f800000u ? 0.0f : v - __uint_as_float(hi);
+}
 template <typename T, int V>
 __device__ __forceinline__ void load_cols(const T* p, int c, int n, float (&v)[V]) {
   if constexpr (V == 8) {
@@ -126,7 +137,21 @@ __global__ __launch_bounds__(kThreads) void dpre_kernel(DpreParams p) {
         if constexpr (ACT != SS_ACT_NONE) v[i][j] *= act_grad(ACT, q[i][j]);
         sum[j] += v[i][j];
       }
-      if (p.d && c < p.ld) {
+      if (!p.d) continue;
+      if (sizeof(T) == 2 && p.sum2) {
+        if (2 * c >= p.ld) continue;
+        uint16_t* d = static_cast<uint16_t*>(p.d) + r * p.ld + (c >> 3) * 16 + (c & 7);
+        float lo[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) lo[j] = rest_of(v[i][j]);
+        if constexpr (V == 8) {
+          store8(d, 0, true, v[i]);
+          store8(d, 8, true, lo);
+        } else {
+          store_out<uint16_t>(d, v[i][0]);
+          store_out<uint16_t>(d + 8, lo[0]);
+        }
+      } else if (c < p.ld) {
         T* d = static_cast<T*>(p.d) + r * p.ld + c;
         if constexpr (V == 8) store8(d, 0, sizeof(T) == 2, v[i]);
         else store_out<T>(d, c < p.N ? v[i][0] : 0.0f);
@@ -201,10 +226,11 @@ double join_us(int64_t nR, int64_t nS, int64_t k) {
 struct Small {
   bool bf16;
   int64_t nR, nS, nT, step, tiles_r, tiles_s, tiles, stages, fit;
-  Small(const ss_linear_desc_t& d, int64_t r, int64_t s, int64_t t) : nR(r), nS(s), nT(t) {
+  Small(const ss_linear_desc_t& d, int64_t r, int64_t s, int64_t t, bool sum2)
+      : nR(r), nS(s), nT(t) {
     bf16 = d.in_dtype == SS_BF16;
     const int64_t side = bf16 ? 128 : 64;
-    step = bf16 ? 64 : 32;
+    step = bf16 && !sum2 ? 64 : 32;
     fit = bf16 ? 512 : 1024;
     tiles_r = (nR + side - 1) / side;
     tiles_s = (nS + side - 1) / side;
@@ -218,9 +244,9 @@ struct Small {
     return Tiling{tile, int32_t(tiles_r), int32_t(tiles_s), int32_t((nT + len - 1) / len), len, us};
   }
 };
-Tiling tiling(const ss_linear_desc_t& d, int64_t nR, int64_t nS, int64_t nT) {
+Tiling tiling(const ss_linear_desc_t& d, int64_t nR, int64_t nS, int64_t nT, bool sum2) {
   const int64_t r256 = (nR + 255) / 256, s256 = (nS + 255) / 256;
-  const Small p(d, nR, nS, nT);
+  const Small p(d, nR, nS, nT, sum2);
   if (p.bf16 && p.tiles > 512 && p.tiles * 100 > 282 * r256 * s256) {
     const int64_t rounds = (r256 * s256 + 255) / 256, per_cu = (p.tiles + 255) / 256;
     const double fill = double(r256 * s256) / double(256 * rounds);
@@ -255,9 +281,9 @@ struct Backward {
   bool both;
   int behind, few;
 };
-Backward tilings_bwd(const ss_linear_desc_t& d) {
-  const Small a(d, d.rows, d.in_dim, d.out_dim), b(d, d.out_dim, d.in_dim, d.rows);
-  Backward t{tiling(d, a.nR, a.nS, a.nT), tiling(d, b.nR, b.nS, b.nT), false, 0, 0};
+Backward tilings_bwd(const ss_linear_desc_t& d, bool sum2) {
+  const Small a(d, d.rows, d.in_dim, d.out_dim, sum2), b(d, d.out_dim, d.in_dim, d.rows, sum2);
+  Backward t{tiling(d, a.nR, a.nS, a.nT, sum2), tiling(d, b.nR, b.nS, b.nT, sum2), false, 0, 0};
   auto longer = [](int64_t u, int64_t v) { return u > v ? u : v; };
   if (t.dx.tile == MmTile::kBig && t.dw.tile == MmTile::kBig) {
     const double ux = big_us(a.stages), uw = big_us(b.stages);
@@ -319,9 +345,10 @@ void join(const MmParams& p, hipStream_t stream) {
   const int64_t n = (p.nR * ((p.nS + 7) / 8) + kThreads - 1) / kThreads;
   join_kernel<<<unsigned(n < kMaxBlocks ? n : kMaxBlocks), kThreads, 0, stream>>>(p);
 }
-void run_mm(MmParams p, const Tiling& t, bool rt, bool st, char* part, hipStream_t stream) {
+void run_mm(MmParams p, const Tiling& t, bool rt, bool st, bool sum2, char* part,
+            hipStream_t stream) {
   p = tiled(p, t, part);
-  launch_mm(p, t.tile, rt, st, stream);
+  launch_mm(p, t.tile, rt, st, sum2, stream);
   join(p, stream);
 }
 
@@ -399,12 +426,16 @@ LinearPlan plan_linear(const ss_linear_desc_t& d, int op) {
     if (d.rows <= kRowsMax) return pl;
     if (pad_x) pl.off_x = take(x_bytes);
     if (pad_k) pl.off_w = take(w_bytes);
-    pl.off_part = take(part_bytes(tiling(d, d.rows, d.out_dim, d.in_dim), d.rows, d.out_dim));
+    pl.off_part =
+        take(part_bytes(tiling(d, d.rows, d.out_dim, d.in_dim, false), d.rows, d.out_dim));
     pl.bytes = off;
     return pl;
   }
   pl.need_dpre = d.act != SS_ACT_NONE || d.out_dtype != d.in_dtype ||
                  (bf16 && d.out_dim % 8 != 0);
+  pl.sum2 = bf16 && d.grad_dtype == SS_F32 &&
+            (d.act != SS_ACT_NONE || d.out_dtype != SS_BF16);
+  pl.ld_dpre = pad_to_unit(d, d.out_dim) * (pl.sum2 ? 2 : 1);
   // about 1024 blocks over the columns and row chunks, at least 16 rows each
   const int64_t span = 64 * dpre_vec(d), cols = (d.out_dim + span - 1) / span;
   int64_t chunks = (1024 + cols - 1) / cols;
@@ -413,12 +444,12 @@ LinearPlan plan_linear(const ss_linear_desc_t& d, int op) {
   pl.chunk_rows = (d.rows + chunks - 1) / chunks;
   pl.chunks = (d.rows + pl.chunk_rows - 1) / pl.chunk_rows;
   if (pl.need_dpre)
-    pl.off_dpre = take(align256(size_t(d.rows) * size_t(pad_to_unit(d, d.out_dim)) * esize));
+    pl.off_dpre = take(align256(size_t(d.rows) * size_t(pl.ld_dpre) * esize));
   if (op == SS_LINEAR_BWD_CKPT || pad_x) pl.off_x = take(x_bytes);
   if (pad_k) pl.off_w = take(w_bytes);
   pl.off_sums = take(align256(size_t(pl.chunks) * size_t(d.out_dim) * 4));
   // dx's and dw's parts: one after the other in one place, or side by side
-  const Backward t = tilings_bwd(d);
+  const Backward t = tilings_bwd(d, pl.sum2);
   const size_t a = part_bytes(t.dx, d.rows, d.in_dim), b = part_bytes(t.dw, d.out_dim, d.in_dim);
   pl.off_part_dw = t.both ? a : 0;
   pl.off_part = take(t.both ? a + b : a > b ? a : b);
@@ -455,9 +486,9 @@ int launch_linear_fwd(const ss_linear_desc_t& d, const void* x, const void* w, c
   p.R = ops.take(x, &p.ldr, d.rows, d.in_dim, ws + pl.off_x);
   p.S = ops.take(w, &p.lds, d.out_dim, d.in_dim, ws + pl.off_w);
   ops.launch(st);
-  Tiling t = tiling(d, p.nR, p.nS, p.nT);
+  Tiling t = tiling(d, p.nR, p.nS, p.nT, false);
   t.tile = ops.tile(t.tile);
-  run_mm(p, t, true, true, ws + pl.off_part, st);
+  run_mm(p, t, true, true, false, ws + pl.off_part, st);
   return int(hipGetLastError());
 }
 
@@ -469,9 +500,10 @@ int launch_linear_bwd(const ss_linear_desc_t& d, const LinearPlan& pl, const voi
   if (dbias || dpre) {
     DpreParams p{dy, pre, dpre ? ws + pl.off_dpre : nullptr,
                  dbias ? reinterpret_cast<float*>(ws + pl.off_sums) : nullptr, d.rows,
-                 pl.chunk_rows, int32_t(d.out_dim), int32_t(pad_to_unit(d, d.out_dim)), d.act};
+                 pl.chunk_rows, int32_t(d.out_dim), int32_t(pl.ld_dpre), d.act, pl.sum2};
     const int v = dpre_vec(d);
-    const dim3 grid(unsigned((p.ld + 64 * v - 1) / (64 * v)), unsigned(pl.chunks));
+    const int64_t cols = pad_to_unit(d, d.out_dim);
+    const dim3 grid(unsigned((cols + 64 * v - 1) / (64 * v)), unsigned(pl.chunks));
     if (v == 8) dpre_types<8>(d, p, grid, st);
     else dpre_types<1>(d, p, grid, st);
     if (dbias)
@@ -479,7 +511,7 @@ int launch_linear_bwd(const ss_linear_desc_t& d, const LinearPlan& pl, const voi
   }
   MmParams p{};
   p.R = dpre ? static_cast<const void*>(ws + pl.off_dpre) : dy;
-  p.ldr = pl.need_dpre ? pad_to_unit(d, d.out_dim) : d.out_dim;
+  p.ldr = pl.need_dpre ? pl.ld_dpre : d.out_dim;
   p.nS = int32_t(d.in_dim);
   p.act = SS_ACT_NONE;
   p.out_bf16 = d.grad_dtype == SS_BF16;
@@ -514,19 +546,19 @@ int launch_linear_bwd(const ss_linear_desc_t& d, const LinearPlan& pl, const voi
   char* const part = ws + pl.off_part;
   // one gradient alone is computed as it is beside the other: the same sums
   if (!dpre && d.out_dim % unit_of(d) != 0) ops.any = true;     // dy in place (fp32)
-  Backward t = tilings_bwd(d);
+  Backward t = tilings_bwd(d, pl.sum2);
   t.dx.tile = ops.tile(t.dx.tile);
   t.dw.tile = ops.tile(t.dw.tile);
   char* const part_dw = part + pl.off_part_dw;
   if (t.both && dx && dw) {
     px = tiled(px, t.dx, part);
     pw = tiled(pw, t.dw, part_dw);
-    launch_mm_both(px, pw, t.dx.tile, t.behind, t.few, st);
+    launch_mm_both(px, pw, t.dx.tile, t.behind, t.few, pl.sum2, st);
     join(px, st);
     join(pw, st);
   } else {
-    if (dx) run_mm(px, t.dx, true, false, part, st);
-    if (dw) run_mm(pw, t.dw, false, false, part_dw, st);
+    if (dx) run_mm(px, t.dx, true, false, pl.sum2, part, st);
+    if (dw) run_mm(pw, t.dw, false, false, pl.sum2, part_dw, st);
   }
   return int(hipGetLastError());
 }

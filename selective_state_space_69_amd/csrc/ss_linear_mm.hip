@@ -29,6 +29,13 @@
 //                   a fragment is two transposing 8-byte reads per lane
 //                   (ds_read_b64_tr_b16: 16 lanes read 4 rows of 16 and each
 //                   receives one column).
+// SUM2 (backward products, R not exact in bf16): R's values are sums of two bf16, hi =
+// bf16(v) and lo = bf16(v - hi), a unit of 8 neighbours' hi followed by the unit of
+// their lo.  A stage then holds 32 of the contraction: positions 16 j .. + 7 are hi and
+// 16 j + 8 .. + 15 lo of the values 8 j .. + 7, and S's rows of these come twice.  The
+// sums are those of R with 16 bits at twice the MFMAs; only the copies' source
+// addresses differ.
+//
 // The transposing reads are written in assembly, with their wait in the same
 // block: before the builtin the compiler waits for every copy in flight.
 //
@@ -46,7 +53,7 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) void* lds_ptr;
 
 constexpr int kTile = 256;
-constexpr int kStep = 64;                          // t per stage
+template <bool SUM2> constexpr int kStep = SUM2 ? 32 : 64;     // t per stage
 constexpr int kThreads = 512;
 constexpr unsigned kCUs = 256;
 // dx's tiles beside dw's: the workgroups below `behind` take `few` of them each
@@ -139,8 +146,9 @@ __device__ __forceinline__ void read_tr8(const uint32_t (&a)[4], bf16x8 (&fa)[4]
 // the stage, BYTES each: 16-byte units, or their elements) from the tile's origin;
 // kOutOfRange outside the operand.  TC: rows of t (128 bytes).  W: columns of the
 // stage; HALF: they are columns 0..63 and 128..191 of the tile (an S half).  tpos: the
-// piece's first t.
-template <typename T, bool TC, int W, bool HALF, int BYTES = 16>
+// piece's first t.  SUM: kPlain, or which operand of sums of two bf16 it is.
+enum { kPlain, kSums, kFactors };
+template <typename T, bool TC, int W, bool HALF, int SUM, int BYTES = 16>
 __device__ __forceinline__ uint32_t copy_offset(int piece, int64_t ld, int64_t i0, int64_t n,
                                                 int* tpos) {
   constexpr int E = 16 / int(sizeof(T));
@@ -148,7 +156,7 @@ __device__ __forceinline__ uint32_t copy_offset(int piece, int64_t ld, int64_t i
   if constexpr (TC) {
     const int q = id / 8, c = (id & 7) ^ (q & 7);
     const int row = HALF ? (q & 63) + (q >> 6) * 128 : q;
-    *tpos = c * E + e;
+    *tpos = (SUM == kPlain ? c : c >> 1) * E + e;
     return i0 + row < n ? uint32_t((row * ld + c * E + e) * int(sizeof(T))) : kOutOfRange;
   } else {
     constexpr int per = W / E;
@@ -161,8 +169,10 @@ __device__ __forceinline__ uint32_t copy_offset(int piece, int64_t ld, int64_t i
       c = c1 ^ (((t >> 2) & 3) << 2);
     }
     const int col = HALF ? (c * E & 63) + (c * E >> 6) * 128 : c * E + e;
-    *tpos = t;
-    return i0 + col < n ? uint32_t((t * ld + col) * int(sizeof(T))) : kOutOfRange;
+    const int at = SUM == kPlain ? t : ((t >> 4) << 3) | (t & 7);
+    const int place = SUM == kSums ? 2 * col + (t & 8) : col;
+    *tpos = at;
+    return i0 + col < n ? uint32_t((at * ld + place) * int(sizeof(T))) : kOutOfRange;
   }
 }
 
@@ -288,7 +298,7 @@ __device__ __forceinline__ T reread_params() {
 }
 
 // AT: where p0 is among the kernel's parameters
-template <bool RT, bool ST, int ACT, int AT, typename Turns>
+template <bool RT, bool ST, int ACT, bool SUM2, int AT, typename Turns>
 __device__ __forceinline__ void mm256_body(const MmParams& p0, const Turns& turn, char* lds) {
   const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int m = lane & 15, g = lane >> 4;
@@ -296,27 +306,29 @@ __device__ __forceinline__ void mm256_body(const MmParams& p0, const Turns& turn
   uint32_t vr[4], vlo[2], vhi[2];
   int tpr[4], tps[2];
   const char *pr, *ps, *psh;
+  constexpr int kR = SUM2 ? kSums : kPlain, kS = SUM2 ? kFactors : kPlain;
+  constexpr int kT = kStep<SUM2>;
   auto place = [&](const MmParams& p, int64_t tr, int ts) {
     r0 = tr * kTile;
     s0 = int64_t(ts) * kTile;
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      vr[j] = copy_offset<uint16_t, RT, 256, false>((j * 8 + wv) * 64 + lane, p.ldr, r0, p.nR,
-                                                    &tpr[j]);
+      vr[j] = copy_offset<uint16_t, RT, 256, false, kR>((j * 8 + wv) * 64 + lane, p.ldr, r0, p.nR,
+                                                        &tpr[j]);
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const int id = (j * 8 + wv) * 64 + lane;
-      vlo[j] = copy_offset<uint16_t, ST, 128, true>(id, p.lds, s0, p.nS, &tps[j]);
-      vhi[j] = copy_offset<uint16_t, ST, 128, true>(id, p.lds, s0 + 64, p.nS, &tps[j]);
+      vlo[j] = copy_offset<uint16_t, ST, 128, true, kS>(id, p.lds, s0, p.nS, &tps[j]);
+      vhi[j] = copy_offset<uint16_t, ST, 128, true, kS>(id, p.lds, s0 + 64, p.nS, &tps[j]);
     }
-    pr = static_cast<const char*>(p.R) + (RT ? r0 * p.ldr : r0) * 2;
+    pr = static_cast<const char*>(p.R) + (RT ? r0 * p.ldr : SUM2 ? 2 * r0 : r0) * 2;
     ps = static_cast<const char*>(p.S) + (ST ? s0 * p.lds : s0) * 2;
     psh = ps + (ST ? 64 * p.lds : 64) * 2;
   };
-  const int64_t dr = RT ? kStep * 2 : p0.ldr * kStep * 2;
-  const int64_t ds = ST ? kStep * 2 : p0.lds * kStep * 2;
-  const int nk = int((p0.nT + kStep - 1) / kStep);
-  const int rem = int(p0.nT - int64_t(nk - 1) * kStep);      // t of the last stage, 1..64
+  const int64_t dr = RT ? 128 : p0.ldr * kT * 2;
+  const int64_t ds = ST ? 128 : p0.lds * kT * 2;
+  const int nk = int((p0.nT + kT - 1) / kT);
+  const int rem = int(p0.nT - int64_t(nk - 1) * kT);         // t of the last stage, 1..kT
 
   // resource of a stage k that starts at base; past the last one no byte is in range
   auto rsrc = [&](const char* base, int k) {
@@ -328,7 +340,7 @@ __device__ __forceinline__ void mm256_body(const MmParams& p0, const Turns& turn
   };
   // a partial last stage: units past the contraction's end read as zero (the empty
   // asm keeps this a branch, taken once: as selects it cost each stage 12 of them)
-  const bool partial = rem < kStep;
+  const bool partial = rem < kT;
   auto mask_all = [&](int k) {
     if (partial && k == nk - 1) {
       asm volatile("");
@@ -518,11 +530,11 @@ __device__ __forceinline__ void mm256_body(const MmParams& p0, const Turns& turn
 }
 #endif
 
-template <bool RT, bool ST, int ACT>
+template <bool RT, bool ST, int ACT, bool SUM2>
 __global__ __launch_bounds__(kThreads, 2) void mm256_kernel(MmParams p) {
 #if defined(__HIP_DEVICE_COMPILE__)
   __shared__ __attribute__((aligned(1024))) char lds[kLds];
-  mm256_body<RT, ST, ACT, 0>(p, EveryRound{}, lds);
+  mm256_body<RT, ST, ACT, SUM2, 0>(p, EveryRound{}, lds);
 #endif
 }
 
@@ -530,13 +542,15 @@ __global__ __launch_bounds__(kThreads, 2) void mm256_kernel(MmParams p) {
 // reach every workgroup, then dx's (16384 rows, 5120 -> 2560: 750 us one after the
 // other, where dw's 200 tiles leave 56 CUs idle, 708 together; 2560 -> 5120 from a
 // checkpoint 757 and 686).
+template <bool SUM2>
 __global__ __launch_bounds__(kThreads, 2) void mm256_both_kernel(MmParams dw, MmParams, Behind) {
 #if defined(__HIP_DEVICE_COMPILE__)
   __shared__ __attribute__((aligned(1024))) char lds[kLds];
   constexpr int kDx = int(sizeof(MmParams)), kTurns = 2 * kDx;
-  mm256_body<false, false, SS_ACT_NONE, 0>(dw, EveryRound{}, lds);
+  mm256_body<false, false, SS_ACT_NONE, SUM2, 0>(dw, EveryRound{}, lds);
   const MmParams dx = reread_params<MmParams, kDx>();
-  mm256_body<true, false, SS_ACT_NONE, kDx>(dx, BehindOthers{reread_params<Behind, kTurns>()}, lds);
+  mm256_body<true, false, SS_ACT_NONE, SUM2, kDx>(
+      dx, BehindOthers{reread_params<Behind, kTurns>()}, lds);
 #endif
 }
 
@@ -585,9 +599,11 @@ __device__ __forceinline__ f32x4 mma(u32x4 a, u32x4 b, f32x4 c) {
 // lds: kSmallLds<T, NB> bytes per group; block: the work item, a tile of a split.
 template <typename T, int NB> constexpr int kSmallLds = 2 * NB * kSmallTile<T> * 128;
 #if defined(__HIP_DEVICE_COMPILE__)
-template <typename T, bool RT, bool ST, int ACT, int G, int NB, int BYTES, bool RES>
+template <typename T, bool RT, bool ST, int ACT, int G, int NB, int BYTES, bool RES, bool SUM2>
 __device__ __forceinline__ void mm_small_body(const MmParams& p, uint32_t block, char* lds) {
-  constexpr int kSz = int(sizeof(T)), kT = 128 / kSz;
+  constexpr int kSz = int(sizeof(T)), kT = 128 / kSz / (SUM2 ? 2 : 1);
+  constexpr int kR = SUM2 ? kSums : kPlain, kS = SUM2 ? kFactors : kPlain;
+  constexpr int kWide = SUM2 ? 2 : 1;                       // elements per value of R
   constexpr int kTileS = kSmallTile<T>, kF = kTileS / 32;   // fragments of a wave per side
   constexpr int kOp = kTileS * 128;                         // bytes of an operand's stage
   constexpr int kCols = kTileS * kSz;                       // bytes of a t-strided row
@@ -608,16 +624,16 @@ __device__ __forceinline__ void mm_small_body(const MmParams& p, uint32_t block,
 #pragma unroll
   for (int j = 0; j < kCopies; ++j) {
     const int id = (j * 4 + wv) * 64 + lane;
-    vr[j] = copy_offset<T, RT, kTileS, false, BYTES>(id, p.ldr, r0, p.nR, &tpr[j]);
-    vs[j] = copy_offset<T, ST, kTileS, false, BYTES>(id, p.lds, s0, p.nS, &tps[j]);
+    vr[j] = copy_offset<T, RT, kTileS, false, kR, BYTES>(id, p.ldr, r0, p.nR, &tpr[j]);
+    vs[j] = copy_offset<T, ST, kTileS, false, kS, BYTES>(id, p.lds, s0, p.nS, &tps[j]);
   }
-  const int64_t dr = RT ? 128 : p.ldr * 128, ds = ST ? 128 : p.lds * 128;
+  const int64_t dr = RT ? 128 : p.ldr * kT * kSz, ds = ST ? 128 : p.lds * kT * kSz;
   const int stages = int((t1 - t0 + kT - 1) / kT);
   const int rem = int(t1 - t0 - int64_t(stages - 1) * kT);
   // the group's stages: nk of them (the walk's length, for both groups) from k0 on
   const int nk = G == 1 ? stages : (stages + 1) / 2, k0 = grp * nk;
   const char* pr = static_cast<const char*>(p.R) +
-                   (RT ? r0 * p.ldr + t0 : t0 * p.ldr + r0) * kSz + k0 * dr;
+                   (RT ? r0 * p.ldr + t0 * kWide : t0 * p.ldr + r0 * kWide) * kSz + k0 * dr;
   const char* ps = static_cast<const char*>(p.S) +
                    (ST ? s0 * p.lds + t0 : t0 * p.lds + s0) * kSz + k0 * ds;
   char* const mine = lds + grp * 4 * kOp;
@@ -780,55 +796,61 @@ __device__ __forceinline__ void mm_small_body(const MmParams& p, uint32_t block,
 }
 #endif
 
-template <typename T, bool RT, bool ST, int ACT, int G, int NB, int BYTES = 16, bool RES = true>
+template <typename T, bool RT, bool ST, int ACT, int G, int NB, int BYTES = 16, bool RES = true,
+          bool SUM2 = false>
 __global__ __launch_bounds__(kSmallThreads * G, NB == 1 ? (RES ? 3 : 4) : 2)
 void mm_small_kernel(MmParams p) {
 #if defined(__HIP_DEVICE_COMPILE__)
   __shared__ __attribute__((aligned(1024))) char lds[kSmallLds<T, NB> * G];
-  mm_small_body<T, RT, ST, ACT, G, NB, BYTES, RES>(p, blockIdx.x, lds);
+  mm_small_body<T, RT, ST, ACT, G, NB, BYTES, RES, SUM2>(p, blockIdx.x, lds);
 #endif
 }
 
 // Both products of a backward pass, dx (R t contiguous) and dw (t strided), side by
 // side: each alone would leave half of the CUs' slots empty.
-template <typename T, int G, int BYTES = 16>
+template <typename T, int G, int BYTES = 16, bool SUM2 = false>
 __global__ __launch_bounds__(kSmallThreads * G, 2) void mm_both_kernel(MmParams dx, MmParams dw) {
 #if defined(__HIP_DEVICE_COMPILE__)
   __shared__ __attribute__((aligned(1024))) char lds[kSmallLds<T, 2> * G];
   const uint32_t items = uint32_t(dw.tiles_r) * uint32_t(dw.tiles_s) * uint32_t(dw.splits);
   if (blockIdx.x < items)
-    mm_small_body<T, false, false, SS_ACT_NONE, G, 2, BYTES, false>(dw, blockIdx.x, lds);
+    mm_small_body<T, false, false, SS_ACT_NONE, G, 2, BYTES, false, SUM2>(dw, blockIdx.x, lds);
   else
-    mm_small_body<T, true, false, SS_ACT_NONE, G, 2, BYTES, false>(dx, blockIdx.x - items, lds);
+    mm_small_body<T, true, false, SS_ACT_NONE, G, 2, BYTES, false, SUM2>(dx, blockIdx.x - items,
+                                                                         lds);
 #endif
 }
 
-template <bool RT, bool ST, int ACT>
+template <bool RT, bool ST, int ACT, bool SUM2 = false>
 void run(const MmParams& p, MmTile tile, hipStream_t stream) {
   const unsigned blocks = unsigned(p.tiles_r) * unsigned(p.tiles_s) * unsigned(p.splits);
   switch (tile) {
     case MmTile::kBig:
-      mm256_kernel<RT, ST, ACT>
+      mm256_kernel<RT, ST, ACT, SUM2>
           <<<blocks < kCUs ? blocks : kCUs, kThreads, 0, stream>>>(p);
       break;
     case MmTile::kSmall:
-      mm_small_kernel<uint16_t, RT, ST, ACT, 1, 2><<<blocks, kSmallThreads, 0, stream>>>(p);
+      mm_small_kernel<uint16_t, RT, ST, ACT, 1, 2, 16, true, SUM2>
+          <<<blocks, kSmallThreads, 0, stream>>>(p);
       break;
     case MmTile::kSmallSingle:
       if (!p.res)
-        mm_small_kernel<uint16_t, RT, ST, ACT, 1, 1, 16, false>
+        mm_small_kernel<uint16_t, RT, ST, ACT, 1, 1, 16, false, SUM2>
             <<<blocks, kSmallThreads, 0, stream>>>(p);
       else if constexpr (RT && ST)
         mm_small_kernel<uint16_t, RT, ST, ACT, 1, 1><<<blocks, kSmallThreads, 0, stream>>>(p);
       break;
     case MmTile::kSmallPair:
-      mm_small_kernel<uint16_t, RT, ST, ACT, 2, 2><<<blocks, 2 * kSmallThreads, 0, stream>>>(p);
+      mm_small_kernel<uint16_t, RT, ST, ACT, 2, 2, 16, true, SUM2>
+          <<<blocks, 2 * kSmallThreads, 0, stream>>>(p);
       break;
     case MmTile::kSmallF32:
-      mm_small_kernel<float, RT, ST, ACT, 1, 2><<<blocks, kSmallThreads, 0, stream>>>(p);
+      if constexpr (!SUM2)
+        mm_small_kernel<float, RT, ST, ACT, 1, 2><<<blocks, kSmallThreads, 0, stream>>>(p);
       break;
     case MmTile::kSmallF32Any:
-      mm_small_kernel<float, RT, ST, ACT, 1, 2, 4><<<blocks, kSmallThreads, 0, stream>>>(p);
+      if constexpr (!SUM2)
+        mm_small_kernel<float, RT, ST, ACT, 1, 2, 4><<<blocks, kSmallThreads, 0, stream>>>(p);
       break;
   }
 }
@@ -836,14 +858,19 @@ void run(const MmParams& p, MmTile tile, hipStream_t stream) {
 }  // namespace
 
 void launch_mm_both(const MmParams& dx, const MmParams& dw, MmTile tile, int behind, int few,
-                    hipStream_t stream) {
+                    bool sum2, hipStream_t stream) {
   if (tile == MmTile::kBig) {
-    mm256_both_kernel<<<kCUs, kThreads, 0, stream>>>(dw, dx, Behind{behind, few});
+    if (sum2) mm256_both_kernel<true><<<kCUs, kThreads, 0, stream>>>(dw, dx, Behind{behind, few});
+    else mm256_both_kernel<false><<<kCUs, kThreads, 0, stream>>>(dw, dx, Behind{behind, few});
     return;
   }
   const unsigned blocks = unsigned(dx.tiles_r) * unsigned(dx.tiles_s) * unsigned(dx.splits) +
                           unsigned(dw.tiles_r) * unsigned(dw.tiles_s) * unsigned(dw.splits);
-  if (tile == MmTile::kSmallPair)
+  if (tile == MmTile::kSmallPair && sum2)
+    mm_both_kernel<uint16_t, 2, 16, true><<<blocks, 2 * kSmallThreads, 0, stream>>>(dx, dw);
+  else if (tile == MmTile::kSmall && sum2)
+    mm_both_kernel<uint16_t, 1, 16, true><<<blocks, kSmallThreads, 0, stream>>>(dx, dw);
+  else if (tile == MmTile::kSmallPair)
     mm_both_kernel<uint16_t, 2><<<blocks, 2 * kSmallThreads, 0, stream>>>(dx, dw);
   else if (tile == MmTile::kSmall)
     mm_both_kernel<uint16_t, 1><<<blocks, kSmallThreads, 0, stream>>>(dx, dw);
@@ -853,7 +880,7 @@ void launch_mm_both(const MmParams& dx, const MmParams& dw, MmTile tile, int beh
     mm_both_kernel<float, 1, 4><<<blocks, kSmallThreads, 0, stream>>>(dx, dw);
 }
 
-void launch_mm(const MmParams& p, MmTile tile, bool rt, bool st, hipStream_t stream) {
+void launch_mm(const MmParams& p, MmTile tile, bool rt, bool st, bool sum2, hipStream_t stream) {
   if (rt && st) {
     // splits leave the activation to the join
     switch (p.splits > 1 ? int(SS_ACT_NONE) : p.act) {
@@ -863,7 +890,9 @@ void launch_mm(const MmParams& p, MmTile tile, bool rt, bool st, hipStream_t str
       default: return run<true, true, SS_ACT_NONE>(p, tile, stream);
     }
   }
-  if (rt) run<true, false, SS_ACT_NONE>(p, tile, stream);
+  if (rt && sum2) run<true, false, SS_ACT_NONE, true>(p, tile, stream);
+  else if (sum2) run<false, false, SS_ACT_NONE, true>(p, tile, stream);
+  else if (rt) run<true, false, SS_ACT_NONE>(p, tile, stream);
   else run<false, false, SS_ACT_NONE>(p, tile, stream);
 }
 

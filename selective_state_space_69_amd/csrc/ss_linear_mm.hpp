@@ -19,12 +19,13 @@ namespace ss {
 // is read.
 // kSmallSingle: 128 x 128 tiles, four to a CU (three with a residual), with one buffer each.
 enum class MmTile { kBig, kSmall, kSmallPair, kSmallSingle, kSmallF32, kSmallF32Any };
-void launch_mm(const MmParams& p, MmTile tile, bool rt, bool st, hipStream_t stream);
+// sum2 (bf16, not with rt and st): R's values are sums of two bf16.
+void launch_mm(const MmParams& p, MmTile tile, bool rt, bool st, bool sum2, hipStream_t stream);
 // dx (rt, not st) and dw (neither) in one launch; not on kSmallSingle.  kBig: the
 // workgroups below `behind`, those that dw's last round reaches (0: it reaches all),
 // take `few` of dx's tiles each, the others the rest.
 void launch_mm_both(const MmParams& dx, const MmParams& dw, MmTile tile, int behind, int few,
-                    hipStream_t stream);
+                    bool sum2, hipStream_t stream);
 
 // O = R S^T for at most kRowsMax rows of R (t contiguous in both), with the
 // epilogue; vec: both operands' rows are 16-byte aligned and nT is a whole number

@@ -1,0 +1,155 @@
+"""Precision of the operators around the scan where sums are long or operands are
+narrower than what they are multiplied with, against 64-bit forms of the same
+inputs.  The bounds count rounding steps of the order in which the kernels add."""
+import pytest
+import torch
+
+from selective_state_space_69_amd import binding as B
+import block_ref as ref
+from block_ref import DT, U, check
+from gpu_util import log
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.fail("no GPU visible")
+    B.load_library()
+    yield
+    torch.cuda.synchronize()
+
+
+def rand(seed, *shape, dtype=torch.float32, scale=1.0, offset=0.0):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return (torch.randn(*shape, generator=g, device="cuda") * scale + offset).to(dtype)
+
+
+# ---------------------------------------- fp32 gradients of bf16 operands
+# hi = bf16(v) is off by at most 2^-8 |v|, what is left of v is exact in fp32, and lo,
+# its bf16, is off by at most 2^-8 of that: the products see v to 2^-16 |v|.
+SUM2 = 2.0 ** -16
+
+
+def bwd_fp32(x, w, dy, pre, name):
+    """(dx, dw, tol_dx, tol_dw), float64: twice the terms of a plain contraction
+    (hi and lo), of sizes that add up to at most (1 + 2^-7) |v|."""
+    d = dy.double()
+    err = torch.zeros_like(d)
+    if name != "none":
+        p = pre.double()
+        d = d * ref.act_grad(name, p)
+        err = U * (8 + 4 * p.abs() + 2 * p * p) * dy.double().abs()    # act' and the product
+    err = err + SUM2 * (d.abs() + err)
+    a = (1 + 2.0 ** -7) * (d.abs() + err)
+    xd, wd = x.double(), w.double()
+    n, m = w.shape[0], x.shape[0]
+    tol_dx = err @ wd.abs() + U * ref.sum_depth(2 * n, w.dtype) * (a @ wd.abs())
+    tol_dw = err.t() @ xd.abs() + U * ref.sum_depth(2 * m, w.dtype) * (a.t() @ xd.abs())
+    return d @ wd, d.t() @ xd, tol_dx, tol_dw
+
+
+FP32_GRADS = [
+    # M, K, N, dy, act, extra columns of x, checkpoint
+    (1, 1, 1, "f32", "none", 0, False),
+    (1, 64, 40, "bf16", "silu", 0, False),
+    (3, 33, 5, "f32", "gelu", 0, False),
+    (17, 40, 7, "f32", "none", 0, True),
+    (31, 72, 31, "bf16", "softplus", 0, False),
+    (32, 96, 33, "f32", "none", 32, False),
+    (33, 136, 16, "f32", "silu", 3, False),
+    (64, 520, 129, "bf16", "gelu", 0, True),
+    (100, 773, 251, "f32", "none", 0, False),
+    (129, 128, 128, "bf16", "silu", 8, False),
+    (300, 1000, 72, "f32", "softplus", 0, True),
+    (520, 4072, 4060, "f32", "none", 0, False),
+    (1003, 264, 520, "bf16", "gelu", 0, False),
+    (1500, 768, 1536, "f32", "none", 0, False),
+    (5003, 768, 1536, "bf16", "silu", 0, False),
+    (3001, 770, 1537, "f32", "gelu", 0, False),
+    # many rows over few columns, and dx over a contraction of few values
+    (40000, 24, 48, "f32", "none", 0, False),
+    (8190, 2560, 44, "bf16", "softplus", 32, False),
+    (8190, 4090, 37, "f32", "silu", 0, False),
+    # 256 x 256 tiles: dx alone, dw alone, both in one launch (the last round of dw
+    # reaching some and all of the workgroups, partial last stages)
+    (4060, 4072, 520, "f32", "none", 0, False),
+    (2600, 4090, 4080, "bf16", "silu", 0, False),
+    (9003, 2950, 2901, "f32", "none", 0, True),
+    (4096, 4096, 4096, "f32", "softplus", 0, False),
+]
+
+
+@pytest.mark.parametrize("case", FP32_GRADS, ids=lambda c: "m%d_k%d_n%d_%s_%s_x%d_q%d" % c)
+def test_fp32_gradients_of_bf16_operands(case):
+    """dpre past an activation or from an fp32 dy is not cut to bf16 before the
+    products of fp32 gradients."""
+    log("fp32 gradients", case)
+    m, k, n, td, name, extra, packed = case
+    sd = 300 + 10 * FP32_GRADS.index(case)
+    x = rand(sd, m, k + extra, dtype=torch.bfloat16, offset=0.1)[:, :k]
+    w = rand(sd + 1, n, k, dtype=torch.bfloat16, scale=k ** -0.5)
+    dy = rand(sd + 2, m, n, dtype=DT[td])
+    pre = rand(sd + 3, m, n, dtype=torch.bfloat16, scale=2.0) if name != "none" else None
+    xin = x
+    if packed:
+        xin = B.ckpt_pack(x)
+        x = B.ckpt_unpack(*xin)
+    got = B.linear_bwd(xin, w, dy, pre=pre, act=name, bias=True, grad_dtype=torch.float32)
+    torch.cuda.synchronize()
+    dx, dw, tx, tw = bwd_fp32(x, w, dy, pre, name)
+    check(got["dx"], dx, tx, "dx")
+    check(got["dw"], dw, tw, "dw")
+    one = B.linear_bwd(xin, w, dy, pre=pre, act=name, grad_dtype=torch.float32, need_dx=False)
+    assert torch.equal(one["dw"], got["dw"])
+    one = B.linear_bwd(None, w, dy, pre=pre, act=name, grad_dtype=torch.float32, need_dw=False)
+    assert torch.equal(one["dx"], got["dx"])
+
+
+@pytest.mark.parametrize("n", [64, 37])
+def test_fp32_gradients_nonfinite_and_extreme_dy(n):
+    """An infinite dy gives infinite gradients (not NaN), NaN stays in its row and
+    column, the smallest and largest dy keep their values."""
+    m, k = 70, 48
+    w = rand(20, n, k).abs().add(0.5).bfloat16()
+    x = rand(21, m, k).abs().add(0.5).bfloat16()
+    dy = rand(22, m, n)
+    clean = B.linear_bwd(x, w, dy, grad_dtype=torch.float32)
+    dy[5, 3] = float("inf")
+    dy[9, 7] = float("nan")
+    got = B.linear_bwd(x, w, dy, grad_dtype=torch.float32)
+    torch.cuda.synchronize()
+    assert bool((got["dx"][5] == float("inf")).all()) and bool(torch.isnan(got["dx"][9]).all())
+    assert bool((got["dw"][3] == float("inf")).all()) and bool(torch.isnan(got["dw"][7]).all())
+    rows = [i for i in range(m) if i not in (5, 9)]
+    cols = [i for i in range(n) if i not in (3, 7)]
+    assert torch.equal(got["dx"][rows], clean["dx"][rows])
+    assert torch.equal(got["dw"][cols], clean["dw"][cols])
+    one = torch.ones(1, 8, dtype=torch.bfloat16, device="cuda")
+    for v in (3.38e38, 1.2345678e-30, -7.654321e30, 0.0):
+        dx = B.linear_bwd(None, one, torch.full((4, 1), v, device="cuda"), need_dw=False,
+                          grad_dtype=torch.float32)["dx"].double()
+        assert bool(((dx - v).abs() <= SUM2 * abs(v)).all()), v
+
+
+def test_fp32_gradients_in_a_graph():
+    """Captured, replayed three times over changed inputs: the eager bits."""
+    x, w = rand(30, 300, 264, dtype=torch.bfloat16), rand(31, 136, 264, dtype=torch.bfloat16)
+    dy, pre = rand(32, 300, 136), rand(33, 300, 136, dtype=torch.bfloat16)
+
+    def call():
+        return B.linear_bwd(x, w, dy, pre=pre, act="silu", bias=True, grad_dtype=torch.float32)
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = call()
+    for i in range(3):
+        dy.copy_(rand(40 + i, 300, 136))
+        graph.replay()
+        torch.cuda.synchronize()
+        want = call()
+        for key in want:
+            assert torch.equal(out[key], want[key]), key
