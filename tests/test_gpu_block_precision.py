@@ -153,3 +153,37 @@ def test_fp32_gradients_in_a_graph():
         want = call()
         for key in want:
             assert torch.equal(out[key], want[key]), key
+
+
+# --------------------------------------------------------- long column sums
+def dbias_depth(m, n):
+    """Additions on the longest way of a term into dbias: a lane's run of 64 rows and
+    its runs (a wave takes every fourth row of a chunk), three waves, a sixteenth of
+    the chunks, 16 sums."""
+    span = 64 * (8 if n % 8 == 0 else 1)
+    cols = -(-n // span)
+    chunks = min(-(-1024 // cols), -(-m // 16))
+    rows = -(-m // chunks)
+    chunks = -(-m // rows)
+    lane = -(-rows // 4)
+    return min(lane, 64) + -(-lane // 64) + 3 + -(-chunks // 16) + 16
+
+
+@pytest.mark.parametrize("m,n", [(1, 7), (33, 1025), (5003, 1536), (70001, 120), (16384, 50281),
+                                 (1 << 20, 1025), (1 << 18, 2049), (1 << 18, 2048)])
+def test_dbias_of_many_rows(m, n):
+    """Terms of one sign and nearly one size, whose roundings add up: the sum stays
+    within the additions on its way, at odd widths as at others, and no chunk of
+    rows is missing."""
+    assert dbias_depth(m, n) < 300
+    col = torch.linspace(0.05, 0.15, n, device="cuda")
+    dy = torch.empty(m, n, device="cuda")
+    dy.copy_(col)
+    dy[m // 3] = 1.0
+    w = torch.zeros(n, 8, device="cuda")
+    db = B.linear_bwd(None, w, dy, bias=True, need_dx=False, need_dw=False)["dbias"]
+    torch.cuda.synchronize()
+    want = (m - 1) * col.double() + 1.0
+    bad = (db.double() - want).abs() / want
+    log("dbias", m, n, "%.3g of the sum, bound %.3g" % (float(bad.max()), dbias_depth(m, n) * U))
+    assert bool((bad <= dbias_depth(m, n) * U).all())
