@@ -187,3 +187,40 @@ def test_dbias_of_many_rows(m, n):
     bad = (db.double() - want).abs() / want
     log("dbias", m, n, "%.3g of the sum, bound %.3g" % (float(bad.max()), dbias_depth(m, n) * U))
     assert bool((bad <= dbias_depth(m, n) * U).all())
+
+
+def norm_depth(rows, dim):
+    """Additions on the longest way of a term into dweight or dbias: a run of 64 rows of
+    one of 512 blocks' groups (64 partial rows past 8192 columns) and its runs, the
+    groups, a sixteenth of the partial rows, 16 sums."""
+    if dim > 8192:
+        parts, groups = min(rows, 64), 1
+        lane = -(-rows // parts)
+    else:
+        waves = -(-dim // 512)
+        groups = 8 // waves if waves < 8 else 1
+        parts = min(-(-rows // groups), 512)
+        lane = -(-rows // (parts * groups))
+    return min(lane, 64) + -(-lane // 64) + groups + -(-parts // 16) + 16
+
+
+@pytest.mark.parametrize("rows,dim", [(1, 9), (100, 9001), (1100, 520), (1 << 19, 4096),
+                                      (1 << 20, 773), (200000, 8200), (300000, 40)])
+def test_norm_column_sums_of_many_rows(rows, dim):
+    """Terms of one sign and nearly one size, whose roundings add up: dweight and dbias
+    stay within the additions on their way, and no row is missing."""
+    assert norm_depth(rows, dim) < 250
+    col = torch.linspace(0.05, 0.15, dim, device="cuda")
+    dy = torch.empty(rows, dim, device="cuda")
+    dy.copy_(col)
+    dy[rows // 3] = 1.0
+    s = torch.zeros(rows, dim, dtype=torch.bfloat16, device="cuda")
+    mean = torch.full((rows,), -1.0, device="cuda")
+    g = B.layernorm_bwd(s, dy, mean, torch.ones(rows, device="cuda"), dx_dtype=torch.bfloat16)
+    torch.cuda.synchronize()
+    want = (rows - 1) * col.double() + 1.0                # xh = 1: dweight is dbias
+    for key in ("dweight", "dbias"):
+        bad = (g[key].double() - want).abs() / want
+        log("norm", key, rows, dim, "%.3g of the sum, bound %.3g" % (
+            float(bad.max()), norm_depth(rows, dim) * U))
+        assert bool((bad <= norm_depth(rows, dim) * U).all()), key
