@@ -189,6 +189,21 @@ def test_dbias_of_many_rows(m, n):
     assert bool((bad <= dbias_depth(m, n) * U).all())
 
 
+@pytest.mark.parametrize("m,n", [(1 << 20, 2049), (1 << 20, 2304)])
+def test_dbias_past_2_31(m, n):
+    """Past 2^31 elements of dy, a chunk of rows in a thousand of the sum."""
+    col = torch.linspace(0.05, 0.15, n, device="cuda").bfloat16()
+    dy = torch.empty(m, n, dtype=torch.bfloat16, device="cuda")
+    dy.copy_(col)
+    w = torch.zeros(n, 8, dtype=torch.bfloat16, device="cuda")
+    db = B.linear_bwd(None, w, dy, bias=True, need_dx=False, need_dw=False)["dbias"]
+    torch.cuda.synchronize()
+    want = m * col.double()
+    bad = (db.double() - want).abs() / want
+    assert dbias_depth(m, n) * U < 1e-3 / 16
+    assert bool((bad <= dbias_depth(m, n) * U).all())
+
+
 def norm_depth(rows, dim):
     """Additions on the longest way of a term into dweight or dbias: a run of 64 rows of
     one of 512 blocks' groups (64 partial rows past 8192 columns) and its runs, the
@@ -205,7 +220,8 @@ def norm_depth(rows, dim):
 
 
 @pytest.mark.parametrize("rows,dim", [(1, 9), (100, 9001), (1100, 520), (1 << 19, 4096),
-                                      (1 << 20, 773), (200000, 8200), (300000, 40)])
+                                      (1 << 20, 773), (200000, 8200), (300000, 40),
+                                      (1 << 20, 2304)])
 def test_norm_column_sums_of_many_rows(rows, dim):
     """Terms of one sign and nearly one size, whose roundings add up: dweight and dbias
     stay within the additions on their way, and no row is missing."""
@@ -224,3 +240,134 @@ def test_norm_column_sums_of_many_rows(rows, dim):
         log("norm", key, rows, dim, "%.3g of the sum, bound %.3g" % (
             float(bad.max()), norm_depth(rows, dim) * U))
         assert bool((bad <= norm_depth(rows, dim) * U).all()), key
+
+
+# ------------------------------------- rows past 8192 columns, many to a block
+def wide_norm_inputs(rows, dim, ti, tr, to, seed):
+    x = rand(seed, rows, dim, dtype=DT[ti], offset=0.5)
+    r = rand(seed + 1, rows, dim, dtype=DT[tr], scale=2.0, offset=-3.0)
+    w, b = rand(seed + 2, dim, scale=0.3, offset=1.0), rand(seed + 3, dim)
+    return x, r, w, b, rand(seed + 4, rows, dim, dtype=DT[to])
+
+
+@pytest.mark.parametrize("with_dsum", [True, False])
+@pytest.mark.parametrize("rows,dim,ti,tr,to", [
+    (700, 8200, "bf16", "f32", "bf16"), (1100, 9001, "f32", "bf16", "bf16"),
+    (1030, 16384, "bf16", "bf16", "f32"), (65, 12345, "bf16", "f32", "f32"),
+    (1537, 8193, "f32", "f32", "f32"), (600, 32768, "bf16", "f32", "bf16")])
+def test_norm_wide_rows(rows, dim, ti, tr, to, with_dsum):
+    """More rows than the 512 blocks of the backward and the 64 partial rows of its
+    column sums, at even and odd widths."""
+    log("norm wide", rows, dim, ti, tr, to, with_dsum)
+    x, r, w, b, dy = wide_norm_inputs(rows, dim, ti, tr, to, 50 + rows)
+    got = B.layernorm_fwd(x, w, b, residual=r, eps=1e-3, out_dtype=DT[to], save_stats=True)
+    y, s, mean, rstd, ty, tm, ts = ref.norm_fwd(x, r, w, b, 0.0010000000474974513)
+    check(got["y"], y, ty, "y")
+    check(got["sum"], s, U * s.abs(), "sum")
+    check(got["mean"], mean, tm + U * mean.abs(), "mean")
+    check(got["rstd"], rstd, ts, "rstd")
+    del y, s, ty
+    ds = r if with_dsum else None
+    g = B.layernorm_bwd(x, dy, got["mean"], got["rstd"], w, dsum=ds, dx_dtype=DT[tr])
+    torch.cuda.synchronize()
+    dx, dw, db, tx = ref.norm_bwd(x, dy, got["mean"], got["rstd"], w, ds)[:4]
+    check(g["dx"], dx, tx, "dx")
+    xh = (x.double() - got["mean"].double()[:, None]) * got["rstd"].double()[:, None]
+    depth = (norm_depth(rows, dim) + 4) * U       # and the roundings of a term
+    check(g["dweight"], dw, depth * (dy.double() * xh).abs().sum(0), "dweight")
+    check(g["dbias"], db, depth * dy.double().abs().sum(0), "dbias")
+    again = B.layernorm_bwd(x, dy, got["mean"], got["rstd"], w, dsum=ds, dx_dtype=DT[tr])
+    for k in g:
+        assert torch.equal(g[k], again[k]), k
+
+
+@pytest.mark.parametrize("dim", [8200, 9001, 32767])
+def test_norm_wide_rows_in_place(dim):
+    """sum over residual and dx over dsum give the same bits."""
+    rows = 600
+    x, r, w, _, dy = wide_norm_inputs(rows, dim, "bf16", "f32", "bf16", 90)
+    want = B.layernorm_fwd(x, w, residual=r, out_dtype=torch.bfloat16, save_stats=True)
+    g = B.layernorm_bwd(want["sum"], dy, want["mean"], want["rstd"], w, dsum=r)
+    d = B.make_norm_desc(rows, dim)
+    rr, y = r.clone(), torch.empty_like(x)
+    assert B.ss_layernorm_fwd(d, x, rr, w, None, y, rr, None, None) == B.SS_OK
+    assert torch.equal(rr, want["sum"]) and torch.equal(y, want["y"])
+    d = B.make_norm_desc(rows, dim, in_dtype=B.SS_F32)
+    nb = B.ss_layernorm_workspace_bytes(d)
+    dx, dw, db = r.clone(), torch.empty(dim, device="cuda"), torch.empty(dim, device="cuda")
+    assert B.ss_layernorm_bwd(d, want["sum"], w, want["mean"], want["rstd"], dy, dx, dx, dw, db,
+                              B.workspace(nb, "cuda"), nb) == B.SS_OK
+    torch.cuda.synchronize()
+    assert torch.equal(dx, g["dx"])
+    assert torch.equal(dw, g["dweight"]) and torch.equal(db, g["dbias"])
+
+
+# --------------------------------------------------- a block in bf16, call by call
+def test_mamba_block_bf16():
+    """A Mamba block's calls in bf16 with its residual stream and the gradients behind
+    the scan and the conv in fp32: every norm and projection of it against its 64-bit
+    form on the inputs that the call in front of it gave."""
+    Bt, L, dm, di, N, R, K = 2, 150, 96, 192, 16, 12, 4
+    bf = torch.bfloat16
+    p = lambda seed, *s, **kw: rand(seed, *s, dtype=bf, **kw)
+    flat = lambda t: t.reshape(-1, t.shape[-1])
+    res, dout = rand(400, Bt, L, dm), rand(401, Bt, L, dm)
+    nw, nb = rand(402, dm, scale=0.2, offset=1.0), rand(403, dm, scale=0.1)
+    wi = p(404, 2 * di, dm, scale=dm ** -0.5)
+    cw, cb = rand(405, di, K, scale=0.5), rand(406, di, scale=0.1)
+    wx, wt = p(407, R + 2 * N, di, scale=di ** -0.5), p(408, di, R, scale=0.3)
+    wo = p(409, dm, di, scale=di ** -0.5)
+    A, D, tb = -torch.exp(0.5 * rand(410, di, N)), rand(411, di), rand(412, di, offset=-1.0)
+
+    def fwd(x, w, residual=None, out_dtype=None):
+        y = B.linear_fwd(x, w, residual=residual, out_dtype=out_dtype)
+        want, _, tol, _ = ref.linear_fwd(flat(x), w, None,
+                                         None if residual is None else flat(residual), "none")
+        check(flat(y), want, tol, "forward %s" % (tuple(w.shape),))
+        return y
+
+    def bwd(x, w, dy, gt):
+        g = B.linear_bwd(x, w, dy, bias=True, grad_dtype=gt)
+        x, dy = flat(x), flat(dy)
+        if gt == torch.float32:
+            dx, dw, tx, tw = bwd_fp32(x, w, dy, None, "none")
+        else:
+            dx, dw, _, tx, tw, _ = ref.linear_bwd(x, w, dy, None, "none")
+        check(flat(g["dx"]), dx, tx, "dx %s" % (tuple(w.shape),))
+        check(g["dw"], dw, tw, "dw %s" % (tuple(w.shape),))
+        d = dy.double()
+        check(g["dbias"], d.sum(0), dbias_depth(*d.shape) * U * d.abs().sum(0), "dbias")
+        return g
+
+    n = B.layernorm_fwd(res, nw, nb, out_dtype=bf, save_stats=True)
+    y, _, mean, rstd, ty, tm, ts = ref.norm_fwd(flat(res), None, nw, nb, 9.999999747378752e-06)
+    check(flat(n["y"]), y, ty, "norm")
+    check(n["mean"].view(-1), mean, tm + U * mean.abs(), "mean")
+    check(n["rstd"].view(-1), rstd, ts, "rstd")
+    xz = fwd(n["y"], wi)
+    xu, z = xz[..., :di].contiguous(), xz[..., di:].contiguous()
+    u = B.conv1d_fwd(xu, cw, cb)
+    xdb = fwd(u, wx)
+    Bm, Cm = xdb[..., R:R + N], xdb[..., R + N:]
+    delta = fwd(xdb[..., :R], wt)
+    y = B.scan_fwd(u, delta, A, Bm, Cm, D=D, delta_bias=tb, z=z, out_dtype=bf)
+    out = fwd(y, wo, residual=res, out_dtype=torch.float32)
+    assert out.dtype == torch.float32 and bool(torch.isfinite(out).all())
+
+    go = bwd(y, wo, dout, bf)
+    gs = B.scan_bwd(u, delta, A, Bm, Cm, go["dx"], D=D, delta_bias=tb, z=z)
+    f32 = torch.float32
+    gt = bwd(xdb[..., :R], wt, gs["ddelta"], f32)
+    gx = bwd(u, wx, torch.cat([gt["dx"], gs["dB"], gs["dC"]], dim=-1), f32)
+    gc = B.conv1d_bwd(xu, cw, gs["du"] + gx["dx"], cb)
+    gi = bwd(n["y"], wi, torch.cat([gc["dx"], gs["dz"]], dim=-1), f32)
+    gn = B.layernorm_bwd(res, gi["dx"], n["mean"], n["rstd"], nw, dsum=dout)
+    torch.cuda.synchronize()
+    dx, dw, db, tx = ref.norm_bwd(flat(res), flat(gi["dx"]), n["mean"].view(-1),
+                                  n["rstd"].view(-1), nw, flat(dout))[:4]
+    check(flat(gn["dx"]), dx, tx, "norm dx")
+    d = flat(gi["dx"]).double()
+    xh = (flat(res).double() - n["mean"].double().view(-1, 1)) * n["rstd"].double().view(-1, 1)
+    depth = (norm_depth(Bt * L, dm) + 4) * U
+    check(gn["dweight"], dw, depth * (d * xh).abs().sum(0), "norm dweight")
+    check(gn["dbias"], db, depth * d.abs().sum(0), "norm dbias")
