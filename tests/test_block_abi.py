@@ -332,3 +332,14 @@ def test_headers_name_every_constant():
     for name in ("SS_ACT_NONE", "SS_ACT_SILU", "SS_ACT_GELU", "SS_ACT_SOFTPLUS"):
         m = re.search(r"%s = (\d+)" % name, text)
         assert m and int(m.group(1)) == getattr(B, name)
+
+
+@pytest.mark.parametrize("n", [64, 61])
+def test_linear_workspace_of_fp32_gradients(n):
+    """Two bf16 values of dpre each, in whole units of eight columns, where bf16 cannot hold
+    it; none where dy is bf16 and reaches the products as it is."""
+    def need(**kw):
+        return B.ss_linear_workspace_bytes(linear_desc(rows=512, out_dim=n, **kw), B.SS_LINEAR_BWD)
+    for kw in (dict(act=B.SS_ACT_GELU), dict(out_dtype=F32)):
+        assert need(grad_dtype=F32, **kw) >= need(grad_dtype=BF, **kw) + 512 * 64 * 2, kw
+    assert need(grad_dtype=F32) == need(grad_dtype=BF)
