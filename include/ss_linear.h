@@ -86,8 +86,9 @@ int ss_linear_fwd(const ss_linear_desc_t* desc, const void* x, const void* w, co
  * bf16 dy without activation enters both products as it is.  Any other dpre is
  * float32, and grad_dtype says what the products see of it: bf16 gradients, its
  * value rounded to bf16; float32 ones, the sum of two bf16 values (2^-16 of it),
- * for twice the work.  dbias is summed before either rounding.  No output may
- * alias another argument.
+ * for twice the matrix work (a caller who wants float32 sums of a rounded dpre at
+ * the single price rounds dy to bf16 first).  dbias is summed before either
+ * rounding.  No output may alias another argument.
  */
 int ss_linear_bwd(const ss_linear_desc_t* desc, const void* x, const void* w, const void* pre,
                   const void* dy, void* dx, void* dw, float* dbias, void* workspace,

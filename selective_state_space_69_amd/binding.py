@@ -811,7 +811,9 @@ def linear_bwd(x, w, dy, pre=None, act="none", bias=False, grad_dtype=None, need
     8-bit checkpoint (q, e) from ckpt_pack (None when need_dw is false).  pre:
     the forward's pre-activation values, with an activation.  Returns a dict: dx
     (..., K) and dw (N, K) in grad_dtype (default w's), dbias (N) float32 when
-    bias is true; what is not asked for is None."""
+    bias is true; what is not asked for is None.  With bf16 operands and a dy that
+    is float32 or passes an activation, float32 gradients keep it to 2^-16 (twice
+    the matrix work), bf16 ones round it to bf16."""
     q, e = x if isinstance(x, tuple) else (None, None)
     x = None if isinstance(x, tuple) else x
     return _on_device(_linear_bwd, stream, (w, dy, x, q, e, pre), x, q, e, w, dy, pre, _ACT[act],

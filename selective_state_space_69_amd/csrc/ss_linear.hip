@@ -73,8 +73,8 @@ __global__ __launch_bounds__(kThreads) void pad_kernel(PadParams q) {
 
 // dpre = dy act'(pre) in the operand type (when asked for), in rows of ld elements
 // that are zero past N, and its column sums before that rounding.  A block takes
-// 64 V columns (V neighbours per lane; 8 where every row of dy and pre is 16-byte
-// aligned) and a chunk of rows, a wave every fourth row of it, four at a time; the
+// 64 V columns (V neighbours per lane; 8 where N is a whole number of 16-byte units,
+// of which bf16 ones are loaded as two halves) and a chunk of rows, a wave every fourth row of it, four at a time; the
 // waves' sums are added in order into one partial row per block.  A lane adds runs of 64
 // rows, then the runs, so that a column sum's rounding does not grow with the rows that
 // the column blocks leave to a chunk (2^20 rows of one value, 2049 columns, 8192 rows to
@@ -198,11 +198,11 @@ int64_t pad_to_unit(const ss_linear_desc_t& d, int64_t n) {
 // takes 0.75 to 1.45 us per stage of 128 bytes (the more CUs are busy the lower is the
 // clock) and 6.5 us around them with nothing beside it, a small one 0.46 and 0.9 us of
 // its CU, whose other tiles cover its waits.  Measured, large and single-buffered
-// tiles (bf16 out, us):
+// tiles (bf16 out, us of a call among 150 in a row, both kinds in turn):
 //   contraction            160            320            640           1280
-//   16384 x 5120      67.6   51.8    80.7   72.3   116.1  115.4   188.0  203.6
-//   with softplus     85.8   62.1   100.7   83.9   137.3  127.0   207.7  217.4
-//   4096 x 5120       25.6   16.0    30.0   22.5    42.9   35.1    67.8   60.0
+//   16384 x 5120      64.3   51.0    79.1   73.0   113.3  116.2   185.9  205.7
+//   with softplus     83.6   65.6    99.3   85.5   132.8  128.2   201.9  216.9
+//   4096 x 5120       24.7   16.0    29.9   20.9    42.5   34.5    66.3   60.1
 // (small and double-buffered against large, contraction 2560: 2048 x 4096, 512 small
 // tiles, 45.9 and 53.6).
 // fp32: 64 x 64, of which five fit.  Where the tiles of a long contraction leave CUs

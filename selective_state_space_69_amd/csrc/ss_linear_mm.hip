@@ -586,12 +586,13 @@ __device__ __forceinline__ f32x4 mma(u32x4 a, u32x4 b, f32x4 c) {
 // in LDS and each group stores half of the tile.
 // NB = 1 (bf16): one buffer, so that four workgroups share a CU: while one waits for
 // its copies or runs its epilogue the others multiply, which pays where a tile has few
-// stages (16384 x 160 x 5120 with softplus: 86 us on 256 x 256 tiles, 62 on these, 95
-// with two buffers and two to a CU; 4096 rows: 33 and 20).  Its outputs are streamed
-// (4096 rows: 23 -> 21 us).
+// stages (16384 x 160 x 5120 with softplus: 82 us on 256 x 256 tiles, 64 on these, 85
+// with two buffers and two to a CU; 4096 rows: 33, 20 and 25).  Its outputs are streamed
+// (4096 rows: 21 -> 20 us).
 // RES: with a residual perhaps; without, its registers leave room for a fourth
-// workgroup on a CU (the same with softplus 78 us with three and 73 with four, without
-// an activation 63 and 50).
+// workgroup on a CU (the same with softplus 72 us with three and 64 with four, without
+// an activation 57 and 51).  All of these are times of a call among 150 in a row, the
+// kinds in turn.
 // BYTES: of a lane's copy, 16, or 4 for fp32 operands that 16-byte units cannot read
 // (odd sizes, odd offsets): four times the instructions, beside fp32 MFMAs that leave
 // time for them, but no aligned copy first (3001 x 770 x 1537: 84 us with the copy, 78

@@ -13,7 +13,7 @@
 // is summed along with it and taken out too (a row of one value gives y = b).  A
 // row belongs to the fewest waves that hold it with one vector per thread (D <=
 // 8192; four vectors beyond).  Both are bound by memory: at 16384 x 2560 (bf16 x,
-// fp32 residual stream) the forward moves 5.2 TB/s (96 us), the backward 5.2 (115
+// fp32 residual stream) the forward moves 5.2 TB/s (96 us), the backward 5.3 (111
 // us, the sums of dw and db included); a large copy reaches 5.1.
 #include "ss_device.hpp"
 
