@@ -73,12 +73,12 @@ __global__ __launch_bounds__(kThreads) void pad_kernel(PadParams q) {
 
 // dpre = dy act'(pre) in the operand type (when asked for), in rows of ld elements
 // that are zero past N, and its column sums before that rounding.  A block takes
-// 64 V columns (V neighbours per lane; 8 where N is a whole number of 16-byte units,
-// of which bf16 ones are loaded as two halves) and a chunk of rows, a wave every fourth row of it, four at a time; the
-// waves' sums are added in order into one partial row per block.  A lane adds runs of 64
-// rows, then the runs, so that a column sum's rounding does not grow with the rows that
-// the column blocks leave to a chunk (2^20 rows of one value, 2049 columns, 8192 rows to
-// a lane: 6.5e-5 off in one chain, 1.0e-6 so; no slower).
+// 64 V columns (V neighbours per lane; 8 where N is a whole number of 16-byte units, of
+// which bf16 ones are loaded as two halves) and a chunk of rows, a wave every fourth row
+// of it, four at a time; the waves' sums are added in order into one partial row per
+// block.  A lane adds runs of 64 rows, then the runs, so that a column sum's rounding does
+// not grow with the rows that the column blocks leave to a chunk (2^20 rows of one value,
+// 2049 columns, 8192 rows to a lane: 6.5e-5 off in one chain, 1.0e-6 so; no slower).
 // What bf16 operands see of a dpre that is not bf16 goes by the gradients' type.  bf16
 // gradients: bf16(dpre), a second half step beside their own (errors of 2.3e-3 instead
 // of 1.7e-3 of a gradient, 2-norms).  fp32 gradients: sum2, each value as hi = bf16(v)
