@@ -1,18 +1,18 @@
 """Thin ctypes binding of libssscan.so (C ABI declared in include/ss_scan.h,
-include/ss_conv.h, include/ss_ssd.h, include/ss_norm.h, include/ss_linear.h and
-include/ss_ckpt.h).
+include/ss_conv.h, include/ss_ssd.h, include/ss_norm.h, include/ss_linear.h,
+include/ss_ckpt.h and include/ss_rec.h).
 
 The functions named like the C entry points (ss_scan_fwd, ss_scan_fwd_noalloc, ss_scan_fwd_dir,
 ss_scan_fwd_complex, ss_scan_fwd_complex_ws, ss_scan_bwd, ss_scan_step, ss_scan_step_complex, ss_scan_workspace_bytes, ss_scan_strerror, ss_scan_version,
 ss_conv1d_fwd, ss_conv1d_bwd, ss_conv1d_step, ss_conv1d_workspace_bytes, ss_ssd_fwd,
 ss_ssd_fwd_state, ss_ssd_step, ss_layernorm_fwd, ss_layernorm_bwd, ss_layernorm_workspace_bytes,
 ss_linear_fwd, ss_linear_bwd, ss_linear_bwd_ckpt, ss_linear_workspace_bytes, ss_ckpt_pack,
-ss_ckpt_unpack) only
+ss_ckpt_unpack, ss_rec_fwd, ss_rec_bwd, ss_rec_step, ss_rec_workspace_bytes) only
 marshal arguments: torch tensors become device pointers, None becomes NULL and
 the stream defaults to torch's current HIP stream.  Every step runs in the HIP
 kernels; there is no fallback.  The convenience wrappers scan_fwd, scan_bwd,
-scan_bidir, scan_fwd_complex, scan_step, scan_step_complex, conv1d_fwd, conv1d_bwd, conv1d_step, ssd_fwd, ssd_step, layernorm_fwd, layernorm_bwd, linear_fwd, linear_bwd, ckpt_pack
-and ckpt_unpack additionally allocate outputs and workspace with torch.
+scan_bidir, scan_fwd_complex, scan_step, scan_step_complex, conv1d_fwd, conv1d_bwd, conv1d_step, ssd_fwd, ssd_step, layernorm_fwd, layernorm_bwd, linear_fwd, linear_bwd, ckpt_pack,
+ckpt_unpack, rec_fwd, rec_bwd and rec_step additionally allocate outputs and workspace with torch.
 """
 from __future__ import annotations
 
@@ -36,6 +36,8 @@ _DTYPE = {torch.float32: SS_F32, torch.bfloat16: SS_BF16}
 SS_ACT_NONE, SS_ACT_SILU, SS_ACT_GELU, SS_ACT_SOFTPLUS = 0, 1, 2, 3
 SS_LINEAR_FWD, SS_LINEAR_BWD, SS_LINEAR_BWD_CKPT = 0, 1, 2
 SS_CKPT_BLOCK = 32
+SS_REC_FWD, SS_REC_BWD = 0, 1
+SS_REC_CHUNK = 64
 _ACT = {"none": SS_ACT_NONE, "silu": SS_ACT_SILU, "gelu": SS_ACT_GELU,
         "softplus": SS_ACT_SOFTPLUS}
 _DISC = {"zoh": SS_ZOH, "euler": SS_EULER}
@@ -79,6 +81,14 @@ class ss_linear_desc_t(ctypes.Structure):
                 ("out_dtype", ctypes.c_int32), ("res_dtype", ctypes.c_int32),
                 ("grad_dtype", ctypes.c_int32), ("act", ctypes.c_int32),
                 ("reserved", ctypes.c_int32)]
+
+
+class ss_rec_desc_t(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64), ("dim", ctypes.c_int64),
+                ("x_stride", ctypes.c_int64), ("r_stride", ctypes.c_int64),
+                ("i_stride", ctypes.c_int64), ("z_stride", ctypes.c_int64),
+                ("in_dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32),
+                ("decay", ctypes.c_float), ("reserved", ctypes.c_int32)]
 
 
 class ScanError(RuntimeError):
@@ -154,6 +164,15 @@ def load_library():
         lib.ss_ckpt_pack.restype = I
         lib.ss_ckpt_unpack.argtypes = [CK] + [P] * 3 + [P]
         lib.ss_ckpt_unpack.restype = I
+        RC = ctypes.POINTER(ss_rec_desc_t)
+        lib.ss_rec_workspace_bytes.argtypes = [RC, I]
+        lib.ss_rec_workspace_bytes.restype = SZ
+        lib.ss_rec_fwd.argtypes = [RC] + [P] * 11 + [P, SZ, P]
+        lib.ss_rec_fwd.restype = I
+        lib.ss_rec_bwd.argtypes = [RC] + [P] * 16 + [P, SZ, P]
+        lib.ss_rec_bwd.restype = I
+        lib.ss_rec_step.argtypes = [RC] + [P] * 7 + [P]
+        lib.ss_rec_step.restype = I
         lib.ss_scan_strerror.argtypes = [I]
         lib.ss_scan_strerror.restype = ctypes.c_char_p
         lib.ss_scan_version.argtypes = []
@@ -374,6 +393,37 @@ def ss_ckpt_pack(desc, x, q, e, stream=None) -> int:
 
 def ss_ckpt_unpack(desc, q, e, x, stream=None) -> int:
     return load_library().ss_ckpt_unpack(ctypes.byref(desc), _p(q), _p(e), _p(x), _stream(stream))
+
+
+def make_rec_desc(batch, seqlen, dim, x_stride=0, r_stride=0, i_stride=0, z_stride=0,
+                  in_dtype=SS_BF16, out_dtype=SS_BF16, decay=8.0) -> ss_rec_desc_t:
+    return ss_rec_desc_t(int(batch), int(seqlen), int(dim), int(x_stride), int(r_stride),
+                         int(i_stride), int(z_stride), int(in_dtype), int(out_dtype),
+                         float(decay), 0)
+
+
+def ss_rec_workspace_bytes(desc: ss_rec_desc_t, op: int) -> int:
+    return int(load_library().ss_rec_workspace_bytes(ctypes.byref(desc), int(op)))
+
+
+def ss_rec_fwd(desc, x, r, i, lam, z, h0, starts, lengths, y, h_last, states, workspace, ws_bytes,
+               stream=None) -> int:
+    return load_library().ss_rec_fwd(ctypes.byref(desc), _p(x), _p(r), _p(i), _p(lam), _p(z),
+                                     _p(h0), _p(starts), _p(lengths), _p(y), _p(h_last),
+                                     _p(states), _p(workspace), int(ws_bytes), _stream(stream))
+
+
+def ss_rec_bwd(desc, x, r, i, lam, z, starts, lengths, states, dy, dh_last, dx, dr, di, dz, dlam,
+               dh0, workspace, ws_bytes, stream=None) -> int:
+    return load_library().ss_rec_bwd(ctypes.byref(desc), _p(x), _p(r), _p(i), _p(lam), _p(z),
+                                     _p(starts), _p(lengths), _p(states), _p(dy), _p(dh_last),
+                                     _p(dx), _p(dr), _p(di), _p(dz), _p(dlam), _p(dh0),
+                                     _p(workspace), int(ws_bytes), _stream(stream))
+
+
+def ss_rec_step(desc, h, x, r, i, lam, z, y, stream=None) -> int:
+    return load_library().ss_rec_step(ctypes.byref(desc), _p(h), _p(x), _p(r), _p(i), _p(lam),
+                                      _p(z), _p(y), _stream(stream))
 
 
 def _check(rc, where):
@@ -890,3 +940,122 @@ def _ckpt_unpack(raw, q, e, dtype):
     _check(load_library().ss_ckpt_unpack(ctypes.byref(desc), qp, ep, x.data_ptr(), raw),
            "ss_ckpt_unpack")
     return x
+
+
+# ------------------------------------------- the operators of a gated recurrent block
+def _rec_desc(x, r, i, z, odt, decay):
+    """Description of a recurrence over x (B, L, D) or, for one token, (B, D)."""
+    shape = x.shape
+    dt = _dt(x.dtype, "x")
+    for t, name in ((r, "r"), (i, "i"), (z, "z")):
+        if t is None:
+            continue
+        if t.shape != shape:
+            raise ValueError("%s must have shape %s (got %s)" % (name, tuple(shape),
+                                                                 tuple(t.shape)))
+        if t.dtype is not x.dtype:
+            raise ValueError("x, r, i and z must have one dtype")
+    return ss_rec_desc_t(shape[0], shape[1] if len(shape) == 3 else 1, shape[-1],
+                         _x_stride(x, "x"), _x_stride(r, "r"), _x_stride(i, "i"),
+                         0 if z is None else _x_stride(z, "z"), dt, _dt(odt, "dtype of y"),
+                         float(decay), 0)
+
+
+def _rec_marks(starts, lengths, batch, seqlen):
+    if starts is not None and starts.dtype not in (torch.uint8, torch.bool):
+        raise ValueError("starts must be uint8 or bool (got %s)" % starts.dtype)
+    if lengths is not None and lengths.dtype is not torch.int32:
+        raise ValueError("lengths must be int32 (got %s)" % lengths.dtype)
+    return _arg(starts, "starts", (batch, seqlen)), _arg(lengths, "lengths", (batch,))
+
+
+def rec_fwd(x, r, i, lam, z=None, h0=None, starts=None, lengths=None, decay=8.0, out_dtype=None,
+            return_last=False, save_states=False, stream=None):
+    """Gated linear recurrence h_t = a_t h_(t-1) + sqrt(1 - a_t^2) sigmoid(i) x with
+    log a = -decay softplus(lam) sigmoid(r); y = h, or h silu(z) with z.  x, r, i, z
+    (B, L, D) of one dtype, each perhaps with a row stride (column ranges of a wider
+    projection); lam (D) and h0 (B, D) float32; starts (B, L) uint8 or bool: nonzero at
+    a document's first token, which sees no earlier state; lengths (B) int32: steps at
+    and behind it leave the state as it is, and their y is 0.  Returns a dict: y (B, L,
+    D) in out_dtype (default x's), h_last (B, D) float32 with return_last, states (B,
+    ceil(L / 64), D) float32, for rec_bwd, with save_states (else None)."""
+    return _on_device(_rec_fwd, stream, (x, r, i, lam, z, h0, starts, lengths), x, r, i, lam, z,
+                      h0, starts, lengths, decay, x.dtype if out_dtype is None else out_dtype,
+                      return_last, save_states)
+
+
+def _rec_fwd(raw, x, r, i, lam, z, h0, starts, lengths, decay, odt, return_last, save_states):
+    if x.dim() != 3:
+        raise ValueError("x must be (batch, seqlen, dim)")
+    desc = _rec_desc(x, r, i, z, odt, decay)
+    b, l, d = x.shape
+    _f32(lam, "lam")
+    _f32(h0, "h0")
+    lp, hp = _arg(lam, "lam", (d,)), _arg(h0, "h0", (b, d))
+    sp, np_ = _rec_marks(starts, lengths, b, l)
+    y = _like(x, odt)
+    f32 = dict(dtype=torch.float32, device=x.device)
+    last = torch.empty((b, d), **f32) if return_last else None
+    states = torch.empty((b, -(-l // SS_REC_CHUNK), d), **f32) if save_states else None
+    lib = load_library()
+    nb = lib.ss_rec_workspace_bytes(ctypes.byref(desc), SS_REC_FWD)
+    ws = workspace(nb, x.device)
+    _check(lib.ss_rec_fwd(ctypes.byref(desc), x.data_ptr(), r.data_ptr(), i.data_ptr(), lp,
+                          _ptr(z), hp, sp, np_, y.data_ptr(), _ptr(last), _ptr(states), _ptr(ws),
+                          nb, raw), "ss_rec_fwd")
+    return {"y": y, "h_last": last, "states": states}
+
+
+def rec_bwd(x, r, i, lam, dy, states, z=None, starts=None, lengths=None, dh_last=None, decay=8.0,
+            stream=None):
+    """Backward of rec_fwd given dy (B, L, D) and the states that it kept; the other
+    arguments are the forward's, dh_last (B, D) float32 the gradient that reaches the
+    state after the last step.  Returns a dict: dx, dr, di, dz (x's dtype; dz None
+    without z), dlam (D) and dh0 (B, D) float32."""
+    return _on_device(_rec_bwd, stream, (x, r, i, lam, dy, states, z, starts, lengths, dh_last),
+                      x, r, i, lam, dy, states, z, starts, lengths, dh_last, decay)
+
+
+def _rec_bwd(raw, x, r, i, lam, dy, states, z, starts, lengths, dh_last, decay):
+    if x.dim() != 3:
+        raise ValueError("x must be (batch, seqlen, dim)")
+    desc = _rec_desc(x, r, i, z, dy.dtype, decay)
+    b, l, d = x.shape
+    for t, name in ((lam, "lam"), (states, "states"), (dh_last, "dh_last")):
+        _f32(t, name)
+    lp, dyp = _arg(lam, "lam", (d,)), _arg(dy, "dy", x.shape)
+    stp = _arg(states, "states", (b, -(-l // SS_REC_CHUNK), d))
+    dhp = _arg(dh_last, "dh_last", (b, d))
+    sp, np_ = _rec_marks(starts, lengths, b, l)
+    dx, dr, di = _like(x, x.dtype), _like(x, x.dtype), _like(x, x.dtype)
+    dz = None if z is None else _like(x, x.dtype)
+    dlam = torch.empty(d, dtype=torch.float32, device=x.device)
+    dh0 = torch.empty((b, d), dtype=torch.float32, device=x.device)
+    lib = load_library()
+    nb = lib.ss_rec_workspace_bytes(ctypes.byref(desc), SS_REC_BWD)
+    ws = workspace(nb, x.device)
+    _check(lib.ss_rec_bwd(ctypes.byref(desc), x.data_ptr(), r.data_ptr(), i.data_ptr(), lp,
+                          _ptr(z), sp, np_, stp, dyp, dhp, dx.data_ptr(), dr.data_ptr(),
+                          di.data_ptr(), _ptr(dz), dlam.data_ptr(), dh0.data_ptr(), _ptr(ws), nb,
+                          raw), "ss_rec_bwd")
+    return {"dx": dx, "dr": dr, "di": di, "dz": dz, "dlam": dlam, "dh0": dh0}
+
+
+def rec_step(h, x, r, i, lam, z=None, decay=8.0, out_dtype=None, stream=None):
+    """One token of rec_fwd for every sequence: h (B, D) float32 is updated in place; x,
+    r, i, z (B, D).  Returns y (B, D)."""
+    return _on_device(_rec_step, stream, (h, x, r, i, lam, z), h, x, r, i, lam, z, decay,
+                      x.dtype if out_dtype is None else out_dtype)
+
+
+def _rec_step(raw, h, x, r, i, lam, z, decay, odt):
+    if x.dim() != 2:
+        raise ValueError("x must be (batch, dim)")
+    desc = _rec_desc(x, r, i, z, odt, decay)
+    _f32(h, "h")
+    _f32(lam, "lam")
+    hp, lp = _arg(h, "h", x.shape), _arg(lam, "lam", (x.shape[1],))
+    y = _like(x, odt)
+    _check(load_library().ss_rec_step(ctypes.byref(desc), hp, x.data_ptr(), r.data_ptr(),
+                                      i.data_ptr(), lp, _ptr(z), y.data_ptr(), raw), "ss_rec_step")
+    return y

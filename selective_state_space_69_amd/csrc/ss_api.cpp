@@ -318,7 +318,7 @@ int fwd_call(const ss_desc_t* desc, int direction, int accumulate, const void* u
 
 extern "C" {
 
-int ss_scan_version(void) { return 20100; }
+int ss_scan_version(void) { return 20200; }
 
 int ss_scan_arch_supported(const char* arch_name) {
   if (!arch_name) return SS_ERR_INVALID_ARG;

@@ -10,6 +10,7 @@
 #include "ss_conv.h"
 #include "ss_linear.h"
 #include "ss_norm.h"
+#include "ss_rec.h"
 #include "ss_ssd.h"
 #include "ss_scan.h"
 
@@ -258,5 +259,25 @@ int launch_linear_fwd(const ss_linear_desc_t& d, const void* x, const void* w, c
 int launch_linear_bwd(const ss_linear_desc_t& d, const LinearPlan& pl, const void* x,
                       const int8_t* q, const uint8_t* e, const void* w, const void* pre,
                       const void* dy, void* dx, void* dw, float* dbias, char* ws, void* stream);
+
+// Gated linear recurrence (ss_rec.hip): time in nchunks chunks of `chunk` steps, one
+// workgroup each per 64 channels.  Workspace, fp32 (B, nchunks, D) arrays, 256-byte
+// aligned: chunks' log decays and carries (nchunks > 1), backward partial sums of dlam.
+struct RecPlan {
+  int64_t chunk = 0, nchunks = 1;
+  size_t off_log = 0, off_carry = 0, off_part = 0, bytes = 0;
+};
+RecPlan plan_rec(const ss_rec_desc_t& d, int op);
+int launch_rec_fwd(const ss_rec_desc_t& d, const RecPlan& pl, const void* x, const void* r,
+                   const void* i, const float* lam, const void* z, const float* h0,
+                   const uint8_t* starts, const int32_t* lengths, void* y, float* h_last,
+                   float* states, char* ws, void* stream);
+int launch_rec_bwd(const ss_rec_desc_t& d, const RecPlan& pl, const void* x, const void* r,
+                   const void* i, const float* lam, const void* z, const uint8_t* starts,
+                   const int32_t* lengths, const float* states, const void* dy,
+                   const float* dh_last, void* dx, void* dr, void* di, void* dz, float* dlam,
+                   float* dh0, char* ws, void* stream);
+int launch_rec_step(const ss_rec_desc_t& d, float* h, const void* x, const void* r, const void* i,
+                    const float* lam, const void* z, void* y, void* stream);
 
 }  // namespace ss
