@@ -1,18 +1,19 @@
 """Thin ctypes binding of libssscan.so (C ABI declared in include/ss_scan.h,
 include/ss_conv.h, include/ss_ssd.h, include/ss_norm.h, include/ss_linear.h,
-include/ss_ckpt.h and include/ss_rec.h).
+include/ss_ckpt.h, include/ss_rec.h, include/ss_glu.h and include/ss_q8.h).
 
 The functions named like the C entry points (ss_scan_fwd, ss_scan_fwd_noalloc, ss_scan_fwd_dir,
 ss_scan_fwd_complex, ss_scan_fwd_complex_ws, ss_scan_bwd, ss_scan_step, ss_scan_step_complex, ss_scan_workspace_bytes, ss_scan_strerror, ss_scan_version,
 ss_conv1d_fwd, ss_conv1d_bwd, ss_conv1d_step, ss_conv1d_workspace_bytes, ss_ssd_fwd,
 ss_ssd_fwd_state, ss_ssd_step, ss_layernorm_fwd, ss_layernorm_bwd, ss_layernorm_workspace_bytes,
 ss_linear_fwd, ss_linear_bwd, ss_linear_bwd_ckpt, ss_linear_workspace_bytes, ss_ckpt_pack,
-ss_ckpt_unpack, ss_rec_fwd, ss_rec_bwd, ss_rec_step, ss_rec_workspace_bytes) only
+ss_ckpt_unpack, ss_rec_fwd, ss_rec_bwd, ss_rec_step, ss_rec_workspace_bytes, ss_glu_fwd,
+ss_glu_bwd, ss_glu_workspace_bytes, ss_q8_pack, ss_q8_linear, ss_q8_workspace_bytes) only
 marshal arguments: torch tensors become device pointers, None becomes NULL and
 the stream defaults to torch's current HIP stream.  Every step runs in the HIP
 kernels; there is no fallback.  The convenience wrappers scan_fwd, scan_bwd,
 scan_bidir, scan_fwd_complex, scan_step, scan_step_complex, conv1d_fwd, conv1d_bwd, conv1d_step, ssd_fwd, ssd_step, layernorm_fwd, layernorm_bwd, linear_fwd, linear_bwd, ckpt_pack,
-ckpt_unpack, rec_fwd, rec_bwd and rec_step additionally allocate outputs and workspace with torch.
+ckpt_unpack, rec_fwd, rec_bwd, rec_step, glu_fwd, glu_bwd, q8_pack and q8_linear additionally allocate outputs and workspace with torch.
 """
 from __future__ import annotations
 
@@ -38,6 +39,7 @@ SS_LINEAR_FWD, SS_LINEAR_BWD, SS_LINEAR_BWD_CKPT = 0, 1, 2
 SS_CKPT_BLOCK = 32
 SS_REC_FWD, SS_REC_BWD = 0, 1
 SS_REC_CHUNK = 64
+SS_GLU_FWD, SS_GLU_BWD = 0, 1
 _ACT = {"none": SS_ACT_NONE, "silu": SS_ACT_SILU, "gelu": SS_ACT_GELU,
         "softplus": SS_ACT_SOFTPLUS}
 _DISC = {"zoh": SS_ZOH, "euler": SS_EULER}
@@ -89,6 +91,27 @@ class ss_rec_desc_t(ctypes.Structure):
                 ("i_stride", ctypes.c_int64), ("z_stride", ctypes.c_int64),
                 ("in_dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32),
                 ("decay", ctypes.c_float), ("reserved", ctypes.c_int32)]
+
+
+class ss_glu_desc_t(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("in_dim", ctypes.c_int64), ("out_dim", ctypes.c_int64),
+                ("x_stride", ctypes.c_int64), ("in_dtype", ctypes.c_int32),
+                ("out_dtype", ctypes.c_int32), ("grad_dtype", ctypes.c_int32),
+                ("act", ctypes.c_int32)]
+
+
+class ss_q8_pack_desc_t(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("dim", ctypes.c_int64), ("x_stride", ctypes.c_int64),
+                ("q_stride", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
+class ss_q8_desc_t(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("in_dim", ctypes.c_int64), ("out_dim", ctypes.c_int64),
+                ("x_stride", ctypes.c_int64), ("w_stride", ctypes.c_int64),
+                ("out_dtype", ctypes.c_int32), ("res_dtype", ctypes.c_int32),
+                ("act", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
 
 
 class ScanError(RuntimeError):
@@ -173,6 +196,20 @@ def load_library():
         lib.ss_rec_bwd.restype = I
         lib.ss_rec_step.argtypes = [RC] + [P] * 7 + [P]
         lib.ss_rec_step.restype = I
+        GL = ctypes.POINTER(ss_glu_desc_t)
+        lib.ss_glu_workspace_bytes.argtypes = [GL, I]
+        lib.ss_glu_workspace_bytes.restype = SZ
+        lib.ss_glu_fwd.argtypes = [GL] + [P] * 5 + [P, SZ, P]
+        lib.ss_glu_fwd.restype = I
+        lib.ss_glu_bwd.argtypes = [GL] + [P] * 7 + [P, SZ, P]
+        lib.ss_glu_bwd.restype = I
+        lib.ss_q8_pack.argtypes = [ctypes.POINTER(ss_q8_pack_desc_t)] + [P] * 3 + [P]
+        lib.ss_q8_pack.restype = I
+        Q8 = ctypes.POINTER(ss_q8_desc_t)
+        lib.ss_q8_workspace_bytes.argtypes = [Q8]
+        lib.ss_q8_workspace_bytes.restype = SZ
+        lib.ss_q8_linear.argtypes = [Q8] + [P] * 7 + [P, SZ, P]
+        lib.ss_q8_linear.restype = I
         lib.ss_scan_strerror.argtypes = [I]
         lib.ss_scan_strerror.restype = ctypes.c_char_p
         lib.ss_scan_version.argtypes = []
@@ -424,6 +461,52 @@ def ss_rec_bwd(desc, x, r, i, lam, z, starts, lengths, states, dy, dh_last, dx, 
 def ss_rec_step(desc, h, x, r, i, lam, z, y, stream=None) -> int:
     return load_library().ss_rec_step(ctypes.byref(desc), _p(h), _p(x), _p(r), _p(i), _p(lam),
                                       _p(z), _p(y), _stream(stream))
+
+
+def make_glu_desc(rows, in_dim, out_dim, x_stride=0, in_dtype=SS_BF16, out_dtype=SS_BF16,
+                  grad_dtype=SS_BF16, act=SS_ACT_SILU) -> ss_glu_desc_t:
+    return ss_glu_desc_t(int(rows), int(in_dim), int(out_dim), int(x_stride), int(in_dtype),
+                         int(out_dtype), int(grad_dtype), int(act))
+
+
+def ss_glu_workspace_bytes(desc: ss_glu_desc_t, op: int) -> int:
+    return int(load_library().ss_glu_workspace_bytes(ctypes.byref(desc), int(op)))
+
+
+def ss_glu_fwd(desc, x, w, bias, y, pre, workspace, ws_bytes, stream=None) -> int:
+    return load_library().ss_glu_fwd(ctypes.byref(desc), _p(x), _p(w), _p(bias), _p(y), _p(pre),
+                                     _p(workspace), int(ws_bytes), _stream(stream))
+
+
+def ss_glu_bwd(desc, x, w, pre, dy, dx, dw, dbias, workspace, ws_bytes, stream=None) -> int:
+    return load_library().ss_glu_bwd(ctypes.byref(desc), _p(x), _p(w), _p(pre), _p(dy), _p(dx),
+                                     _p(dw), _p(dbias), _p(workspace), int(ws_bytes),
+                                     _stream(stream))
+
+
+def make_q8_pack_desc(rows, dim, x_stride=0, q_stride=0, dtype=SS_BF16) -> ss_q8_pack_desc_t:
+    return ss_q8_pack_desc_t(int(rows), int(dim), int(x_stride), int(q_stride), int(dtype), 0)
+
+
+def ss_q8_pack(desc, x, q, s, stream=None) -> int:
+    return load_library().ss_q8_pack(ctypes.byref(desc), _p(x), _p(q), _p(s), _stream(stream))
+
+
+def make_q8_desc(rows, in_dim, out_dim, x_stride=0, w_stride=0, out_dtype=SS_BF16,
+                 res_dtype=SS_BF16, act=SS_ACT_NONE) -> ss_q8_desc_t:
+    return ss_q8_desc_t(int(rows), int(in_dim), int(out_dim), int(x_stride), int(w_stride),
+                        int(out_dtype), int(res_dtype), int(act), 0)
+
+
+def ss_q8_workspace_bytes(desc: ss_q8_desc_t) -> int:
+    return int(load_library().ss_q8_workspace_bytes(ctypes.byref(desc)))
+
+
+def ss_q8_linear(desc, xq, xs, wq, ws, bias, residual, y, workspace, ws_bytes,
+                 stream=None) -> int:
+    return load_library().ss_q8_linear(ctypes.byref(desc), _p(xq), _p(xs), _p(wq), _p(ws),
+                                       _p(bias), _p(residual), _p(y), _p(workspace),
+                                       int(ws_bytes), _stream(stream))
 
 
 def _check(rc, where):
@@ -1058,4 +1141,137 @@ def _rec_step(raw, h, x, r, i, lam, z, decay, odt):
     y = _like(x, odt)
     _check(load_library().ss_rec_step(ctypes.byref(desc), hp, x.data_ptr(), r.data_ptr(),
                                       i.data_ptr(), lp, _ptr(z), y.data_ptr(), raw), "ss_rec_step")
+    return y
+
+
+_GLU_ACT = {k: v for k, v in _ACT.items() if k != "softplus"}
+
+
+def glu_fwd(x, w, bias=None, act="silu", out_dtype=None, save_pre=False, stream=None):
+    """act(x wg^T + bg) (x wu^T + bu) for x (..., K) and w = [wg; wu] (2 F, K) of one
+    dtype; x may have a row stride.  bias (2 F) is float32, act one of "none", "silu",
+    "gelu".  Returns y (..., F) in out_dtype (default x's), and with save_pre both
+    pre-activations (..., 2 F) in x's dtype as well, gate first.  The projection back is
+    linear_fwd, with the block's residual."""
+    return _on_device(_glu_fwd, stream, (x, w, bias), x, w, bias, _GLU_ACT[act],
+                      x.dtype if out_dtype is None else out_dtype, save_pre)
+
+
+def _glu_halves(w):
+    n, k = w.shape
+    if n % 2:
+        raise ValueError("w must have the gate's rows and as many of the other factor's (got %d)"
+                         % n)
+    return n // 2, k
+
+
+def _glu_fwd(raw, x, w, bias, act, odt, save_pre):
+    f, k = _glu_halves(w)
+    if x.shape[-1] != k:
+        raise ValueError("x must have %d columns (got %d)" % (k, x.shape[-1]))
+    if x.dtype != w.dtype:
+        raise ValueError("x and w must have one dtype")
+    _f32(bias, "bias")
+    desc = ss_glu_desc_t(x.numel() // k if k else 0, k, f, _x_stride(x, "x"), _dt(x.dtype, "x"),
+                         _dt(odt, "out_dtype"), SS_F32, act)
+    wp, bp = _arg(w, "w", (2 * f, k)), _arg(bias, "bias", (2 * f,))
+    y = torch.empty((*x.shape[:-1], f), dtype=odt, device=x.device)
+    pre = torch.empty((*x.shape[:-1], 2 * f), dtype=x.dtype, device=x.device) if save_pre else None
+    lib = load_library()
+    nb = lib.ss_glu_workspace_bytes(ctypes.byref(desc), SS_GLU_FWD)
+    ws = workspace(nb, x.device)
+    _check(lib.ss_glu_fwd(ctypes.byref(desc), x.data_ptr(), wp, bp, y.data_ptr(), _ptr(pre),
+                          _ptr(ws), nb, raw), "ss_glu_fwd")
+    return (y, pre) if save_pre else y
+
+
+def glu_bwd(x, w, dy, pre, act="silu", bias=False, grad_dtype=None, need_dx=True, need_dw=True,
+            stream=None):
+    """Backward of glu_fwd given dy (..., F) and pre (..., 2 F).  x: the forward's input
+    (None when need_dw is false).  Returns a dict: dx (..., K) and dw (2 F, K) in
+    grad_dtype (default w's), dbias (2 F) float32 when bias is true; what is not asked for
+    is None.  With bf16 operands, float32 gradients keep both factors' gradients to 2^-16
+    (twice the matrix work), bf16 ones round them to bf16."""
+    return _on_device(_glu_bwd, stream, (w, dy, pre, x), x, w, dy, pre, _GLU_ACT[act], bias,
+                      w.dtype if grad_dtype is None else grad_dtype, need_dx, need_dw)
+
+
+def _glu_bwd(raw, x, w, dy, pre, act, bias, gdt, need_dx, need_dw):
+    f, k = _glu_halves(w)
+    lead = dy.shape[:-1]
+    if pre.dtype != w.dtype:
+        raise ValueError("pre must have w's dtype")
+    if need_dw and x is None:
+        raise ValueError("dw needs x")
+    dyp, wp = _arg(dy, "dy", (*lead, f)), _arg(w, "w", (2 * f, k))
+    prep = _arg(pre, "pre", (*lead, 2 * f))
+    xs = 0
+    if x is not None:
+        if x.shape != (*lead, k):
+            raise ValueError("x must have shape %s (got %s)" % ((*lead, k), tuple(x.shape)))
+        if x.dtype != w.dtype:
+            raise ValueError("x and w must have one dtype")
+        xs = _x_stride(x, "x")
+    desc = ss_glu_desc_t(dy.numel() // f if f else 0, k, f, xs, _dt(w.dtype, "w"),
+                         _dt(dy.dtype, "dy"), _dt(gdt, "grad_dtype"), act)
+    dx = torch.empty((*lead, k), dtype=gdt, device=w.device) if need_dx else None
+    dw = _like(w, gdt) if need_dw else None
+    db = torch.empty(2 * f, dtype=torch.float32, device=w.device) if bias else None
+    lib = load_library()
+    nb = lib.ss_glu_workspace_bytes(ctypes.byref(desc), SS_GLU_BWD)
+    ws = workspace(nb, w.device)
+    _check(lib.ss_glu_bwd(ctypes.byref(desc), _ptr(x), wp, prep, dyp, _ptr(dx), _ptr(dw), _ptr(db),
+                          _ptr(ws), nb, raw), "ss_glu_bwd")
+    return {"dx": dx, "dw": dw, "dbias": db}
+
+
+def q8_pack(x, stream=None):
+    """Rows of x (..., K) as 8-bit integers: (q, s), int8 values (..., K) and one float32
+    scale per row, x ~ q s.  x may have a row stride.  q's rows lie a multiple of 16 bytes
+    apart, so it is a view of a wider buffer where K is odd."""
+    return _on_device(_q8_pack, stream, (x,), x)
+
+
+def _q8_pack(raw, x):
+    dim = x.shape[-1]
+    ldq = -(-dim // 16) * 16
+    desc = ss_q8_pack_desc_t(x.numel() // dim if dim else 0, dim, _x_stride(x, "x"), ldq,
+                             _dt(x.dtype, "x"), 0)
+    q = torch.empty((*x.shape[:-1], ldq), dtype=torch.int8, device=x.device)
+    s = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+    _check(load_library().ss_q8_pack(ctypes.byref(desc), x.data_ptr(), q.data_ptr(), s.data_ptr(),
+                                     raw), "ss_q8_pack")
+    return (q if ldq == dim else q[..., :dim]), s
+
+
+def q8_linear(x, w, bias=None, residual=None, act="none", out_dtype=torch.bfloat16, stream=None):
+    """act(x w^T + bias) + residual for packed x = (q, s) of (..., K) and w = (q, s) of (N,
+    K), as from q8_pack: exact sums of the integers, times both scales.  Either's values
+    may have a row stride.  bias (N) is float32, residual (..., N) float32 or bfloat16, act one of "none", "silu", "gelu",
+    "softplus".  Returns y (..., N) in out_dtype."""
+    (xq, xs), (wq, ws) = x, w
+    return _on_device(_q8_linear, stream, (xq, xs, wq, ws, bias, residual), xq, xs, wq, ws, bias,
+                      residual, _ACT[act], out_dtype)
+
+
+def _q8_linear(raw, xq, xs, wq, ws, bias, residual, act, odt):
+    n, k = wq.shape
+    lead = xq.shape[:-1]
+    if xq.shape[-1] != k:
+        raise ValueError("x must have %d columns (got %d)" % (k, xq.shape[-1]))
+    if xq.dtype != torch.int8 or wq.dtype != torch.int8:
+        raise ValueError("packed values are int8 (got %s and %s)" % (xq.dtype, wq.dtype))
+    for t, name in ((xs, "x's scales"), (ws, "w's scales"), (bias, "bias")):
+        _f32(t, name)
+    od = _dt(odt, "out_dtype")
+    desc = ss_q8_desc_t(xq.numel() // k if k else 0, k, n, _x_stride(xq, "x"), _x_stride(wq, "w"), od,
+                        od if residual is None else _dt(residual.dtype, "residual"), act, 0)
+    xsp, wsp = _arg(xs, "x's scales", lead), _arg(ws, "w's scales", (n,))
+    bp, rp = _arg(bias, "bias", (n,)), _arg(residual, "residual", (*lead, n))
+    y = torch.empty((*lead, n), dtype=odt, device=xq.device)
+    lib = load_library()
+    nb = lib.ss_q8_workspace_bytes(ctypes.byref(desc))
+    work = workspace(nb, xq.device)
+    _check(lib.ss_q8_linear(ctypes.byref(desc), xq.data_ptr(), xsp, wq.data_ptr(), wsp, bp, rp,
+                            y.data_ptr(), _ptr(work), nb, raw), "ss_q8_linear")
     return y

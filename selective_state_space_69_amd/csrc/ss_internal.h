@@ -8,8 +8,10 @@
 
 #include "ss_ckpt.h"
 #include "ss_conv.h"
+#include "ss_glu.h"
 #include "ss_linear.h"
 #include "ss_norm.h"
+#include "ss_q8.h"
 #include "ss_rec.h"
 #include "ss_ssd.h"
 #include "ss_scan.h"
@@ -279,5 +281,25 @@ int launch_rec_bwd(const ss_rec_desc_t& d, const RecPlan& pl, const void* x, con
                    float* dh0, char* ws, void* stream);
 int launch_rec_step(const ss_rec_desc_t& d, float* h, const void* x, const void* r, const void* i,
                     const float* lam, const void* z, void* y, void* stream);
+
+// Gated half of a feed-forward block (ss_linear.hip): the projection's plan for both
+// halves' columns.
+LinearPlan plan_glu(const ss_glu_desc_t& d, int op);
+int launch_glu_fwd(const ss_glu_desc_t& d, const LinearPlan& pl, const void* x, const void* w,
+                   const float* bias, void* y, void* pre, char* ws, void* stream);
+int launch_glu_bwd(const ss_glu_desc_t& d, const LinearPlan& pl, const void* x, const void* w,
+                   const void* pre, const void* dy, void* dx, void* dw, float* dbias, char* ws,
+                   void* stream);
+
+// Projection in 8-bit integers (ss_linear.hip, ss_q8.hip).  Workspace: rows of xq and wq at
+// a 16-byte aligned stride where they cannot be read in place, int32 partial sums.
+struct Q8Plan {
+  size_t off_x = 0, off_w = 0, off_part = 0, bytes = 0;
+};
+Q8Plan plan_q8(const ss_q8_desc_t& d);
+int launch_q8_pack(const ss_q8_pack_desc_t& d, const void* x, int8_t* q, float* s, void* stream);
+int launch_q8_linear(const ss_q8_desc_t& d, const Q8Plan& pl, const int8_t* xq, const float* xs,
+                     const int8_t* wq, const float* wsc, const float* bias, const void* residual,
+                     void* y, char* ws, void* stream);
 
 }  // namespace ss

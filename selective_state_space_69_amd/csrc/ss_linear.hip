@@ -40,8 +40,38 @@ __global__ __launch_bounds__(kThreads) void join_kernel(MmParams p) {
   }
 }
 
-// bf16 rows of one or two tensors (blockIdx.y) at a 16-byte aligned stride, zero past
-// their end: one 16-byte unit of the copy per thread.
+// Sum of the splits' partials of both gated products, in order, and their epilogue.
+__global__ __launch_bounds__(kThreads) void join_glu_kernel(MmParams p) {
+  const int64_t total = p.nR * p.nS, step = 2 * total;
+  for (int64_t i = int64_t(blockIdx.x) * kThreads + threadIdx.x; i < total;
+       i += int64_t(gridDim.x) * kThreads) {
+    const int64_t r = i / p.nS;
+    const int32_t c = int32_t(i - r * p.nS);
+    const float* src = p.part + 2 * r * p.nS + c;
+    float gate = 0.0f, up = 0.0f;
+    for (int k = 0; k < p.splits; ++k) {
+      gate += src[k * step];
+      up += src[k * step + p.nS];
+    }
+    glu1(p, p.act, r, c, gate, up);
+  }
+}
+// Sum of the splits' whole numbers, their scales and the epilogue.
+__global__ __launch_bounds__(kThreads) void join_q8_kernel(MmParams p) {
+  const int64_t total = p.nR * p.nS;
+  const int32_t* part = reinterpret_cast<const int32_t*>(p.part);
+  for (int64_t i = int64_t(blockIdx.x) * kThreads + threadIdx.x; i < total;
+       i += int64_t(gridDim.x) * kThreads) {
+    const int64_t r = i / p.nS;
+    const int32_t c = int32_t(i - r * p.nS);
+    int32_t sum = 0;
+    for (int k = 0; k < p.splits; ++k) sum += part[k * total + i];
+    epilogue1(p, p.act, r, c, float(sum) * (p.row_scale[r] * p.col_scale[c]));
+  }
+}
+
+// Rows of one or two tensors (blockIdx.y) at a 16-byte aligned stride, zero past
+// their end: one 16-byte unit of the copy per thread.  T: bf16 or bytes.
 struct PadJob {
   const void* src;
   void* dst;
@@ -51,21 +81,22 @@ struct PadJob {
 struct PadParams {
   PadJob job[2];
 };
+template <typename T>
 __global__ __launch_bounds__(kThreads) void pad_kernel(PadParams q) {
-  constexpr int E = 8;
+  constexpr int E = 16 / int(sizeof(T));
   const PadJob p = q.job[blockIdx.y];
   const int64_t total = p.rows * p.units;
   for (int64_t i = int64_t(blockIdx.x) * kThreads + threadIdx.x; i < total;
        i += int64_t(gridDim.x) * kThreads) {
     const int64_t r = total <= INT32_MAX ? int64_t(uint32_t(i) / uint32_t(p.units)) : i / p.units;
     const int c = int(i - r * p.units) * E;
-    const uint16_t* src = static_cast<const uint16_t*>(p.src) + r * p.ld_src + c;
-    struct __attribute__((packed, aligned(2))) Elems { uint16_t e[E]; } v;
+    const T* src = static_cast<const T*>(p.src) + r * p.ld_src + c;
+    struct __attribute__((packed, aligned(sizeof(T)))) Elems { T e[E]; } v;
     if (c + E <= p.cols) {
       v = *reinterpret_cast<const Elems*>(src);      // 16 bytes at any element address
     } else {
 #pragma unroll
-      for (int j = 0; j < E; ++j) v.e[j] = c + j < p.cols ? src[j] : uint16_t(0);
+      for (int j = 0; j < E; ++j) v.e[j] = c + j < p.cols ? src[j] : T(0);
     }
     reinterpret_cast<u32x4*>(p.dst)[i] = __builtin_bit_cast(u32x4, v);
   }
@@ -183,6 +214,109 @@ __global__ __launch_bounds__(kThreads) void dpre_kernel(DpreParams p) {
   }
 }
 
+// Both halves of a gated dpre, d = [dy up act'(gate), dy act(gate)], in rows of ld
+// elements that are zero past 2 F, and their column sums: as dpre_kernel, a lane taking V
+// columns of each half.  V is 8 where F is a whole number of 16-byte units.
+struct DgluParams {
+  const void* dy;     // (M, F)
+  const void* pre;    // (M, 2 F)
+  void* d;            // or null
+  float* part;        // (gridDim.y, 2 F) or null
+  int64_t M, rows;    // rows per block
+  int32_t F, ld, sum2;
+};
+template <typename T, int V>
+__device__ __forceinline__ void put_cols(const DgluParams& p, int64_t r, int32_t c,
+                                         const float (&v)[V]) {
+  if (sizeof(T) == 2 && p.sum2) {
+    uint16_t* d = static_cast<uint16_t*>(p.d) + r * p.ld + (c >> 3) * 16 + (c & 7);
+    float lo[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) lo[j] = rest_of(v[j]);
+    if constexpr (V == 8) {
+      store8(d, 0, true, v);
+      store8(d, 8, true, lo);
+    } else {
+      store_out<uint16_t>(d, v[0]);
+      store_out<uint16_t>(d + 8, lo[0]);
+    }
+  } else {
+    T* d = static_cast<T*>(p.d) + r * p.ld + c;
+    if constexpr (V == 8) store8(d, 0, sizeof(T) == 2, v);
+    else store_out<T>(d, v[0]);
+  }
+}
+template <typename Dy, typename T, int V, int ACT>
+__global__ __launch_bounds__(kThreads) void dglu_kernel(DgluParams p) {
+  __shared__ float part[4][2][64 * V];
+  constexpr int kRows = 2;
+  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+  const int c = (int(blockIdx.x) * 64 + lane) * V;
+  const int64_t m0 = int64_t(blockIdx.y) * p.rows;
+  const int64_t m1 = m0 + p.rows < p.M ? m0 + p.rows : p.M;
+  constexpr int kRun = 64 / kRows;      // turns of a run
+  float sum[2][V], run[2][V];
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+#pragma unroll
+    for (int j = 0; j < V; ++j) sum[k][j] = run[k][j] = 0.0f;
+  int turn = 0;
+  for (int64_t m = m0 + wv; m < m1; m += 4 * kRows) {
+    if (++turn > kRun) {
+      turn = 1;
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          sum[k][j] += run[k][j];
+          run[k][j] = 0.0f;
+        }
+    }
+    float v[kRows][V], gate[kRows][V], up[kRows][V];
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      const int64_t r = m + 4 * i < m1 ? m + 4 * i : m1 - 1;
+      const T* pre = static_cast<const T*>(p.pre) + 2 * r * p.F;
+      load_cols<Dy, V>(static_cast<const Dy*>(p.dy) + r * p.F, c, p.F, v[i]);
+      load_cols<T, V>(pre, c, p.F, gate[i]);
+      load_cols<T, V>(pre + p.F, c, p.F, up[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      const int64_t r = m + 4 * i;
+      if (r >= m1) break;
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const float g = gate[i][j], dy = v[i][j];
+        gate[i][j] = dy * up[i][j] * act_grad(ACT, g);
+        up[i][j] = dy * apply_act(ACT, g);
+        run[0][j] += gate[i][j];
+        run[1][j] += up[i][j];
+      }
+      if (!p.d) continue;
+      if (c < p.F) {
+        put_cols<T, V>(p, r, c, gate[i]);
+        put_cols<T, V>(p, r, p.F + c, up[i]);
+      } else if (V == 1 && 2 * p.F + (c - p.F) < p.ld / (p.sum2 ? 2 : 1)) {
+        const float zero[V] = {};
+        put_cols<T, V>(p, r, p.F + c, zero);
+      }
+    }
+  }
+  if (!p.part) return;
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+#pragma unroll
+    for (int j = 0; j < V; ++j) part[wv][k][lane * V + j] = sum[k][j] + run[k][j];
+  __syncthreads();
+  for (int i = threadIdx.x; i < 2 * 64 * V; i += kThreads) {
+    const int k = i / (64 * V), n = i % (64 * V), col = int(blockIdx.x) * 64 * V + n;
+    if (col < p.F)
+      p.part[(int64_t(blockIdx.y) * 2 + k) * p.F + col] =
+          (part[0][k][n] + part[1][k][n]) + (part[2][k][n] + part[3][k][n]);
+  }
+}
+
 size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 bool ptr16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 int unit_of(const ss_linear_desc_t& d) { return d.in_dtype == SS_BF16 ? 8 : 4; }
@@ -239,11 +373,10 @@ double join_us(int64_t nR, int64_t nS, int64_t k) {
 struct Small {
   bool bf16;
   int64_t nR, nS, nT, step, tiles_r, tiles_s, tiles, stages, fit;
-  Small(const ss_linear_desc_t& d, int64_t r, int64_t s, int64_t t, bool sum2)
-      : nR(r), nS(s), nT(t) {
-    bf16 = d.in_dtype == SS_BF16;
+  // size: bytes of an element of the contraction, for bf16 as the sum of two 4
+  Small(bool fp32, int size, int64_t r, int64_t s, int64_t t) : bf16(!fp32), nR(r), nS(s), nT(t) {
     const int64_t side = bf16 ? 128 : 64;
-    step = bf16 && !sum2 ? 64 : 32;
+    step = 128 / size;
     fit = bf16 ? 512 : 1024;
     tiles_r = (nR + side - 1) / side;
     tiles_s = (nS + side - 1) / side;
@@ -257,9 +390,9 @@ struct Small {
     return Tiling{tile, int32_t(tiles_r), int32_t(tiles_s), int32_t((nT + len - 1) / len), len, us};
   }
 };
-Tiling tiling(const ss_linear_desc_t& d, int64_t nR, int64_t nS, int64_t nT, bool sum2) {
+Tiling tiling(const Small& p) {
+  const int64_t nR = p.nR, nS = p.nS, nT = p.nT;
   const int64_t r256 = (nR + 255) / 256, s256 = (nS + 255) / 256;
-  const Small p(d, nR, nS, nT, sum2);
   if (p.bf16 && p.tiles > 512 && p.tiles * 100 > 282 * r256 * s256) {
     const int64_t rounds = (r256 * s256 + 255) / 256, per_cu = (p.tiles + 255) / 256;
     const double fill = double(r256 * s256) / double(256 * rounds);
@@ -284,6 +417,11 @@ Tiling tiling(const ss_linear_desc_t& d, int64_t nR, int64_t nS, int64_t nT, boo
   }
   return best;
 }
+// a forward's tiles (n: its columns, both halves of gated ones)
+Tiling tiling_fwd(const ss_linear_desc_t& d, int64_t n) {
+  const bool fp32 = d.in_dtype == SS_F32;
+  return tiling(Small(fp32, fp32 ? 4 : 2, d.rows, n, d.in_dim));
+}
 // The tiles of a backward pass.  One launch computes dx and dw where the model finds
 // that faster than one after the other: small tiles that all fit on the GPU at once
 // (bf16 5003 x 768 x 1536, whole call: 48 us, both 37), or 256 x 256 ones, where the
@@ -295,8 +433,10 @@ struct Backward {
   int behind, few;
 };
 Backward tilings_bwd(const ss_linear_desc_t& d, bool sum2) {
-  const Small a(d, d.rows, d.in_dim, d.out_dim, sum2), b(d, d.out_dim, d.in_dim, d.rows, sum2);
-  Backward t{tiling(d, a.nR, a.nS, a.nT, sum2), tiling(d, b.nR, b.nS, b.nT, sum2), false, 0, 0};
+  const bool fp32 = d.in_dtype == SS_F32;
+  const int size = fp32 || sum2 ? 4 : 2;
+  const Small a(fp32, size, d.rows, d.in_dim, d.out_dim), b(fp32, size, d.out_dim, d.in_dim, d.rows);
+  Backward t{tiling(a), tiling(b), false, 0, 0};
   auto longer = [](int64_t u, int64_t v) { return u > v ? u : v; };
   if (t.dx.tile == MmTile::kBig && t.dw.tile == MmTile::kBig) {
     const double ux = big_us(a.stages), uw = big_us(b.stages);
@@ -369,20 +509,21 @@ void run_mm(MmParams p, const Tiling& t, bool rt, bool st, bool sum2, char* part
 // to rows of pad_to_unit(cols) elements by one launch, for fp32 ones the products are
 // told to read single elements.
 struct Operands {
-  const ss_linear_desc_t& d;
+  int esize;         // bytes of an element
   PadParams pad{};
   int n = 0;
   bool any = false;
   // rows x cols of src, rows *ld elements apart: where the products read it
   const void* take(const void* src, int64_t* ld, int64_t rows, int64_t cols, char* dst) {
-    const int e = unit_of(d);
+    const int e = 16 / esize;
     if (ptr16(src) && *ld % e == 0 && cols % e == 0) return src;
-    if (d.in_dtype == SS_F32) {
+    if (esize == 4) {
       any = true;
       return src;
     }
-    pad.job[n++] = PadJob{src, dst, *ld, rows, int32_t(cols), int32_t(pad_to_unit(d, cols) / e)};
-    *ld = pad_to_unit(d, cols);
+    const int64_t units = (cols + e - 1) / e;
+    pad.job[n++] = PadJob{src, dst, *ld, rows, int32_t(cols), int32_t(units)};
+    *ld = units * e;
     return dst;
   }
   MmTile tile(MmTile t) const { return any && t == MmTile::kSmallF32 ? MmTile::kSmallF32Any : t; }
@@ -394,7 +535,8 @@ struct Operands {
       if (b > blocks) blocks = b;
     }
     const dim3 grid(unsigned(blocks < kMaxBlocks ? blocks : kMaxBlocks), unsigned(n));
-    pad_kernel<<<grid, kThreads, 0, st>>>(pad);
+    if (esize == 1) pad_kernel<uint8_t><<<grid, kThreads, 0, st>>>(pad);
+    else pad_kernel<uint16_t><<<grid, kThreads, 0, st>>>(pad);
   }
 };
 
@@ -421,7 +563,9 @@ int dpre_vec(const ss_linear_desc_t& d) { return d.out_dim % 8 == 0 ? 8 : 1; }
 
 }  // namespace
 
-LinearPlan plan_linear(const ss_linear_desc_t& d, int op) {
+// gated: out_dim counts both halves, and the kernel that makes dpre takes a column of
+// each at once
+static LinearPlan plan_bwd_fwd(const ss_linear_desc_t& d, int op, bool gated) {
   LinearPlan pl;
   const size_t esize = d.in_dtype == SS_BF16 ? 2 : 4;
   const size_t x_bytes = align256(size_t(d.rows) * size_t(pad_to_unit(d, d.in_dim)) * esize);
@@ -440,7 +584,7 @@ LinearPlan plan_linear(const ss_linear_desc_t& d, int op) {
     if (pad_x) pl.off_x = take(x_bytes);
     if (pad_k) pl.off_w = take(w_bytes);
     pl.off_part =
-        take(part_bytes(tiling(d, d.rows, d.out_dim, d.in_dim, false), d.rows, d.out_dim));
+        take(part_bytes(tiling_fwd(d, d.out_dim), d.rows, d.out_dim));
     pl.bytes = off;
     return pl;
   }
@@ -450,7 +594,7 @@ LinearPlan plan_linear(const ss_linear_desc_t& d, int op) {
             (d.act != SS_ACT_NONE || d.out_dtype != SS_BF16);
   pl.ld_dpre = pad_to_unit(d, d.out_dim) * (pl.sum2 ? 2 : 1);
   // about 1024 blocks over the columns and row chunks, at least 16 rows each
-  const int64_t span = 64 * dpre_vec(d), cols = (d.out_dim + span - 1) / span;
+  const int64_t span = 64 * dpre_vec(d) * (gated ? 2 : 1), cols = (d.out_dim + span - 1) / span;
   int64_t chunks = (1024 + cols - 1) / cols;
   const int64_t most = (d.rows + 15) / 16;
   if (chunks > most) chunks = most;
@@ -469,6 +613,8 @@ LinearPlan plan_linear(const ss_linear_desc_t& d, int op) {
   pl.bytes = off;
   return pl;
 }
+
+LinearPlan plan_linear(const ss_linear_desc_t& d, int op) { return plan_bwd_fwd(d, op, false); }
 
 int launch_linear_fwd(const ss_linear_desc_t& d, const void* x, const void* w, const float* bias,
                       const void* residual, void* y, void* pre, char* ws, void* stream) {
@@ -495,40 +641,29 @@ int launch_linear_fwd(const ss_linear_desc_t& d, const void* x, const void* w, c
     return int(hipGetLastError());
   }
   const LinearPlan pl = plan_linear(d, SS_LINEAR_FWD);
-  Operands ops{d};
+  Operands ops{d.in_dtype == SS_BF16 ? 2 : 4};
   p.R = ops.take(x, &p.ldr, d.rows, d.in_dim, ws + pl.off_x);
   p.S = ops.take(w, &p.lds, d.out_dim, d.in_dim, ws + pl.off_w);
   ops.launch(st);
-  Tiling t = tiling(d, p.nR, p.nS, p.nT, false);
+  Tiling t = tiling_fwd(d, d.out_dim);
   t.tile = ops.tile(t.tile);
   run_mm(p, t, true, true, false, ws + pl.off_part, st);
   return int(hipGetLastError());
 }
 
-int launch_linear_bwd(const ss_linear_desc_t& d, const LinearPlan& pl, const void* x,
-                      const int8_t* q, const uint8_t* e, const void* w, const void* pre,
-                      const void* dy, void* dx, void* dw, float* dbias, char* ws, void* stream) {
-  hipStream_t st = static_cast<hipStream_t>(stream);
-  const bool dpre = pl.need_dpre && (dx || dw);
-  if (dbias || dpre) {
-    DpreParams p{dy, pre, dpre ? ws + pl.off_dpre : nullptr,
-                 dbias ? reinterpret_cast<float*>(ws + pl.off_sums) : nullptr, d.rows,
-                 pl.chunk_rows, int32_t(d.out_dim), int32_t(pl.ld_dpre), d.act, pl.sum2};
-    const int v = dpre_vec(d);
-    const int64_t cols = pad_to_unit(d, d.out_dim);
-    const dim3 grid(unsigned((cols + 64 * v - 1) / (64 * v)), unsigned(pl.chunks));
-    if (v == 8) dpre_types<8>(d, p, grid, st);
-    else dpre_types<1>(d, p, grid, st);
-    if (dbias)
-      launch_column_sums(p.part, dbias, nullptr, nullptr, pl.chunks, int32_t(d.out_dim), stream);
-  }
+// dx and dw of a dpre (rows of pl.ld_dpre, or d.out_dim, elements); odd: fp32 rows of it
+// that 16-byte units cannot read.
+static int backward_products(const ss_linear_desc_t& d, const LinearPlan& pl, const void* dpre,
+                             bool odd, const void* x, const int8_t* q, const uint8_t* e,
+                             const void* w, void* dx, void* dw, char* ws, void* stream) {
   MmParams p{};
-  p.R = dpre ? static_cast<const void*>(ws + pl.off_dpre) : dy;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  p.R = dpre;
   p.ldr = pl.need_dpre ? pl.ld_dpre : d.out_dim;
   p.nS = int32_t(d.in_dim);
   p.act = SS_ACT_NONE;
   p.out_bf16 = d.grad_dtype == SS_BF16;
-  Operands ops{d};
+  Operands ops{d.in_dtype == SS_BF16 ? 2 : 4};
   MmParams px = p, pw = p;
   px.lds = d.in_dim;
   pw.lds = d.x_stride ? d.x_stride : d.in_dim;
@@ -558,7 +693,7 @@ int launch_linear_bwd(const ss_linear_desc_t& d, const LinearPlan& pl, const voi
   ops.launch(st);
   char* const part = ws + pl.off_part;
   // one gradient alone is computed as it is beside the other: the same sums
-  if (!dpre && d.out_dim % unit_of(d) != 0) ops.any = true;     // dy in place (fp32)
+  if (odd) ops.any = true;
   Backward t = tilings_bwd(d, pl.sum2);
   t.dx.tile = ops.tile(t.dx.tile);
   t.dw.tile = ops.tile(t.dw.tile);
@@ -572,6 +707,182 @@ int launch_linear_bwd(const ss_linear_desc_t& d, const LinearPlan& pl, const voi
   } else {
     if (dx) run_mm(px, t.dx, true, false, pl.sum2, part, st);
     if (dw) run_mm(pw, t.dw, false, false, pl.sum2, part_dw, st);
+  }
+  return int(hipGetLastError());
+}
+
+int launch_linear_bwd(const ss_linear_desc_t& d, const LinearPlan& pl, const void* x,
+                      const int8_t* q, const uint8_t* e, const void* w, const void* pre,
+                      const void* dy, void* dx, void* dw, float* dbias, char* ws, void* stream) {
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  const bool dpre = pl.need_dpre && (dx || dw);
+  if (dbias || dpre) {
+    DpreParams p{dy, pre, dpre ? ws + pl.off_dpre : nullptr,
+                 dbias ? reinterpret_cast<float*>(ws + pl.off_sums) : nullptr, d.rows,
+                 pl.chunk_rows, int32_t(d.out_dim), int32_t(pl.ld_dpre), d.act, pl.sum2};
+    const int v = dpre_vec(d);
+    const int64_t cols = pad_to_unit(d, d.out_dim);
+    const dim3 grid(unsigned((cols + 64 * v - 1) / (64 * v)), unsigned(pl.chunks));
+    if (v == 8) dpre_types<8>(d, p, grid, st);
+    else dpre_types<1>(d, p, grid, st);
+    if (dbias)
+      launch_column_sums(p.part, dbias, nullptr, nullptr, pl.chunks, int32_t(d.out_dim), stream);
+  }
+  return backward_products(d, pl, dpre ? static_cast<const void*>(ws + pl.off_dpre) : dy,
+                           !dpre && d.out_dim % unit_of(d) != 0, x, q, e, w, dx, dw, ws, stream);
+}
+
+// Gated products: the projection's plan and launches with twice the columns.
+static ss_linear_desc_t both_halves(const ss_glu_desc_t& d) {
+  ss_linear_desc_t l{};
+  l.rows = d.rows;
+  l.in_dim = d.in_dim;
+  l.out_dim = 2 * d.out_dim;
+  l.x_stride = d.x_stride;
+  l.in_dtype = d.in_dtype;
+  l.out_dtype = d.out_dtype;
+  l.grad_dtype = d.grad_dtype;
+  l.act = SS_ACT_SILU;       // dpre is never dy itself
+  return l;
+}
+LinearPlan plan_glu(const ss_glu_desc_t& d, int op) {
+  const ss_linear_desc_t l = both_halves(d);
+  LinearPlan pl = plan_bwd_fwd(l, op == SS_GLU_FWD ? SS_LINEAR_FWD : SS_LINEAR_BWD, true);
+  return pl;
+}
+
+int launch_glu_fwd(const ss_glu_desc_t& d, const LinearPlan& pl, const void* x, const void* w,
+                   const float* bias, void* y, void* pre, char* ws, void* stream) {
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  const ss_linear_desc_t l = both_halves(d);
+  MmParams p{};
+  p.ldr = d.x_stride ? d.x_stride : d.in_dim;
+  p.lds = d.in_dim;
+  p.nR = d.rows;
+  p.nS = int32_t(d.out_dim);
+  p.nT = d.in_dim;
+  p.bias = bias;
+  p.out = y;
+  p.pre = pre;
+  p.act = d.act;
+  p.out_bf16 = d.out_dtype == SS_BF16;
+  p.pre_bf16 = d.in_dtype == SS_BF16;
+  if (d.rows <= kRowsMax) {
+    const int e = unit_of(l);
+    p.R = x;
+    p.S = w;
+    launch_rows_glu(p, d.in_dtype == SS_BF16, ptr16(x) && p.ldr % e == 0 && p.nT % e == 0, st);
+    return int(hipGetLastError());
+  }
+  Operands ops{d.in_dtype == SS_BF16 ? 2 : 4};
+  p.R = ops.take(x, &p.ldr, d.rows, d.in_dim, ws + pl.off_x);
+  p.S = ops.take(w, &p.lds, 2 * d.out_dim, d.in_dim, ws + pl.off_w);
+  ops.launch(st);
+  const Tiling t = tiling_fwd(l, l.out_dim);
+  p = tiled(p, t, ws + pl.off_part);
+  launch_mm_glu(p, ops.tile(t.tile), st);
+  if (p.splits > 1) {
+    const int64_t n = (p.nR * p.nS + kThreads - 1) / kThreads;
+    join_glu_kernel<<<unsigned(n < kMaxBlocks ? n : kMaxBlocks), kThreads, 0, st>>>(p);
+  }
+  return int(hipGetLastError());
+}
+
+template <typename Dy, typename T, int V>
+static void dglu_act(const DgluParams& p, int act, dim3 grid, hipStream_t st) {
+  switch (act) {
+    case SS_ACT_SILU: dglu_kernel<Dy, T, V, SS_ACT_SILU><<<grid, kThreads, 0, st>>>(p); break;
+    case SS_ACT_GELU: dglu_kernel<Dy, T, V, SS_ACT_GELU><<<grid, kThreads, 0, st>>>(p); break;
+    default: dglu_kernel<Dy, T, V, SS_ACT_NONE><<<grid, kThreads, 0, st>>>(p);
+  }
+}
+template <int V>
+static void dglu_types(const ss_glu_desc_t& d, const DgluParams& p, dim3 grid, hipStream_t st) {
+  const bool yb = d.out_dtype == SS_BF16, tb = d.in_dtype == SS_BF16;
+  if (yb && tb) dglu_act<uint16_t, uint16_t, V>(p, d.act, grid, st);
+  else if (yb) dglu_act<uint16_t, float, V>(p, d.act, grid, st);
+  else if (tb) dglu_act<float, uint16_t, V>(p, d.act, grid, st);
+  else dglu_act<float, float, V>(p, d.act, grid, st);
+}
+
+int launch_glu_bwd(const ss_glu_desc_t& d, const LinearPlan& pl, const void* x, const void* w,
+                   const void* pre, const void* dy, void* dx, void* dw, float* dbias, char* ws,
+                   void* stream) {
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  const ss_linear_desc_t l = both_halves(d);
+  const bool dpre = dx || dw;
+  const DgluParams p{dy, pre, dpre ? ws + pl.off_dpre : nullptr,
+                     dbias ? reinterpret_cast<float*>(ws + pl.off_sums) : nullptr, d.rows,
+                     pl.chunk_rows, int32_t(d.out_dim), int32_t(pl.ld_dpre), pl.sum2};
+  const int v = d.out_dim % 8 == 0 ? 8 : 1;
+  // with single columns, lanes past F clear the rows' last unit
+  const int64_t cols = v == 8 ? d.out_dim : d.out_dim + pad_to_unit(l, l.out_dim) - l.out_dim;
+  const dim3 grid(unsigned((cols + 64 * v - 1) / (64 * v)), unsigned(pl.chunks));
+  if (v == 8) dglu_types<8>(d, p, grid, st);
+  else dglu_types<1>(d, p, grid, st);
+  if (dbias)
+    launch_column_sums(p.part, dbias, nullptr, nullptr, pl.chunks, int32_t(l.out_dim), stream);
+  if (!dpre) return int(hipGetLastError());
+  return backward_products(l, pl, ws + pl.off_dpre, false, x, nullptr, nullptr, w, dx, dw, ws,
+                           stream);
+}
+
+// 8-bit integers: tiles, stages and splits as for bf16, at 128 of the contraction a stage.
+static Tiling tiling_q8(const ss_q8_desc_t& d) {
+  return tiling(Small(false, 1, d.rows, d.out_dim, d.in_dim));
+}
+Q8Plan plan_q8(const ss_q8_desc_t& d) {
+  Q8Plan pl;
+  if (d.rows <= kRowsMax) return pl;
+  auto take = [&](size_t bytes) {
+    const size_t at = pl.bytes;
+    pl.bytes += align256(bytes);
+    return at;
+  };
+  const int64_t units = (d.in_dim + 15) / 16 * 16;
+  if (d.in_dim % 16 != 0 || d.x_stride != 0) pl.off_x = take(size_t(d.rows) * size_t(units));
+  if (d.in_dim % 16 != 0 || d.w_stride != 0) pl.off_w = take(size_t(d.out_dim) * size_t(units));
+  pl.off_part = take(part_bytes(tiling_q8(d), d.rows, d.out_dim));
+  return pl;
+}
+int launch_q8_linear(const ss_q8_desc_t& d, const Q8Plan& pl, const int8_t* xq, const float* xs,
+                     const int8_t* wq, const float* wsc, const float* bias, const void* residual,
+                     void* y, char* ws, void* stream) {
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  MmParams p{};
+  p.ldr = d.x_stride ? d.x_stride : d.in_dim;
+  p.lds = d.w_stride ? d.w_stride : d.in_dim;
+  p.nR = d.rows;
+  p.nS = int32_t(d.out_dim);
+  p.nT = d.in_dim;
+  p.bias = bias;
+  p.res = residual;
+  p.out = y;
+  p.act = d.act;
+  p.out_bf16 = d.out_dtype == SS_BF16;
+  p.res_bf16 = d.res_dtype == SS_BF16;
+  p.row_scale = xs;
+  p.col_scale = wsc;
+  if (d.rows <= kRowsMax) {
+    p.R = xq;
+    p.S = wq;
+    launch_rows_q8(p, ptr16(xq) && ptr16(wq) && p.ldr % 16 == 0 && p.lds % 16 == 0 &&
+                          p.nT % 16 == 0, st);
+    return int(hipGetLastError());
+  }
+  Operands ops{1};
+  // rows of xq whose units are aligned are read in place: what lies behind an odd
+  // contraction's end, in the row's last unit, meets the zeros of w's copy
+  if (ptr16(xq) && p.ldr % 16 == 0) p.R = xq;
+  else p.R = ops.take(xq, &p.ldr, d.rows, d.in_dim, ws + pl.off_x);
+  p.S = ops.take(wq, &p.lds, d.out_dim, d.in_dim, ws + pl.off_w);
+  ops.launch(st);
+  const Tiling t = tiling_q8(d);
+  p = tiled(p, t, ws + pl.off_part);
+  launch_mm_q8(p, t.tile, st);
+  if (p.splits > 1) {
+    const int64_t n = (p.nR * p.nS + kThreads - 1) / kThreads;
+    join_q8_kernel<<<unsigned(n < kMaxBlocks ? n : kMaxBlocks), kThreads, 0, st>>>(p);
   }
   return int(hipGetLastError());
 }

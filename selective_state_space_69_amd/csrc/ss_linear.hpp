@@ -17,6 +17,7 @@ namespace ss {
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
 
 struct MmParams {
   const void* R;
@@ -35,6 +36,9 @@ struct MmParams {
   void* pre;             // (nR, nS) or null
   float* part;           // (splits, nR, nS) when splits > 1
   int32_t act, out_bf16, res_bf16, pre_bf16;
+  // 8-bit integers: R's and S's unit per row
+  const float* row_scale;
+  const float* col_scale;
 };
 
 // max(v, 0) in one instruction (fmaxf spends two more on quieting NaNs; a NaN here

@@ -27,11 +27,20 @@ void launch_mm(const MmParams& p, MmTile tile, bool rt, bool st, bool sum2, hipS
 void launch_mm_both(const MmParams& dx, const MmParams& dw, MmTile tile, int behind, int few,
                     bool sum2, hipStream_t stream);
 
+// Gated products (rt and st; tiles_s: of 128 outputs on kBig, 64 on the small bf16 tiles,
+// 32 on fp32 ones; no residual): S has 2 nS rows, bias 2 nS elements, pre rows of 2 nS.
+void launch_mm_glu(const MmParams& p, MmTile tile, hipStream_t stream);
+// 8-bit integers (rt and st; nT below 2^17), with row_scale and col_scale; a split's
+// partial sums are int32.
+void launch_mm_q8(const MmParams& p, MmTile tile, hipStream_t stream);
+
 // O = R S^T for at most kRowsMax rows of R (t contiguous in both), with the
 // epilogue; vec: both operands' rows are 16-byte aligned and nT is a whole number
-// of 16-byte units.  One launch, no splits.
+// of 16-byte units.  One launch, no splits.  _glu, _q8: as above.
 constexpr int64_t kRowsMax = 32;
 void launch_rows(const MmParams& p, bool bf16, bool vec, hipStream_t stream);
+void launch_rows_glu(const MmParams& p, bool bf16, bool vec, hipStream_t stream);
+void launch_rows_q8(const MmParams& p, bool vec, hipStream_t stream);
 
 // Accesses of the epilogue: to global memory (said so, since the parameters may have
 // come back from memory as plain words), eight neighbours at any element address
@@ -85,6 +94,20 @@ __device__ __forceinline__ void epilogue1(const MmParams& p, int act, int64_t r,
   v = apply_act(act, v);
   if (p.res) v += load1(p.res, o, p.res_bf16);
   store1(p.out, o, p.out_bf16, v);
+}
+
+// The same of two gated products: their sums, gate and up.
+__device__ __forceinline__ void glu1(const MmParams& p, int act, int64_t r, int32_t s, float gate,
+                                     float up) {
+  if (p.bias) {
+    gate += load1(p.bias, s, 0);
+    up += load1(p.bias, p.nS + s, 0);
+  }
+  if (p.pre) {
+    store1(p.pre, 2 * r * p.nS + s, p.pre_bf16, gate);
+    store1(p.pre, (2 * r + 1) * p.nS + s, p.pre_bf16, up);
+  }
+  store1(p.out, r * p.nS + s, p.out_bf16, up * apply_act(act, gate));
 }
 
 // Eight neighbours of the residual from element o on, fetched ahead in their storage

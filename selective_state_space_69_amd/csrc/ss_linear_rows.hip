@@ -12,6 +12,10 @@
 // Bound by memory and a launch's ramp: 8 rows, 2560 -> 10240 bf16 take 13.6 us (3.9
 // TB/s of w; 15.4 us with w always out of cache).  4 or 16 waves, twice the loads in
 // flight, whole lines per wave or streamed loads were no faster (15.4 to 17.6).
+//
+// Gated products: the 16 rows of w are 8 of each half, so that a workgroup has both
+// factors of 8 outputs.  8-bit integers: 64 of the contraction per MFMA; rows that are not
+// whole 16-byte units are read from any address, their last unit byte by byte.
 #include "ss_linear_mm.hpp"
 
 namespace ss {
@@ -20,9 +24,15 @@ namespace {
 constexpr int kWaves = 8;
 constexpr int kUnroll = 5;      // loads of w in flight per wave
 
-template <typename T>
-__device__ __forceinline__ f32x4 mma16(u32x4 a, u32x4 b, f32x4 c) {
-  if constexpr (sizeof(T) == 2) {
+enum { kMm, kGlu, kInt8 };     // what is multiplied and what comes of it
+
+template <typename T, typename Acc>
+__device__ __forceinline__ Acc mma16(u32x4 a, u32x4 b, Acc c) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  if constexpr (sizeof(T) == 1) {
+    return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, a),
+                                                 __builtin_bit_cast(i32x4, b), c, 0, 0, 0);
+  } else if constexpr (sizeof(T) == 2) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
                                                    __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
   } else {
@@ -30,8 +40,9 @@ __device__ __forceinline__ f32x4 mma16(u32x4 a, u32x4 b, f32x4 c) {
     for (int i = 0; i < 4; ++i)
       c = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(a[i]), __uint_as_float(b[i]), c, 0,
                                                0, 0);
-    return c;
   }
+#endif
+  return c;
 }
 
 // 16 bytes of a row from element t of n; VEC: n and the row's alignment allow
@@ -41,6 +52,13 @@ __device__ __forceinline__ u32x4 load_unit(const T* row, int t, int n) {
   constexpr int E = 16 / int(sizeof(T));
   if constexpr (VEC) {
     return t < n ? *reinterpret_cast<const u32x4*>(row + t) : u32x4{0, 0, 0, 0};
+  } else if constexpr (sizeof(T) == 1) {
+    struct __attribute__((packed, aligned(1))) Bytes { u32x4 v; };
+    if (t + E <= n) return reinterpret_cast<const Bytes*>(row + t)->v;
+    struct { T e[E]; } v;
+#pragma unroll
+    for (int j = 0; j < E; ++j) v.e[j] = t + j < n ? row[t + j] : T(0);
+    return __builtin_bit_cast(u32x4, v);
   } else {
     struct Elems { T e[E]; } v;
 #pragma unroll
@@ -50,23 +68,28 @@ __device__ __forceinline__ u32x4 load_unit(const T* row, int t, int n) {
 }
 
 // MB: fragments of x, 16 rows each
-template <typename T, int MB, bool VEC>
+template <typename T, int MB, bool VEC, int KIND>
 __global__ __launch_bounds__(kWaves * kWave) void rows_kernel(MmParams p) {
-  __shared__ float part[kWaves][MB][16][17];
+  using Acc = std::conditional_t<KIND == kInt8, i32x4, f32x4>;
+  using Sum = std::conditional_t<KIND == kInt8, int32_t, float>;
+  __shared__ Sum part[kWaves][MB][16][17];
   constexpr int E = 16 / int(sizeof(T));
   constexpr int kSpan = 4 * E;              // t per wave and step
+  constexpr int kCols = KIND == kGlu ? 8 : 16;
   const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
   const int m = lane & 15, g = lane >> 4;
-  const int s0 = int(blockIdx.x) * 16;
+  const int s0 = int(blockIdx.x) * kCols;
   const int K = int(p.nT);
-  const T* w = static_cast<const T*>(p.S) + int64_t(s0 + m < p.nS ? s0 + m : p.nS - 1) * p.lds;
+  int64_t col = s0 + m % kCols < p.nS ? s0 + m % kCols : p.nS - 1;
+  if (KIND == kGlu && m >= kCols) col += p.nS;
+  const T* w = static_cast<const T*>(p.S) + col * p.lds;
   const T* x[MB];
-  f32x4 acc[MB];
+  Acc acc[MB];
 #pragma unroll
   for (int b = 0; b < MB; ++b) {
     const int64_t r = b * 16 + m;
     x[b] = static_cast<const T*>(p.R) + (r < p.nR ? r : p.nR - 1) * p.ldr;
-    acc[b] = f32x4{0, 0, 0, 0};
+    acc[b] = Acc{0, 0, 0, 0};
   }
   for (int t0 = wv * kSpan + g * E; t0 - g * E < K; t0 += kUnroll * kWaves * kSpan) {
     u32x4 a[kUnroll], v[kUnroll][MB];
@@ -81,40 +104,52 @@ __global__ __launch_bounds__(kWaves * kWave) void rows_kernel(MmParams p) {
 #pragma unroll
       for (int b = 0; b < MB; ++b) acc[b] = mma16<T>(a[u], v[u][b], acc[b]);
   }
-  // lane: columns s0 + 4 g .. + 3 of row m
+  // lane: rows s0 + 4 g .. + 3 of w, row m of x
 #pragma unroll
   for (int b = 0; b < MB; ++b)
 #pragma unroll
     for (int j = 0; j < 4; ++j) part[wv][b][m][4 * g + j] = acc[b][j];
   __syncthreads();
-  for (int i = threadIdx.x; i < MB * 256; i += kWaves * kWave) {
-    const int b = i >> 8, row = (i >> 4) & 15, s = i & 15;
+  for (int i = threadIdx.x; i < MB * 16 * kCols; i += kWaves * kWave) {
+    const int b = i / (16 * kCols), row = i / kCols % 16, s = i % kCols;
     const int64_t r = b * 16 + row;
     if (r >= p.nR || s0 + s >= p.nS) continue;
-    float f = 0.0f;
+    Sum f = 0, up = 0;
 #pragma unroll
-    for (int k = 0; k < kWaves; ++k) f += part[k][b][row][s];
-    epilogue1(p, p.act, r, s0 + s, f);
+    for (int k = 0; k < kWaves; ++k) {
+      f += part[k][b][row][s];
+      if (KIND == kGlu) up += part[k][b][row][8 + s];
+    }
+    if constexpr (KIND == kGlu) glu1(p, p.act, r, s0 + s, f, up);
+    else if constexpr (KIND == kInt8)
+      epilogue1(p, p.act, r, s0 + s, float(f) * (p.row_scale[r] * p.col_scale[s0 + s]));
+    else epilogue1(p, p.act, r, s0 + s, f);
   }
 }
 
-template <typename T>
+template <typename T, int KIND>
 void run(const MmParams& p, bool vec, hipStream_t st) {
-  const unsigned blocks = unsigned((p.nS + 15) / 16), threads = kWaves * kWave;
+  constexpr int kCols = KIND == kGlu ? 8 : 16;
+  const unsigned blocks = unsigned((p.nS + kCols - 1) / kCols), threads = kWaves * kWave;
   if (p.nR <= 16) {
-    if (vec) rows_kernel<T, 1, true><<<blocks, threads, 0, st>>>(p);
-    else rows_kernel<T, 1, false><<<blocks, threads, 0, st>>>(p);
+    if (vec) rows_kernel<T, 1, true, KIND><<<blocks, threads, 0, st>>>(p);
+    else rows_kernel<T, 1, false, KIND><<<blocks, threads, 0, st>>>(p);
   } else {
-    if (vec) rows_kernel<T, 2, true><<<blocks, threads, 0, st>>>(p);
-    else rows_kernel<T, 2, false><<<blocks, threads, 0, st>>>(p);
+    if (vec) rows_kernel<T, 2, true, KIND><<<blocks, threads, 0, st>>>(p);
+    else rows_kernel<T, 2, false, KIND><<<blocks, threads, 0, st>>>(p);
   }
 }
 
 }  // namespace
 
 void launch_rows(const MmParams& p, bool bf16, bool vec, hipStream_t st) {
-  if (bf16) run<uint16_t>(p, vec, st);
-  else run<float>(p, vec, st);
+  if (bf16) run<uint16_t, kMm>(p, vec, st);
+  else run<float, kMm>(p, vec, st);
 }
+void launch_rows_glu(const MmParams& p, bool bf16, bool vec, hipStream_t st) {
+  if (bf16) run<uint16_t, kGlu>(p, vec, st);
+  else run<float, kGlu>(p, vec, st);
+}
+void launch_rows_q8(const MmParams& p, bool vec, hipStream_t st) { run<uint8_t, kInt8>(p, vec, st); }
 
 }  // namespace ss

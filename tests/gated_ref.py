@@ -1,10 +1,11 @@
-"""Plain 64-bit forms of a gated recurrent block's operators (gated linear recurrence),
-in torch on the CPU or the GPU, and the rounding bounds their tests use."""
+"""Plain 64-bit forms of a gated recurrent block's operators (gated linear recurrence, gated
+feed-forward half, projection in 8-bit integers), in torch on the CPU or the GPU, and the rounding bounds their tests use."""
 import math
 
 import torch
 
-from block_ref import U, HALF, check      # noqa: F401  (check: |got - ref| <= tol + half a step)
+from block_ref import U, HALF, act, act_grad, check, sum_depth      # noqa: F401
+# check: |got - ref| <= tol + half a step of got's type
 
 CHUNK = 64
 
@@ -163,3 +164,85 @@ class Rec:
             tol["dz"] = (dy * slope).abs() * self.tol_h + (dy * self.h).abs() * U * (
                 8 + 4 * zz.abs() + 2 * zz * zz)
         return out, {n: t + 1e-30 for n, t in tol.items()}
+
+
+# ------------------------------------------------- gated feed-forward half
+def _act_err(v):
+    """Rounding of act(v) and act'(v) at a given v (the functions: a few roundings of v and
+    of the result)."""
+    return U * (8 + 4 * v.abs() + 2 * v * v)
+
+
+def glu_fwd(x, w, bias, name):
+    """(y, pre, tol_y, tol_pre), float64, of x (M, K) and w (2 F, K)."""
+    xd, wd = x.double(), w.double()
+    pre = xd @ wd.t()
+    tol = U * sum_depth(x.shape[1], x.dtype) * (xd.abs() @ wd.abs().t())
+    if bias is not None:
+        pre = pre + bias.double()
+    tol = tol + U * pre.abs()
+    (gate, up), (tg, tu) = pre.chunk(2, 1), tol.chunk(2, 1)
+    a = act(name, gate)
+    ta = tg if name == "none" else 1.13 * tg + _act_err(gate)      # |act'| < 1.13
+    y = a * up
+    return y, pre, ta * (up.abs() + tu) + a.abs() * tu + 2 * U * y.abs(), tol
+
+
+def glu_bwd(x, w, dy, pre, name, grad_dtype):
+    """(dx, dw, dbias, tol_dx, tol_dw, tol_db), float64.  Bounds: d's own rounding, what the
+    products see of it (2^-8 of it with bf16 gradients of bf16 operands, 2^-16 with fp32
+    ones), and the contractions'."""
+    dt = w.dtype
+    xd, wd, d0 = x.double(), w.double(), dy.double()
+    gate, up = pre.double().chunk(2, 1)
+    d = torch.cat([d0 * up * act_grad(name, gate), d0 * act(name, gate)], 1)
+    fn = torch.cat([(d0 * up).abs() * _act_err(gate), d0.abs() * _act_err(gate)], 1) + 3 * U * d.abs()
+    seen = 0.0
+    if dt == torch.bfloat16:
+        seen = 2.0 ** -16 if grad_dtype == torch.float32 else HALF[dt]
+    err = fn + seen * d.abs()
+    a = d.abs() + err
+    dx, dw, db = d @ wd, d.t() @ xd, d.sum(0)
+    tol_dx = err @ wd.abs() + U * sum_depth(w.shape[0], dt) * (a @ wd.abs())
+    tol_dw = err.t() @ xd.abs() + U * sum_depth(x.shape[0], dt) * (a.t() @ xd.abs())
+    # a column sum: runs of 64 rows, the runs of a chunk, at most a quarter of 2048 chunks
+    rows = x.shape[0]
+    depth = min(rows, 64) + rows / 256 + 520
+    return dx, dw, db, tol_dx, tol_dw, fn.sum(0) + depth * U * a.sum(0)
+
+
+# ------------------------------------------------- 8-bit integers
+def q8_pack(x):
+    """(q, s) by exact integer arithmetic in 64 bits: q = round(127 x / max), ties to even, by
+    comparing 2 * 127 |x| with odd multiples of max."""
+    d = x.double()
+    top = d.abs().amax(-1, keepdim=True)
+    fine = torch.isfinite(top)
+    m = torch.where(fine & (top > 0), top, torch.ones_like(top))
+    v = torch.where(fine, d.abs(), torch.zeros_like(d))
+    f = torch.floor(127.0 * v / m)
+    f = torch.where(127.0 * v < f * m, f - 1, f)
+    f = torch.where(127.0 * v >= (f + 1) * m, f + 1, f)
+    a, b = 254.0 * v, (2 * f + 1) * m
+    f = f + ((a > b) | ((a == b) & (f % 2 == 1)))
+    q = torch.where(d < 0, -f, f).to(torch.int8)
+    # (by a tensor: torch multiplies by the rounded reciprocal of a plain number)
+    s = (torch.where(fine, top, torch.full_like(top, math.nan)) / torch.full_like(top, 127.0))[..., 0].float()
+    return q, s
+
+
+def q8_linear(x, w, bias, residual, name):
+    """(y, tol) of packed x and w, float64: the sums are exact, the epilogue rounds."""
+    (xq, xs), (wq, ws) = x, w
+    v = (xq.double() @ wq.double().t()) * xs.double()[:, None] * ws.double()
+    tol = 3 * U * v.abs()                    # the sum to fp32, both scales
+    if bias is not None:
+        v = v + bias.double()
+        tol = tol + U * v.abs()
+    y = act(name, v)
+    if name != "none":
+        tol = 1.13 * tol + _act_err(v)
+    if residual is not None:
+        y = y + residual.double()
+        tol = tol + U * y.abs()
+    return y, tol

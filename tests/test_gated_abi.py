@@ -126,8 +126,10 @@ def test_rec_workspace_follows_the_plan():
 
 
 def test_descriptors_match_the_headers(tmp_path):
-    structs = [("ss_rec_desc_t", B.ss_rec_desc_t)]
-    src = ['#include <stdio.h>', '#include <stddef.h>', '#include "ss_rec.h"', "int main(void) {"]
+    structs = [("ss_rec_desc_t", B.ss_rec_desc_t), ("ss_glu_desc_t", B.ss_glu_desc_t),
+               ("ss_q8_pack_desc_t", B.ss_q8_pack_desc_t), ("ss_q8_desc_t", B.ss_q8_desc_t)]
+    src = ['#include <stdio.h>', '#include <stddef.h>', '#include "ss_rec.h"', '#include "ss_glu.h"',
+           '#include "ss_q8.h"', "int main(void) {"]
     want = []
     for name, t in structs:
         src.append('printf("%%zu\\n", sizeof(%s));' % name)
@@ -144,8 +146,8 @@ def test_descriptors_match_the_headers(tmp_path):
 
 
 def test_headers_name_every_constant():
-    text = open(os.path.join(ROOT, "include", "ss_rec.h")).read()
-    for name in ("SS_REC_CHUNK", "SS_REC_FWD", "SS_REC_BWD"):
+    text = "".join(open(os.path.join(ROOT, "include", h)).read() for h in ("ss_rec.h", "ss_glu.h"))
+    for name in ("SS_REC_CHUNK", "SS_REC_FWD", "SS_REC_BWD", "SS_GLU_FWD", "SS_GLU_BWD"):
         m = re.search(r"#define %s (\d+)" % name, text)
         assert m and int(m.group(1)) == getattr(B, name)
     assert ref.CHUNK == B.SS_REC_CHUNK
@@ -180,7 +182,191 @@ def test_binding_refuses():
         B._rec_step(0, torch.zeros(2, 8), x, x, x, lam, None, 8.0, torch.float32)
 
 
+# ------------------------------------------------ gated feed-forward half
+def glu_desc(**kw):
+    return B.make_glu_desc(**{**dict(rows=64, in_dim=64, out_dim=64), **kw})
+
+
+def glu_fwd(d, **kw):
+    a = {**dict(x=at(0), w=at(1), bias=None, y=at(2), pre=None, workspace=at(3), ws_bytes=1 << 40), **kw}
+    return B.ss_glu_fwd(d, *a.values(), stream=0)
+
+
+def glu_bwd(d, **kw):
+    a = {**dict(x=at(0), w=at(1), pre=at(2), dy=at(3), dx=at(4), dw=at(5), dbias=None, workspace=at(6),
+                ws_bytes=1 << 40), **kw}
+    return B.ss_glu_bwd(d, *a.values(), stream=0)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(rows=0), INV), (dict(rows=(1 << 28) + 1), INV), (dict(in_dim=0), INV),
+    (dict(in_dim=(1 << 20) + 1), INV), (dict(out_dim=0), INV), (dict(out_dim=(1 << 19) + 1), INV),
+    (dict(rows=1 << 28, in_dim=256), INV), (dict(rows=1 << 28, out_dim=65), INV),
+    (dict(in_dim=1 << 20, out_dim=1 << 15), INV), (dict(x_stride=63), INV),
+    (dict(x_stride=(1 << 20) + 1), INV), (dict(in_dtype=2), UNS), (dict(out_dtype=-1), UNS),
+    (dict(act=B.SS_ACT_SOFTPLUS), UNS), (dict(act=-1), UNS),
+])
+def test_glu_descriptor(kw, code):
+    if kw == dict(in_dim=1 << 20, out_dim=1 << 15):       # w of 2^36 elements
+        kw = {**kw, "rows": 1}
+    d = glu_desc(**kw)
+    assert glu_fwd(d) == code and glu_bwd(d) == code
+    for op in (0, 1):
+        assert B.ss_glu_workspace_bytes(d, op) == 0
+    assert B.ss_glu_workspace_bytes(glu_desc(), 2) == 0
+    assert glu_bwd(glu_desc(grad_dtype=5)) == UNS
+    assert glu_fwd(glu_desc(grad_dtype=5), y=None) == INV        # not read by the forward
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(x=None), INV), (dict(w=None), INV), (dict(y=None), INV), (dict(y=at(0)), INV),
+    (dict(y=at(4), pre=at(4)), INV), (dict(pre=at(1)), INV), (dict(bias=at(2)), INV),
+    (dict(x=at(0) + 2), INV), (dict(w=at(1) + 8), INV), (dict(pre=at(5) + 2), INV),
+])
+def test_glu_fwd_arguments(kw, code):
+    assert glu_fwd(glu_desc(), **kw) == code
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(w=None), INV), (dict(pre=None), INV), (dict(dy=None), INV), (dict(x=None), INV),
+    (dict(dx=None, dw=None), INV), (dict(dx=at(3)), INV), (dict(dw=at(0)), INV), (dict(dx=at(5)), INV),
+    (dict(dbias=at(2)), INV), (dict(dy=at(3) + 2), INV), (dict(dw=at(5) + 8), INV),
+    (dict(workspace=None), WSP), (dict(ws_bytes=64), WSP), (dict(workspace=at(6) + 16), WSP),
+])
+def test_glu_bwd_arguments(kw, code):
+    assert glu_bwd(glu_desc(), **kw) == code
+
+
+def test_glu_workspace():
+    """d of both halves, doubled where one bf16 per value cannot hold it; none to decode."""
+    assert B.ss_glu_workspace_bytes(glu_desc(rows=8), B.SS_GLU_FWD) == 0
+    one = B.ss_glu_workspace_bytes(glu_desc(rows=512), B.SS_GLU_BWD)
+    two = B.ss_glu_workspace_bytes(glu_desc(rows=512, grad_dtype=B.SS_F32), B.SS_GLU_BWD)
+    assert one >= 512 * 128 * 2 and two >= one + 512 * 128 * 2
+
+
+# ------------------------------------------------ 8-bit integers
+def q8_linear(d, **kw):
+    a = {**dict(xq=at(0), xs=at(1), wq=at(2), ws=at(3), bias=None, residual=None, y=at(4), workspace=at(5),
+                ws_bytes=1 << 40), **kw}
+    return B.ss_q8_linear(d, *a.values(), stream=0)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(rows=0), INV), (dict(rows=1 << 31), INV), (dict(dim=0), INV), (dict(dim=(1 << 20) + 1), INV),
+    (dict(x_stride=63), INV), (dict(q_stride=63), INV), (dict(q_stride=(1 << 20) + 1), INV), (dict(dtype=2), UNS),
+])
+def test_q8_pack_descriptor(kw, code):
+    d = B.make_q8_pack_desc(**{**dict(rows=4, dim=64), **kw})
+    assert B.ss_q8_pack(d, at(0), at(1), at(2), stream=0) == code
+
+
+def test_q8_pack_arguments():
+    d = B.make_q8_pack_desc(4, 64)
+    for a in ((None, at(1), at(2)), (at(0), None, at(2)), (at(0), at(1), None), (at(0), at(0), at(2)),
+              (at(0), at(1), at(1)), (at(0), at(1), at(0)), (at(0) + 2, at(1), at(2)), (at(0), at(1) + 8, at(2)),
+              (at(0), at(1), at(2) + 4)):
+        assert B.ss_q8_pack(d, *a, stream=0) == INV
+    d.reserved = 1
+    assert B.ss_q8_pack(d, at(0), at(1), at(2), stream=0) == INV
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(rows=0), INV), (dict(rows=(1 << 28) + 1), INV), (dict(in_dim=0), INV), (dict(in_dim=(1 << 16) + 1), INV),
+    (dict(out_dim=0), INV), (dict(out_dim=(1 << 20) + 1), INV), (dict(rows=1 << 28, in_dim=129), INV),
+    (dict(rows=1 << 28, out_dim=129), INV), (dict(x_stride=63), INV), (dict(w_stride=63), INV),
+    (dict(w_stride=(1 << 20) + 1), INV), (dict(out_dtype=2), UNS), (dict(res_dtype=7), UNS), (dict(act=4), UNS),
+])
+def test_q8_descriptor(kw, code):
+    d = B.make_q8_desc(**{**dict(rows=64, in_dim=64, out_dim=64), **kw})
+    assert q8_linear(d) == code
+    assert B.ss_q8_workspace_bytes(d) == 0
+    d.reserved = 1
+    assert q8_linear(d) != B.SS_OK
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(xq=None), INV), (dict(xs=None), INV), (dict(wq=None), INV), (dict(ws=None), INV), (dict(y=None), INV),
+    (dict(y=at(0)), INV), (dict(y=at(3)), INV), (dict(bias=at(4)), INV), (dict(xq=at(0) + 8), INV),
+    (dict(wq=at(2) + 1), INV), (dict(xs=at(1) + 4), INV), (dict(residual=at(6) + 2), INV),
+    (dict(workspace=None), WSP), (dict(ws_bytes=64), WSP),
+])
+def test_q8_arguments(kw, code):
+    assert q8_linear(B.make_q8_desc(64, 63, 64), **kw) == code
+    if code == INV:
+        d = B.make_q8_desc(64, 63, 64, out_dtype=B.SS_F32, res_dtype=B.SS_BF16)
+        assert q8_linear(d, residual=at(4)) == INV         # in place only in one type
+
+
+def test_more_binding_refusals():
+    x, w = torch.zeros(3, 8), torch.zeros(10, 8)
+    with pytest.raises(ValueError, match="on the GPU"):
+        B.glu_fwd(x, w)
+    with pytest.raises(KeyError):
+        B.glu_fwd(x, w, act="softplus")
+    fwd = B._glu_fwd
+    for a, what in [((x, torch.zeros(9, 8), None), "rows"), ((torch.zeros(3, 7), w, None), "columns"),
+                    ((x.bfloat16(), w, None), "one dtype"), ((x, w, torch.zeros(5)), "bias must have shape"),
+                    ((x, w, torch.zeros(10).bfloat16()), "bias must be float32")]:
+        with pytest.raises(ValueError, match=what):
+            fwd(0, *a, B.SS_ACT_SILU, torch.float32, False)
+    pre, dy = torch.zeros(3, 10), torch.zeros(3, 5)
+    for a, what in [((None, w, dy, pre), "dw needs x"), ((x, w, torch.zeros(3, 4), pre), "dy must have shape"),
+                    ((x, w, dy, pre[:, :8]), "pre must have shape"), ((x, w, dy, pre.bfloat16()), "w's dtype"),
+                    ((x[:2], w, dy, pre), "x must have shape"), ((x.bfloat16(), w, dy, pre), "one dtype")]:
+        with pytest.raises(ValueError, match=what):
+            B._glu_bwd(0, *a, B.SS_ACT_SILU, False, torch.float32, True, True)
+    q, s = torch.zeros(3, 8, dtype=torch.int8), torch.zeros(3)
+    wq, ws = torch.zeros(5, 8, dtype=torch.int8), torch.zeros(5)
+    with pytest.raises(ValueError, match="on the GPU"):
+        B.q8_linear((q, s), (wq, ws))
+    for a, what in [((q[:, :7], s, wq, ws), "columns"), ((q.float(), s, wq, ws), "int8"),
+                    ((q, s.bfloat16(), wq, ws), "float32"), ((q, s[:2], wq, ws), "x's scales must have shape"),
+                    ((q, s, wq, ws[:4]), "w's scales must have shape")]:
+        with pytest.raises(ValueError, match=what):
+            B._q8_linear(0, *a, None, None, 0, torch.float32)
+    with pytest.raises(ValueError, match="residual must have shape"):
+        B._q8_linear(0, q, s, wq, ws, None, torch.zeros(3, 4), 0, torch.float32)
+
+
 # ------------------------------------------------ the 64-bit forms
+def test_reference_glu_gradients():
+    g = torch.Generator().manual_seed(3)
+    x, w, dy = (torch.randn(s, generator=g, dtype=torch.float64) for s in ((5, 4), (6, 4), (5, 3)))
+    b = torch.randn(6, generator=g, dtype=torch.float64)
+    for name in ("silu", "gelu", "none"):
+        def loss():
+            return float((ref.glu_fwd(x, w, b, name)[0] * dy).sum())
+        pre = x @ w.t() + b
+        grads = ref.glu_bwd(x, w, dy, pre, name, torch.float64)[:3]
+        for t, grad in zip((x, w, b), grads):
+            for i in range(t.numel()):
+                old = float(t.view(-1)[i])
+                t.view(-1)[i] = old + 1e-6
+                up = loss()
+                t.view(-1)[i] = old - 1e-6
+                dn = loss()
+                t.view(-1)[i] = old
+                assert abs((up - dn) / 2e-6 - float(grad.reshape(-1)[i])) < 1e-7
+
+
+def test_reference_q8_is_its_definition():
+    """Against whole-number arithmetic without rounding."""
+    from fractions import Fraction
+    g = torch.Generator().manual_seed(4)
+    x = torch.randn(6, 50, generator=g)
+    x[0] = torch.arange(50) * 0.5                  # many ties: 127 x / 24.5 in halves
+    x[0, 49] = 63.5
+    x[1] = 0.0
+    x[2, 7] = float("inf")
+    q, s = ref.q8_pack(x)
+    assert not bool(q[1:3].any()) and float(s[1]) == 0.0 and bool(torch.isnan(s[2]))
+    for row in (0, 3, 4, 5):
+        top = max(abs(Fraction(float(v))) for v in x[row])
+        for c in range(50):
+            assert int(q[row, c]) == round(127 * Fraction(float(x[row, c])) / top)     # ties to even
+
+
 def _rec_inputs(b=2, l=9, d=3):
     g = torch.Generator().manual_seed(7)
 

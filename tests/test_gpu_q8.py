@@ -1,0 +1,169 @@
+"""Rows as 8-bit integers and their product on the GPU against exact arithmetic."""
+import pytest
+import torch
+
+import gated_ref as ref
+from selective_state_space_69_amd import binding as B
+
+pytestmark = pytest.mark.gpu
+DT = {"f32": torch.float32, "bf16": torch.bfloat16}
+BF, F32 = torch.bfloat16, torch.float32
+
+
+def rng(seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return lambda *s: torch.randn(*s, generator=g, device="cuda")
+
+
+def same_pack(x):
+    q, s = B.q8_pack(x)
+    wq, ws = ref.q8_pack(x)
+    assert torch.equal(q, wq)
+    assert torch.equal(torch.isnan(s), torch.isnan(ws))
+    assert torch.equal(torch.nan_to_num(s), torch.nan_to_num(ws))
+    return q, s
+
+
+@pytest.mark.parametrize("m,k", [(1, 1), (3, 7), (8, 2560), (5, 16), (4, 2049), (7, 5000), (2, 20001),
+                                 (5000, 33), (4096, 512), (4100, 1000), (4097, 2048), (300, 8192), (1, 131072)])
+@pytest.mark.parametrize("in_t", ["bf16", "f32"])
+def test_pack(m, k, in_t):
+    r = rng(m + k)
+    same_pack((r(m, k) * torch.exp(r(m, 1))).to(DT[in_t]))
+    wide = r(m, k + 5).to(DT[in_t])
+    same_pack(wide[:, 3:3 + k])
+
+
+def test_pack_ties_and_extremes():
+    """Quotients at and next to halves, rows of zeros, of one value, denormal, largest and
+    non-finite."""
+    half = torch.arange(-127, 127, device="cuda", dtype=torch.float64) + 0.5
+    for top in (127.0, 254.0, 127.0 * 2 ** -100, 127.0 * 2.0 ** 100):
+        v = half * top / 127.0
+        rows = [torch.cat([v, torch.tensor([top, -top], device="cuda", dtype=torch.float64)]).float()]
+        rows += [torch.cat([torch.nextafter(rows[0][:254], torch.full((254,), s, device="cuda")), rows[0][254:]])
+                 for s in (1e38, -1e38)]
+        q, _ = same_pack(torch.stack(rows))
+        assert int(q[0, 0]) == -126 and int(q[0, 126]) == 0 and int(q[0, 128]) == 2      # ties to even
+    r = rng(1)
+    x = r(9, 100)
+    x[0] = 0.0
+    x[1] = -3.0
+    x[2] *= 1e-42
+    x[3] *= 1e38
+    x[4, 50] = float("inf")
+    x[5, 51] = float("nan")
+    x[6, 1:] *= 1e-30
+    q, s = same_pack(x)
+    assert not bool(q[0].any()) and float(s[0]) == 0.0
+    assert bool((q[1] == -127).all())
+    assert bool(torch.isnan(s[4:6]).all()) and not bool(q[4:6].any())
+    # the error of a value is at most half a unit
+    err = (q.double() * s.double()[:, None] - x.double()).abs()
+    ok = torch.isfinite(s) & (s > 1e-36)
+    assert bool((err[ok] <= 0.5000002 * s[ok].double()[:, None]).all())
+    same_pack(x.bfloat16())
+
+
+def make(m, k, n, seed=0, in_t=BF):
+    r = rng(seed + m + 3 * k + 7 * n)
+    x = (r(m, k) * torch.exp(0.5 * r(m, 1))).to(in_t)
+    w = r(n, k) / k ** 0.5
+    return B.q8_pack(x), B.q8_pack(w), 0.3 * r(n), r(m, n)
+
+
+# the few-row kernels, every tile kernel, splits, ragged edges
+SHAPES = [(1, 1, 1), (1, 16, 16), (5, 100, 33), (8, 2560, 640), (32, 333, 70), (33, 16, 64),
+          (64, 96, 200), (100, 257, 129), (128, 128, 128), (300, 770, 331), (1024, 160, 1280),
+          (2048, 768, 1536), (511, 1000, 130), (70, 5000, 64), (700, 65536, 40), (4100, 200, 4200)]
+
+
+@pytest.mark.parametrize("m,k,n", SHAPES)
+@pytest.mark.parametrize("name", ["none", "silu", "gelu", "softplus"])
+def test_linear(m, k, n, name):
+    x, w, b, res = make(m, k, n)
+    for out, bias, r in ((BF, None, None), (F32, b, res), (BF, b, res.to(BF)), (F32, None, res.to(BF))):
+        y, tol = ref.q8_linear(x, w, bias, r, name)
+        got = B.q8_linear(x, w, bias, residual=r, act=name, out_dtype=out)
+        ref.check(got, y, tol, "y")
+        assert torch.equal(got, B.q8_linear(x, w, bias, residual=r, act=name, out_dtype=out))
+
+
+@pytest.mark.parametrize("m", [20, 200, 4100])
+def test_sums_are_exact(m):
+    """Integers of every value, -128 among them, at unit scales: the sums themselves."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(m)
+    xq = torch.randint(-128, 128, (m, 300), generator=g, device="cuda", dtype=torch.int8)
+    wq = torch.randint(-128, 128, (500, 300), generator=g, device="cuda", dtype=torch.int8)
+    one = torch.ones(max(m, 500), device="cuda")
+    got = B.q8_linear((xq, one[:m]), (wq, one[:500]), out_dtype=F32)
+    assert torch.equal(got.double(), xq.double() @ wq.double().t())
+    xq.fill_(-128)
+    wq.fill_(-128)
+    got = B.q8_linear((xq, one[:m]), (wq, one[:500]), out_dtype=F32)
+    assert bool((got == 300 * 16384).all())
+
+
+@pytest.mark.parametrize("m", [9, 150])
+@pytest.mark.parametrize("k,xs,xo,ws,wo", [(64, 80, 0, 64, 0), (64, 80, 16, 96, 32), (61, 64, 0, 64, 0), (61, 70, 3, 67, 5),
+                                           (50, 64, 1, 50, 0), (48, 48, 0, 51, 2)])
+def test_strided(m, k, xs, xo, ws, wo):
+    """Rows apart, at odd offsets, with bytes between them that must not count."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(k + xs)
+    x = torch.randint(-127, 128, (m, xs + xo), generator=g, device="cuda", dtype=torch.int8)
+    w = torch.randint(-127, 128, (70, ws + wo), generator=g, device="cuda", dtype=torch.int8)
+    one = torch.ones(m + 70, device="cuda")
+    xq, wq = x[:, xo:xo + k], w[:, wo:wo + k]
+    got = B.q8_linear((xq, one[:m]), (wq, one[:70]), out_dtype=F32)
+    assert torch.equal(got.double(), xq.double() @ wq.double().t())
+
+
+def test_non_finite_rows():
+    x, w, b, _ = make(40, 64, 48)
+    y = B.q8_linear(x, w, b, out_dtype=F32)
+    x[1][3] = float("nan")
+    w[1][5] = float("inf")
+    z = B.q8_linear(x, w, b, out_dtype=F32)
+    assert bool(torch.isnan(z[3]).all()) and not bool(torch.isfinite(z[:, 5]).any())
+    z[3], z[:, 5] = y[3], y[:, 5]
+    assert torch.equal(z, y)
+
+
+def test_residual_in_place():
+    x, w, b, res = make(200, 96, 130)
+    want = B.q8_linear(x, w, b, residual=res, out_dtype=F32)
+    d = B.make_q8_desc(200, 96, 130, out_dtype=B.SS_F32, res_dtype=B.SS_F32)
+    n = B.ss_q8_workspace_bytes(d)
+    ws = B.workspace(n, res.device)
+    y = res.clone()
+    assert B.ss_q8_linear(d, x[0], x[1], w[0], w[1], b, y, y, ws, n) == 0
+    assert torch.equal(y, want)
+
+
+def test_graph_and_stream():
+    for m in (8, 300):
+        r = rng(m)
+        x = r(m, 300).to(BF)
+        w = B.q8_pack(r(400, 300))
+
+        def call():
+            return B.q8_linear(B.q8_pack(x), w, act="silu")
+        call()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            held = call()
+        for turn in range(3):
+            x.copy_(r(m, 300))
+            graph.replay()
+            want = call()
+            torch.cuda.synchronize()
+            assert torch.equal(held, want)
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        y = B.q8_linear(B.q8_pack(x, stream=side), w, act="silu", stream=side)
+        torch.cuda.current_stream().wait_stream(side)
+        assert torch.equal(y, want)
