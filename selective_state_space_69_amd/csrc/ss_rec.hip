@@ -1,7 +1,7 @@
 // Gated linear recurrence for gfx950: forward, chunk carries, decode step, plan.
-// Decay codes and the layout of a wave are those of ss_rec.hpp.
+// Layout and accuracy: ss_rec.hpp.
 //
-// The forward moves each tensor once and is bound by memory.  A workgroup takes 64
+// The forward moves each tensor once and is bound by memory.  A workgroup takes 32
 // channels of one batch row and walks its time in blocks, the next block's rows being
 // loaded while the present one is computed; one barrier per block joins the waves.  Few
 // channels (one long sequence) would leave the GPU empty: their time is cut into chunks,
@@ -11,7 +11,9 @@
 namespace ss {
 namespace {
 
-constexpr int kWaves = 8;
+constexpr int kS = 8;                       // steps of a lane's stretch
+constexpr int kWaveSteps = kSubs * kS;
+constexpr int kWaves = 4;
 constexpr int kBlock = kWaves * kWaveSteps;
 static_assert(SS_REC_CHUNK % kWaveSteps == 0 && kBlock % SS_REC_CHUNK == 0,
               "states are kept at a wave's first step");
@@ -25,7 +27,7 @@ struct FwdParams {
   const int32_t* lengths;
   void* y;
   float *h_last, *states;
-  float *clog, *cend;        // (B, nchunks, D) chunks' log decays; end, then start states
+  float *cdec, *cend;        // (B, nchunks, D) chunks' decays; end, then start states
   int32_t out_bf16;
 };
 
@@ -34,7 +36,6 @@ template <typename T, bool Z, bool MASK, bool ANY, bool SUM>
 __global__ __launch_bounds__(kWaves * 64, 4) void rec_fwd_kernel(FwdParams p) {
 #if defined(__HIP_DEVICE_COMPILE__)
   __shared__ float tc[2][kWaves][kRecChans], ts[2][kWaves][kRecChans];
-  __shared__ float tl[SUM ? 2 : 1][SUM ? kWaves : 1][kRecChans];
   const Place at(p.s);
   const int32_t D = p.s.D;
   const int64_t L = p.s.L, row0 = int64_t(at.b) * L;
@@ -42,16 +43,16 @@ __global__ __launch_bounds__(kWaves * 64, 4) void rec_fwd_kernel(FwdParams p) {
   Masks masks;
   masks.init<MASK>(p.starts, p.lengths, at.b, L, t0, p.s.chunk);
   const int64_t crow = int64_t(at.b * p.s.nchunks + at.chunk) * D + at.c;
-  float k[4], H[4] = {0, 0, 0, 0}, lsum[4] = {0, 0, 0, 0};
+  float k[kV], H[kV] = {0, 0}, dec[kV] = {1, 1};
   load_f32(p.lam + at.c, at.n, k);
 #pragma unroll
-  for (int j = 0; j < 4; ++j) k[j] = rec_rate(p.s.decay, k[j]);
+  for (int j = 0; j < kV; ++j) k[j] = rec_rate(p.s.decay, k[j]);
   if (!SUM) {
     if (p.s.nchunks > 1) load_f32(p.cend + crow, at.n, H);
     else if (p.h0) load_f32(p.h0 + int64_t(at.b) * D + at.c, at.n, H);
   }
   const int off = at.wv * kWaveSteps + at.sub * kS;      // of the lane's stretch in a block
-  const int li = (at.lane & 15) * 4;
+  const int li = at.lane % kRecLanes * kV;
 
   Stream<ANY> px, pr, pi, pz, py;
   px.init(p.x, p.ldx, sizeof(T), p.s, row0 + t0, off, at);
@@ -59,7 +60,7 @@ __global__ __launch_bounds__(kWaves * 64, 4) void rec_fwd_kernel(FwdParams p) {
   pi.init(p.i, p.ldi, sizeof(T), p.s, row0 + t0, off, at);
   if constexpr (Z && !SUM) pz.init(p.z, p.ldz, sizeof(T), p.s, row0 + t0, off, at);
   if constexpr (!SUM) py.init(p.y, D, p.out_bf16 ? 2 : 4, p.s, row0 + t0, off, at);
-  Rows<T, ANY> x, r, i, z;
+  Rows<T, kS, ANY> x, r, i, z;
   int valid = masks.steps - off;           // steps of the lane's stretch inside the chunk
   x.load(px, valid);
   r.load(pr, valid);
@@ -67,27 +68,30 @@ __global__ __launch_bounds__(kWaves * 64, 4) void rec_fwd_kernel(FwdParams p) {
   if constexpr (Z && !SUM) z.load(pz, valid);
   for (int tb = 0, buf = 0; tb < masks.steps; tb += kBlock, buf ^= 1) {
     const int live = masks.len - tb - off;
-    bool start[kS] = {false, false, false, false};
+    bool start[kS] = {};
     if constexpr (MASK) masks.marks(tb + off, start);
-    float c[kS][4], g[kS][4], l[4] = {0, 0, 0, 0}, s[4] = {0, 0, 0, 0};
+    float c[kS][kV], g[kS][kV], l[kV] = {0, 0}, s[kV] = {0, 0};
+    bool cuts = false;
 #pragma unroll
     for (int e = 0; e < kS; ++e) {
-      float xv[4], rv[4], iv[4];
+      float xv[kV], rv[kV], iv[kV];
       unpack(x.q[e], xv);
       unpack(r.q[e], rv);
       unpack(i.q[e], iv);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const bool in = e < live, cut = MASK && start[e] && in;
+      for (int j = 0; j < kV; ++j) {
+        const bool in = e < live;
         float l2 = k[j] * sigmoid(rv[j]);
         l2 = in ? l2 : 0.0f;
-        const float E = precise_expm1(l2), code = rec_code(E);
-        const float add = __builtin_amdgcn_sqrtf(-E * (2.0f + E)) * sigmoid(iv[j]) * xv[j];
-        c[e][j] = cut ? 0.0f : code;
+        const Decay d = rec_decay(l2);
+        const float add = d.beta * sigmoid(iv[j]) * xv[j];
+        const bool cut = MASK && start[e] && in;
+        c[e][j] = MASK ? (cut ? 0.0f : __builtin_fmaxf(d.a, kTiny)) : d.a;
         g[e][j] = in ? add : 0.0f;
-        l[j] += cut ? -__builtin_inff() : l2;
+        l[j] += l2;
         s[j] = rec_apply<MASK>(c[e][j], s[j], g[e][j]);
       }
+      if (MASK) cuts |= start[e] && e < live;
     }
     // the next block's rows arrive under the rest of this one's work (z under the next's)
     const int now = valid;
@@ -101,50 +105,29 @@ __global__ __launch_bounds__(kWaves * 64, 4) void rec_fwd_kernel(FwdParams p) {
       r.load(pr, valid);
       i.load(pi, valid);
     }
-    // the wave's stretches: pairs of rows, then halves
-    float cx[4], sx[4];                   // of the rows below this lane's
-    float cw[4], sw[4], lw[4];            // of the wave
+    float cx[kV], sx[kV], cw[kV];            // of the stretches in front of the lane's, of the wave
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      float l0, l1, s0, s1, c0, c1;
-      swap_rows(l[j], l0, l1);
-      swap_rows(s[j], s0, s1);
-      swap_rows(rec_code_log2<MASK>(l[j]), c0, c1);
-      const float lp = l0 + l1, sp = rec_apply<MASK>(c1, s0, s1);
-      float p0, p1, q0, q1, u0, u1;
-      swap_halves(lp, p0, p1);
-      swap_halves(sp, q0, q1);
-      swap_halves(rec_code_log2<MASK>(lp), u0, u1);
-      lw[j] = p0 + p1;
-      cw[j] = rec_code_log2<MASK>(lw[j]);
-      sw[j] = rec_apply<MASK>(u1, q0, q1);
-      const float lb = at.sub >= 2 ? p0 : 0.0f, sb = at.sub >= 2 ? q0 : 0.0f;
-      const float lo = at.sub & 1 ? l0 : 0.0f, so = rec_apply<MASK>(c0, sb, s0);
-      cx[j] = rec_code_log2<MASK>(lb + lo);
-      sx[j] = at.sub & 1 ? so : sb;
+    for (int j = 0; j < kV; ++j) {
+      cw[j] = rec_decay_of<MASK>(l[j], cuts);
+      join_up<MASK>(at.sub, cw[j], s[j], cx[j], sx[j]);
     }
     if (at.sub == 0) {
-      *reinterpret_cast<float4*>(&tc[buf][at.wv][li]) = make_float4(cw[0], cw[1], cw[2], cw[3]);
-      *reinterpret_cast<float4*>(&ts[buf][at.wv][li]) = make_float4(sw[0], sw[1], sw[2], sw[3]);
-      if constexpr (SUM)
-        *reinterpret_cast<float4*>(&tl[buf][at.wv][li]) = make_float4(lw[0], lw[1], lw[2], lw[3]);
+      *reinterpret_cast<float2*>(&tc[buf][at.wv][li]) = make_float2(cw[0], cw[1]);
+      *reinterpret_cast<float2*>(&ts[buf][at.wv][li]) = make_float2(s[0], s[1]);
     }
     __syncthreads();
     if constexpr (Z && !SUM) z.fresh();
-    float h[4] = {0, 0, 0, 0};
+    float h[kV] = {0, 0};
 #pragma unroll 2
     for (int w = 0; w < kWaves; ++w) {
-      const float4 cv = *reinterpret_cast<const float4*>(&tc[buf][w][li]);
-      const float4 sv = *reinterpret_cast<const float4*>(&ts[buf][w][li]);
-      const float c4[4] = {cv.x, cv.y, cv.z, cv.w}, s4[4] = {sv.x, sv.y, sv.z, sv.w};
-      if constexpr (SUM) {
-        const float4 lv = *reinterpret_cast<const float4*>(&tl[buf][w][li]);
-        lsum[0] += lv.x; lsum[1] += lv.y; lsum[2] += lv.z; lsum[3] += lv.w;
-      }
+      const float2 cv = *reinterpret_cast<const float2*>(&tc[buf][w][li]);
+      const float2 sv = *reinterpret_cast<const float2*>(&ts[buf][w][li]);
+      const float cw4[kV] = {cv.x, cv.y}, s4[kV] = {sv.x, sv.y};
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < kV; ++j) {
+        if (SUM) dec[j] = rec_both<MASK>(dec[j], cw4[j]);
         h[j] = w == at.wv ? H[j] : h[j];
-        H[j] = rec_apply<MASK>(c4[j], H[j], s4[j]);
+        H[j] = rec_apply<MASK>(cw4[j], H[j], s4[j]);
       }
     }
     if constexpr (!SUM) {
@@ -154,14 +137,14 @@ __global__ __launch_bounds__(kWaves * 64, 4) void rec_fwd_kernel(FwdParams p) {
         store_f32(p.states + (at.b * n_states + (t0 + tw) / SS_REC_CHUNK) * D + at.c, at.n, h);
       }
 #pragma unroll
-      for (int j = 0; j < 4; ++j) h[j] = rec_apply<MASK>(cx[j], h[j], sx[j]);
-      float out[kS][4];
+      for (int j = 0; j < kV; ++j) h[j] = rec_apply<MASK>(cx[j], h[j], sx[j]);
+      float out[kS][kV];
 #pragma unroll
       for (int e = 0; e < kS; ++e) {
-        float zv[4];
+        float zv[kV];
         if constexpr (Z) unpack(z.q[e], zv);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < kV; ++j) {
           h[j] = rec_apply<MASK>(c[e][j], h[j], g[e][j]);
           out[e][j] = Z ? h[j] * silu(zv[j]) : h[j];
           if (MASK) out[e][j] = e < live ? out[e][j] : 0.0f;
@@ -183,7 +166,7 @@ __global__ __launch_bounds__(kWaves * 64, 4) void rec_fwd_kernel(FwdParams p) {
   }
   if (at.wv == 0 && at.sub == 0) {
     if constexpr (SUM) {
-      store_f32(p.clog + crow, at.n, lsum);
+      store_f32(p.cdec + crow, at.n, dec);
       store_f32(p.cend + crow, at.n, H);
     } else if (p.h_last && at.chunk == p.s.nchunks - 1) {
       store_f32(p.h_last + int64_t(at.b) * D + at.c, at.n, H);
@@ -194,7 +177,7 @@ __global__ __launch_bounds__(kWaves * 64, 4) void rec_fwd_kernel(FwdParams p) {
 
 // A thread walks the chunks of one channel.  first: what enters the first of them, or
 // null (0).
-__global__ __launch_bounds__(64) void rec_carry_kernel(const float* clog, float* carry,
+__global__ __launch_bounds__(64) void rec_carry_kernel(const float* decay, float* carry,
                                                        const float* first, int64_t chans,
                                                        int32_t D, int32_t n, int reverse) {
   const int64_t i = int64_t(blockIdx.x) * 64 + threadIdx.x;
@@ -204,9 +187,9 @@ __global__ __launch_bounds__(64) void rec_carry_kernel(const float* clog, float*
 #pragma unroll 8
   for (int k = 0; k < n; ++k) {
     const int64_t o = at + int64_t(reverse ? n - 1 - k : k) * D;
-    const float l = clog[o], s = carry[o];
+    const float p = decay[o], s = carry[o];
     carry[o] = h;
-    h = rec_apply<true>(rec_code_log2<true>(l), h, s);
+    h = rec_apply<true>(p, h, s);
   }
 }
 
@@ -229,8 +212,12 @@ __global__ __launch_bounds__(64) void rec_step_kernel(StepParams p) {
   float x[V], r[V], i[V], z[V], lam[V], h[V], out[V];
   auto get = [&](const void* src, int64_t ld, float (&v)[V]) {
     const T* q = static_cast<const T*>(src) + b * ld + c;
-    if constexpr (V == 4) unpack(Quad<T>{load_raw4(q)}, v);
-    else v[0] = to_f32(*q);
+    if constexpr (V == 4) {
+      const float4 f = unpack4(load_raw4(q));
+      v[0] = f.x; v[1] = f.y; v[2] = f.z; v[3] = f.w;
+    } else {
+      v[0] = to_f32(*q);
+    }
   };
   get(p.x, p.ldx, x);
   get(p.r, p.ldr, r);
@@ -243,9 +230,11 @@ __global__ __launch_bounds__(64) void rec_step_kernel(StepParams p) {
   }
 #pragma unroll
   for (int j = 0; j < V; ++j) {
-    const float E = precise_expm1(rec_rate(p.decay, lam[j]) * sigmoid(r[j]));
-    const float beta = __builtin_amdgcn_sqrtf(-E * (2.0f + E));
-    h[j] = rec_apply<false>(rec_code(E), h[j], beta * sigmoid(i[j]) * x[j]);
+    const Decay d = rec_decay(rec_rate(p.decay, lam[j]) * sigmoid(r[j]));
+    // a near 1 enters as a - 1: a long loop of steps does not add up a's rounding
+    const float g = d.beta * sigmoid(i[j]) * x[j];
+    const float near = h[j] + __builtin_fmaf(d.E, h[j], g), far = __builtin_fmaf(d.a, h[j], g);
+    h[j] = d.E > -0.25f ? near : far;
     out[j] = Z ? h[j] * silu(z[j]) : h[j];
     p.h[b * p.D + c + j] = h[j];
   }
@@ -258,15 +247,15 @@ __global__ __launch_bounds__(64) void rec_step_kernel(StepParams p) {
 
 }  // namespace
 
-// Time is cut only where the channels leave the GPU empty: below 192 workgroups in one
-// pass, into enough chunks for 512, of whole blocks (of either pass).
+// Time is cut only where the channels leave the GPU empty: below 256 workgroups in one
+// pass, into enough chunks for 1024, of whole blocks (of either pass).
 RecPlan plan_rec(const ss_rec_desc_t& d, int op) {
   RecPlan pl;
   const int64_t groups = d.batch * ((d.dim + kRecChans - 1) / kRecChans);
   const int64_t blocks = (d.seqlen + kBlock - 1) / kBlock;
   int64_t per = blocks;
-  if (groups < 192) {
-    const int64_t want = (512 + groups - 1) / groups;
+  if (groups < 256) {
+    const int64_t want = (1024 + groups - 1) / groups;
     per = (blocks + want - 1) / want;
     if (per < 4) per = 4;
   }
@@ -286,10 +275,10 @@ RecPlan plan_rec(const ss_rec_desc_t& d, int op) {
   return pl;
 }
 
-void launch_rec_carry(const float* clog, float* carry, const float* first, int64_t batch,
+void launch_rec_carry(const float* decay, float* carry, const float* first, int64_t batch,
                       int32_t D, int32_t nchunks, bool reverse, hipStream_t stream) {
   const int64_t chans = batch * D;
-  rec_carry_kernel<<<unsigned((chans + 63) / 64), 64, 0, stream>>>(clog, carry, first, chans, D,
+  rec_carry_kernel<<<unsigned((chans + 63) / 64), 64, 0, stream>>>(decay, carry, first, chans, D,
                                                                    nchunks, reverse);
 }
 
@@ -302,7 +291,7 @@ int launch_rec_fwd(const ss_rec_desc_t& d, const RecPlan& pl, const void* x, con
                     stride_of(d.z_stride, d.dim), lam, h0, starts, lengths, y, h_last, states,
                     reinterpret_cast<float*>(ws + pl.off_log),
                     reinterpret_cast<float*>(ws + pl.off_carry), d.out_dtype == SS_BF16};
-  const bool any = d.dim % 4 != 0 || odd_rows(x, p.ldx, d.in_dtype) ||
+  const bool any = d.dim % kV != 0 || odd_rows(x, p.ldx, d.in_dtype) ||
                    odd_rows(r, p.ldr, d.in_dtype) || odd_rows(i, p.ldi, d.in_dtype) ||
                    odd_rows(z, p.ldz, d.in_dtype);
   hipStream_t st = static_cast<hipStream_t>(stream);
@@ -313,7 +302,7 @@ int launch_rec_fwd(const ss_rec_desc_t& d, const RecPlan& pl, const void* x, con
       using T = decltype(type);
       if (pl.nchunks > 1) {
         rec_fwd_kernel<T, false, M, A, true><<<blocks, kWaves * 64, 0, st>>>(p);
-        launch_rec_carry(p.clog, p.cend, h0, d.batch, p.s.D, p.s.nchunks, false, st);
+        launch_rec_carry(p.cdec, p.cend, h0, d.batch, p.s.D, p.s.nchunks, false, st);
       }
       rec_fwd_kernel<T, Z, M, A, false><<<blocks, kWaves * 64, 0, st>>>(p);
     };

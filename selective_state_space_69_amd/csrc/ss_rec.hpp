@@ -1,20 +1,17 @@
-// What the kernels of the gated linear recurrence share: its coefficients, decays in
-// coded form, and the joining of stretches of time across a wave.
+// What the kernels of the gated linear recurrence share: its coefficients, the rows of a
+// workgroup, and the joining of stretches of time.
 //
-// Decays in coded form.  A step h <- a h + b with a near 1 is remembered for 1 / (1 - a)
-// steps, so the rounding of a itself would add up to 2^-24 / (1 - a) of the state; a
-// small a must not carry an error of the old state's size either.  So a decay is held
-// as one float c: a - 1 (negative) while a > 3/4, a itself (not negative) below, both
-// with full relative accuracy, and
-//     a h + b = c h + b + (c < 0 ? h : 0).
-// a = 1 is coded as the smallest negative normal number, an a below the smallest
-// positive one as that; 0 is a start, which drops even an h that is not finite.
+// Layout.  A workgroup holds kRecChans channels, two neighbours per lane; a wave's lanes
+// hold kSubs stretches of time of S steps each, its waves follow each other in time.
+// Every lane runs its stretch from a zero state; a stretch is then summed up by its decay
+// P (the exponential of the sum of log decays, so that it is rounded once) and its end
+// state s, h <- P h + s.  Stretches are joined in the wave by row swaps and across waves in
+// LDS, and each lane runs its steps again from its true state.
 //
-// Layout.  A wave holds 64 channels, four neighbours per lane (16 lanes), by four
-// stretches of time (its rows of 16 lanes) of S steps each; a workgroup's waves follow
-// each other in time.  Every lane runs its stretch from a zero state, keeping its total
-// log decay and end state; the stretches are joined in the wave by row swaps and across
-// waves in LDS, and each lane runs its steps again from its true state.
+// Accuracy.  A state that a step hardly decays is remembered for 1 / (1 - a) steps, and a
+// decay rounded to fp32 at every step would add up to 2^-24 / (1 - a) of it.  What carries
+// a state on is P, once per stretch, so the rounding of a single step's a stays within its
+// stretch; sqrt(1 - a^2) comes from a - 1 with full relative accuracy (a series near 0).
 #pragma once
 
 #include <type_traits>
@@ -23,8 +20,11 @@
 
 namespace ss {
 
-constexpr int kRecChans = 64;                    // channels of a workgroup
-constexpr float kOne = -1.17549435e-38f;         // the code of a = 1
+constexpr int kV = 2;                            // channels of a lane
+constexpr int kRecLanes = 16;                    // lanes of one step's channels
+constexpr int kRecChans = kV * kRecLanes;        // channels of a workgroup
+constexpr int kSubs = 64 / kRecLanes;            // stretches of a wave
+constexpr float kTiny = 1.17549435e-38f;         // smallest normal number
 
 struct RecShape {
   int64_t B, L;
@@ -41,37 +41,49 @@ __device__ __forceinline__ float rec_rate(float decay, float lam) {
   return -decay * softplus_log2(lam * kLog2e);
 }
 
-__device__ __forceinline__ float rec_code(float E) {       // of a = 1 + E
-  const float near = __builtin_fminf(E, kOne), far = __builtin_fmaxf(1.0f + E, -kOne);
-  return E > -0.25f ? near : far;
-}
-// of a total log decay; CUT: minus infinity is a start's
-template <bool CUT> __device__ __forceinline__ float rec_code_log2(float l2) {
-  const float c = rec_code(precise_expm1(l2));
-  return CUT && l2 == -__builtin_inff() ? 0.0f : c;
+// A step's decay a, E = a - 1 and sqrt(1 - a^2) from its log2 decay.
+struct Decay { float a, E, beta; };
+__device__ __forceinline__ Decay rec_decay(float l2) {
+  const float a = hw_exp2(l2), near = l2 * expm1_factor(l2), far = a - 1.0f;
+  const float E = __builtin_unpredictable(l2 > -kSeries2) ? near : far;
+  return Decay{a, E, __builtin_amdgcn_sqrtf(-E * (2.0f + E))};
 }
 
-// a h + b.  CUT: there may be starts
-template <bool CUT>
-__device__ __forceinline__ float rec_apply(float c, float h, float b) {
-  const float rest = c < 0.0f ? h : 0.0f, v = __builtin_fmaf(c, h, b) + rest;
-  return CUT && c == 0.0f ? b : v;
+// Decays of steps and stretches.  CUT: there may be starts, whose decay is 0 (every other
+// one is at least kTiny): a start drops even a state that is not finite.
+template <bool CUT> __device__ __forceinline__ float rec_decay_of(float l2, bool cut) {
+  const float a = hw_exp2(l2), v = __builtin_fmaxf(a, kTiny);
+  return CUT ? (cut ? 0.0f : v) : a;
+}
+// one decay after the other
+template <bool CUT> __device__ __forceinline__ float rec_both(float p, float q) {
+  const float v = p * q, w = __builtin_fmaxf(v, kTiny);
+  return CUT ? (__builtin_fminf(p, q) == 0.0f ? 0.0f : w) : v;
+}
+// h decayed, and b added
+template <bool CUT> __device__ __forceinline__ float rec_apply(float p, float h, float b) {
+  const float v = __builtin_fmaf(p, h, b);
+  return CUT && p == 0.0f ? b : v;
 }
 
-// Four neighbouring channels of a row, as stored, so that a prefetch is not waited for.
-template <typename T> struct Quad { typename Raw4<T>::type v; };
-template <typename T> __device__ __forceinline__ void unpack(const Quad<T>& q, float (&v)[4]) {
-  const float4 f = unpack4(q.v);
-  v[0] = f.x; v[1] = f.y; v[2] = f.z; v[3] = f.w;
+// A lane's channels of a row, as stored, so that a prefetch is not waited for.
+template <typename T> struct Pair { uint32_t w[kV * sizeof(T) / 4]; };
+__device__ __forceinline__ void unpack(const Pair<float>& q, float (&v)[kV]) {
+  v[0] = __uint_as_float(q.w[0]);
+  v[1] = __uint_as_float(q.w[1]);
 }
-// n of four floats (a (B, D) array or lam; the others 0)
-__device__ __forceinline__ void load_f32(const float* p, int n, float (&v)[4]) {
-#pragma unroll
-  for (int j = 0; j < 4; ++j) v[j] = j < n ? p[j] : 0.0f;
+__device__ __forceinline__ void unpack(const Pair<uint16_t>& q, float (&v)[kV]) {
+  v[0] = __uint_as_float(q.w[0] << 16);
+  v[1] = __uint_as_float(q.w[0] & 0xffff0000u);
 }
-__device__ __forceinline__ void store_f32(float* p, int n, const float (&v)[4]) {
+// A lane's n channels of a (D) row of floats; others repeat the first.
+__device__ __forceinline__ void load_f32(const float* p, int n, float (&v)[kV]) {
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
+  for (int j = 0; j < kV; ++j) v[j] = p[j < n ? j : 0];
+}
+__device__ __forceinline__ void store_f32(float* p, int n, const float (&v)[kV]) {
+#pragma unroll
+  for (int j = 0; j < kV; ++j)
     if (j < n) p[j] = v[j];
 }
 
@@ -92,28 +104,71 @@ __device__ __forceinline__ void swap_halves(float x, float& lower, float& upper)
 #endif
 }
 
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+// The stretches of a wave, joined: (P, s) of the lane's own on entry, of the whole wave on
+// return; (Px, sx): of the stretches in front of the lane's.
+template <bool CUT>
+__device__ __forceinline__ void join_up(int sub, float& P, float& s, float& Px, float& sx) {
+  float p0, p1, s0, s1;
+  swap_rows(P, p0, p1);
+  swap_rows(s, s0, s1);
+  Px = sub & 1 ? p0 : 1.0f;
+  sx = sub & 1 ? s0 : 0.0f;
+  swap_halves(rec_both<CUT>(p0, p1), p0, P);
+  swap_halves(rec_apply<CUT>(p1, s0, s1), s0, s);
+  const float q = rec_both<CUT>(p0, Px), t = rec_apply<CUT>(Px, s0, sx);
+  Px = sub & 2 ? q : Px;
+  sx = sub & 2 ? t : sx;
+  s = rec_apply<CUT>(P, s0, s);
+  P = rec_both<CUT>(p0, P);
+}
+// Both walks of a backward pass: forward as above, and q, what leaves a stretch at its
+// first step, joined from behind; (Py, qy): of the stretches behind the lane's.
+template <bool CUT, bool UP>
+__device__ __forceinline__ void join_both(int sub, float& P, float& s, float& q, float& Px,
+                                          float& sx, float& Py, float& qy) {
+  float p0, p1, q0, q1, r0, r1, u0, u1;
+  swap_rows(P, p0, p1);
+  swap_rows(q, q0, q1);
+  Py = sub & 1 ? 1.0f : p1;
+  qy = sub & 1 ? 0.0f : q1;
+  swap_halves(rec_both<CUT>(p0, p1), r0, r1);
+  swap_halves(rec_apply<CUT>(p0, q1, q0), u0, u1);
+  q = rec_apply<CUT>(r0, u1, u0);
+  const float y = rec_both<CUT>(Py, r1), v = rec_apply<CUT>(Py, u1, qy);
+  Py = sub & 2 ? Py : y;
+  qy = sub & 2 ? qy : v;
+  if constexpr (UP) {
+    float s0, s1, t0, t1;
+    swap_rows(s, s0, s1);
+    Px = sub & 1 ? p0 : 1.0f;
+    sx = sub & 1 ? s0 : 0.0f;
+    swap_halves(rec_apply<CUT>(p1, s0, s1), t0, t1);
+    s = rec_apply<CUT>(r1, t0, t1);
+    const float x = rec_both<CUT>(r0, Px), w = rec_apply<CUT>(Px, t0, sx);
+    Px = sub & 2 ? x : Px;
+    sx = sub & 2 ? w : sx;
+  }
+  P = rec_both<CUT>(r0, r1);
+}
 
-constexpr int kS = 4;                       // steps of a lane's stretch
-constexpr int kWaveSteps = 4 * kS;
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
 // Which stretch of which channels a lane has.
 struct Place {
-  int lane, wv, sub, n;      // sub: row of the wave; n: channels that exist (0..4)
+  int lane, wv, sub, n;      // sub: stretch of the wave; n: channels that exist (0..kV)
   int32_t b, chunk;
   int32_t c;                 // first channel (0 where none exists)
   __device__ __forceinline__ Place(const RecShape& s) {
     lane = threadIdx.x & 63;
     wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    sub = lane >> 4;
+    sub = lane / kRecLanes;
     const uint32_t id = uint32_t(xcd_contiguous(blockIdx.x, gridDim.x));
     const uint32_t row = id / uint32_t(s.groups);
     const int32_t g = int32_t(id - row * uint32_t(s.groups));
     b = int32_t(row / uint32_t(s.nchunks));
     chunk = int32_t(row - uint32_t(b) * uint32_t(s.nchunks));
-    const int32_t c0 = g * kRecChans + (lane & 15) * 4;
-    n = s.D - c0 < 4 ? s.D - c0 : 4;
+    const int32_t c0 = g * kRecChans + lane % kRecLanes * kV;
+    n = s.D - c0 < kV ? s.D - c0 : kV;
     if (n <= 0) n = 0;
     c = n ? c0 : 0;
   }
@@ -121,7 +176,7 @@ struct Place {
 
 // One tensor as a workgroup walks it: `p` is the first row of a block, a lane's stretch
 // starts `first` bytes behind it.  Accesses take a scalar base and 32-bit lane offsets.
-// ANY: rows at any element address and quads that end behind their row, read element by
+// ANY: rows at any element address and pairs that end behind their row, read element by
 // element; what lies behind the tensor's last element then reads 0.
 template <bool ANY> struct Stream {
   const char* p;
@@ -147,32 +202,27 @@ template <bool ANY> struct Stream {
 };
 
 // The rows of a lane's stretch of one tensor; those from `valid` on hold anything.
-template <typename T, bool ANY> struct Rows {
-  Quad<T> q[kS];
+template <typename T, int S, bool ANY> struct Rows {
+  Pair<T> q[S];
   __device__ __forceinline__ void load(const Stream<ANY>& st, int valid) {
     const Rsrc v = st.rsrc();
 #pragma unroll
-    for (int s = 0; s < kS; ++s) {
+    for (int s = 0; s < S; ++s) {
       if constexpr (!ANY) {
         const uint32_t at = s < valid ? st.first : kOutOfRange, row = uint32_t(s) * st.row;
         if constexpr (sizeof(T) == 4)
-          q[s] = __builtin_bit_cast(Quad<T>, __builtin_amdgcn_raw_buffer_load_b128(v, at, row, 0));
+          q[s] = __builtin_bit_cast(Pair<T>, __builtin_amdgcn_raw_buffer_load_b64(v, at, row, 0));
         else
-          q[s] = __builtin_bit_cast(Quad<T>, __builtin_amdgcn_raw_buffer_load_b64(v, at, row, 0));
+          q[s] = __builtin_bit_cast(Pair<T>, __builtin_amdgcn_raw_buffer_load_b32(v, at, row, 0));
       } else {
         const uint32_t at = s < valid ? st.first + uint32_t(s) * st.row : kOutOfRange;
         if constexpr (sizeof(T) == 4) {
-          uint32_t e[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            e[j] = __builtin_amdgcn_raw_buffer_load_b32(v, at + 4 * j, 0, 0);
-          q[s] = __builtin_bit_cast(Quad<T>, u32x4{e[0], e[1], e[2], e[3]});
+          q[s].w[0] = __builtin_amdgcn_raw_buffer_load_b32(v, at, 0, 0);
+          q[s].w[1] = __builtin_amdgcn_raw_buffer_load_b32(v, at + 4, 0, 0);
         } else {
-          uint32_t e[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            e[j] = uint16_t(__builtin_amdgcn_raw_buffer_load_b16(v, at + 2 * j, 0, 0));
-          q[s] = __builtin_bit_cast(Quad<T>, u32x2{e[0] | e[1] << 16, e[2] | e[3] << 16});
+          const uint32_t e0 = uint16_t(__builtin_amdgcn_raw_buffer_load_b16(v, at, 0, 0));
+          const uint32_t e1 = uint16_t(__builtin_amdgcn_raw_buffer_load_b16(v, at + 2, 0, 0));
+          q[s].w[0] = e0 | e1 << 16;
         }
       }
     }
@@ -182,9 +232,9 @@ template <typename T, bool ANY> struct Rows {
   __device__ __forceinline__ void fresh() {
 #if defined(__HIP_DEVICE_COMPILE__)
 #pragma unroll
-    for (int s = 0; s < kS; ++s) {
-      asm volatile("" : "+v"(q[s].v.x), "+v"(q[s].v.y));
-      if constexpr (sizeof(T) == 4) asm volatile("" : "+v"(q[s].v.z), "+v"(q[s].v.w));
+    for (int s = 0; s < S; ++s) {
+      asm volatile("" : "+v"(q[s].w[0]));
+      if constexpr (sizeof(T) == 4) asm volatile("" : "+v"(q[s].w[1]));
     }
 #endif
   }
@@ -194,22 +244,20 @@ template <typename T, bool ANY> struct Rows {
 // ANY: element by element.
 template <typename T, bool ANY>
 __device__ __forceinline__ void put(const Stream<ANY>& st, int s, int valid, int n,
-                                    const float (&f)[4]) {
+                                    const float (&f)[kV]) {
   const Rsrc v = st.rsrc();
   if constexpr (ANY) {
     const uint32_t at = s < valid ? st.first + uint32_t(s) * st.row : kOutOfRange;
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < kV; ++j)
       buf_store<T>(v, j < n ? at + j * uint32_t(sizeof(T)) : kOutOfRange, 0, f[j]);
   } else {
     const uint32_t at = s < valid ? st.first : kOutOfRange, row = uint32_t(s) * st.row;
     if constexpr (sizeof(T) == 2)
-      __builtin_amdgcn_raw_buffer_store_b64(u32x2{cvt_bf16x2(f[0], f[1]), cvt_bf16x2(f[2], f[3])},
-                                            v, at, row, 0);
+      __builtin_amdgcn_raw_buffer_store_b32(cvt_bf16x2(f[0], f[1]), v, at, row, 0);
     else
-      __builtin_amdgcn_raw_buffer_store_b128(
-          u32x4{__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
-                __float_as_uint(f[3])}, v, at, row, 0);
+      __builtin_amdgcn_raw_buffer_store_b64(u32x2{__float_as_uint(f[0]), __float_as_uint(f[1])}, v,
+                                            at, row, 0);
   }
 }
 
@@ -233,9 +281,9 @@ struct Masks {
     }
   }
   // the marks of a lane's steps, from step `at` on
-  __device__ __forceinline__ void marks(int at, bool (&m)[kS]) const {
+  template <int S> __device__ __forceinline__ void marks(int at, bool (&m)[S]) const {
 #pragma unroll
-    for (int s = 0; s < kS; ++s)
+    for (int s = 0; s < S; ++s)
       m[s] = __builtin_amdgcn_raw_buffer_load_b8(starts, uint32_t(at + s), 0, 0) != 0;
   }
 };
@@ -260,14 +308,14 @@ inline RecShape rec_shape(const ss_rec_desc_t& d, const RecPlan& pl) {
                   pl.chunk, int32_t(pl.nchunks), d.decay};
 }
 inline int64_t stride_of(int64_t stride, int64_t dim) { return stride ? stride : dim; }
-// whether quads of bf16 rows are not 4-byte aligned
+// whether pairs of bf16 rows are not 4-byte aligned
 inline bool odd_rows(const void* p, int64_t ld, int32_t dtype) {
   return p && dtype == SS_BF16 && (ld % 2 != 0 || reinterpret_cast<uintptr_t>(p) % 4 != 0);
 }
 
-// Chunks' end states (from a zero start) to their start states, or in reverse the
-// adjoints that leave them (with none entering) to those that enter.
-void launch_rec_carry(const float* clog, float* carry, const float* first, int64_t batch,
+// Chunks' decays and end states (from a zero start) to their start states, or in reverse
+// the adjoints that leave them (with none entering) to those that enter.
+void launch_rec_carry(const float* decay, float* carry, const float* first, int64_t batch,
                       int32_t D, int32_t nchunks, bool reverse, hipStream_t stream);
 
 }  // namespace ss

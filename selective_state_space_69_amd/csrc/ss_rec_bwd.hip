@@ -1,9 +1,9 @@
-// Backward of the gated linear recurrence for gfx950.  Layout, decay codes and chunks are
-// the forward's (ss_rec.hpp, ss_rec.hip); time runs backward.
+// Backward of the gated linear recurrence for gfx950.  Layout and chunks are the
+// forward's (ss_rec.hpp, ss_rec.hip); time runs backward.
 //
 // The adjoint that leaves a step, w_t = a_t (v_t + w_(t+1)), is a recurrence of the same
 // decays in reverse, and the states are recomputed from the kept one in front of each
-// SS_REC_CHUNK steps.  So a stretch is summed up by one log decay, an end state and a
+// SS_REC_CHUNK steps.  So a stretch is summed up by one decay, an end state and a
 // leaving adjoint; both walks are joined by one barrier per block, then every lane runs
 // its steps forward (states) and backward (adjoints, gradients) from true values.
 #include "ss_rec.hpp"
@@ -11,6 +11,8 @@
 namespace ss {
 namespace {
 
+constexpr int kS = 4;                       // steps of a lane's stretch
+constexpr int kWaveSteps = kSubs * kS;
 constexpr int kWaves = 4;
 constexpr int kBlock = kWaves * kWaveSteps;
 constexpr int kRun = 16;                                 // blocks of a run of dlam's sums
@@ -28,17 +30,11 @@ struct BwdParams {
   const float *states, *dh_last;
   void *dx, *dr, *di, *dz;
   float* dh0;
-  float *clog, *cadj;        // (B, nchunks, D) chunks' log decays; adjoints leaving, then entering them
+  float *cdec, *cadj;        // (B, nchunks, D) chunks' decays; adjoints leaving, then entering them
   float* part;               // (B * nchunks, D) sums of dlam
 };
 
-// adjoint over a decay: a g
-template <bool CUT> __device__ __forceinline__ float rec_scale(float c, float g) {
-  const float rest = c < 0.0f ? g : 0.0f, v = __builtin_fmaf(c, g, rest);
-  return CUT && c == 0.0f ? 0.0f : v;
-}
-
-// SUM: only the chunks' carries (log decay, and the adjoint that leaves with none
+// SUM: only the chunks' carries (decay, and the adjoint that leaves with none
 // entering).
 template <typename T, typename Dy, bool Z, bool MASK, bool ANY, bool SUM>
 __global__ __launch_bounds__(kWaves * 64, 2) void rec_bwd_kernel(BwdParams p) {
@@ -52,17 +48,17 @@ __global__ __launch_bounds__(kWaves * 64, 2) void rec_bwd_kernel(BwdParams p) {
   masks.init<MASK>(p.starts, p.lengths, at.b, L, t0, p.s.chunk);
   const int64_t crow = int64_t(at.b * p.s.nchunks + at.chunk) * D + at.c;
   const int64_t n_states = (L + SS_REC_CHUNK - 1) / SS_REC_CHUNK;
-  float k[4], W[4] = {0, 0, 0, 0}, lsum[4] = {0, 0, 0, 0};
-  float run[4] = {0, 0, 0, 0}, sum[4] = {0, 0, 0, 0};     // of dlam: of kRun blocks, of the chunk
+  float k[kV], W[kV] = {0, 0}, dec[kV] = {1, 1};
+  float run[kV] = {0, 0}, sum[kV] = {0, 0};     // of dlam: of kRun blocks, of the chunk
   load_f32(p.lam + at.c, at.n, k);
 #pragma unroll
-  for (int j = 0; j < 4; ++j) k[j] = rec_rate(p.s.decay, k[j]);
+  for (int j = 0; j < kV; ++j) k[j] = rec_rate(p.s.decay, k[j]);
   if (!SUM) {
     if (p.s.nchunks > 1) load_f32(p.cadj + crow, at.n, W);
     else if (p.dh_last) load_f32(p.dh_last + int64_t(at.b) * D + at.c, at.n, W);
   }
   const int off = at.wv * kWaveSteps + at.sub * kS;      // of the lane's stretch in a block
-  const int li = (at.lane & 15) * 4;
+  const int li = at.lane % kRecLanes * kV;
   int tb = (masks.steps - 1) / kBlock * kBlock;          // the block's first step
 
   Stream<ANY> px, pr, pi, pz, pd, ox, or_, oi, oz;
@@ -78,14 +74,14 @@ __global__ __launch_bounds__(kWaves * 64, 2) void rec_bwd_kernel(BwdParams p) {
     if constexpr (Z) oz.init(p.dz, D, sizeof(T), p.s, row0 + t0 + tb, off, at);
   }
   // the kept state in front of the wave's steps (its stretch of SS_REC_CHUNK)
-  auto state = [&](int tb, float (&st)[4]) {
+  auto state = [&](int tb, float (&st)[kV]) {
     int64_t ks = (t0 + tb + at.wv * kWaveSteps) / SS_REC_CHUNK;
     ks = ks < n_states ? ks : n_states - 1;
     load_f32(p.states + (at.b * n_states + ks) * D + at.c, at.n, st);
   };
-  Rows<T, ANY> x, r, i, z, nx, nz;
-  Rows<Dy, ANY> dy, ndy;
-  float st[4] = {0, 0, 0, 0};
+  Rows<T, kS, ANY> x, r, i, z, nx, nz;
+  Rows<Dy, kS, ANY> dy, ndy;
+  float st[kV] = {0, 0};
   int valid = masks.steps - tb - off;           // steps of the lane's stretch inside the chunk
   r.load(pr, valid);
   dy.load(pd, valid);
@@ -111,13 +107,15 @@ __global__ __launch_bounds__(kWaves * 64, 2) void rec_bwd_kernel(BwdParams p) {
         nx.load(px, valid);
       }
     }
-    bool start[kS] = {false, false, false, false};
+    bool start[kS] = {};
     if constexpr (MASK) masks.marks(tb + off, start);
-    float c[kS][4], sr[kS][4], si[kS][4], beta[kS][4], v[kS][4];
-    float l[4] = {0, 0, 0, 0}, s[4] = {0, 0, 0, 0}, q[4] = {0, 0, 0, 0};
+    float c[kS][kV], sr[kS][kV], si[kS][kV], beta[kS][kV], v[kS][kV];
+    float l[kV] = {0, 0}, s[kV] = {0, 0}, q[kV] = {0, 0};
+    bool cuts = false;
 #pragma unroll
     for (int e = 0; e < kS; ++e) {
-      float xv[4], rv[4], iv[4], zv[4], dv[4];
+      __builtin_amdgcn_sched_barrier(0);
+      float xv[kV], rv[kV], iv[kV], zv[kV], dv[kV];
       unpack(r.q[e], rv);
       unpack(dy.q[e], dv);
       if constexpr (Z) unpack(z.q[e], zv);
@@ -126,20 +124,21 @@ __global__ __launch_bounds__(kWaves * 64, 2) void rec_bwd_kernel(BwdParams p) {
         unpack(i.q[e], iv);
       }
       const bool in = e < live, cut = MASK && start[e] && in;
+      if (MASK) cuts |= cut;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < kV; ++j) {
         sr[e][j] = sigmoid(rv[j]);
         float l2 = k[j] * sr[e][j];
         l2 = in ? l2 : 0.0f;
-        const float E = precise_expm1(l2), code = rec_code(E);
-        c[e][j] = cut ? 0.0f : code;
+        const Decay f = rec_decay(l2);
+        c[e][j] = MASK ? (cut ? 0.0f : __builtin_fmaxf(f.a, kTiny)) : f.a;
         const float d = Z ? dv[j] * silu(zv[j]) : dv[j];
         v[e][j] = in ? d : 0.0f;
-        l[j] += cut ? -__builtin_inff() : l2;
+        l[j] += l2;
         if constexpr (!SUM) {
-          beta[e][j] = __builtin_amdgcn_sqrtf(-E * (2.0f + E));
+          beta[e][j] = f.beta;
           si[e][j] = sigmoid(iv[j]);
-          const float add = beta[e][j] * si[e][j] * xv[j];
+          const float add = f.beta * si[e][j] * xv[j];
           s[j] = rec_apply<MASK>(c[e][j], s[j], in ? add : 0.0f);
         }
       }
@@ -155,45 +154,19 @@ __global__ __launch_bounds__(kWaves * 64, 2) void rec_bwd_kernel(BwdParams p) {
 #pragma unroll
     for (int e = kS - 1; e >= 0; --e)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) q[j] = rec_scale<MASK>(c[e][j], v[e][j] + q[j]);
-    // the wave's stretches, forward (s) from below and backward (q) from above
-    float cx[4], sx[4], cy[4], qy[4];      // of the rows below this lane's, above it
-    float cw[4], sw[4], qw[4];             // of the wave
+      for (int j = 0; j < kV; ++j) q[j] = rec_apply<MASK>(c[e][j], v[e][j] + q[j], 0.0f);
+    // of the stretches in front of the lane's, behind it, of the wave
+    float cx[kV], sx[kV], cy[kV], qy[kV], cw[kV];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      float l0, l1, c0, c1, q0, q1, p0, p1, u0, u1, y0, y1;
-      swap_rows(l[j], l0, l1);
-      swap_rows(q[j], q0, q1);
-      swap_rows(rec_code_log2<MASK>(l[j]), c0, c1);
-      const float lp = l0 + l1;
-      swap_halves(lp, p0, p1);
-      swap_halves(q0 + rec_scale<MASK>(c0, q1), y0, y1);
-      swap_halves(rec_code_log2<MASK>(lp), u0, u1);
-      const float lw = p0 + p1;
-      cw[j] = rec_code_log2<MASK>(lw);
-      qw[j] = y0 + rec_scale<MASK>(u0, y1);
-      if constexpr (SUM) {
-        lsum[j] += at.sub == 0 ? lw : 0.0f;
-      } else {
-        const float la = at.sub < 2 ? p1 : 0.0f, qa = at.sub < 2 ? y1 : 0.0f;
-        const float up = at.sub & 1 ? 0.0f : l1, qo = q1 + rec_scale<MASK>(c1, qa);
-        cy[j] = rec_code_log2<MASK>(la + up);
-        qy[j] = at.sub & 1 ? qa : qo;
-        float s0, s1, x0, x1;
-        swap_rows(s[j], s0, s1);
-        swap_halves(rec_apply<MASK>(c1, s0, s1), x0, x1);
-        sw[j] = rec_apply<MASK>(u1, x0, x1);
-        const float lb = at.sub >= 2 ? p0 : 0.0f, sb = at.sub >= 2 ? x0 : 0.0f;
-        const float lo = at.sub & 1 ? l0 : 0.0f, so = rec_apply<MASK>(c0, sb, s0);
-        cx[j] = rec_code_log2<MASK>(lb + lo);
-        sx[j] = at.sub & 1 ? so : sb;
-      }
+    for (int j = 0; j < kV; ++j) {
+      cw[j] = rec_decay_of<MASK>(l[j], cuts);
+      join_both<MASK, !SUM>(at.sub, cw[j], s[j], q[j], cx[j], sx[j], cy[j], qy[j]);
     }
     if (at.sub == 0) {
-      *reinterpret_cast<float4*>(&tc[buf][at.wv][li]) = make_float4(cw[0], cw[1], cw[2], cw[3]);
-      *reinterpret_cast<float4*>(&tq[buf][at.wv][li]) = make_float4(qw[0], qw[1], qw[2], qw[3]);
+      *reinterpret_cast<float2*>(&tc[buf][at.wv][li]) = make_float2(cw[0], cw[1]);
+      *reinterpret_cast<float2*>(&tq[buf][at.wv][li]) = make_float2(q[0], q[1]);
       if constexpr (!SUM)
-        *reinterpret_cast<float4*>(&ts[buf][at.wv][li]) = make_float4(sw[0], sw[1], sw[2], sw[3]);
+        *reinterpret_cast<float2*>(&ts[buf][at.wv][li]) = make_float2(s[0], s[1]);
     }
     __syncthreads();
     if constexpr (!SUM) {
@@ -201,62 +174,64 @@ __global__ __launch_bounds__(kWaves * 64, 2) void rec_bwd_kernel(BwdParams p) {
       dy.fresh();
       if constexpr (Z) z.fresh();
     }
-    float w[4] = {0, 0, 0, 0}, h[4];
+    float w[kV] = {0, 0}, h[kV];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) h[j] = st[j];
+    for (int j = 0; j < kV; ++j) h[j] = st[j];
 #pragma unroll 2
     for (int o = kWaves - 1; o >= 0; --o) {
-      const float4 cv = *reinterpret_cast<const float4*>(&tc[buf][o][li]);
-      const float4 qv = *reinterpret_cast<const float4*>(&tq[buf][o][li]);
-      const float c4[4] = {cv.x, cv.y, cv.z, cv.w}, q4[4] = {qv.x, qv.y, qv.z, qv.w};
+      const float2 cv = *reinterpret_cast<const float2*>(&tc[buf][o][li]);
+      const float2 qv = *reinterpret_cast<const float2*>(&tq[buf][o][li]);
+      const float cw4[kV] = {cv.x, cv.y}, q4[kV] = {qv.x, qv.y};
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < kV; ++j) {
+        if (SUM) dec[j] = rec_both<MASK>(dec[j], cw4[j]);
         w[j] = o == at.wv ? W[j] : w[j];
-        W[j] = q4[j] + rec_scale<MASK>(c4[j], W[j]);
+        W[j] = rec_apply<MASK>(cw4[j], W[j], q4[j]);
       }
     }
     if constexpr (!SUM) {
       // the waves between the kept state and this one
       for (int o = at.wv / kPerState * kPerState; o < at.wv; ++o) {
-        const float4 cv = *reinterpret_cast<const float4*>(&tc[buf][o][li]);
-        const float4 sv = *reinterpret_cast<const float4*>(&ts[buf][o][li]);
-        const float c4[4] = {cv.x, cv.y, cv.z, cv.w}, s4[4] = {sv.x, sv.y, sv.z, sv.w};
+        const float2 cv = *reinterpret_cast<const float2*>(&tc[buf][o][li]);
+        const float2 sv = *reinterpret_cast<const float2*>(&ts[buf][o][li]);
+        const float cw4[kV] = {cv.x, cv.y}, s4[kV] = {sv.x, sv.y};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) h[j] = rec_apply<MASK>(c4[j], h[j], s4[j]);
+        for (int j = 0; j < kV; ++j) h[j] = rec_apply<MASK>(cw4[j], h[j], s4[j]);
       }
       if (more) state(tb - kBlock, st);
-      float hs[kS + 1][4];       // the state in front of each step, behind the last
+      float hs[kS + 1][kV];       // the state in front of each step, behind the last
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < kV; ++j) {
         hs[0][j] = rec_apply<MASK>(cx[j], h[j], sx[j]);
-        w[j] = qy[j] + rec_scale<MASK>(cy[j], w[j]);
+        w[j] = rec_apply<MASK>(cy[j], w[j], qy[j]);
       }
 #pragma unroll
       for (int e = 0; e < kS; ++e) {
-        float xv[4];
+        float xv[kV];
         unpack(x.q[e], xv);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < kV; ++j) {
           const float add = beta[e][j] * si[e][j] * xv[j];
           hs[e + 1][j] = rec_apply<MASK>(c[e][j], hs[e][j], e < live ? add : 0.0f);
         }
       }
 #pragma unroll
       for (int e = kS - 1; e >= 0; --e) {
-        float xv[4], zv[4], dv[4], gx[4], gr[4], gi[4], gz[4];
+        __builtin_amdgcn_sched_barrier(0);
+        float xv[kV], zv[kV], dv[kV], gx[kV], gr[kV], gi[kV], gz[kV];
         unpack(x.q[e], xv);
         if constexpr (Z) {
           unpack(z.q[e], zv);
           unpack(dy.q[e], dv);
         }
-        const bool in = e < live, cut = MASK && start[e];
+        const bool in = e < live;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < kV; ++j) {
           const float u = v[e][j] + w[j], bt = beta[e][j], la = k[j] * sr[e][j] * kLn2;
-          w[j] = rec_scale<MASK>(c[e][j], u);
+          w[j] = rec_apply<MASK>(c[e][j], u, 0.0f);
           // log a / sqrt(1 - a^2): 0 where a rounds to 1
           const float ratio = la * hw_rcp(bt), lb = bt > 0.0f ? ratio : 0.0f;
-          const float ah = rec_scale<MASK>(c[e][j], cut ? 0.0f : hs[e][j]) * la;
+          const float ah = rec_apply<MASK>(c[e][j], hs[e][j], 0.0f) * la;
           const float dl = u * (ah - __builtin_fmaf(-bt, bt, 1.0f) * lb * (si[e][j] * xv[j]));
           const float vx = u * bt * si[e][j], vi = vx * xv[j] * (1.0f - si[e][j]);
           const float vr = dl * (1.0f - sr[e][j]);         // dl: of log a, times log a
@@ -282,7 +257,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void rec_bwd_kernel(BwdParams p) {
       if (++turn == kRun || !more) {
         turn = 0;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < kV; ++j) {
           sum[j] += run[j];
           run[j] = 0.0f;
         }
@@ -292,38 +267,35 @@ __global__ __launch_bounds__(kWaves * 64, 2) void rec_bwd_kernel(BwdParams p) {
     dy = ndy;
     if constexpr (Z) z = nz;
   }
-  // sums over the workgroup's stretches, in order
-  __syncthreads();
-  float* const box = &tc[0][0][0];
-#pragma unroll
-  for (int pass = 0; pass < 4; ++pass) {
-    if (at.sub == pass) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float f = SUM ? lsum[j] : sum[j];
-        float* d = box + at.wv * kRecChans + li + j;
-        *d = pass > 0 ? *d + f : f;
-      }
-    }
-    __syncthreads();
-  }
-  if (at.wv == 0 && at.sub == 0) {
-    float tot[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      tot[j] = 0.0f;
-#pragma unroll
-      for (int o = 0; o < kWaves; ++o) tot[j] += box[o * kRecChans + li + j];
-    }
-    if constexpr (SUM) {
-      store_f32(p.clog + crow, at.n, tot);
+  if constexpr (SUM) {
+    if (at.wv == 0 && at.sub == 0) {
+      store_f32(p.cdec + crow, at.n, dec);
       store_f32(p.cadj + crow, at.n, W);
-    } else {
+    }
+  } else {
+    // dlam: the workgroup's stretches, in order
+    __syncthreads();
+    float* const box = &tc[0][0][0];
+#pragma unroll
+    for (int pass = 0; pass < kSubs; ++pass) {
+      if (at.sub == pass) {
+#pragma unroll
+        for (int j = 0; j < kV; ++j) {
+          float* d = box + at.wv * kRecChans + li + j;
+          *d = pass > 0 ? *d + sum[j] : sum[j];
+        }
+      }
+      __syncthreads();
+    }
+    if (at.wv == 0 && at.sub == 0) {
       // d log a / d lam = log a sigmoid(lam) / softplus(lam); the ratio is 1 far below 0
-      float lam[4];
+      float tot[kV], lam[kV];
       load_f32(p.lam + at.c, at.n, lam);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < kV; ++j) {
+        tot[j] = 0.0f;
+#pragma unroll
+        for (int o = 0; o < kWaves; ++o) tot[j] += box[o * kRecChans + li + j];
         const float sp = softplus_log2(lam[j] * kLog2e) * kLn2, ratio = sigmoid(lam[j]) / sp;
         tot[j] *= sp > 0.0f ? ratio : 1.0f;
       }
@@ -347,7 +319,7 @@ int launch_rec_bwd(const ss_rec_desc_t& d, const RecPlan& pl, const void* x, con
                     di, dz, dh0, reinterpret_cast<float*>(ws + pl.off_log),
                     reinterpret_cast<float*>(ws + pl.off_carry),
                     reinterpret_cast<float*>(ws + pl.off_part)};
-  const bool any = d.dim % 4 != 0 || odd_rows(x, p.ldx, d.in_dtype) ||
+  const bool any = d.dim % kV != 0 || odd_rows(x, p.ldx, d.in_dtype) ||
                    odd_rows(r, p.ldr, d.in_dtype) || odd_rows(i, p.ldi, d.in_dtype) ||
                    odd_rows(z, p.ldz, d.in_dtype);
   hipStream_t st = static_cast<hipStream_t>(stream);
@@ -360,7 +332,7 @@ int launch_rec_bwd(const ss_rec_desc_t& d, const RecPlan& pl, const void* x, con
       using Dy = decltype(dtype);
       if (pl.nchunks > 1) {
         rec_bwd_kernel<T, Dy, Z, M, A, true><<<blocks, kWaves * 64, 0, st>>>(p);
-        launch_rec_carry(p.clog, p.cadj, dh_last, d.batch, p.s.D, p.s.nchunks, true, st);
+        launch_rec_carry(p.cdec, p.cadj, dh_last, d.batch, p.s.D, p.s.nchunks, true, st);
       }
       rec_bwd_kernel<T, Dy, Z, M, A, false><<<blocks, kWaves * 64, 0, st>>>(p);
     };
