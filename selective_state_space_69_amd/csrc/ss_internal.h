@@ -263,7 +263,7 @@ int launch_linear_bwd(const ss_linear_desc_t& d, const LinearPlan& pl, const voi
                       const void* dy, void* dx, void* dw, float* dbias, char* ws, void* stream);
 
 // Gated linear recurrence (ss_rec.hip): time in nchunks chunks of `chunk` steps, one
-// workgroup each per 64 channels.  Workspace, fp32 (B, nchunks, D) arrays, 256-byte
+// workgroup each per group of channels.  Workspace, fp32 (B, nchunks, D) arrays, 256-byte
 // aligned: chunks' log decays and carries (nchunks > 1), backward partial sums of dlam.
 struct RecPlan {
   int64_t chunk = 0, nchunks = 1;

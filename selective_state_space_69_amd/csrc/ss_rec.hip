@@ -2,7 +2,7 @@
 // Layout and accuracy: ss_rec.hpp.
 //
 // The forward moves each tensor once and is bound by memory.  A workgroup takes 32
-// channels of one batch row and walks its time in blocks, the next block's rows being
+// channels of one batch row and walks its time in blocks, the rows of the next two being
 // loaded while the present one is computed; one barrier per block joins the waves.  Few
 // channels (one long sequence) would leave the GPU empty: their time is cut into chunks,
 // whose carries a first pass over the inputs provides.
@@ -11,10 +11,13 @@
 namespace ss {
 namespace {
 
-constexpr int kS = 8;                       // steps of a lane's stretch
+constexpr int kS = 4;                       // steps of a lane's stretch
 constexpr int kWaveSteps = kSubs * kS;
-constexpr int kWaves = 4;
+constexpr int kWaves = 8;
 constexpr int kBlock = kWaves * kWaveSteps;
+// Steps of a lane, waves (bf16 8 x 2048 x 2560 with a gate, us): 4, 8 117; 4, 4 146; 8, 4 145
+// (more loads than the counter of those in flight holds); 4, 16 139.  Rows 5120 bytes apart
+// are the slow ones of these: 8 x 2048 x 2592 takes 110, 107, 112 and 124.
 static_assert(SS_REC_CHUNK % kWaveSteps == 0 && kBlock % SS_REC_CHUNK == 0,
               "states are kept at a wave's first step");
 
@@ -28,12 +31,14 @@ struct FwdParams {
   void* y;
   float *h_last, *states;
   float *cdec, *cend;        // (B, nchunks, D) chunks' decays; end, then start states
-  int32_t out_bf16;
 };
 
 // Z: with a gate.  MASK: starts or lengths given.  SUM: only the chunks' carries.
-template <typename T, bool Z, bool MASK, bool ANY, bool SUM>
-__global__ __launch_bounds__(kWaves * 64, 4) void rec_fwd_kernel(FwdParams p) {
+// No branch skips a load or a store: the compiler then knows how many are in flight, and
+// waits for the oldest alone.
+template <typename T, typename Out, bool Z, bool MASK, bool ANY, bool SUM>
+__global__ __launch_bounds__(kWaves * 64, sizeof(T) == 2 && !ANY ? 4 : 2)
+void rec_fwd_kernel(FwdParams p) {
 #if defined(__HIP_DEVICE_COMPILE__)
   __shared__ float tc[2][kWaves][kRecChans], ts[2][kWaves][kRecChans];
   const Place at(p.s);
@@ -43,8 +48,10 @@ __global__ __launch_bounds__(kWaves * 64, 4) void rec_fwd_kernel(FwdParams p) {
   Masks masks;
   masks.init<MASK>(p.starts, p.lengths, at.b, L, t0, p.s.chunk);
   const int64_t crow = int64_t(at.b * p.s.nchunks + at.chunk) * D + at.c;
-  float k[kV], H[kV] = {0, 0}, dec[kV] = {1, 1};
+  float k[kV], H[kV] = {}, dec[kV];
   load_f32(p.lam + at.c, at.n, k);
+#pragma unroll
+  for (int j = 0; j < kV; ++j) dec[j] = 1.0f;
 #pragma unroll
   for (int j = 0; j < kV; ++j) k[j] = rec_rate(p.s.decay, k[j]);
   if (!SUM) {
@@ -59,18 +66,39 @@ __global__ __launch_bounds__(kWaves * 64, 4) void rec_fwd_kernel(FwdParams p) {
   pr.init(p.r, p.ldr, sizeof(T), p.s, row0 + t0, off, at);
   pi.init(p.i, p.ldi, sizeof(T), p.s, row0 + t0, off, at);
   if constexpr (Z && !SUM) pz.init(p.z, p.ldz, sizeof(T), p.s, row0 + t0, off, at);
-  if constexpr (!SUM) py.init(p.y, D, p.out_bf16 ? 2 : 4, p.s, row0 + t0, off, at);
-  Rows<T, kS, ANY> x, r, i, z;
-  int valid = masks.steps - off;           // steps of the lane's stretch inside the chunk
-  x.load(px, valid);
-  r.load(pr, valid);
-  i.load(pi, valid);
-  if constexpr (Z && !SUM) z.load(pz, valid);
-  for (int tb = 0, buf = 0; tb < masks.steps; tb += kBlock, buf ^= 1) {
-    const int live = masks.len - tb - off;
+  if constexpr (!SUM) py.init(p.y, D, sizeof(Out), p.s, row0 + t0, off, at);
+  // two blocks in turn: each one's rows are loaded as soon as those before are used up
+  struct Block { Rows<T, kS, ANY> x, r, i, z; } even, odd;
+  auto load = [&](Block& b, int valid) {       // x, r, i
+    b.x.load(px, valid);
+    b.r.load(pr, valid);
+    b.i.load(pi, valid);
+    px.move(kBlock);
+    pr.move(kBlock);
+    pi.move(kBlock);
+    __builtin_amdgcn_sched_barrier(0);       // loads stay in the order of their use
+  };
+  auto load_z = [&](Block& b, int valid) {
+    if constexpr (Z && !SUM) {
+      b.z.load(pz, valid);
+      pz.move(kBlock);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  load(even, masks.steps - off);
+  load_z(even, masks.steps - off);
+  load(odd, masks.steps - off - kBlock);
+  load_z(odd, masks.steps - off - kBlock);
+  auto run = [&](Block& in_, int tb, int buf) {
+    // steps of the lane's stretch inside the chunk, this time and the next; before the length
+    const int now = masks.steps - tb - off, next = now - 2 * kBlock, live = masks.len - tb - off;
+    auto& x = in_.x;
+    auto& r = in_.r;
+    auto& i = in_.i;
+    auto& z = in_.z;
     bool start[kS] = {};
     if constexpr (MASK) masks.marks(tb + off, start);
-    float c[kS][kV], g[kS][kV], l[kV] = {0, 0}, s[kV] = {0, 0};
+    float c[kS][kV], g[kS][kV], l[kV] = {}, s[kV] = {};
     bool cuts = false;
 #pragma unroll
     for (int e = 0; e < kS; ++e) {
@@ -93,18 +121,7 @@ __global__ __launch_bounds__(kWaves * 64, 4) void rec_fwd_kernel(FwdParams p) {
       }
       if (MASK) cuts |= start[e] && e < live;
     }
-    // the next block's rows arrive under the rest of this one's work (z under the next's)
-    const int now = valid;
-    const bool more = tb + kBlock < masks.steps;
-    if (more) {
-      valid -= kBlock;
-      px.move(kBlock);
-      pr.move(kBlock);
-      pi.move(kBlock);
-      x.load(px, valid);
-      r.load(pr, valid);
-      i.load(pi, valid);
-    }
+    load(in_, next);
     float cx[kV], sx[kV], cw[kV];            // of the stretches in front of the lane's, of the wave
 #pragma unroll
     for (int j = 0; j < kV; ++j) {
@@ -112,22 +129,21 @@ __global__ __launch_bounds__(kWaves * 64, 4) void rec_fwd_kernel(FwdParams p) {
       join_up<MASK>(at.sub, cw[j], s[j], cx[j], sx[j]);
     }
     if (at.sub == 0) {
-      *reinterpret_cast<float2*>(&tc[buf][at.wv][li]) = make_float2(cw[0], cw[1]);
-      *reinterpret_cast<float2*>(&ts[buf][at.wv][li]) = make_float2(s[0], s[1]);
+      put_lds(&tc[buf][at.wv][li], cw);
+      put_lds(&ts[buf][at.wv][li], s);
     }
     __syncthreads();
     if constexpr (Z && !SUM) z.fresh();
-    float h[kV] = {0, 0};
+    float h[kV] = {};
 #pragma unroll 2
     for (int w = 0; w < kWaves; ++w) {
-      const float2 cv = *reinterpret_cast<const float2*>(&tc[buf][w][li]);
-      const float2 sv = *reinterpret_cast<const float2*>(&ts[buf][w][li]);
-      const float cw4[kV] = {cv.x, cv.y}, s4[kV] = {sv.x, sv.y};
+      const Floats cv = get_lds(&tc[buf][w][li]);
+      const Floats sv = get_lds(&ts[buf][w][li]);
 #pragma unroll
       for (int j = 0; j < kV; ++j) {
-        if (SUM) dec[j] = rec_both<MASK>(dec[j], cw4[j]);
+        if (SUM) dec[j] = rec_both<MASK>(dec[j], cv.v[j]);
         h[j] = w == at.wv ? H[j] : h[j];
-        H[j] = rec_apply<MASK>(cw4[j], H[j], s4[j]);
+        H[j] = rec_apply<MASK>(cv.v[j], H[j], sv.v[j]);
       }
     }
     if constexpr (!SUM) {
@@ -150,19 +166,15 @@ __global__ __launch_bounds__(kWaves * 64, 4) void rec_fwd_kernel(FwdParams p) {
           if (MASK) out[e][j] = e < live ? out[e][j] : 0.0f;
         }
       }
-      if (Z && more) {
-        pz.move(kBlock);
-        z.load(pz, valid);
-      }
-      if (p.out_bf16) {
+      load_z(in_, next);
 #pragma unroll
-        for (int e = 0; e < kS; ++e) put<uint16_t>(py, e, now, at.n, out[e]);
-      } else {
-#pragma unroll
-        for (int e = 0; e < kS; ++e) put<float>(py, e, now, at.n, out[e]);
-      }
+      for (int e = 0; e < kS; ++e) put<Out>(py, e, now, at.n, out[e]);
       py.move(kBlock);
     }
+  };
+  for (int tb = 0; tb < masks.steps; tb += 2 * kBlock) {
+    run(even, tb, 0);
+    run(odd, tb + kBlock, 1);
   }
   if (at.wv == 0 && at.sub == 0) {
     if constexpr (SUM) {
@@ -290,7 +302,7 @@ int launch_rec_fwd(const ss_rec_desc_t& d, const RecPlan& pl, const void* x, con
                     stride_of(d.r_stride, d.dim), stride_of(d.i_stride, d.dim),
                     stride_of(d.z_stride, d.dim), lam, h0, starts, lengths, y, h_last, states,
                     reinterpret_cast<float*>(ws + pl.off_log),
-                    reinterpret_cast<float*>(ws + pl.off_carry), d.out_dtype == SS_BF16};
+                    reinterpret_cast<float*>(ws + pl.off_carry)};
   const bool any = d.dim % kV != 0 || odd_rows(x, p.ldx, d.in_dtype) ||
                    odd_rows(r, p.ldr, d.in_dtype) || odd_rows(i, p.ldi, d.in_dtype) ||
                    odd_rows(z, p.ldz, d.in_dtype);
@@ -301,10 +313,13 @@ int launch_rec_fwd(const ss_rec_desc_t& d, const RecPlan& pl, const void* x, con
     auto run = [&](auto type) {
       using T = decltype(type);
       if (pl.nchunks > 1) {
-        rec_fwd_kernel<T, false, M, A, true><<<blocks, kWaves * 64, 0, st>>>(p);
+        rec_fwd_kernel<T, float, false, M, A, true><<<blocks, kWaves * 64, 0, st>>>(p);
         launch_rec_carry(p.cdec, p.cend, h0, d.batch, p.s.D, p.s.nchunks, false, st);
       }
-      rec_fwd_kernel<T, Z, M, A, false><<<blocks, kWaves * 64, 0, st>>>(p);
+      if (d.out_dtype == SS_BF16)
+        rec_fwd_kernel<T, uint16_t, Z, M, A, false><<<blocks, kWaves * 64, 0, st>>>(p);
+      else
+        rec_fwd_kernel<T, float, Z, M, A, false><<<blocks, kWaves * 64, 0, st>>>(p);
     };
     if (d.in_dtype == SS_BF16) run(uint16_t{});
     else run(float{});

@@ -28,7 +28,7 @@ constexpr float kTiny = 1.17549435e-38f;         // smallest normal number
 
 struct RecShape {
   int64_t B, L;
-  int32_t D, groups;          // groups: of 64 channels
+  int32_t D, groups;          // groups: of kRecChans channels
   int64_t chunk;              // steps of a chunk, one workgroup's
   int32_t nchunks;
   float decay;
@@ -67,14 +67,40 @@ template <bool CUT> __device__ __forceinline__ float rec_apply(float p, float h,
 }
 
 // A lane's channels of a row, as stored, so that a prefetch is not waited for.
-template <typename T> struct Pair { uint32_t w[kV * sizeof(T) / 4]; };
-__device__ __forceinline__ void unpack(const Pair<float>& q, float (&v)[kV]) {
-  v[0] = __uint_as_float(q.w[0]);
-  v[1] = __uint_as_float(q.w[1]);
+template <typename T> constexpr int kWords = kV * int(sizeof(T)) / 4;
+template <typename T> struct Chans { uint32_t w[kWords<T>]; };
+__device__ __forceinline__ void unpack(const Chans<float>& q, float (&v)[kV]) {
+#pragma unroll
+  for (int j = 0; j < kV; ++j) v[j] = __uint_as_float(q.w[j]);
 }
-__device__ __forceinline__ void unpack(const Pair<uint16_t>& q, float (&v)[kV]) {
-  v[0] = __uint_as_float(q.w[0] << 16);
-  v[1] = __uint_as_float(q.w[0] & 0xffff0000u);
+__device__ __forceinline__ void unpack(const Chans<uint16_t>& q, float (&v)[kV]) {
+#pragma unroll
+  for (int j = 0; j < kV; ++j)
+    v[j] = __uint_as_float(j & 1 ? q.w[j / 2] & 0xffff0000u : q.w[j / 2] << 16);
+}
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+template <typename T>
+__device__ __forceinline__ Chans<T> buf_chans(Rsrc v, uint32_t at, uint32_t row) {
+  if constexpr (kWords<T> == 1)
+    return __builtin_bit_cast(Chans<T>, __builtin_amdgcn_raw_buffer_load_b32(v, at, row, 0));
+  else if constexpr (kWords<T> == 2)
+    return __builtin_bit_cast(Chans<T>, __builtin_amdgcn_raw_buffer_load_b64(v, at, row, 0));
+  else
+    return __builtin_bit_cast(Chans<T>, __builtin_amdgcn_raw_buffer_load_b128(v, at, row, 0));
+}
+template <typename T>
+__device__ __forceinline__ void buf_put(Rsrc v, uint32_t at, uint32_t row, const float (&f)[kV]) {
+  Chans<T> q;
+#pragma unroll
+  for (int j = 0; j < kWords<T>; ++j)
+    q.w[j] = sizeof(T) == 2 ? cvt_bf16x2(f[2 * j % kV], f[(2 * j + 1) % kV]) : __float_as_uint(f[j]);
+  if constexpr (kWords<T> == 1)
+    __builtin_amdgcn_raw_buffer_store_b32(q.w[0], v, at, row, 0);
+  else if constexpr (kWords<T> == 2)
+    __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, q), v, at, row, 0);
+  else
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, q), v, at, row, 0);
 }
 // A lane's n channels of a (D) row of floats; others repeat the first.
 __device__ __forceinline__ void load_f32(const float* p, int n, float (&v)[kV]) {
@@ -181,7 +207,7 @@ struct Place {
 template <bool ANY> struct Stream {
   const char* p;
   uint32_t first, row;       // bytes; row: from one row to the next
-  int64_t left;              // ANY: bytes from p to the tensor's end
+  int64_t left;              // ANY: bytes from p to the tensor's end (negative behind it)
   // size: of an element
   __device__ __forceinline__ void init(const void* base, int64_t ld, uint32_t size,
                                        const RecShape& s, int64_t row0, int off, const Place& at) {
@@ -196,33 +222,34 @@ template <bool ANY> struct Stream {
   }
   __device__ __forceinline__ Rsrc rsrc() const {
     int n = 0x7fffffff;
-    if constexpr (ANY) n = left < 0x7fffffff ? int(left) : 0x7fffffff;
+    if constexpr (ANY) n = left < 0 ? 0 : left < 0x7fffffff ? int(left) : 0x7fffffff;
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(p), short(0), n, 0x00020000);
   }
 };
 
 // The rows of a lane's stretch of one tensor; those from `valid` on hold anything.
 template <typename T, int S, bool ANY> struct Rows {
-  Pair<T> q[S];
+  Chans<T> q[S];
   __device__ __forceinline__ void load(const Stream<ANY>& st, int valid) {
     const Rsrc v = st.rsrc();
 #pragma unroll
     for (int s = 0; s < S; ++s) {
       if constexpr (!ANY) {
-        const uint32_t at = s < valid ? st.first : kOutOfRange, row = uint32_t(s) * st.row;
-        if constexpr (sizeof(T) == 4)
-          q[s] = __builtin_bit_cast(Pair<T>, __builtin_amdgcn_raw_buffer_load_b64(v, at, row, 0));
-        else
-          q[s] = __builtin_bit_cast(Pair<T>, __builtin_amdgcn_raw_buffer_load_b32(v, at, row, 0));
+        q[s] = buf_chans<T>(v, s < valid ? st.first : kOutOfRange, uint32_t(s) * st.row);
       } else {
         const uint32_t at = s < valid ? st.first + uint32_t(s) * st.row : kOutOfRange;
         if constexpr (sizeof(T) == 4) {
-          q[s].w[0] = __builtin_amdgcn_raw_buffer_load_b32(v, at, 0, 0);
-          q[s].w[1] = __builtin_amdgcn_raw_buffer_load_b32(v, at + 4, 0, 0);
+#pragma unroll
+          for (int j = 0; j < kV; ++j)
+            q[s].w[j] = __builtin_amdgcn_raw_buffer_load_b32(v, at + 4 * j, 0, 0);
         } else {
-          const uint32_t e0 = uint16_t(__builtin_amdgcn_raw_buffer_load_b16(v, at, 0, 0));
-          const uint32_t e1 = uint16_t(__builtin_amdgcn_raw_buffer_load_b16(v, at + 2, 0, 0));
-          q[s].w[0] = e0 | e1 << 16;
+#pragma unroll
+          for (int j = 0; j < kV; j += 2) {
+            const uint32_t e0 = uint16_t(__builtin_amdgcn_raw_buffer_load_b16(v, at + 2 * j, 0, 0));
+            const uint32_t e1 =
+                uint16_t(__builtin_amdgcn_raw_buffer_load_b16(v, at + 2 * j + 2, 0, 0));
+            q[s].w[j / 2] = e0 | e1 << 16;
+          }
         }
       }
     }
@@ -233,8 +260,8 @@ template <typename T, int S, bool ANY> struct Rows {
 #if defined(__HIP_DEVICE_COMPILE__)
 #pragma unroll
     for (int s = 0; s < S; ++s) {
-      asm volatile("" : "+v"(q[s].w[0]));
-      if constexpr (sizeof(T) == 4) asm volatile("" : "+v"(q[s].w[1]));
+#pragma unroll
+      for (int j = 0; j < kWords<T>; ++j) asm volatile("" : "+v"(q[s].w[j]));
     }
 #endif
   }
@@ -252,12 +279,7 @@ __device__ __forceinline__ void put(const Stream<ANY>& st, int s, int valid, int
     for (int j = 0; j < kV; ++j)
       buf_store<T>(v, j < n ? at + j * uint32_t(sizeof(T)) : kOutOfRange, 0, f[j]);
   } else {
-    const uint32_t at = s < valid ? st.first : kOutOfRange, row = uint32_t(s) * st.row;
-    if constexpr (sizeof(T) == 2)
-      __builtin_amdgcn_raw_buffer_store_b32(cvt_bf16x2(f[0], f[1]), v, at, row, 0);
-    else
-      __builtin_amdgcn_raw_buffer_store_b64(u32x2{__float_as_uint(f[0]), __float_as_uint(f[1])}, v,
-                                            at, row, 0);
+    buf_put<T>(v, s < valid ? st.first : kOutOfRange, uint32_t(s) * st.row, f);
   }
 }
 
@@ -308,6 +330,18 @@ inline RecShape rec_shape(const ss_rec_desc_t& d, const RecPlan& pl) {
                   pl.chunk, int32_t(pl.nchunks), d.decay};
 }
 inline int64_t stride_of(int64_t stride, int64_t dim) { return stride ? stride : dim; }
+// The floats of a lane's channels in LDS.
+struct alignas(4 * kV) Floats { float v[kV]; };
+__device__ __forceinline__ void put_lds(float* p, const float (&v)[kV]) {
+  Floats f;
+#pragma unroll
+  for (int j = 0; j < kV; ++j) f.v[j] = v[j];
+  *reinterpret_cast<Floats*>(p) = f;
+}
+__device__ __forceinline__ Floats get_lds(const float* p) {
+  return *reinterpret_cast<const Floats*>(p);
+}
+
 // whether pairs of bf16 rows are not 4-byte aligned
 inline bool odd_rows(const void* p, int64_t ld, int32_t dtype) {
   return p && dtype == SS_BF16 && (ld % 2 != 0 || reinterpret_cast<uintptr_t>(p) % 4 != 0);

@@ -34,10 +34,13 @@ struct BwdParams {
   float* part;               // (B * nchunks, D) sums of dlam
 };
 
+// Two waves to a SIMD: at three the registers do not suffice (bf16 8 x 2048 x 2560 with a gate
+// 290 us, 237 so; 8 waves of 2 steps 252, 8 of 4 259).
 // SUM: only the chunks' carries (decay, and the adjoint that leaves with none
 // entering).
 template <typename T, typename Dy, bool Z, bool MASK, bool ANY, bool SUM>
-__global__ __launch_bounds__(kWaves * 64, 2) void rec_bwd_kernel(BwdParams p) {
+__global__ __launch_bounds__(kWaves * 64, 2)
+void rec_bwd_kernel(BwdParams p) {
 #if defined(__HIP_DEVICE_COMPILE__)
   __shared__ float tc[2][kWaves][kRecChans], ts[2][kWaves][kRecChans], tq[2][kWaves][kRecChans];
   const Place at(p.s);
@@ -48,9 +51,11 @@ __global__ __launch_bounds__(kWaves * 64, 2) void rec_bwd_kernel(BwdParams p) {
   masks.init<MASK>(p.starts, p.lengths, at.b, L, t0, p.s.chunk);
   const int64_t crow = int64_t(at.b * p.s.nchunks + at.chunk) * D + at.c;
   const int64_t n_states = (L + SS_REC_CHUNK - 1) / SS_REC_CHUNK;
-  float k[kV], W[kV] = {0, 0}, dec[kV] = {1, 1};
-  float run[kV] = {0, 0}, sum[kV] = {0, 0};     // of dlam: of kRun blocks, of the chunk
+  float k[kV], W[kV] = {}, dec[kV];
+  float run[kV] = {}, sum[kV] = {};     // of dlam: of kRun blocks, of the chunk
   load_f32(p.lam + at.c, at.n, k);
+#pragma unroll
+  for (int j = 0; j < kV; ++j) dec[j] = 1.0f;
 #pragma unroll
   for (int j = 0; j < kV; ++j) k[j] = rec_rate(p.s.decay, k[j]);
   if (!SUM) {
@@ -79,38 +84,55 @@ __global__ __launch_bounds__(kWaves * 64, 2) void rec_bwd_kernel(BwdParams p) {
     ks = ks < n_states ? ks : n_states - 1;
     load_f32(p.states + (at.b * n_states + ks) * D + at.c, at.n, st);
   };
-  Rows<T, kS, ANY> x, r, i, z, nx, nz;
-  Rows<Dy, kS, ANY> dy, ndy;
-  float st[kV] = {0, 0};
-  int valid = masks.steps - tb - off;           // steps of the lane's stretch inside the chunk
-  r.load(pr, valid);
-  dy.load(pd, valid);
-  if constexpr (Z) z.load(pz, valid);
-  if constexpr (!SUM) {
-    x.load(px, valid);
-    i.load(pi, valid);
-    state(tb, st);
-  }
-  for (int buf = 0, turn = 0; tb >= 0; tb -= kBlock, buf ^= 1) {
-    const bool more = tb > 0;
-    const int now = valid, live = masks.len - tb - off;
-    if (more) {
-      valid = kS;
-      pd.move(-kBlock);
-      ndy.load(pd, valid);
-      if constexpr (Z) {
-        pz.move(-kBlock);
-        nz.load(pz, valid);
-      }
-      if constexpr (!SUM) {
-        px.move(-kBlock);
-        nx.load(px, valid);
-      }
+  // two blocks in turn: each one's rows are loaded as soon as those before are used up
+  struct Block {
+    Rows<T, kS, ANY> x, r, i, z;
+    Rows<Dy, kS, ANY> dy;
+    float st[kV];
+  } even, odd;
+  auto load_gates = [&](Block& b, int valid) {
+    b.r.load(pr, valid);
+    pr.move(-kBlock);
+    if constexpr (!SUM) {
+      b.i.load(pi, valid);
+      pi.move(-kBlock);
     }
+    __builtin_amdgcn_sched_barrier(0);       // loads stay in the order of their use
+  };
+  auto load_rest = [&](Block& b, int tb, int valid) {
+    b.dy.load(pd, valid);
+    pd.move(-kBlock);
+    if constexpr (Z) {
+      b.z.load(pz, valid);
+      pz.move(-kBlock);
+    }
+    if constexpr (!SUM) {
+      b.x.load(px, valid);
+      px.move(-kBlock);
+      state(tb < 0 ? 0 : tb, b.st);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  // steps of the lane's stretch inside the chunk, of the block from step tb on
+  auto inside = [&](int tb) { return tb < 0 ? 0 : masks.steps - tb - off; };
+  load_gates(even, inside(tb));
+  load_rest(even, tb, inside(tb));
+  load_gates(odd, inside(tb - kBlock));
+  load_rest(odd, tb - kBlock, inside(tb - kBlock));
+  int turn = 0;
+  auto work = [&](Block& in_, int tb, int buf) {
+    // a block in front of the chunk's first step is empty
+    const int now = inside(tb), next = inside(tb - 2 * kBlock), live = tb < 0 ? 0 : masks.len - tb - off;
+    auto& x = in_.x;
+    auto& r = in_.r;
+    auto& i = in_.i;
+    auto& z = in_.z;
+    auto& dy = in_.dy;
+    auto& st = in_.st;
     bool start[kS] = {};
     if constexpr (MASK) masks.marks(tb + off, start);
     float c[kS][kV], sr[kS][kV], si[kS][kV], beta[kS][kV], v[kS][kV];
-    float l[kV] = {0, 0}, s[kV] = {0, 0}, q[kV] = {0, 0};
+    float l[kV] = {}, s[kV] = {}, q[kV] = {};
     bool cuts = false;
 #pragma unroll
     for (int e = 0; e < kS; ++e) {
@@ -143,14 +165,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void rec_bwd_kernel(BwdParams p) {
         }
       }
     }
-    if (more) {
-      pr.move(-kBlock);
-      r.load(pr, valid);
-      if constexpr (!SUM) {
-        pi.move(-kBlock);
-        i.load(pi, valid);
-      }
-    }
+    load_gates(in_, next);
 #pragma unroll
     for (int e = kS - 1; e >= 0; --e)
 #pragma unroll
@@ -163,10 +178,10 @@ __global__ __launch_bounds__(kWaves * 64, 2) void rec_bwd_kernel(BwdParams p) {
       join_both<MASK, !SUM>(at.sub, cw[j], s[j], q[j], cx[j], sx[j], cy[j], qy[j]);
     }
     if (at.sub == 0) {
-      *reinterpret_cast<float2*>(&tc[buf][at.wv][li]) = make_float2(cw[0], cw[1]);
-      *reinterpret_cast<float2*>(&tq[buf][at.wv][li]) = make_float2(q[0], q[1]);
+      put_lds(&tc[buf][at.wv][li], cw);
+      put_lds(&tq[buf][at.wv][li], q);
       if constexpr (!SUM)
-        *reinterpret_cast<float2*>(&ts[buf][at.wv][li]) = make_float2(s[0], s[1]);
+        put_lds(&ts[buf][at.wv][li], s);
     }
     __syncthreads();
     if constexpr (!SUM) {
@@ -174,31 +189,28 @@ __global__ __launch_bounds__(kWaves * 64, 2) void rec_bwd_kernel(BwdParams p) {
       dy.fresh();
       if constexpr (Z) z.fresh();
     }
-    float w[kV] = {0, 0}, h[kV];
+    float w[kV] = {}, h[kV];
 #pragma unroll
     for (int j = 0; j < kV; ++j) h[j] = st[j];
 #pragma unroll 2
     for (int o = kWaves - 1; o >= 0; --o) {
-      const float2 cv = *reinterpret_cast<const float2*>(&tc[buf][o][li]);
-      const float2 qv = *reinterpret_cast<const float2*>(&tq[buf][o][li]);
-      const float cw4[kV] = {cv.x, cv.y}, q4[kV] = {qv.x, qv.y};
+      const Floats cv = get_lds(&tc[buf][o][li]);
+      const Floats qv = get_lds(&tq[buf][o][li]);
 #pragma unroll
       for (int j = 0; j < kV; ++j) {
-        if (SUM) dec[j] = rec_both<MASK>(dec[j], cw4[j]);
+        if (SUM) dec[j] = rec_both<MASK>(dec[j], cv.v[j]);
         w[j] = o == at.wv ? W[j] : w[j];
-        W[j] = rec_apply<MASK>(cw4[j], W[j], q4[j]);
+        W[j] = rec_apply<MASK>(cv.v[j], W[j], qv.v[j]);
       }
     }
     if constexpr (!SUM) {
       // the waves between the kept state and this one
       for (int o = at.wv / kPerState * kPerState; o < at.wv; ++o) {
-        const float2 cv = *reinterpret_cast<const float2*>(&tc[buf][o][li]);
-        const float2 sv = *reinterpret_cast<const float2*>(&ts[buf][o][li]);
-        const float cw4[kV] = {cv.x, cv.y}, s4[kV] = {sv.x, sv.y};
-#pragma unroll
-        for (int j = 0; j < kV; ++j) h[j] = rec_apply<MASK>(cw4[j], h[j], s4[j]);
+        const Floats cv = get_lds(&tc[buf][o][li]);
+        const Floats sv = get_lds(&ts[buf][o][li]);
+  #pragma unroll
+        for (int j = 0; j < kV; ++j) h[j] = rec_apply<MASK>(cv.v[j], h[j], sv.v[j]);
       }
-      if (more) state(tb - kBlock, st);
       float hs[kS + 1][kV];       // the state in front of each step, behind the last
 #pragma unroll
       for (int j = 0; j < kV; ++j) {
@@ -254,7 +266,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void rec_bwd_kernel(BwdParams p) {
       or_.move(-kBlock);
       oi.move(-kBlock);
       if constexpr (Z) oz.move(-kBlock);
-      if (++turn == kRun || !more) {
+      if (++turn == kRun || tb <= 0) {
         turn = 0;
 #pragma unroll
         for (int j = 0; j < kV; ++j) {
@@ -263,9 +275,11 @@ __global__ __launch_bounds__(kWaves * 64, 2) void rec_bwd_kernel(BwdParams p) {
         }
       }
     }
-    x = nx;
-    dy = ndy;
-    if constexpr (Z) z = nz;
+    load_rest(in_, tb - 2 * kBlock, next);
+  };
+  for (; tb >= 0; tb -= 2 * kBlock) {
+    work(even, tb, 0);
+    work(odd, tb - kBlock, 1);
   }
   if constexpr (SUM) {
     if (at.wv == 0 && at.sub == 0) {
