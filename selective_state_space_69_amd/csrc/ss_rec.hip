@@ -1,11 +1,12 @@
-// Gated linear recurrence for gfx950: forward, chunk carries, decode step, plan.
+// Gated linear recurrence for gfx950: forward, decode step, plan.
 // Layout and accuracy: ss_rec.hpp.
 //
 // The forward moves each tensor once and is bound by memory.  A workgroup takes 32
 // channels of one batch row and walks its time in blocks, the rows of the next two being
 // loaded while the present one is computed; one barrier per block joins the waves.  Few
 // channels (one long sequence) would leave the GPU empty: their time is cut into chunks,
-// whose carries a first pass over the inputs provides.
+// whose decays and end states a first pass over the inputs provides; every chunk folds
+// those in front of it.
 #include "ss_rec.hpp"
 
 namespace ss {
@@ -30,7 +31,7 @@ struct FwdParams {
   const int32_t* lengths;
   void* y;
   float *h_last, *states;
-  float *cdec, *cend;        // (B, nchunks, D) chunks' decays; end, then start states
+  float *cdec, *cend;        // (B, nchunks, D) chunks' decays and end states from a zero start
 };
 
 // Z: with a gate.  MASK: starts or lengths given.  SUM: only the chunks' carries.
@@ -54,10 +55,7 @@ void rec_fwd_kernel(FwdParams p) {
   for (int j = 0; j < kV; ++j) dec[j] = 1.0f;
 #pragma unroll
   for (int j = 0; j < kV; ++j) k[j] = rec_rate(p.s.decay, k[j]);
-  if (!SUM) {
-    if (p.s.nchunks > 1) load_f32(p.cend + crow, at.n, H);
-    else if (p.h0) load_f32(p.h0 + int64_t(at.b) * D + at.c, at.n, H);
-  }
+  if (!SUM && p.h0) load_f32(p.h0 + int64_t(at.b) * D + at.c, at.n, H);
   const int off = at.wv * kWaveSteps + at.sub * kS;      // of the lane's stretch in a block
   const int li = at.lane % kRecLanes * kV;
 
@@ -85,13 +83,17 @@ void rec_fwd_kernel(FwdParams p) {
       __builtin_amdgcn_sched_barrier(0);
     }
   };
-  load(even, masks.steps - off);
-  load_z(even, masks.steps - off);
-  load(odd, masks.steps - off - kBlock);
-  load_z(odd, masks.steps - off - kBlock);
+  load(even, masks.len - off);
+  load_z(even, masks.len - off);
+  load(odd, masks.len - off - kBlock);
+  load_z(odd, masks.len - off - kBlock);
+  if (!SUM && at.chunk > 0) {
+    const int64_t first = int64_t(at.b) * p.s.nchunks * D + at.c;
+    fold_chunks<MASK, kWaves>(p.cdec + first, p.cend + first, D, at.chunk, at, tc[1], ts[1], H);
+  }
   auto run = [&](Block& in_, int tb, int buf) {
-    // steps of the lane's stretch inside the chunk, this time and the next; before the length
-    const int now = masks.steps - tb - off, next = now - 2 * kBlock, live = masks.len - tb - off;
+    // steps of the lane's stretch inside the chunk; before the length, this time and the next
+    const int now = masks.steps - tb - off, live = masks.len - tb - off, next = live - 2 * kBlock;
     auto& x = in_.x;
     auto& r = in_.r;
     auto& i = in_.i;
@@ -187,24 +189,6 @@ void rec_fwd_kernel(FwdParams p) {
 #endif
 }
 
-// A thread walks the chunks of one channel.  first: what enters the first of them, or
-// null (0).
-__global__ __launch_bounds__(64) void rec_carry_kernel(const float* decay, float* carry,
-                                                       const float* first, int64_t chans,
-                                                       int32_t D, int32_t n, int reverse) {
-  const int64_t i = int64_t(blockIdx.x) * 64 + threadIdx.x;
-  if (i >= chans) return;
-  const int64_t b = i / D, at = b * n * D + (i - b * D);
-  float h = first ? first[i] : 0.0f;
-#pragma unroll 8
-  for (int k = 0; k < n; ++k) {
-    const int64_t o = at + int64_t(reverse ? n - 1 - k : k) * D;
-    const float p = decay[o], s = carry[o];
-    carry[o] = h;
-    h = rec_apply<true>(p, h, s);
-  }
-}
-
 struct StepParams {
   float* h;
   const void *x, *r, *i, *z;
@@ -260,16 +244,19 @@ __global__ __launch_bounds__(64) void rec_step_kernel(StepParams p) {
 }  // namespace
 
 // Time is cut only where the channels leave the GPU empty: below 256 workgroups in one
-// pass, into enough chunks for 1024, of whole blocks (of either pass).
+// pass, into enough chunks for about 1024, of whole pairs of the pass's blocks.  Sequences
+// of up to 4 forward blocks stay whole: the pass over their inputs costs a launch more (1 x
+// 512 x 768 forward 14.5 us, 18.6 in two chunks; 1 x 2048 x 2560 35 in four chunks, 28 in
+// eight).
 RecPlan plan_rec(const ss_rec_desc_t& d, int op) {
   RecPlan pl;
   const int64_t groups = d.batch * ((d.dim + kRecChans - 1) / kRecChans);
   const int64_t blocks = (d.seqlen + kBlock - 1) / kBlock;
   int64_t per = blocks;
-  if (groups < 256) {
-    const int64_t want = (1024 + groups - 1) / groups;
-    per = (blocks + want - 1) / want;
-    if (per < 4) per = 4;
+  if (groups < 256 && blocks > 4) {
+    const int64_t want = (1024 + groups - 1) / groups, least = op == SS_REC_FWD ? 2 : 1;
+    per = (blocks + want - 1) / want / least * least;
+    if (per < least) per = least;
   }
   pl.chunk = per * kBlock;
   pl.nchunks = (d.seqlen + pl.chunk - 1) / pl.chunk;
@@ -285,13 +272,6 @@ RecPlan plan_rec(const ss_rec_desc_t& d, int op) {
     pl.bytes += sz;
   }
   return pl;
-}
-
-void launch_rec_carry(const float* decay, float* carry, const float* first, int64_t batch,
-                      int32_t D, int32_t nchunks, bool reverse, hipStream_t stream) {
-  const int64_t chans = batch * D;
-  rec_carry_kernel<<<unsigned((chans + 63) / 64), 64, 0, stream>>>(decay, carry, first, chans, D,
-                                                                   nchunks, reverse);
 }
 
 int launch_rec_fwd(const ss_rec_desc_t& d, const RecPlan& pl, const void* x, const void* r,
@@ -312,10 +292,8 @@ int launch_rec_fwd(const ss_rec_desc_t& d, const RecPlan& pl, const void* x, con
     constexpr bool Z = decltype(zc)::value, M = decltype(mc)::value, A = decltype(ac)::value;
     auto run = [&](auto type) {
       using T = decltype(type);
-      if (pl.nchunks > 1) {
+      if (pl.nchunks > 1)
         rec_fwd_kernel<T, float, false, M, A, true><<<blocks, kWaves * 64, 0, st>>>(p);
-        launch_rec_carry(p.cdec, p.cend, h0, d.batch, p.s.D, p.s.nchunks, false, st);
-      }
       if (d.out_dtype == SS_BF16)
         rec_fwd_kernel<T, uint16_t, Z, M, A, false><<<blocks, kWaves * 64, 0, st>>>(p);
       else

@@ -200,6 +200,61 @@ struct Place {
   }
 };
 
+// The floats of a lane's channels in LDS.
+struct alignas(4 * kV) Floats { float v[kV]; };
+__device__ __forceinline__ void put_lds(float* p, const float (&v)[kV]) {
+  Floats f;
+#pragma unroll
+  for (int j = 0; j < kV; ++j) f.v[j] = v[j];
+  *reinterpret_cast<Floats*>(p) = f;
+}
+__device__ __forceinline__ Floats get_lds(const float* p) {
+  return *reinterpret_cast<const Floats*>(p);
+}
+
+// What the chunks in front of one's own do to a state, folded by the whole workgroup:
+// decay[k], end[k] (from a zero start), k < n, are `step` floats apart.  The lanes of a
+// channel take equal runs of them, which are joined as stretches are, through tc and ts
+// (kWaves rows each); H is advanced.
+template <bool CUT, int kWaves>
+__device__ __forceinline__ void fold_chunks(const float* decay, const float* end, int64_t step,
+                                            int n, const Place& at, float (*tc)[kRecChans],
+                                            float (*ts)[kRecChans], float (&H)[kV]) {
+  const int units = kWaves * kSubs, per = (n + units - 1) / units;
+  const int k0 = (at.wv * kSubs + at.sub) * per, k1 = k0 + per < n ? k0 + per : n;
+  const int li = at.lane % kRecLanes * kV;
+  float P[kV], s[kV], Px, sx;
+#pragma unroll
+  for (int j = 0; j < kV; ++j) {
+    P[j] = 1.0f;
+    s[j] = 0.0f;
+  }
+#pragma unroll 4
+  for (int k = k0; k < k1; ++k) {
+    float p[kV], e[kV];
+    load_f32(decay + k * step, at.n, p);
+    load_f32(end + k * step, at.n, e);
+#pragma unroll
+    for (int j = 0; j < kV; ++j) {
+      s[j] = rec_apply<CUT>(p[j], s[j], e[j]);
+      P[j] = rec_both<CUT>(P[j], p[j]);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < kV; ++j) join_up<CUT>(at.sub, P[j], s[j], Px, sx);
+  if (at.sub == 0) {
+    put_lds(&tc[at.wv][li], P);
+    put_lds(&ts[at.wv][li], s);
+  }
+  __syncthreads();
+#pragma unroll 2
+  for (int w = 0; w < kWaves; ++w) {
+    const Floats cv = get_lds(&tc[w][li]), sv = get_lds(&ts[w][li]);
+#pragma unroll
+    for (int j = 0; j < kV; ++j) H[j] = rec_apply<CUT>(cv.v[j], H[j], sv.v[j]);
+  }
+}
+
 // One tensor as a workgroup walks it: `p` is the first row of a block, a lane's stretch
 // starts `first` bytes behind it.  Accesses take a scalar base and 32-bit lane offsets.
 // ANY: rows at any element address and pairs that end behind their row, read element by
@@ -286,7 +341,7 @@ __device__ __forceinline__ void put(const Stream<ANY>& st, int s, int valid, int
 // A chunk's steps, counted from its first, and what the masks say of a lane's.
 struct Masks {
   int steps;               // of the chunk
-  int len;                 // those at and behind it leave the state as it is
+  int len;                 // those at and behind it leave the state as it is, and are not read
   Rsrc starts;
   template <bool MASK>
   __device__ __forceinline__ void init(const uint8_t* st, const int32_t* lengths, int32_t b,
@@ -330,26 +385,9 @@ inline RecShape rec_shape(const ss_rec_desc_t& d, const RecPlan& pl) {
                   pl.chunk, int32_t(pl.nchunks), d.decay};
 }
 inline int64_t stride_of(int64_t stride, int64_t dim) { return stride ? stride : dim; }
-// The floats of a lane's channels in LDS.
-struct alignas(4 * kV) Floats { float v[kV]; };
-__device__ __forceinline__ void put_lds(float* p, const float (&v)[kV]) {
-  Floats f;
-#pragma unroll
-  for (int j = 0; j < kV; ++j) f.v[j] = v[j];
-  *reinterpret_cast<Floats*>(p) = f;
-}
-__device__ __forceinline__ Floats get_lds(const float* p) {
-  return *reinterpret_cast<const Floats*>(p);
-}
-
 // whether pairs of bf16 rows are not 4-byte aligned
 inline bool odd_rows(const void* p, int64_t ld, int32_t dtype) {
   return p && dtype == SS_BF16 && (ld % 2 != 0 || reinterpret_cast<uintptr_t>(p) % 4 != 0);
 }
-
-// Chunks' decays and end states (from a zero start) to their start states, or in reverse
-// the adjoints that leave them (with none entering) to those that enter.
-void launch_rec_carry(const float* decay, float* carry, const float* first, int64_t batch,
-                      int32_t D, int32_t nchunks, bool reverse, hipStream_t stream);
 
 }  // namespace ss

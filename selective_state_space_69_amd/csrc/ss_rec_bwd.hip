@@ -30,7 +30,7 @@ struct BwdParams {
   const float *states, *dh_last;
   void *dx, *dr, *di, *dz;
   float* dh0;
-  float *cdec, *cadj;        // (B, nchunks, D) chunks' decays; adjoints leaving, then entering them
+  float *cdec, *cadj;        // (B, nchunks, D) chunks' decays and the adjoints that leave them
   float* part;               // (B * nchunks, D) sums of dlam
 };
 
@@ -58,10 +58,7 @@ void rec_bwd_kernel(BwdParams p) {
   for (int j = 0; j < kV; ++j) dec[j] = 1.0f;
 #pragma unroll
   for (int j = 0; j < kV; ++j) k[j] = rec_rate(p.s.decay, k[j]);
-  if (!SUM) {
-    if (p.s.nchunks > 1) load_f32(p.cadj + crow, at.n, W);
-    else if (p.dh_last) load_f32(p.dh_last + int64_t(at.b) * D + at.c, at.n, W);
-  }
+  if (!SUM && p.dh_last) load_f32(p.dh_last + int64_t(at.b) * D + at.c, at.n, W);
   const int off = at.wv * kWaveSteps + at.sub * kS;      // of the lane's stretch in a block
   const int li = at.lane % kRecLanes * kV;
   int tb = (masks.steps - 1) / kBlock * kBlock;          // the block's first step
@@ -113,16 +110,22 @@ void rec_bwd_kernel(BwdParams p) {
     }
     __builtin_amdgcn_sched_barrier(0);
   };
-  // steps of the lane's stretch inside the chunk, of the block from step tb on
-  auto inside = [&](int tb) { return tb < 0 ? 0 : masks.steps - tb - off; };
-  load_gates(even, inside(tb));
-  load_rest(even, tb, inside(tb));
-  load_gates(odd, inside(tb - kBlock));
-  load_rest(odd, tb - kBlock, inside(tb - kBlock));
+  // steps of the lane's stretch in front of `end`, of the block from step tb on (a block in
+  // front of the chunk's first step is empty)
+  auto steps = [&](int end, int tb) { return tb < 0 ? 0 : end - tb - off; };
+  load_gates(even, steps(masks.len, tb));
+  load_rest(even, tb, steps(masks.len, tb));
+  load_gates(odd, steps(masks.len, tb - kBlock));
+  load_rest(odd, tb - kBlock, steps(masks.len, tb - kBlock));
+  if (!SUM && at.chunk < p.s.nchunks - 1) {       // from the last chunk on
+    const int64_t last = (int64_t(at.b + 1) * p.s.nchunks - 1) * D + at.c;
+    fold_chunks<MASK, kWaves>(p.cdec + last, p.cadj + last, -int64_t(D),
+                              p.s.nchunks - 1 - at.chunk, at, tc[1], tq[1], W);
+  }
   int turn = 0;
   auto work = [&](Block& in_, int tb, int buf) {
-    // a block in front of the chunk's first step is empty
-    const int now = inside(tb), next = inside(tb - 2 * kBlock), live = tb < 0 ? 0 : masks.len - tb - off;
+    const int now = steps(masks.steps, tb), live = steps(masks.len, tb);
+    const int next = steps(masks.len, tb - 2 * kBlock);
     auto& x = in_.x;
     auto& r = in_.r;
     auto& i = in_.i;
@@ -344,10 +347,8 @@ int launch_rec_bwd(const ss_rec_desc_t& d, const RecPlan& pl, const void* x, con
     auto run = [&](auto type, auto dtype) {
       using T = decltype(type);
       using Dy = decltype(dtype);
-      if (pl.nchunks > 1) {
+      if (pl.nchunks > 1)
         rec_bwd_kernel<T, Dy, Z, M, A, true><<<blocks, kWaves * 64, 0, st>>>(p);
-        launch_rec_carry(p.cdec, p.cadj, dh_last, d.batch, p.s.D, p.s.nchunks, true, st);
-      }
       rec_bwd_kernel<T, Dy, Z, M, A, false><<<blocks, kWaves * 64, 0, st>>>(p);
     };
     if (xb && yb) run(uint16_t{}, uint16_t{});
