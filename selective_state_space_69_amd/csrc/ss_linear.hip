@@ -246,10 +246,13 @@ __device__ __forceinline__ void put_cols(const DgluParams& p, int64_t r, int32_t
     else store_out<T>(d, v[0]);
   }
 }
-template <typename Dy, typename T, int V, int ACT>
+// SUMS: with the column sums, for which a block walks its rows, two at a time; without
+// them it takes four rows, one a wave (bf16 16384 x 6912: 349 us walking, 250 so).
+constexpr int64_t kDgluRows = 4;
+template <typename Dy, typename T, int V, int ACT, bool SUMS>
 __global__ __launch_bounds__(kThreads) void dglu_kernel(DgluParams p) {
-  __shared__ float part[4][2][64 * V];
-  constexpr int kRows = 2;
+  __shared__ float part[SUMS ? 4 : 1][2][64 * V];
+  constexpr int kRows = SUMS ? 2 : 1;
   const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
   const int c = (int(blockIdx.x) * 64 + lane) * V;
   const int64_t m0 = int64_t(blockIdx.y) * p.rows;
@@ -262,7 +265,7 @@ __global__ __launch_bounds__(kThreads) void dglu_kernel(DgluParams p) {
     for (int j = 0; j < V; ++j) sum[k][j] = run[k][j] = 0.0f;
   int turn = 0;
   for (int64_t m = m0 + wv; m < m1; m += 4 * kRows) {
-    if (++turn > kRun) {
+    if (SUMS && ++turn > kRun) {
       turn = 1;
 #pragma unroll
       for (int k = 0; k < 2; ++k)
@@ -290,8 +293,10 @@ __global__ __launch_bounds__(kThreads) void dglu_kernel(DgluParams p) {
         const float g = gate[i][j], dy = v[i][j];
         gate[i][j] = dy * up[i][j] * act_grad(ACT, g);
         up[i][j] = dy * apply_act(ACT, g);
-        run[0][j] += gate[i][j];
-        run[1][j] += up[i][j];
+        if constexpr (SUMS) {
+          run[0][j] += gate[i][j];
+          run[1][j] += up[i][j];
+        }
       }
       if (!p.d) continue;
       if (c < p.F) {
@@ -303,7 +308,7 @@ __global__ __launch_bounds__(kThreads) void dglu_kernel(DgluParams p) {
       }
     }
   }
-  if (!p.part) return;
+  if constexpr (!SUMS) return;
 #pragma unroll
   for (int k = 0; k < 2; ++k)
 #pragma unroll
@@ -788,12 +793,17 @@ int launch_glu_fwd(const ss_glu_desc_t& d, const LinearPlan& pl, const void* x, 
   return int(hipGetLastError());
 }
 
+template <typename Dy, typename T, int V, int ACT>
+static void dglu_sums(const DgluParams& p, dim3 grid, hipStream_t st) {
+  if (p.part) dglu_kernel<Dy, T, V, ACT, true><<<grid, kThreads, 0, st>>>(p);
+  else dglu_kernel<Dy, T, V, ACT, false><<<grid, kThreads, 0, st>>>(p);
+}
 template <typename Dy, typename T, int V>
 static void dglu_act(const DgluParams& p, int act, dim3 grid, hipStream_t st) {
   switch (act) {
-    case SS_ACT_SILU: dglu_kernel<Dy, T, V, SS_ACT_SILU><<<grid, kThreads, 0, st>>>(p); break;
-    case SS_ACT_GELU: dglu_kernel<Dy, T, V, SS_ACT_GELU><<<grid, kThreads, 0, st>>>(p); break;
-    default: dglu_kernel<Dy, T, V, SS_ACT_NONE><<<grid, kThreads, 0, st>>>(p);
+    case SS_ACT_SILU: dglu_sums<Dy, T, V, SS_ACT_SILU>(p, grid, st); break;
+    case SS_ACT_GELU: dglu_sums<Dy, T, V, SS_ACT_GELU>(p, grid, st); break;
+    default: dglu_sums<Dy, T, V, SS_ACT_NONE>(p, grid, st);
   }
 }
 template <int V>
@@ -811,13 +821,18 @@ int launch_glu_bwd(const ss_glu_desc_t& d, const LinearPlan& pl, const void* x, 
   hipStream_t st = static_cast<hipStream_t>(stream);
   const ss_linear_desc_t l = both_halves(d);
   const bool dpre = dx || dw;
-  const DgluParams p{dy, pre, dpre ? ws + pl.off_dpre : nullptr,
-                     dbias ? reinterpret_cast<float*>(ws + pl.off_sums) : nullptr, d.rows,
-                     pl.chunk_rows, int32_t(d.out_dim), int32_t(pl.ld_dpre), pl.sum2};
   const int v = d.out_dim % 8 == 0 ? 8 : 1;
   // with single columns, lanes past F clear the rows' last unit
   const int64_t cols = v == 8 ? d.out_dim : d.out_dim + pad_to_unit(l, l.out_dim) - l.out_dim;
-  const dim3 grid(unsigned((cols + 64 * v - 1) / (64 * v)), unsigned(pl.chunks));
+  const int64_t across = (cols + 64 * v - 1) / (64 * v);
+  // without column sums a block has no reason to walk but the grid's limits
+  const int64_t most = kMaxBlocks / across < 32768 ? kMaxBlocks / across : 32768;
+  const int64_t turns = (d.rows + kDgluRows * most - 1) / (kDgluRows * most);
+  const int64_t rows = dbias ? pl.chunk_rows : kDgluRows * turns;
+  const DgluParams p{dy, pre, dpre ? ws + pl.off_dpre : nullptr,
+                     dbias ? reinterpret_cast<float*>(ws + pl.off_sums) : nullptr, d.rows, rows,
+                     int32_t(d.out_dim), int32_t(pl.ld_dpre), pl.sum2};
+  const dim3 grid(unsigned(across), unsigned((d.rows + rows - 1) / rows));
   if (v == 8) dglu_types<8>(d, p, grid, st);
   else dglu_types<1>(d, p, grid, st);
   if (dbias)

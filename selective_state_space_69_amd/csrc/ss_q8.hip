@@ -2,16 +2,17 @@
 //
 // A row is read once: its elements stay in registers between the largest magnitude
 // (taken on the bits, where NaN and infinity are above every number) and the quotients.
-// 127 x / max is formed in 64 bits, with an error below 2^-51 of it; where that leaves
-// the nearest whole number open (a tie, or nearly), 254 |x| is compared with (2 k + 1)
-// max, both exact in 64 bits.  So the bits are those of the definition, whatever
-// computes them.  Memory bound.
+// 127 x / max is formed in 32 bits, with an error below 2^-15 (127 times three roundings
+// of 2^-24); where that leaves the nearest whole number open (within 2^-13 of a tie, one
+// value in 4096) 254 |x| is compared with (2 k + 1) max, both exact in 64 bits.  So the
+// bits are those of the definition.  Memory bound.
 #include "ss_device.hpp"
 
 namespace ss {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int64_t kMaxBlocks = int64_t(1) << 22;    // a grid's threads stay below 2^32
 
 struct PackParams {
   const void* x;
@@ -46,22 +47,28 @@ template <typename T> struct Eight {
   }
 };
 
-__device__ __forceinline__ int nearest(float x, double scale, double most) {
-  const double t = double(x) * scale, r = __builtin_rint(t);
-  int k = int(r);
-  if (__builtin_fabs(__builtin_fabs(t - r) - 0.5) < 1e-9) {
-    const double m = __builtin_fabs(t);
-    int f = int(m);                                 // between f and f + 1
-    const double a = 254.0 * __builtin_fabs(double(x)), b = double(2 * f + 1) * most;
-    f += a > b || (a == b && (f & 1));
-    k = x < 0.0f ? -f : f;
+// scale: 127 / most, or 0 where that is too large for fp32 (then the quotient is formed
+// in 64 bits)
+__device__ __forceinline__ int nearest(float x, float scale, float most) {
+  const float t = x * scale;
+  int k = int(__builtin_rintf(t));
+  const float f = __builtin_fabsf(t) - __builtin_floorf(__builtin_fabsf(t));
+  if (__builtin_fabsf(f - 0.5f) < 0x1p-13f || scale == 0.0f) {
+    const double a = 254.0 * __builtin_fabs(double(x)), m = double(most);
+    // within one of the quotient's whole part: the comparisons settle it
+    int n = int(scale == 0.0f ? a / (2.0 * m) : double(__builtin_fabsf(t)));
+    if (a < 2.0 * n * m) --n;
+    if (a >= 2.0 * (n + 1) * m) ++n;
+    const double b = (2 * n + 1) * m;
+    n += a > b || (a == b && (n & 1));
+    k = x < 0.0f ? -n : n;
   }
   return k;
 }
 
 template <typename T>
 __device__ __forceinline__ void store_eight(int8_t* row, int c, int span, const Eight<T>& v,
-                                            double scale, double most, bool zero) {
+                                            float scale, float most, bool zero) {
   uint32_t w[2] = {0, 0};
   if (!zero) {
 #pragma unroll
@@ -121,7 +128,7 @@ __global__ __launch_bounds__(kThreads) void pack_kernel(PackParams p) {
     }
     const bool finite = top < 0x7f800000u, zero = !finite || top == 0;
     const float most = __uint_as_float(top);
-    const double scale = zero ? 0.0 : 127.0 / double(most);
+    const float scale = most > 1e-35f ? 127.0f / most : 0.0f;
     if (!here) continue;
     int8_t* q = p.q + row * p.ldq;
     if (tid == 0) p.s[row] = finite ? most / 127.0f : __uint_as_float(0x7fc00000u);
@@ -129,36 +136,44 @@ __global__ __launch_bounds__(kThreads) void pack_kernel(PackParams p) {
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         const int c = (i * kPer + tid) * 8;
-        if (c < p.span) store_eight(q, c, p.span, v[i], scale, double(most), zero);
+        if (c < p.span) store_eight(q, c, p.span, v[i], scale, most, zero);
       }
     } else {
       for (int c = tid * 8; c < p.span; c += kPer * 8) {
         v[0].load(x, c, p.dim);
-        store_eight(q, c, p.span, v[0], scale, double(most), zero);
+        store_eight(q, c, p.span, v[0], scale, most, zero);
       }
     }
   }
 }
 
+template <typename T, int N>
+void run_narrow(const PackParams& p, hipStream_t st) {
+  const int64_t n = (p.rows + 3) / 4;
+  pack_kernel<T, N, 1><<<unsigned(n < kMaxBlocks ? n : kMaxBlocks), kThreads, 0, st>>>(p);
+}
+template <typename T, int N>
+void run_wide(const PackParams& p, hipStream_t st) {
+  pack_kernel<T, N, 4><<<unsigned(p.rows < kMaxBlocks ? p.rows : kMaxBlocks), kThreads, 0, st>>>(p);
+}
 template <typename T>
 void run(const PackParams& p, hipStream_t st) {
-  // a wave to a row of up to 2048 bytes of q, if the rows then still fill the GPU
-  const bool narrow = p.span <= 2048 && p.rows >= 4096;
-  const int64_t per = narrow ? 4 : 1, blocks64 = (p.rows + per - 1) / per;
-  const unsigned blocks = unsigned(blocks64 < (int64_t(1) << 22) ? blocks64 : int64_t(1) << 22);
-  if (narrow) {
-    if (p.span <= 512) pack_kernel<T, 1, 1><<<blocks, kThreads, 0, st>>>(p);
-    else if (p.span <= 1024) pack_kernel<T, 2, 1><<<blocks, kThreads, 0, st>>>(p);
-    else pack_kernel<T, 4, 1><<<blocks, kThreads, 0, st>>>(p);
-  } else if (p.span <= 2048) {
-    pack_kernel<T, 1, 4><<<blocks, kThreads, 0, st>>>(p);
-  } else if (p.span <= 4096) {
-    pack_kernel<T, 2, 4><<<blocks, kThreads, 0, st>>>(p);
-  } else if (p.span <= 8192) {
-    pack_kernel<T, 4, 4><<<blocks, kThreads, 0, st>>>(p);
-  } else {
-    pack_kernel<T, 0, 4><<<blocks, kThreads, 0, st>>>(p);
+  // a wave to a row where the rows then still fill the GPU, else four
+  if (p.span <= 4096 && p.rows >= 1024) {
+    switch ((p.span + 511) / 512) {
+      case 1: return run_narrow<T, 1>(p, st);
+      case 2: return run_narrow<T, 2>(p, st);
+      case 3: return run_narrow<T, 3>(p, st);
+      case 4: return run_narrow<T, 4>(p, st);
+      case 5: return run_narrow<T, 5>(p, st);
+      case 6: return run_narrow<T, 6>(p, st);
+      default: return run_narrow<T, 8>(p, st);
+    }
   }
+  if (p.span <= 2048) run_wide<T, 1>(p, st);
+  else if (p.span <= 4096) run_wide<T, 2>(p, st);
+  else if (p.span <= 8192) run_wide<T, 4>(p, st);
+  else run_wide<T, 0>(p, st);
 }
 
 }  // namespace
