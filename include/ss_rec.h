@@ -53,7 +53,7 @@ extern "C" {
 
 #define SS_REC_CHUNK 64 /* steps between two kept states */
 
-/* batch, seqlen, dim >= 1; seqlen < 2^31; dim <= 2^20; batch * ceil(dim / 64) <= 2^22; a tensor
+/* batch, seqlen, dim >= 1; seqlen < 2^31; dim <= 2^20; batch * ceil(dim / 64) <= 2^21; a tensor
  * spans at most 2^40 elements. */
 typedef struct ss_rec_desc {
   int64_t batch;     /* B */

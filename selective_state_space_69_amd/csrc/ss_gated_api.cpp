@@ -12,7 +12,8 @@ namespace {
 
 constexpr int64_t kMaxElems = int64_t(1) << 40;
 constexpr int64_t kMaxDim = int64_t(1) << 20;
-constexpr int64_t kMaxGroups = int64_t(1) << 22;     // of 64 channels: a grid's threads stay below 2^32
+constexpr int64_t kMaxGroups = int64_t(1) << 21;     // of 64 channels, two workgroups of 512 threads each:
+                                                     // a grid's threads stay below 2^32
 
 size_t elem(int32_t dtype) { return dtype == SS_BF16 ? 2 : 4; }
 

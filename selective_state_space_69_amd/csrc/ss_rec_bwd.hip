@@ -15,8 +15,9 @@ constexpr int kS = 4;                       // steps of a lane's stretch
 constexpr int kWaveSteps = kSubs * kS;
 constexpr int kWaves = 4;
 constexpr int kBlock = kWaves * kWaveSteps;
-constexpr int kRun = 16;                                 // blocks of a run of dlam's sums
-constexpr int kPerState = SS_REC_CHUNK / kWaveSteps;     // waves between two kept states
+[[maybe_unused]] constexpr int kRun = 16;                  // blocks of a run of dlam's sums
+// waves between two kept states
+[[maybe_unused]] constexpr int kPerState = SS_REC_CHUNK / kWaveSteps;
 static_assert(SS_REC_CHUNK % kWaveSteps == 0 && kBlock % SS_REC_CHUNK == 0,
               "states are kept at a wave's first step");
 

@@ -75,6 +75,15 @@ def test_rec_descriptor(kw, code):
     assert B.ss_rec_workspace_bytes(rec_desc(), 2) == 0
 
 
+def test_rec_grid():
+    # workgroups of 512 threads and 32 channels: their threads have to stay below 2^32
+    for batch, dim in (((1 << 21) + 1, 64), ((1 << 20) + 1, 65), ((1 << 21) // 3 + 1, 150)):
+        assert rec_fwd(rec_desc(batch=batch, dim=dim)) == INV
+        assert B.ss_rec_workspace_bytes(rec_desc(batch=batch, dim=dim), B.SS_REC_BWD) == 0
+    for batch, dim in ((1 << 21, 64), (1 << 20, 65), ((1 << 21) // 3, 150)):
+        assert B.ss_rec_workspace_bytes(rec_desc(batch=batch, dim=dim), B.SS_REC_BWD) > 0
+
+
 @pytest.mark.parametrize("kw,code", [
     (dict(x=None), INV), (dict(r=None), INV), (dict(i=None), INV), (dict(lam=None), INV),
     (dict(y=None), INV), (dict(y=at(0)), INV), (dict(h_last=at(4)), INV), (dict(states=at(5)), INV),
