@@ -885,14 +885,16 @@ int launch_q8_linear(const ss_q8_desc_t& d, const Q8Plan& pl, const int8_t* xq, 
                           p.nT % 16 == 0, st);
     return int(hipGetLastError());
   }
+  const Tiling t = tiling_q8(d);
   Operands ops{1};
-  // rows of xq whose units are aligned are read in place: what lies behind an odd
-  // contraction's end, in the row's last unit, meets the zeros of w's copy
+  // Rows whose units are aligned are read in place.  What lies behind an odd contraction's
+  // end, in the row's last unit, is cleared in small tiles' registers, and meets the zeros of
+  // w's copy in large ones.
   if (ptr16(xq) && p.ldr % 16 == 0) p.R = xq;
   else p.R = ops.take(xq, &p.ldr, d.rows, d.in_dim, ws + pl.off_x);
-  p.S = ops.take(wq, &p.lds, d.out_dim, d.in_dim, ws + pl.off_w);
+  if (t.tile != MmTile::kBig && ptr16(wq) && p.lds % 16 == 0) p.S = wq;
+  else p.S = ops.take(wq, &p.lds, d.out_dim, d.in_dim, ws + pl.off_w);
   ops.launch(st);
-  const Tiling t = tiling_q8(d);
   p = tiled(p, t, ws + pl.off_part);
   launch_mm_q8(p, t.tile, st);
   if (p.splits > 1) {

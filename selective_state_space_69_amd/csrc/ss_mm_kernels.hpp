@@ -219,8 +219,16 @@ __device__ __forceinline__ uint32_t copy_offset(int piece, int64_t ld, int64_t i
 // whole rows, 8 columns per lane, 2 F lanes to a row.  Bias is fetched once per
 // column, a piece's residual before the stores of the piece in front of it: a wave's
 // loads wait for its older stores.  The loop over rows is rolled: unrolled, the
-// epilogue outgrew the instruction cache and cost 20 us a tile.
-template <int F>
+// epilogue outgrew the instruction cache and cost 20 us a tile.  kInt8 also fetches the
+// rows' scales and the elements of a row's end ahead (3001 x 256 -> 773: 14.2 -> 9.5 us,
+// with a residual 20.2 -> 15.6; 16384 x 2560 -> 10240 with one 488 -> 467).
+// the columns in front of n of the eight from s on
+__device__ __forceinline__ void load_to(const float* base, int32_t s, int32_t n, float (&v)[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (s + j < n) v[j] = load1(base, s + j, 0);
+}
+template <int F, int KIND = kMm>
 struct Piece {
   static constexpr int kPer = 2 * F;                // lanes of a row
   static constexpr int kRows = 64 / kPer;           // rows of one pass
@@ -229,24 +237,40 @@ struct Piece {
   int32_t s;      // its first column
   int64_t o;      // their element of the output
   Res8 res[kPasses];
+  float scale[kPasses];      // kInt8: the rows'
   __device__ __forceinline__ void place(const MmParams& p, int64_t r0, int32_t s0) {
     const int lane = threadIdx.x & 63;
     r = r0 + lane / kPer;
     s = s0 + (lane % kPer) * 8;
     o = r * p.nS + s;
+    if constexpr (KIND == kInt8) {
+#pragma unroll
+      for (int h = 0; h < kPasses; ++h)
+        if (r + h * kRows < p.nR) scale[h] = load1(p.row_scale, r + h * kRows, 0);
+    }
   }
   __device__ __forceinline__ void fetch(const MmParams& p, int64_t r0, int32_t s0) {
     place(p, r0, s0);
     if (!p.res) return;
 #pragma unroll
-    for (int h = 0; h < kPasses; ++h)
+    for (int h = 0; h < kPasses; ++h) {
       res[h] = fetch_res8(p, o + h * kRows * int64_t(p.nS), r + h * kRows < p.nR && s + 8 <= p.nS);
+      if (KIND == kInt8 && r + h * kRows < p.nR && s + 8 > p.nS) {      // a row's end: as fp32
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (s + j < p.nS)
+            res[h].w[j] =
+                __float_as_uint(load1(p.res, o + h * kRows * int64_t(p.nS) + j, p.res_bf16));
+      }
+    }
   }
 };
+template <int KIND>
 __device__ __forceinline__ void fetch_bias(const MmParams& p, int32_t s, float (&bias)[8]) {
 #pragma unroll
   for (int j = 0; j < 8; ++j) bias[j] = 0.0f;
   if (p.bias && s + 8 <= p.nS) load8(p.bias + s, bias);
+  else if (KIND == kInt8 && p.bias) load_to(p.bias, s, p.nS, bias);
 }
 
 // One piece of 16 rows x 16 F columns.  SPLIT: to a split's partial sums instead;
@@ -258,7 +282,7 @@ __device__ __forceinline__ float value_of(float v, float row_scale, float scale)
 }
 template <int ACT, bool SPLIT, bool STREAM, bool RES, int KIND, int F, typename Acc>
 __device__ __forceinline__ void piece_out(const MmParams& p, char* sl, const Acc (&q)[F],
-                                          const Piece<F>& at, const float (&bias)[8],
+                                          const Piece<F, KIND>& at, const float (&bias)[8],
                                           const float (&scale)[8], int split) {
   const int lane = threadIdx.x & 63, m = lane & 15, g = lane >> 4;
 #pragma unroll
@@ -268,14 +292,14 @@ __device__ __forceinline__ void piece_out(const MmParams& p, char* sl, const Acc
   const int u = (lane % Piece<F>::kPer) * 2;
   Res8 res;
   if constexpr (RES) res = at.res[0];
+  float rs = 1.0f;
+  if constexpr (KIND == kInt8) rs = at.scale[0];
 #pragma nounroll
   for (int h = 0; h < Piece<F>::kPasses; ++h) {
     const int row = h * Piece<F>::kRows + lane / Piece<F>::kPer;
     const int64_t r = at.r + h * Piece<F>::kRows, o = at.o + h * Piece<F>::kRows * int64_t(p.nS);
     const int32_t s = at.s;
     if (r < p.nR && s < p.nS) {
-      float rs = 1.0f;
-      if constexpr (KIND == kInt8 && !SPLIT) rs = load1(p.row_scale, r, 0);
       if (s + 8 <= p.nS) {
         const f32x4 x = *reinterpret_cast<const f32x4*>(sl + row * 256 + ((u ^ row) << 4));
         const f32x4 y = *reinterpret_cast<const f32x4*>(sl + row * 256 + (((u + 1) ^ row) << 4));
@@ -289,21 +313,30 @@ __device__ __forceinline__ void piece_out(const MmParams& p, char* sl, const Acc
           }
           epilogue8<ACT, STREAM, RES>(p, o, v, bias, res);
         }
+      } else if constexpr (KIND == kInt8 && !SPLIT) {
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          v[j] = *reinterpret_cast<const float*>(sl + row * 256 + (((u + j / 4) ^ row) << 4) +
+                                                 (j & 3) * 4);
+          v[j] = apply_act(ACT, value_of<KIND>(v[j], rs, scale[j]) + bias[j]);
+          if (RES && p.res) v[j] += __uint_as_float(res.w[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (s + j < p.nS) store1(p.out, o + j, p.out_bf16, v[j]);
       } else {
 #pragma nounroll
         for (int j = 0; s + j < p.nS; ++j) {
           float v = *reinterpret_cast<const float*>(
               sl + row * 256 + (((u + j / 4) ^ row) << 4) + (j & 3) * 4);
-          if constexpr (SPLIT) {
-            store1(p.part, split * p.nR * p.nS + o + j, 0, v);
-          } else {
-            if constexpr (KIND == kInt8) v = value_of<KIND>(v, rs, load1(p.col_scale, s + j, 0));
-            epilogue1(p, ACT, r, s + j, v);
-          }
+          if constexpr (SPLIT) store1(p.part, split * p.nR * p.nS + o + j, 0, v);
+          else epilogue1(p, ACT, r, s + j, v);
         }
       }
     }
     if constexpr (RES && Piece<F>::kPasses > 1) res = at.res[Piece<F>::kPasses - 1];
+    if constexpr (KIND == kInt8 && Piece<F>::kPasses > 1) rs = at.scale[Piece<F>::kPasses - 1];
   }
   asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
 }
@@ -311,7 +344,10 @@ __device__ __forceinline__ void piece_out(const MmParams& p, char* sl, const Acc
 template <int KIND>
 __device__ __forceinline__ void fetch_scale(const MmParams& p, int32_t s, float (&scale)[8]) {
   if constexpr (KIND == kInt8) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) scale[j] = 0.0f;
     if (s + 8 <= p.nS) load8(p.col_scale + s, scale);
+    else load_to(p.col_scale, s, p.nS, scale);
   }
 }
 
@@ -672,13 +708,13 @@ __device__ __forceinline__ void mm256_body(const MmParams& p0, const Turns& turn
         glu_out<ACT, false, true>(p, lds + kOffEpi + wv * 4096, gate, up, r + 16 * j, c0, 0);
       }
     } else {
-      Piece<4> now, next;
-      float bias[2][8];
-      fetch_bias(p, c0 + (lane & 7) * 8, bias[0]);
-      fetch_bias(p, c0 + 64 + (lane & 7) * 8, bias[1]);
-      float scale[2][8];
-      fetch_scale<KIND>(p, c0 + (lane & 7) * 8, scale[0]);
-      fetch_scale<KIND>(p, c0 + 64 + (lane & 7) * 8, scale[1]);
+      Piece<4, KIND> now, next;
+      float bias[2][8], scale[2][8];
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        fetch_bias<KIND>(p, c0 + 64 * c + (lane & 7) * 8, bias[c]);
+        fetch_scale<KIND>(p, c0 + 64 * c + (lane & 7) * 8, scale[c]);
+      }
       now.fetch(p, r, c0);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {       // rows 16 (i / 2), columns 64 (i & 1)
@@ -854,7 +890,9 @@ __device__ __forceinline__ void mm_small_body(const MmParams& p, uint32_t block,
               a[i] + h * 16 * kCols + e * kCols));
     }
   };
-  auto part = [&](auto h_c) {
+  // an odd contraction of bytes: what lies behind its end in S's last unit is cleared
+  const bool odd = KIND == kInt8 && t1 == p.nT && (rem & 15);
+  auto part = [&](auto h_c, bool last) {
     u32x4 a[kF], b[kF];
     if constexpr (kSz == 2 && !RT && !ST) {
       constexpr int h = decltype(h_c)::value;
@@ -869,6 +907,16 @@ __device__ __forceinline__ void mm_small_body(const MmParams& p, uint32_t block,
       read(std::integral_constant<bool, RT>{}, h_c, ar, b);
       read(std::integral_constant<bool, ST>{}, h_c, as, a);
     }
+    if (KIND == kInt8 && odd && last) {
+      const int left = rem - (decltype(h_c)::value * 64 + g * 16);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int n = left - 4 * e;
+        const uint32_t keep = n >= 4 ? ~0u : n > 0 ? (1u << (8 * n)) - 1 : 0u;
+#pragma unroll
+        for (int i = 0; i < kF; ++i) a[i][e] &= keep;
+      }
+    }
 #pragma unroll
     for (int i = 0; i < kF; ++i)
 #pragma unroll
@@ -879,10 +927,12 @@ __device__ __forceinline__ void mm_small_body(const MmParams& p, uint32_t block,
     wait_copies<0>();
     turn_end();       // stage k is whole, and stage k - 1 has been read by every wave
     if (NB == 2 && k + 1 < nk) copy(k + 1);
-    part(std::integral_constant<int, 0>{});
+    const bool last = k0 + k == stages - 1;
+    part(std::integral_constant<int, 0>{}, last);
     // the second half of the last stage may lie past the contraction's end (fp32 takes
     // it all the same: the branch between its halves costs 89 -> 96 us)
-    if (kSz == 4 || k0 + k < stages - 1 || rem > kT / 2) part(std::integral_constant<int, 1>{});
+    if (kSz == 4 || k0 + k < stages - 1 || rem > kT / 2)
+      part(std::integral_constant<int, 1>{}, last);
     if constexpr (NB == 2) {
 #pragma unroll
       for (int i = 0; i < kF; ++i) {
@@ -937,9 +987,9 @@ __device__ __forceinline__ void mm_small_body(const MmParams& p, uint32_t block,
     return;
   }
   const int32_t c = int32_t(s0) + wsn;
-  Piece<kF> now, next;
+  Piece<kF, KIND> now, next;
   float bias[8];
-  fetch_bias(p, c + (lane % Piece<kF>::kPer) * 8, bias);
+  fetch_bias<KIND>(p, c + (lane % Piece<kF>::kPer) * 8, bias);
   float scale[8];
   fetch_scale<KIND>(p, c + (lane % Piece<kF>::kPer) * 8, scale);
   if (RES && p.splits == 1) now.fetch(p, r, c);
