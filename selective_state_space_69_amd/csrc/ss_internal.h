@@ -267,7 +267,7 @@ int launch_linear_bwd(const ss_linear_desc_t& d, const LinearPlan& pl, const voi
 // aligned: chunks' log decays and carries (nchunks > 1), backward partial sums of dlam.
 struct RecPlan {
   int64_t chunk = 0, nchunks = 1;
-  size_t off_log = 0, off_carry = 0, off_part = 0, bytes = 0;
+  size_t off_log = 0, off_carry = 0, off_first = 0, off_part = 0, bytes = 0;
 };
 RecPlan plan_rec(const ss_rec_desc_t& d, int op);
 int launch_rec_fwd(const ss_rec_desc_t& d, const RecPlan& pl, const void* x, const void* r,

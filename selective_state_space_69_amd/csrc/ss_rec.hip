@@ -32,6 +32,8 @@ struct FwdParams {
   void* y;
   float *h_last, *states;
   float *cdec, *cend;        // (B, nchunks, D) chunks' decays and end states from a zero start
+  float* first;              // SUM: (B, D), h0 as the outputs' pass reads it (h_last may take
+                             // its place before every chunk has)
 };
 
 // Z: with a gate.  MASK: starts or lengths given.  SUM: only the chunks' carries.
@@ -180,6 +182,11 @@ void rec_fwd_kernel(FwdParams p) {
   }
   if (at.wv == 0 && at.sub == 0) {
     if constexpr (SUM) {
+      if (p.h0 && at.chunk == 0) {
+        float first[kV];
+        load_f32(p.h0 + int64_t(at.b) * D + at.c, at.n, first);
+        store_f32(p.first + int64_t(at.b) * D + at.c, at.n, first);
+      }
       store_f32(p.cdec + crow, at.n, dec);
       store_f32(p.cend + crow, at.n, H);
     } else if (p.h_last && at.chunk == p.s.nchunks - 1) {
@@ -266,6 +273,10 @@ RecPlan plan_rec(const ss_rec_desc_t& d, int op) {
     pl.off_log = pl.bytes;
     pl.off_carry = pl.bytes + sz;
     pl.bytes += 2 * sz;
+    if (op == SS_REC_FWD) {
+      pl.off_first = pl.bytes;
+      pl.bytes += (size_t(d.batch) * size_t(d.dim) * 4 + kAlign - 1) / kAlign * kAlign;
+    }
   }
   if (op == SS_REC_BWD) {
     pl.off_part = pl.bytes;
@@ -282,7 +293,10 @@ int launch_rec_fwd(const ss_rec_desc_t& d, const RecPlan& pl, const void* x, con
                     stride_of(d.r_stride, d.dim), stride_of(d.i_stride, d.dim),
                     stride_of(d.z_stride, d.dim), lam, h0, starts, lengths, y, h_last, states,
                     reinterpret_cast<float*>(ws + pl.off_log),
-                    reinterpret_cast<float*>(ws + pl.off_carry)};
+                    reinterpret_cast<float*>(ws + pl.off_carry),
+                    reinterpret_cast<float*>(ws + pl.off_first)};
+  FwdParams out = p;
+  if (h0 && pl.nchunks > 1) out.h0 = p.first;
   const bool any = d.dim % kV != 0 || odd_rows(x, p.ldx, d.in_dtype) ||
                    odd_rows(r, p.ldr, d.in_dtype) || odd_rows(i, p.ldi, d.in_dtype) ||
                    odd_rows(z, p.ldz, d.in_dtype);
@@ -295,9 +309,9 @@ int launch_rec_fwd(const ss_rec_desc_t& d, const RecPlan& pl, const void* x, con
       if (pl.nchunks > 1)
         rec_fwd_kernel<T, float, false, M, A, true><<<blocks, kWaves * 64, 0, st>>>(p);
       if (d.out_dtype == SS_BF16)
-        rec_fwd_kernel<T, uint16_t, Z, M, A, false><<<blocks, kWaves * 64, 0, st>>>(p);
+        rec_fwd_kernel<T, uint16_t, Z, M, A, false><<<blocks, kWaves * 64, 0, st>>>(out);
       else
-        rec_fwd_kernel<T, float, Z, M, A, false><<<blocks, kWaves * 64, 0, st>>>(p);
+        rec_fwd_kernel<T, float, Z, M, A, false><<<blocks, kWaves * 64, 0, st>>>(out);
     };
     if (d.in_dtype == SS_BF16) run(uint16_t{});
     else run(float{});

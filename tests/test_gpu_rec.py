@@ -209,6 +209,24 @@ def test_state_in_place():
     assert torch.equal(h, want["h_last"]) and torch.equal(y, want["y"])
 
 
+def test_state_in_place_of_a_long_sequence():
+    """h_last in h0's place where many chunks start from h0."""
+    b, l, d = 2, 40000, 70
+    a, _ = make(b, l, d, "bf16", seed=19, h0=True, z=True)
+    want = B.rec_fwd(**a, return_last=True, save_states=True)
+    y, states = torch.empty_like(a["x"]), torch.empty_like(want["states"])
+    desc = B.make_rec_desc(b, l, d, in_dtype=B.SS_BF16, out_dtype=B.SS_BF16)
+    n = B.ss_rec_workspace_bytes(desc, B.SS_REC_FWD)
+    assert n > 0
+    ws = B.workspace(n, y.device)
+    for _ in range(3):
+        h = a["h0"].clone()
+        assert B.ss_rec_fwd(desc, a["x"], a["r"], a["i"], a["lam"], a["z"], h, None, None, y, h, states,
+                            ws, n) == 0
+        assert torch.equal(h, want["h_last"]) and torch.equal(y, want["y"])
+        assert torch.equal(states, want["states"])
+
+
 @pytest.mark.parametrize("b,l,d", [(2, 300, 192), (1, 6000, 64)])
 def test_graph_and_stream(b, l, d):
     """Captured once and replayed with new inputs, eager work in between; another stream."""
