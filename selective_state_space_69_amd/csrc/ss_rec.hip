@@ -44,7 +44,7 @@ __global__ __launch_bounds__(kWaves * 64, sizeof(T) == 2 && !ANY ? 4 : 2)
 void rec_fwd_kernel(FwdParams p) {
 #if defined(__HIP_DEVICE_COMPILE__)
   __shared__ float tc[2][kWaves][kRecChans], ts[2][kWaves][kRecChans];
-  const Place at(p.s);
+  const Place at(p.s, !SUM && p.s.nchunks > 1);
   const int32_t D = p.s.D;
   const int64_t L = p.s.L, row0 = int64_t(at.b) * L;
   const int64_t t0 = at.chunk * p.s.chunk;

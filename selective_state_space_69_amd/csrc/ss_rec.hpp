@@ -184,11 +184,13 @@ struct Place {
   int lane, wv, sub, n;      // sub: stretch of the wave; n: channels that exist (0..kV)
   int32_t b, chunk;
   int32_t c;                 // first channel (0 where none exists)
-  __device__ __forceinline__ Place(const RecShape& s) {
+  // back: the workgroups in reverse order
+  __device__ __forceinline__ Place(const RecShape& s, bool back) {
     lane = threadIdx.x & 63;
     wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     sub = lane / kRecLanes;
-    const uint32_t id = uint32_t(xcd_contiguous(blockIdx.x, gridDim.x));
+    const uint32_t id0 = uint32_t(xcd_contiguous(blockIdx.x, gridDim.x));
+    const uint32_t id = back ? gridDim.x - 1 - id0 : id0;
     const uint32_t row = id / uint32_t(s.groups);
     const int32_t g = int32_t(id - row * uint32_t(s.groups));
     b = int32_t(row / uint32_t(s.nchunks));
