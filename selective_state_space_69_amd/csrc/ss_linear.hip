@@ -247,7 +247,7 @@ __device__ __forceinline__ void put_cols(const DgluParams& p, int64_t r, int32_t
   }
 }
 // SUMS: with the column sums, for which a block walks its rows, two at a time; without
-// them it takes four rows, one a wave (bf16 16384 x 6912: 349 us walking, 250 so).
+// them it takes four rows, one a wave (bf16 16384 x 6912: 349 us walking, 198 so, 5.7 TB/s).
 constexpr int64_t kDgluRows = 4;
 template <typename Dy, typename T, int V, int ACT, bool SUMS>
 __global__ __launch_bounds__(kThreads) void dglu_kernel(DgluParams p) {

@@ -15,7 +15,8 @@
 //
 // Gated products: the 16 rows of w are 8 of each half, so that a workgroup has both
 // factors of 8 outputs.  8-bit integers: 64 of the contraction per MFMA; rows that are not
-// whole 16-byte units are read from any address, their last unit byte by byte.
+// whole 16-byte units are read from any address, their last unit byte by byte.  8 rows: 2560 ->
+// 2 x 6912 bf16 17.4 us (4.1 TB/s of w), 2560 -> 10240 in bytes 8.2 us (3.2).
 #include "ss_linear_mm.hpp"
 
 namespace ss {

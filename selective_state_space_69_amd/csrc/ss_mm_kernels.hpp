@@ -53,7 +53,8 @@
 // Measured, 16384 rows: 2560 -> 10240 forward 651 us (1320 TFLOP/s; the matrix cores
 // are busy 65% of the cycles, at the 1.9 GHz that power allows), dx and dw of 5120
 // -> 2560 in fp32 714 us together (1200; 360 and 369 us each alone, dw's 200 tiles on
-// 256 CUs).
+// 256 CUs).  Gated, 2560 -> 2 x 6912 with SiLU: 930 us (1250 TFLOP/s; the matrix cores busy
+// 60%); 8-bit integers, 2560 -> 10240: 385 to 405 us (2.2 POP/s, 50%).
 #pragma once
 
 #include "ss_linear_mm.hpp"
