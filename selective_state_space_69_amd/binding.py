@@ -1247,8 +1247,8 @@ def _q8_pack(raw, x):
 def q8_linear(x, w, bias=None, residual=None, act="none", out_dtype=torch.bfloat16, stream=None):
     """act(x w^T + bias) + residual for packed x = (q, s) of (..., K) and w = (q, s) of (N,
     K), as from q8_pack: exact sums of the integers, times both scales.  Either's values
-    may have a row stride.  bias (N) is float32, residual (..., N) float32 or bfloat16, act one of "none", "silu", "gelu",
-    "softplus".  Returns y (..., N) in out_dtype."""
+    may have a row stride.  bias (N) is float32, residual (..., N) float32 or bfloat16, act
+    one of "none", "silu", "gelu", "softplus".  Returns y (..., N) in out_dtype."""
     (xq, xs), (wq, ws) = x, w
     return _on_device(_q8_linear, stream, (xq, xs, wq, ws, bias, residual), xq, xs, wq, ws, bias,
                       residual, _ACT[act], out_dtype)

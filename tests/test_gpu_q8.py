@@ -121,6 +121,24 @@ def test_strided(m, k, xs, xo, ws, wo):
     assert torch.equal(got.double(), xq.double() @ wq.double().t())
 
 
+@pytest.mark.parametrize("m,k,n", [(70, 4999, 60), (40, 129, 300), (300, 143, 200), (3001, 1537, 773),
+                                   (4096, 150, 5120), (4096, 257, 2600)])
+@pytest.mark.parametrize("residual", [False, True])
+def test_odd_contractions_in_place(m, k, n, residual):
+    """Aligned rows whose last unit holds other bytes behind the contraction's end, on every
+    kind of tile, with split contractions and ragged edges."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(m + k)
+    ld = -(-k // 16) * 16
+    x = torch.randint(-127, 128, (m, ld), generator=g, device="cuda", dtype=torch.int8)[:, :k]
+    w = torch.randint(-127, 128, (n, ld + 16), generator=g, device="cuda", dtype=torch.int8)[:, :k]
+    r = torch.randint(-99, 99, (m, n), generator=g, device="cuda").float() if residual else None
+    one = torch.ones(max(m, n), device="cuda")
+    got = B.q8_linear((x, one[:m]), (w, one[:n]), residual=r, out_dtype=F32)
+    want = (x.double() @ w.double().t()).float()      # whole numbers: one rounding to fp32
+    assert torch.equal(got, want + r if residual else want)
+
+
 def test_non_finite_rows():
     x, w, b, _ = make(40, 64, 48)
     y = B.q8_linear(x, w, b, out_dtype=F32)
