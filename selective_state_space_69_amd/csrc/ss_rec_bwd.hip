@@ -246,12 +246,15 @@ void rec_bwd_kernel(BwdParams p) {
         const bool in = e < live;
 #pragma unroll
         for (int j = 0; j < kV; ++j) {
-          const float u = v[e][j] + w[j], bt = beta[e][j], la = k[j] * sr[e][j] * kLn2;
+          const float u = v[e][j] + w[j], bt = beta[e][j], l2 = k[j] * sr[e][j], la = l2 * kLn2;
           w[j] = rec_apply<MASK>(c[e][j], u, 0.0f);
-          // log a / sqrt(1 - a^2): 0 where a rounds to 1
+          // log a / sqrt(1 - a^2): 0 where log a underflows to 0
           const float ratio = la * hw_rcp(bt), lb = bt > 0.0f ? ratio : 0.0f;
           const float ah = rec_apply<MASK>(c[e][j], hs[e][j], 0.0f) * la;
-          const float dl = u * (ah - __builtin_fmaf(-bt, bt, 1.0f) * lb * (si[e][j] * xv[j]));
+          // a^2 with its relative accuracy, which 1 - (1 - a^2) loses where a is small (a = e^-16:
+          // dr 1.4e-5 off); a start's own a is not in c
+          const float aa = MASK && c[e][j] == 0.0f ? hw_exp2(2.0f * l2) : c[e][j] * c[e][j];
+          const float dl = u * (ah - aa * lb * (si[e][j] * xv[j]));
           const float vx = u * bt * si[e][j], vi = vx * xv[j] * (1.0f - si[e][j]);
           const float vr = dl * (1.0f - sr[e][j]);         // dl: of log a, times log a
           gx[j] = in ? vx : 0.0f;
