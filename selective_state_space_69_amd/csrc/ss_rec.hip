@@ -124,7 +124,7 @@ void rec_fwd_kernel(FwdParams p) {
         const Decay d = rec_decay(l2);
         const float add = d.beta * sigmoid(iv[j]) * xv[j];
         const bool cut = MASK && start[e] && in;
-        c[e][j] = MASK ? (cut ? 0.0f : __builtin_fmaxf(d.a, kTiny)) : d.a;
+        c[e][j] = rec_decay_of<MASK>(d.a, cut);
         g[e][j] = in ? add : 0.0f;
         l[j] += l2;
         s[j] = rec_apply<MASK>(c[e][j], s[j], g[e][j]);
@@ -135,7 +135,7 @@ void rec_fwd_kernel(FwdParams p) {
     float cx[kV], sx[kV], cw[kV];            // of the stretches in front of the lane's, of the wave
 #pragma unroll
     for (int j = 0; j < kV; ++j) {
-      cw[j] = rec_decay_of<MASK>(l[j], cuts);
+      cw[j] = rec_decay_of<MASK>(hw_exp2(l[j]), cuts);
       join_up<MASK>(at.sub, cw[j], s[j], cx[j], sx[j]);
     }
     if (at.sub == 0) {

@@ -49,15 +49,16 @@ __device__ __forceinline__ Decay rec_decay(float l2) {
   return Decay{a, E, __builtin_amdgcn_sqrtf(-E * (2.0f + E))};
 }
 
-// Decays of steps and stretches.  CUT: there may be starts, whose decay is 0 (every other
-// one is at least kTiny): a start drops even a state that is not finite.
-template <bool CUT> __device__ __forceinline__ float rec_decay_of(float l2, bool cut) {
-  const float a = hw_exp2(l2), v = __builtin_fmaxf(a, kTiny);
-  return CUT ? (cut ? 0.0f : v) : a;
+// Decays of steps and stretches.  CUT: there may be starts, whose decay is 0; every other one
+// is at least kTiny, added so that a NaN stays one (a maximum drops it), and changes no decay
+// above 2^-102: a start drops even a state that is not finite, and a gate that is NaN reaches
+// all of its document, forward and backward, as it does without CUT.
+template <bool CUT> __device__ __forceinline__ float rec_decay_of(float a, bool cut) {
+  return CUT ? (cut ? 0.0f : a + kTiny) : a;
 }
 // one decay after the other
 template <bool CUT> __device__ __forceinline__ float rec_both(float p, float q) {
-  const float v = p * q, w = __builtin_fmaxf(v, kTiny);
+  const float v = p * q, w = v + kTiny;
   return CUT ? (__builtin_fminf(p, q) == 0.0f ? 0.0f : w) : v;
 }
 // h decayed, and b added

@@ -160,7 +160,7 @@ void rec_bwd_kernel(BwdParams p) {
         float l2 = k[j] * sr[e][j];
         l2 = in ? l2 : 0.0f;
         const Decay f = rec_decay(l2);
-        c[e][j] = MASK ? (cut ? 0.0f : __builtin_fmaxf(f.a, kTiny)) : f.a;
+        c[e][j] = rec_decay_of<MASK>(f.a, cut);
         const float d = Z ? dv[j] * silu(zv[j]) : dv[j];
         v[e][j] = in ? d : 0.0f;
         l[j] += l2;
@@ -181,7 +181,7 @@ void rec_bwd_kernel(BwdParams p) {
     float cx[kV], sx[kV], cy[kV], qy[kV], cw[kV];
 #pragma unroll
     for (int j = 0; j < kV; ++j) {
-      cw[j] = rec_decay_of<MASK>(l[j], cuts);
+      cw[j] = rec_decay_of<MASK>(hw_exp2(l[j]), cuts);
       join_both<MASK, !SUM>(at.sub, cw[j], s[j], q[j], cx[j], sx[j], cy[j], qy[j]);
     }
     if (at.sub == 0) {

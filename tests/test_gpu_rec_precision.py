@@ -1,5 +1,5 @@
 """Accuracy of the gated linear recurrence where it is easily lost, with bounds of their
-own: gradients at strong decays."""
+own: gradients at strong decays; and what a gate that is NaN reaches."""
 import pytest
 import torch
 
@@ -64,3 +64,38 @@ def test_gradients_at_strong_decays(shape, masked):
     dlam = dl.sum((0, 1)) * k
     ref.check(got["dlam"], dlam,
               (tol.sum((0, 1)) + U * depth * dl.abs().sum((0, 1))) * k + 20 * U * dlam.abs(), "dlam")
+
+
+def documents(l, cuts):
+    """[start, end) of the documents of a row of l tokens."""
+    at = [0, *cuts, l]
+    return [(p, q) for p, q in zip(at, at[1:])]
+
+
+@pytest.mark.parametrize("l,d,cuts,bad", [(300, 64, [130, 131, 200], [60, 250]), (300, 64, [], [150]),
+                                          (300, 33, [128], [64, 129]), (4000, 32, [1500, 2100], [700, 3000])])
+@pytest.mark.parametrize("in_t", ["f32", "bf16"])
+def test_nan_gate_stays_in_its_document(l, d, cuts, bad, in_t):
+    """A NaN in r: what it reaches forward and backward is what it reaches where each
+    document is a call of its own, without masks; nothing of another document."""
+    n = rng(7 + l)
+    x, rr, i, z, dy = (n(1, l, d).to(DT[in_t]) for _ in range(5))
+    rr[:, bad] = float("nan")
+    lam = -4.0 + n(d)
+    starts = torch.zeros(1, l, dtype=torch.uint8, device="cuda")
+    starts[:, cuts] = 1
+    full = torch.full((1,), l, dtype=torch.int32, device="cuda")
+    f = B.rec_fwd(x, rr, i, lam, z=z, starts=starts, lengths=full, save_states=True, return_last=True)
+    g = B.rec_bwd(x, rr, i, lam, dy, f["states"], z=z, starts=starts, lengths=full)
+    if d % 2:        # documents of their own at an even width: the kernels without masks
+        x, rr, i, z, dy = (torch.cat([t, torch.zeros_like(t[..., :1])], 2) for t in (x, rr, i, z, dy))
+        lam = torch.cat([lam, lam[:1]])
+    for p, q in documents(l, cuts):
+        part = [t[:, p:q].contiguous() for t in (x, rr, i)]
+        zp, dyp = z[:, p:q].contiguous(), dy[:, p:q].contiguous()
+        fp = B.rec_fwd(*part, lam, z=zp, save_states=True, return_last=True)
+        gp = B.rec_bwd(*part, lam, dyp, fp["states"], z=zp)
+        for name, whole, own in (("y", f["y"], fp["y"]), *((k, g[k], gp[k]) for k in ("dx", "dr", "di", "dz"))):
+            assert torch.equal(torch.isnan(whole[:, p:q]), torch.isnan(own[..., :d])), (name, p)
+    if cuts:
+        assert bool(torch.isnan(f["y"]).any()) and not bool(torch.isnan(f["y"]).all())
