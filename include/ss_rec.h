@@ -35,9 +35,11 @@
  * caller, 16-byte aligned (a tensor with a row stride: aligned to its element
  * size; starts: any address).  Asynchronous on `stream`; validation before any HIP
  * call; no allocation; deterministic.  Status codes of ss_scan.h.  Everything
- * between input and output is float32, and the decay keeps its relative accuracy
- * near 1; y and the gradients are rounded once.  What is NaN or infinite behind a
- * length or in front of a start does not reach the other side.
+ * between input and output is float32, and a decay near 1 keeps the relative
+ * accuracy of 1 - a however long its state is remembered (ss_rec_step rounds the
+ * state to float32 once a token); y and the gradients are rounded once.  What is NaN
+ * or infinite behind a length or in front of a start does not reach the other side;
+ * within a document an infinite state may turn into NaN.
  */
 #ifndef SS_REC_H
 #define SS_REC_H

@@ -8,11 +8,11 @@
 // whose decays and end states a first pass over the inputs provides; every chunk folds
 // those in front of it.
 //
-// Measured (bf16): 8 x 2048 x 2560 with a gate 118 us, 3.55 TB/s of the least traffic (which
+// Measured (bf16): 8 x 2048 x 2560 with a gate 121 us, 3.47 TB/s of the least traffic (which
 // is what the counters see) against a copy's 5.1; the vector ALU is busy 56% of it.  What holds
 // it back is how the rows lie: 335 MB as 7 x 2048 x 2336 take 79 us, as 8 x 2048 x 2048, rows
 // 4096 bytes apart, 102.  A batch row's workgroups on one XCD matter most (in plain order 155
-// us).  1 x 262144 x 256: 250 us, of them 110 the sums' pass.
+// us, when the kernel took 118).  1 x 262144 x 256: 252 us, of them 110 the sums' pass.
 #include "ss_rec.hpp"
 
 namespace ss {
@@ -22,7 +22,8 @@ constexpr int kS = 4;                       // steps of a lane's stretch
 constexpr int kWaveSteps = kSubs * kS;
 constexpr int kWaves = 8;
 constexpr int kBlock = kWaves * kWaveSteps;
-// Steps of a lane, waves (bf16 8 x 2048 x 2560 with a gate, us): 4, 8 117; 4, 4 146; 8, 4 145
+// Steps of a lane, waves (bf16 8 x 2048 x 2560 with a gate, us; with decays joined as fp32
+// numbers, 3 us less than now): 4, 8 117; 4, 4 146; 8, 4 145
 // (more loads than the counter of those in flight holds); 4, 16 139.  Rows 5120 bytes apart
 // are the slow ones of these: 8 x 2048 x 2592 takes 110, 107, 112 and 124.
 static_assert(SS_REC_CHUNK % kWaveSteps == 0 && kBlock % SS_REC_CHUNK == 0,
@@ -37,7 +38,7 @@ struct FwdParams {
   const int32_t* lengths;
   void* y;
   float *h_last, *states;
-  float *cdec, *cend;        // (B, nchunks, D) chunks' decays and end states from a zero start
+  float *clog, *cend;        // (B, nchunks, D) chunks' log decays and end states from a zero start
   float* first;              // SUM: (B, D), h0 as the outputs' pass reads it (h_last may take
                              // its place before every chunk has)
 };
@@ -57,13 +58,15 @@ void rec_fwd_kernel(FwdParams p) {
   Masks masks;
   masks.init<MASK>(p.starts, p.lengths, at.b, L, t0, p.s.chunk);
   const int64_t crow = int64_t(at.b * p.s.nchunks + at.chunk) * D + at.c;
-  float k[kV], H[kV] = {}, dec[kV];
+  float k[kV], start_state[kV] = {};
   load_f32(p.lam + at.c, at.n, k);
 #pragma unroll
-  for (int j = 0; j < kV; ++j) dec[j] = 1.0f;
-#pragma unroll
   for (int j = 0; j < kV; ++j) k[j] = rec_rate(p.s.decay, k[j]);
-  if (!SUM && p.h0) load_f32(p.h0 + int64_t(at.b) * D + at.c, at.n, H);
+  if (!SUM && p.h0) load_f32(p.h0 + int64_t(at.b) * D + at.c, at.n, start_state);
+  Carry H[kV];
+#pragma unroll
+  for (int j = 0; j < kV; ++j) H[j] = Carry{start_state[j], 0.0f};
+  [[maybe_unused]] LogSum chunk_log[kV];
   const int off = at.wv * kWaveSteps + at.sub * kS;      // of the lane's stretch in a block
   const int li = at.lane % kRecLanes * kV;
 
@@ -97,7 +100,7 @@ void rec_fwd_kernel(FwdParams p) {
   load_z(odd, masks.len - off - kBlock);
   if (!SUM && at.chunk > 0) {
     const int64_t first = int64_t(at.b) * p.s.nchunks * D + at.c;
-    fold_chunks<MASK, kWaves>(p.cdec + first, p.cend + first, D, at.chunk, at, tc[1], ts[1], H);
+    fold_chunks<MASK, kWaves>(p.clog + first, p.cend + first, D, at.chunk, at, tc[1], ts[1], H);
   }
   auto run = [&](Block& in_, int tb, int buf) {
     // steps of the lane's stretch inside the chunk; before the length, this time and the next
@@ -124,10 +127,10 @@ void rec_fwd_kernel(FwdParams p) {
         const Decay d = rec_decay(l2);
         const float add = d.beta * sigmoid(iv[j]) * xv[j];
         const bool cut = MASK && start[e] && in;
-        c[e][j] = rec_decay_of<MASK>(d.a, cut);
+        c[e][j] = step_decay<MASK>(d.a, cut);
         g[e][j] = in ? add : 0.0f;
         l[j] += l2;
-        s[j] = rec_apply<MASK>(c[e][j], s[j], g[e][j]);
+        s[j] = step_apply<MASK>(c[e][j], s[j], g[e][j]);
       }
       if (MASK) cuts |= start[e] && e < live;
     }
@@ -135,8 +138,11 @@ void rec_fwd_kernel(FwdParams p) {
     float cx[kV], sx[kV], cw[kV];            // of the stretches in front of the lane's, of the wave
 #pragma unroll
     for (int j = 0; j < kV; ++j) {
-      cw[j] = rec_decay_of<MASK>(hw_exp2(l[j]), cuts);
-      join_up<MASK>(at.sub, cw[j], s[j], cx[j], sx[j]);
+      float P = step_decay<MASK>(hw_exp2(l[j]), cuts);
+      join_up<MASK>(at.sub, P, s[j], cx[j], sx[j]);
+      const float lw = wave_log(stretch_log<MASK>(l[j], cuts));
+      cw[j] = rec_decay_of<MASK>(lw);
+      if constexpr (SUM) chunk_log[j].add(lw);
     }
     if (at.sub == 0) {
       put_lds(&tc[buf][at.wv][li], cw);
@@ -151,11 +157,12 @@ void rec_fwd_kernel(FwdParams p) {
       const Floats sv = get_lds(&ts[buf][w][li]);
 #pragma unroll
       for (int j = 0; j < kV; ++j) {
-        if (SUM) dec[j] = rec_both<MASK>(dec[j], cv.v[j]);
-        h[j] = w == at.wv ? H[j] : h[j];
-        H[j] = rec_apply<MASK>(cv.v[j], H[j], sv.v[j]);
+        if constexpr (!SUM) h[j] = w == at.wv ? H[j].value() : h[j];
+        H[j].apply<MASK>(cv.v[j], sv.v[j]);
       }
     }
+#pragma unroll
+    for (int j = 0; j < kV; ++j) H[j].settle();
     if constexpr (!SUM) {
       const int tw = tb + at.wv * kWaveSteps;          // the wave's first step
       if (p.states && at.sub == 0 && tw < masks.steps && tw % SS_REC_CHUNK == 0) {
@@ -163,7 +170,7 @@ void rec_fwd_kernel(FwdParams p) {
         store_f32(p.states + (at.b * n_states + (t0 + tw) / SS_REC_CHUNK) * D + at.c, at.n, h);
       }
 #pragma unroll
-      for (int j = 0; j < kV; ++j) h[j] = rec_apply<MASK>(cx[j], h[j], sx[j]);
+      for (int j = 0; j < kV; ++j) h[j] = step_apply<MASK>(cx[j], h[j], sx[j]);
       float out[kS][kV];
 #pragma unroll
       for (int e = 0; e < kS; ++e) {
@@ -171,7 +178,7 @@ void rec_fwd_kernel(FwdParams p) {
         if constexpr (Z) unpack(z.q[e], zv);
 #pragma unroll
         for (int j = 0; j < kV; ++j) {
-          h[j] = rec_apply<MASK>(c[e][j], h[j], g[e][j]);
+          h[j] = step_apply<MASK>(c[e][j], h[j], g[e][j]);
           out[e][j] = Z ? h[j] * silu(zv[j]) : h[j];
           if (MASK) out[e][j] = e < live ? out[e][j] : 0.0f;
         }
@@ -186,6 +193,10 @@ void rec_fwd_kernel(FwdParams p) {
     run(even, tb, 0);
     run(odd, tb + kBlock, 1);
   }
+  float end[kV], log_decay[kV];
+#pragma unroll
+  for (int j = 0; j < kV; ++j) end[j] = H[j].base;
+  if constexpr (SUM) sum_logs<kWaves>(at, tc[0], chunk_log, log_decay);
   if (at.wv == 0 && at.sub == 0) {
     if constexpr (SUM) {
       if (p.h0 && at.chunk == 0) {
@@ -193,10 +204,10 @@ void rec_fwd_kernel(FwdParams p) {
         load_f32(p.h0 + int64_t(at.b) * D + at.c, at.n, first);
         store_f32(p.first + int64_t(at.b) * D + at.c, at.n, first);
       }
-      store_f32(p.cdec + crow, at.n, dec);
-      store_f32(p.cend + crow, at.n, H);
+      store_f32(p.clog + crow, at.n, log_decay);
+      store_f32(p.cend + crow, at.n, end);
     } else if (p.h_last && at.chunk == p.s.nchunks - 1) {
-      store_f32(p.h_last + int64_t(at.b) * D + at.c, at.n, H);
+      store_f32(p.h_last + int64_t(at.b) * D + at.c, at.n, end);
     }
   }
 #endif

@@ -3,15 +3,21 @@
 //
 // Layout.  A workgroup holds kRecChans channels, two neighbours per lane; a wave's lanes
 // hold kSubs stretches of time of S steps each, its waves follow each other in time.
-// Every lane runs its stretch from a zero state; a stretch is then summed up by its decay
-// P (the exponential of the sum of log decays, so that it is rounded once) and its end
-// state s, h <- P h + s.  Stretches are joined in the wave by row swaps and across waves in
-// LDS, and each lane runs its steps again from its true state.
+// Every lane runs its stretch from a zero state; a stretch is then summed up by its decay P
+// (the exponential of the sum of log decays) and its end state s, h <- P h + s.  Stretches are
+// joined in the wave by row swaps and across waves in LDS, and each lane runs its steps again
+// from its true state.
 //
 // Accuracy.  A state that a step hardly decays is remembered for 1 / (1 - a) steps, and a
-// decay rounded to fp32 at every step would add up to 2^-24 / (1 - a) of it.  What carries
-// a state on is P, once per stretch, so the rounding of a single step's a stays within its
-// stretch; sqrt(1 - a^2) comes from a - 1 with full relative accuracy (a series near 0).
+// decay rounded to fp32 wherever it meets the state that is carried on would add up to 2^-24 /
+// (1 - a) of it, every time to the same side where the gates repeat.  Decays of steps and
+// stretches therefore stay within their wave.  A wave's and a chunk's are sums of logs, and
+// are applied as a - 1 where they are near 1, h <- h + ((a - 1) h + s) (rec_decay_of,
+// rec_apply).  The state's own rounding would add up the same way, half a step at every join:
+// it is carried on as a sum of two numbers (Carry).  sqrt(1 - a^2) comes from a - 1 with full
+// relative accuracy (a series near 0).  Inputs of one sign over 262144 steps, 1 - a from 1e-13
+// to 5e-4: states and adjoints are 1.2e-6 of themselves off at most (9.3e-4 with fp32 decays
+// all the way; 8 x 2048 x 2560 forward 118 -> 121 us, backward 242 -> 245).
 #pragma once
 
 #include <type_traits>
@@ -49,23 +55,63 @@ __device__ __forceinline__ Decay rec_decay(float l2) {
   return Decay{a, E, __builtin_amdgcn_sqrtf(-E * (2.0f + E))};
 }
 
-// Decays of steps and stretches.  CUT: there may be starts, whose decay is 0; every other one
-// is at least kTiny, added so that a NaN stays one (a maximum drops it), and changes no decay
-// above 2^-102: a start drops even a state that is not finite, and a gate that is NaN reaches
-// all of its document, forward and backward, as it does without CUT.
-template <bool CUT> __device__ __forceinline__ float rec_decay_of(float a, bool cut) {
+// Steps.  CUT: there may be starts, whose decay is 0; every other one is at least kTiny, added
+// so that a NaN stays one (a maximum drops it), and changes no decay above 2^-102: a start
+// drops even a state that is not finite, and a gate that is NaN reaches all of its document,
+// forward and backward, as it does without CUT.
+template <bool CUT> __device__ __forceinline__ float step_decay(float a, bool cut) {
   return CUT ? (cut ? 0.0f : a + kTiny) : a;
 }
+// h decayed, and b added
+template <bool CUT> __device__ __forceinline__ float step_apply(float a, float h, float b) {
+  const float v = __builtin_fmaf(a, h, b);
+  return CUT && a == 0.0f ? b : v;
+}
+
 // one decay after the other
-template <bool CUT> __device__ __forceinline__ float rec_both(float p, float q) {
+template <bool CUT> __device__ __forceinline__ float step_both(float p, float q) {
   const float v = p * q, w = v + kTiny;
   return CUT ? (__builtin_fminf(p, q) == 0.0f ? 0.0f : w) : v;
 }
-// h decayed, and b added
-template <bool CUT> __device__ __forceinline__ float rec_apply(float p, float h, float b) {
-  const float v = __builtin_fmaf(p, h, b);
-  return CUT && p == 0.0f ? b : v;
+
+// Stretches.  Their log2 decays are at most 0 and add up; that of one with a start is -infinity.
+// (CUT: no other one is, nor a NaN, which the end state and the leaving adjoint carry on.)
+constexpr float kCutLog = -__builtin_inff();
+template <bool CUT> __device__ __forceinline__ float stretch_log(float l, bool cut) {
+  const float v = __builtin_fmaxf(l, -1e30f);
+  return CUT ? (cut ? kCutLog : v) : l;
 }
+// A decay as it is applied: a - 1, and then below 0, where a is near 1, else a (of CUT: 0 for
+// a start alone).
+constexpr float kNoDecay = -kTiny;
+template <bool CUT> __device__ __forceinline__ float rec_decay_of(float l2) {
+  const float near = __builtin_fmaf(l2, expm1_factor(l2), kNoDecay);
+  float far = hw_exp2(l2);
+  if (CUT) far += l2 == kCutLog ? 0.0f : kTiny;
+  return __builtin_unpredictable(l2 > -kSeries2) ? near : far;
+}
+template <bool CUT> __device__ __forceinline__ float rec_apply(float q, float h0, float b) {
+  const float h = CUT && q == 0.0f ? 0.0f : h0;
+  return __builtin_fmaf(q, h, b) + (q < 0.0f ? h : 0.0f);
+}
+// A state (or adjoint) between blocks, base + rest: joins near 1 add to the rest, whose
+// rounding is that of what a block adds; others start a new one.
+struct Carry {
+  float base, rest;
+  __device__ __forceinline__ float value() const { return base + rest; }
+  template <bool CUT> __device__ __forceinline__ void apply(float q, float b) {
+    const bool near = q < 0.0f;
+    const float v = value(), h = CUT && q == 0.0f ? 0.0f : v;
+    rest = __builtin_fmaf(q, h, b) + (near ? rest : 0.0f);
+    base = near ? base : 0.0f;
+  }
+  // base becomes the value, rest what that leaves
+  __device__ __forceinline__ void settle() {
+    const float v = value();
+    rest -= v - base;
+    base = v;
+  }
+};
 
 // A lane's channels of a row, as stored, so that a prefetch is not waited for.
 template <typename T> constexpr int kWords = kV * int(sizeof(T)) / 4;
@@ -140,13 +186,13 @@ __device__ __forceinline__ void join_up(int sub, float& P, float& s, float& Px, 
   swap_rows(s, s0, s1);
   Px = sub & 1 ? p0 : 1.0f;
   sx = sub & 1 ? s0 : 0.0f;
-  swap_halves(rec_both<CUT>(p0, p1), p0, P);
-  swap_halves(rec_apply<CUT>(p1, s0, s1), s0, s);
-  const float q = rec_both<CUT>(p0, Px), t = rec_apply<CUT>(Px, s0, sx);
+  swap_halves(step_both<CUT>(p0, p1), p0, P);
+  swap_halves(step_apply<CUT>(p1, s0, s1), s0, s);
+  const float q = step_both<CUT>(p0, Px), t = step_apply<CUT>(Px, s0, sx);
   Px = sub & 2 ? q : Px;
   sx = sub & 2 ? t : sx;
-  s = rec_apply<CUT>(P, s0, s);
-  P = rec_both<CUT>(p0, P);
+  s = step_apply<CUT>(P, s0, s);
+  P = step_both<CUT>(p0, P);
 }
 // Both walks of a backward pass: forward as above, and q, what leaves a stretch at its
 // first step, joined from behind; (Py, qy): of the stretches behind the lane's.
@@ -158,10 +204,10 @@ __device__ __forceinline__ void join_both(int sub, float& P, float& s, float& q,
   swap_rows(q, q0, q1);
   Py = sub & 1 ? 1.0f : p1;
   qy = sub & 1 ? 0.0f : q1;
-  swap_halves(rec_both<CUT>(p0, p1), r0, r1);
-  swap_halves(rec_apply<CUT>(p0, q1, q0), u0, u1);
-  q = rec_apply<CUT>(r0, u1, u0);
-  const float y = rec_both<CUT>(Py, r1), v = rec_apply<CUT>(Py, u1, qy);
+  swap_halves(step_both<CUT>(p0, p1), r0, r1);
+  swap_halves(step_apply<CUT>(p0, q1, q0), u0, u1);
+  q = step_apply<CUT>(r0, u1, u0);
+  const float y = step_both<CUT>(Py, r1), v = step_apply<CUT>(Py, u1, qy);
   Py = sub & 2 ? Py : y;
   qy = sub & 2 ? qy : v;
   if constexpr (UP) {
@@ -169,13 +215,35 @@ __device__ __forceinline__ void join_both(int sub, float& P, float& s, float& q,
     swap_rows(s, s0, s1);
     Px = sub & 1 ? p0 : 1.0f;
     sx = sub & 1 ? s0 : 0.0f;
-    swap_halves(rec_apply<CUT>(p1, s0, s1), t0, t1);
-    s = rec_apply<CUT>(r1, t0, t1);
-    const float x = rec_both<CUT>(r0, Px), w = rec_apply<CUT>(Px, t0, sx);
+    swap_halves(step_apply<CUT>(p1, s0, s1), t0, t1);
+    s = step_apply<CUT>(r1, t0, t1);
+    const float x = step_both<CUT>(r0, Px), w = step_apply<CUT>(Px, t0, sx);
     Px = sub & 2 ? x : Px;
     sx = sub & 2 ? w : sx;
   }
-  P = rec_both<CUT>(r0, r1);
+  P = step_both<CUT>(r0, r1);
+}
+// Runs of chunks in the lanes of a wave, joined: (l, s) of the lane's own on entry, of the
+// whole wave on return.  A run is long: its decay is applied as rec_apply does.
+template <bool CUT> __device__ __forceinline__ void join_runs(float& l, float& s) {
+  float l0, l1, d0, d1, s0, s1;
+  swap_rows(l, l0, l1);
+  swap_rows(rec_decay_of<CUT>(l), d0, d1);
+  swap_rows(s, s0, s1);
+  l = l0 + l1;
+  s = rec_apply<CUT>(d1, s0, s1);
+  swap_halves(l, l0, l1);
+  swap_halves(rec_decay_of<CUT>(l), d0, d1);
+  swap_halves(s, s0, s1);
+  l = l0 + l1;
+  s = rec_apply<CUT>(d1, s0, s1);
+}
+// The log decay of a wave's stretches, from the lane's own
+__device__ __forceinline__ float wave_log(float l) {
+  float a, b;
+  swap_rows(l, a, b);
+  swap_halves(a + b, a, b);
+  return a + b;
 }
 
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
@@ -215,38 +283,50 @@ __device__ __forceinline__ Floats get_lds(const float* p) {
   return *reinterpret_cast<const Floats*>(p);
 }
 
+// A chunk's log decay, of a wave's stretches block after block: sum + rest, so that its rounding
+// does not grow with the blocks.
+struct LogSum {
+  float sum = 0.0f, rest = 0.0f;
+  __device__ __forceinline__ void add(float l) {
+    const float v = sum + l;
+    rest += l - (v - sum);
+    sum = v;
+  }
+  __device__ __forceinline__ float value() const { return sum == kCutLog ? kCutLog : sum + rest; }
+};
+
 // What the chunks in front of one's own do to a state, folded by the whole workgroup:
-// decay[k], end[k] (from a zero start), k < n, are `step` floats apart.  The lanes of a
+// logs[k], end[k] (from a zero start), k < n, are `step` floats apart.  The lanes of a
 // channel take equal runs of them, which are joined as stretches are, through tc and ts
 // (kWaves rows each); H is advanced.
 template <bool CUT, int kWaves>
-__device__ __forceinline__ void fold_chunks(const float* decay, const float* end, int64_t step,
+__device__ __forceinline__ void fold_chunks(const float* logs, const float* end, int64_t step,
                                             int n, const Place& at, float (*tc)[kRecChans],
-                                            float (*ts)[kRecChans], float (&H)[kV]) {
+                                            float (*ts)[kRecChans], Carry (&H)[kV]) {
   const int units = kWaves * kSubs, per = (n + units - 1) / units;
   const int k0 = (at.wv * kSubs + at.sub) * per, k1 = k0 + per < n ? k0 + per : n;
   const int li = at.lane % kRecLanes * kV;
-  float P[kV], s[kV], Px, sx;
+  float l[kV], s[kV];
 #pragma unroll
-  for (int j = 0; j < kV; ++j) {
-    P[j] = 1.0f;
-    s[j] = 0.0f;
-  }
+  for (int j = 0; j < kV; ++j) l[j] = s[j] = 0.0f;
 #pragma unroll 4
   for (int k = k0; k < k1; ++k) {
     float p[kV], e[kV];
-    load_f32(decay + k * step, at.n, p);
+    load_f32(logs + k * step, at.n, p);
     load_f32(end + k * step, at.n, e);
 #pragma unroll
     for (int j = 0; j < kV; ++j) {
-      s[j] = rec_apply<CUT>(p[j], s[j], e[j]);
-      P[j] = rec_both<CUT>(P[j], p[j]);
+      s[j] = rec_apply<CUT>(rec_decay_of<CUT>(p[j]), s[j], e[j]);
+      l[j] = l[j] + p[j];
     }
   }
 #pragma unroll
-  for (int j = 0; j < kV; ++j) join_up<CUT>(at.sub, P[j], s[j], Px, sx);
+  for (int j = 0; j < kV; ++j) {
+    join_runs<CUT>(l[j], s[j]);
+    l[j] = rec_decay_of<CUT>(l[j]);
+  }
   if (at.sub == 0) {
-    put_lds(&tc[at.wv][li], P);
+    put_lds(&tc[at.wv][li], l);
     put_lds(&ts[at.wv][li], s);
   }
   __syncthreads();
@@ -254,7 +334,28 @@ __device__ __forceinline__ void fold_chunks(const float* decay, const float* end
   for (int w = 0; w < kWaves; ++w) {
     const Floats cv = get_lds(&tc[w][li]), sv = get_lds(&ts[w][li]);
 #pragma unroll
-    for (int j = 0; j < kV; ++j) H[j] = rec_apply<CUT>(cv.v[j], H[j], sv.v[j]);
+    for (int j = 0; j < kV; ++j) H[j].template apply<CUT>(cv.v[j], sv.v[j]);
+  }
+#pragma unroll
+  for (int j = 0; j < kV; ++j) H[j].settle();
+}
+// The waves' log decays of a chunk, added, in all of a channel's lanes.  box: kWaves rows that
+// no wave reads any more.
+template <int kWaves>
+__device__ __forceinline__ void sum_logs(const Place& at, float (*box)[kRecChans],
+                                         const LogSum (&sum)[kV], float (&l)[kV]) {
+  const int li = at.lane % kRecLanes * kV;
+#pragma unroll
+  for (int j = 0; j < kV; ++j) l[j] = sum[j].value();
+  __syncthreads();
+  if (at.sub == 0) put_lds(&box[at.wv][li], l);
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < kV; ++j) l[j] = 0.0f;
+  for (int w = 0; w < kWaves; ++w) {
+    const Floats v = get_lds(&box[w][li]);
+#pragma unroll
+    for (int j = 0; j < kV; ++j) l[j] = l[j] + v.v[j];
   }
 }
 

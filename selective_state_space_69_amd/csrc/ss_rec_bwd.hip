@@ -7,7 +7,7 @@
 // leaving adjoint; both walks are joined by one barrier per block, then every lane runs
 // its steps forward (states) and backward (adjoints, gradients) from true values.
 //
-// Measured (bf16): 8 x 2048 x 2560 with a gate 237 us, 3.4 TB/s; the vector ALU is busy 55% of
+// Measured (bf16): 8 x 2048 x 2560 with a gate 245 us, 3.1 TB/s; the vector ALU is busy 55% of
 // it (104 operations an element), and what else holds is the forward's.
 #include "ss_rec.hpp"
 
@@ -34,12 +34,12 @@ struct BwdParams {
   const float *states, *dh_last;
   void *dx, *dr, *di, *dz;
   float* dh0;
-  float *cdec, *cadj;        // (B, nchunks, D) chunks' decays and the adjoints that leave them
+  float *clog, *cadj;        // (B, nchunks, D) chunks' log decays and the adjoints that leave them
   float* part;               // (B * nchunks, D) sums of dlam
 };
 
 // Two waves to a SIMD: at three the registers do not suffice (bf16 8 x 2048 x 2560 with a gate
-// 290 us, 237 so; 8 waves of 2 steps 252, 8 of 4 259).
+// 290 us, 237 so, 245 now; 8 waves of 2 steps 252, 8 of 4 259).
 // SUM: only the chunks' carries (decay, and the adjoint that leaves with none
 // entering).
 template <typename T, typename Dy, bool Z, bool MASK, bool ANY, bool SUM>
@@ -55,14 +55,16 @@ void rec_bwd_kernel(BwdParams p) {
   masks.init<MASK>(p.starts, p.lengths, at.b, L, t0, p.s.chunk);
   const int64_t crow = int64_t(at.b * p.s.nchunks + at.chunk) * D + at.c;
   const int64_t n_states = (L + SS_REC_CHUNK - 1) / SS_REC_CHUNK;
-  float k[kV], W[kV] = {}, dec[kV];
+  float k[kV], entering[kV] = {};
   float run[kV] = {}, sum[kV] = {};     // of dlam: of kRun blocks, of the chunk
   load_f32(p.lam + at.c, at.n, k);
 #pragma unroll
-  for (int j = 0; j < kV; ++j) dec[j] = 1.0f;
-#pragma unroll
   for (int j = 0; j < kV; ++j) k[j] = rec_rate(p.s.decay, k[j]);
-  if (!SUM && p.dh_last) load_f32(p.dh_last + int64_t(at.b) * D + at.c, at.n, W);
+  if (!SUM && p.dh_last) load_f32(p.dh_last + int64_t(at.b) * D + at.c, at.n, entering);
+  Carry W[kV];
+#pragma unroll
+  for (int j = 0; j < kV; ++j) W[j] = Carry{entering[j], 0.0f};
+  [[maybe_unused]] LogSum chunk_log[kV];
   const int off = at.wv * kWaveSteps + at.sub * kS;      // of the lane's stretch in a block
   const int li = at.lane % kRecLanes * kV;
   int tb = (masks.steps - 1) / kBlock * kBlock;          // the block's first step
@@ -123,7 +125,7 @@ void rec_bwd_kernel(BwdParams p) {
   load_rest(odd, tb - kBlock, steps(masks.len, tb - kBlock));
   if (!SUM && at.chunk < p.s.nchunks - 1) {       // from the last chunk on
     const int64_t last = (int64_t(at.b + 1) * p.s.nchunks - 1) * D + at.c;
-    fold_chunks<MASK, kWaves>(p.cdec + last, p.cadj + last, -int64_t(D),
+    fold_chunks<MASK, kWaves>(p.clog + last, p.cadj + last, -int64_t(D),
                               p.s.nchunks - 1 - at.chunk, at, tc[1], tq[1], W);
   }
   int turn = 0;
@@ -160,7 +162,7 @@ void rec_bwd_kernel(BwdParams p) {
         float l2 = k[j] * sr[e][j];
         l2 = in ? l2 : 0.0f;
         const Decay f = rec_decay(l2);
-        c[e][j] = rec_decay_of<MASK>(f.a, cut);
+        c[e][j] = step_decay<MASK>(f.a, cut);
         const float d = Z ? dv[j] * silu(zv[j]) : dv[j];
         v[e][j] = in ? d : 0.0f;
         l[j] += l2;
@@ -168,7 +170,7 @@ void rec_bwd_kernel(BwdParams p) {
           beta[e][j] = f.beta;
           si[e][j] = sigmoid(iv[j]);
           const float add = f.beta * si[e][j] * xv[j];
-          s[j] = rec_apply<MASK>(c[e][j], s[j], in ? add : 0.0f);
+          s[j] = step_apply<MASK>(c[e][j], s[j], in ? add : 0.0f);
         }
       }
     }
@@ -176,13 +178,16 @@ void rec_bwd_kernel(BwdParams p) {
 #pragma unroll
     for (int e = kS - 1; e >= 0; --e)
 #pragma unroll
-      for (int j = 0; j < kV; ++j) q[j] = rec_apply<MASK>(c[e][j], v[e][j] + q[j], 0.0f);
+      for (int j = 0; j < kV; ++j) q[j] = step_apply<MASK>(c[e][j], v[e][j] + q[j], 0.0f);
     // of the stretches in front of the lane's, behind it, of the wave
     float cx[kV], sx[kV], cy[kV], qy[kV], cw[kV];
 #pragma unroll
     for (int j = 0; j < kV; ++j) {
-      cw[j] = rec_decay_of<MASK>(hw_exp2(l[j]), cuts);
-      join_both<MASK, !SUM>(at.sub, cw[j], s[j], q[j], cx[j], sx[j], cy[j], qy[j]);
+      float P = step_decay<MASK>(hw_exp2(l[j]), cuts);
+      join_both<MASK, !SUM>(at.sub, P, s[j], q[j], cx[j], sx[j], cy[j], qy[j]);
+      const float lw = wave_log(stretch_log<MASK>(l[j], cuts));
+      cw[j] = rec_decay_of<MASK>(lw);
+      if constexpr (SUM) chunk_log[j].add(lw);
     }
     if (at.sub == 0) {
       put_lds(&tc[buf][at.wv][li], cw);
@@ -205,24 +210,25 @@ void rec_bwd_kernel(BwdParams p) {
       const Floats qv = get_lds(&tq[buf][o][li]);
 #pragma unroll
       for (int j = 0; j < kV; ++j) {
-        if (SUM) dec[j] = rec_both<MASK>(dec[j], cv.v[j]);
-        w[j] = o == at.wv ? W[j] : w[j];
-        W[j] = rec_apply<MASK>(cv.v[j], W[j], qv.v[j]);
+        if constexpr (!SUM) w[j] = o == at.wv ? W[j].value() : w[j];
+        W[j].apply<MASK>(cv.v[j], qv.v[j]);
       }
     }
+#pragma unroll
+    for (int j = 0; j < kV; ++j) W[j].settle();
     if constexpr (!SUM) {
       // the waves between the kept state and this one
       for (int o = at.wv / kPerState * kPerState; o < at.wv; ++o) {
         const Floats cv = get_lds(&tc[buf][o][li]);
         const Floats sv = get_lds(&ts[buf][o][li]);
-  #pragma unroll
+#pragma unroll
         for (int j = 0; j < kV; ++j) h[j] = rec_apply<MASK>(cv.v[j], h[j], sv.v[j]);
       }
       float hs[kS + 1][kV];       // the state in front of each step, behind the last
 #pragma unroll
       for (int j = 0; j < kV; ++j) {
-        hs[0][j] = rec_apply<MASK>(cx[j], h[j], sx[j]);
-        w[j] = rec_apply<MASK>(cy[j], w[j], qy[j]);
+        hs[0][j] = step_apply<MASK>(cx[j], h[j], sx[j]);
+        w[j] = step_apply<MASK>(cy[j], w[j], qy[j]);
       }
 #pragma unroll
       for (int e = 0; e < kS; ++e) {
@@ -231,7 +237,7 @@ void rec_bwd_kernel(BwdParams p) {
 #pragma unroll
         for (int j = 0; j < kV; ++j) {
           const float add = beta[e][j] * si[e][j] * xv[j];
-          hs[e + 1][j] = rec_apply<MASK>(c[e][j], hs[e][j], e < live ? add : 0.0f);
+          hs[e + 1][j] = step_apply<MASK>(c[e][j], hs[e][j], e < live ? add : 0.0f);
         }
       }
 #pragma unroll
@@ -247,10 +253,10 @@ void rec_bwd_kernel(BwdParams p) {
 #pragma unroll
         for (int j = 0; j < kV; ++j) {
           const float u = v[e][j] + w[j], bt = beta[e][j], l2 = k[j] * sr[e][j], la = l2 * kLn2;
-          w[j] = rec_apply<MASK>(c[e][j], u, 0.0f);
+          w[j] = step_apply<MASK>(c[e][j], u, 0.0f);
           // log a / sqrt(1 - a^2): 0 where log a underflows to 0
           const float ratio = la * hw_rcp(bt), lb = bt > 0.0f ? ratio : 0.0f;
-          const float ah = rec_apply<MASK>(c[e][j], hs[e][j], 0.0f) * la;
+          const float ah = step_apply<MASK>(c[e][j], hs[e][j], 0.0f) * la;
           // a^2 with its relative accuracy, which 1 - (1 - a^2) loses where a is small (a = e^-16:
           // dr 1.4e-5 off); a start's own a is not in c
           const float aa = MASK && c[e][j] == 0.0f ? hw_exp2(2.0f * l2) : c[e][j] * c[e][j];
@@ -291,10 +297,15 @@ void rec_bwd_kernel(BwdParams p) {
     work(even, tb, 0);
     work(odd, tb - kBlock, 1);
   }
+  float leaving[kV];
+#pragma unroll
+  for (int j = 0; j < kV; ++j) leaving[j] = W[j].base;
   if constexpr (SUM) {
+    float log_decay[kV];
+    sum_logs<kWaves>(at, tc[0], chunk_log, log_decay);
     if (at.wv == 0 && at.sub == 0) {
-      store_f32(p.cdec + crow, at.n, dec);
-      store_f32(p.cadj + crow, at.n, W);
+      store_f32(p.clog + crow, at.n, log_decay);
+      store_f32(p.cadj + crow, at.n, leaving);
     }
   } else {
     // dlam: the workgroup's stretches, in order
@@ -324,7 +335,7 @@ void rec_bwd_kernel(BwdParams p) {
         tot[j] *= sp > 0.0f ? ratio : 1.0f;
       }
       store_f32(p.part + crow, at.n, tot);
-      if (p.dh0 && at.chunk == 0) store_f32(p.dh0 + int64_t(at.b) * D + at.c, at.n, W);
+      if (p.dh0 && at.chunk == 0) store_f32(p.dh0 + int64_t(at.b) * D + at.c, at.n, leaving);
     }
   }
 #endif

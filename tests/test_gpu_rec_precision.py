@@ -1,5 +1,6 @@
 """Accuracy of the gated linear recurrence where it is easily lost, with bounds of their
-own: gradients at strong decays; and what a gate that is NaN reaches."""
+own: gradients at strong decays, states that are remembered long; and what a gate that is
+NaN reaches."""
 import pytest
 import torch
 
@@ -99,3 +100,71 @@ def test_nan_gate_stays_in_its_document(l, d, cuts, bad, in_t):
             assert torch.equal(torch.isnan(whole[:, p:q]), torch.isnan(own[..., :d])), (name, p)
     if cuts:
         assert bool(torch.isnan(f["y"]).any()) and not bool(torch.isnan(f["y"]).all())
+
+
+def slow_bound(lam):
+    """Relative bound of a state that decays by far less than 2^-10 a step, gates at r = i =
+    0 and inputs of one sign, so that nothing cancels.  log a: the rounded exponent of
+    softplus moves it by |lam| U, exponential, logarithm, product and sigmoid by 14 U more;
+    it enters the state by the decay (at most once: a longer or shorter memory) and by
+    sqrt(1 - a^2) (half).  24 U: a - 1 and its sums.  The input's product, square root and
+    gate: 13 U.  A stretch's own four steps and the joins in front of an output: 24 U.  No
+    term grows with the length."""
+    return (1.5 * (lam.abs().double() + 14) + 24 + 13 + 24) * U
+
+
+def slow_inputs(l, lam, seed):
+    n = rng(seed)
+    d = lam.numel()
+    x = 0.25 + n(1, l, d).abs()
+    x[..., ::2] = 1.0                       # every other channel: the same term at every step
+    zero = torch.zeros_like(x)
+    return x, zero, zero.clone()
+
+
+def per_step_fp32(x, lam):
+    """The recurrence with a decay rounded to fp32 at every step, as a plain loop has it."""
+    la = (-8.0 * ref.softplus(lam.double()) * 0.5).cpu()
+    a, g = la.exp().float(), ((-torch.expm1(2 * la)).sqrt() * 0.5).float()
+    h, x = torch.zeros_like(a), x[0].cpu()
+    for t in range(x.shape[0]):
+        h = a * h + g * x[t]
+    return h
+
+
+@pytest.mark.parametrize("batch,l,masked", [(256, 16384, False), (1, 16384, False), (1, 16384, True),
+                                            (1, 262144, False), (2, 5000, True)])
+@pytest.mark.parametrize("in_t", ["f32", "bf16"])
+def test_long_lived_states(batch, l, masked, in_t):
+    """States remembered for 10^3 to 10^13 steps keep their accuracy over the whole length, in
+    one pass (256 rows) and in chunks, forward and backward; a recurrence that rounds its
+    decay at every step would fail here."""
+    lam = torch.cat([torch.linspace(-15.0, -9.0, 28, device="cuda"),
+                     torch.linspace(-30.0, -16.0, 4, device="cuda")])
+    x, rr, i = (t.to(DT[in_t]) for t in slow_inputs(l, lam, l + batch))
+    r = ref.Rec(x, rr, i, lam)
+    bound = slow_bound(lam)
+    if l == 16384 and in_t == "f32":
+        lost = (per_step_fp32(x, lam).double().cuda() / r.h[0, -1] - 1).abs()
+        assert int((lost > 2 * bound).sum()) > 16
+    dy = torch.rand_like(x).flip(1) + 0.5
+    n = None if not masked else torch.full((batch,), l, dtype=torch.int32, device="cuda")
+    st = torch.zeros(batch, l, dtype=torch.uint8, device="cuda") if masked else None
+
+    def rows(t):
+        return t.expand(batch, -1, -1).contiguous()
+    f = B.rec_fwd(rows(x), rows(rr), rows(i), lam, lengths=n, starts=st, out_dtype=torch.float32,
+                  return_last=True, save_states=True)
+    dh = torch.ones(batch, lam.numel(), device="cuda")
+    g = B.rec_bwd(rows(x), rows(rr), rows(i), lam, rows(dy), f["states"], lengths=n, starts=st, dh_last=dh)
+
+    def near(got, want, bound, what):
+        for row in (0, batch - 1):
+            ref.check(got[row], want[0], bound * want[0].abs(), what)
+    near(f["h_last"], r.h[:, -1], bound, "h_last")
+    near(f["y"], r.h, bound, "y")
+    near(f["states"][:, 1:], r.h[:, 63:l - 1:64], bound, "states")
+    back = torch.cat([torch.ones_like(r.h0)[:, None], r.carry[:, 1:].flip(1)], 1)
+    u = ref.walk(back, dy.double().flip(1), dh[:1].double()).flip(1)
+    near(g["dh0"], r.carry[:, 0] * u[:, 0], bound, "dh0")
+    near(g["dx"], u * r.beta * r.si, bound, "dx")
