@@ -66,7 +66,7 @@ __global__ __launch_bounds__(kThreads) void join_q8_kernel(MmParams p) {
     const int32_t c = int32_t(i - r * p.nS);
     int32_t sum = 0;
     for (int k = 0; k < p.splits; ++k) sum += part[k * total + i];
-    epilogue1(p, p.act, r, c, float(sum) * (p.row_scale[r] * p.col_scale[c]));
+    epilogue1(p, p.act, r, c, scaled(sum, RowScale(p.row_scale[r]), p.col_scale[c]));
   }
 }
 

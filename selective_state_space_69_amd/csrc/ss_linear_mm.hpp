@@ -85,6 +85,22 @@ __device__ __forceinline__ float load1(const void* base, int64_t i, int bf16) {
               : float(((const Global<float>*)base)[i]);
 }
 
+// A sum of 8-bit products times its row's and its column's scale, three roundings.  One
+// after the other: the scales' product may be 0, or infinite beside a sum of 0, where the
+// result is neither.  A sum, a whole number of at most 2^30, loses nothing to any row's scale,
+// and leaves fp32's range only where that is above 2^97, which then is 2^64 less in between.
+struct RowScale {
+  float unit, up;
+  __device__ __forceinline__ explicit RowScale(float scale) {
+    const bool large = __builtin_fabsf(scale) > 0x1p97f;
+    unit = large ? scale * 0x1p-64f : scale;
+    up = large ? 0x1p64f : 1.0f;
+  }
+};
+__device__ __forceinline__ float scaled(int32_t sum, const RowScale& row, float col_scale) {
+  return float(sum) * row.unit * col_scale * row.up;
+}
+
 // One element of the output: bias, activation, residual, stores.
 __device__ __forceinline__ void epilogue1(const MmParams& p, int act, int64_t r, int32_t s,
                                           float v) {

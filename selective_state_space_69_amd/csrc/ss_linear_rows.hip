@@ -123,7 +123,7 @@ __global__ __launch_bounds__(kWaves * kWave) void rows_kernel(MmParams p) {
     }
     if constexpr (KIND == kGlu) glu1(p, p.act, r, s0 + s, f, up);
     else if constexpr (KIND == kInt8)
-      epilogue1(p, p.act, r, s0 + s, float(f) * (p.row_scale[r] * p.col_scale[s0 + s]));
+      epilogue1(p, p.act, r, s0 + s, scaled(f, RowScale(p.row_scale[r]), p.col_scale[s0 + s]));
     else epilogue1(p, p.act, r, s0 + s, f);
   }
 }

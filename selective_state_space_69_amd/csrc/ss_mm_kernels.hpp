@@ -277,10 +277,6 @@ __device__ __forceinline__ void fetch_bias(const MmParams& p, int32_t s, float (
 // One piece of 16 rows x 16 F columns.  SPLIT: to a split's partial sums instead;
 // STREAM: past the caches; RES: with a residual perhaps.  kInt8: the sums are whole
 // numbers, scale those of this lane's columns.
-template <int KIND>
-__device__ __forceinline__ float value_of(float v, float row_scale, float scale) {
-  return KIND == kInt8 ? float(__float_as_int(v)) * (row_scale * scale) : v;
-}
 template <int ACT, bool SPLIT, bool STREAM, bool RES, int KIND, int F, typename Acc>
 __device__ __forceinline__ void piece_out(const MmParams& p, char* sl, const Acc (&q)[F],
                                           const Piece<F, KIND>& at, const float (&bias)[8],
@@ -310,7 +306,7 @@ __device__ __forceinline__ void piece_out(const MmParams& p, char* sl, const Acc
         } else {
           if constexpr (KIND == kInt8) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = value_of<KIND>(v[j], rs, scale[j]);
+            for (int j = 0; j < 8; ++j) v[j] = scaled(__float_as_int(v[j]), RowScale(rs), scale[j]);
           }
           epilogue8<ACT, STREAM, RES>(p, o, v, bias, res);
         }
@@ -320,7 +316,7 @@ __device__ __forceinline__ void piece_out(const MmParams& p, char* sl, const Acc
         for (int j = 0; j < 8; ++j) {
           v[j] = *reinterpret_cast<const float*>(sl + row * 256 + (((u + j / 4) ^ row) << 4) +
                                                  (j & 3) * 4);
-          v[j] = apply_act(ACT, value_of<KIND>(v[j], rs, scale[j]) + bias[j]);
+          v[j] = apply_act(ACT, scaled(__float_as_int(v[j]), RowScale(rs), scale[j]) + bias[j]);
           if (RES && p.res) v[j] += __uint_as_float(res.w[j]);
         }
 #pragma unroll
