@@ -564,7 +564,8 @@ void dpre_types(const ss_linear_desc_t& d, const DpreParams& p, dim3 grid, hipSt
   else if (tb) dpre_act<float, uint16_t, V>(p, grid, st);
   else dpre_act<float, float, V>(p, grid, st);
 }
-int dpre_vec(const ss_linear_desc_t& d) { return d.out_dim % 8 == 0 ? 8 : 1; }
+// columns of a lane that makes dpre, of rows (or halves of rows) of n
+int dpre_vec(int64_t n) { return n % 8 == 0 ? 8 : 1; }
 
 }  // namespace
 
@@ -598,10 +599,15 @@ static LinearPlan plan_bwd_fwd(const ss_linear_desc_t& d, int op, bool gated) {
   pl.sum2 = bf16 && d.grad_dtype == SS_F32 &&
             (d.act != SS_ACT_NONE || d.out_dtype != SS_BF16);
   pl.ld_dpre = pad_to_unit(d, d.out_dim) * (pl.sum2 ? 2 : 1);
-  // about 1024 blocks over the columns and row chunks, at least 16 rows each
-  const int64_t span = 64 * dpre_vec(d) * (gated ? 2 : 1), cols = (d.out_dim + span - 1) / span;
-  int64_t chunks = (1024 + cols - 1) / cols;
-  const int64_t most = (d.rows + 15) / 16;
+  // about 1024 blocks over the columns and row chunks, at least 16 rows each; gated ones of
+  // single columns, whose lanes load an element at a time, 8192 in at most 1024 chunks
+  // (dbias of bf16 16384 x 1004: 46 us, with 1024 blocks 73)
+  const int64_t width = gated ? d.out_dim / 2 : d.out_dim, span = 64 * dpre_vec(width);
+  const int64_t cols = (width + span - 1) / span;
+  const int64_t blocks = gated && span == 64 ? 8192 : 1024;
+  int64_t chunks = (blocks + cols - 1) / cols;
+  int64_t most = (d.rows + 15) / 16;
+  if (most > 1024) most = 1024;
   if (chunks > most) chunks = most;
   pl.chunk_rows = (d.rows + chunks - 1) / chunks;
   pl.chunks = (d.rows + pl.chunk_rows - 1) / pl.chunk_rows;
@@ -725,7 +731,7 @@ int launch_linear_bwd(const ss_linear_desc_t& d, const LinearPlan& pl, const voi
     DpreParams p{dy, pre, dpre ? ws + pl.off_dpre : nullptr,
                  dbias ? reinterpret_cast<float*>(ws + pl.off_sums) : nullptr, d.rows,
                  pl.chunk_rows, int32_t(d.out_dim), int32_t(pl.ld_dpre), d.act, pl.sum2};
-    const int v = dpre_vec(d);
+    const int v = dpre_vec(d.out_dim);
     const int64_t cols = pad_to_unit(d, d.out_dim);
     const dim3 grid(unsigned((cols + 64 * v - 1) / (64 * v)), unsigned(pl.chunks));
     if (v == 8) dpre_types<8>(d, p, grid, st);
@@ -821,7 +827,7 @@ int launch_glu_bwd(const ss_glu_desc_t& d, const LinearPlan& pl, const void* x, 
   hipStream_t st = static_cast<hipStream_t>(stream);
   const ss_linear_desc_t l = both_halves(d);
   const bool dpre = dx || dw;
-  const int v = d.out_dim % 8 == 0 ? 8 : 1;
+  const int v = dpre_vec(d.out_dim);
   // with single columns, lanes past F clear the rows' last unit
   const int64_t cols = v == 8 ? d.out_dim : d.out_dim + pad_to_unit(l, l.out_dim) - l.out_dim;
   const int64_t across = (cols + 64 * v - 1) / (64 * v);
