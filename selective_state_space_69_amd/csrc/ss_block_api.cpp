@@ -20,23 +20,6 @@ constexpr int64_t kMaxLinearRows = int64_t(1) << 28;
 constexpr int64_t kMaxLinearElems = int64_t(1) << 35;
 constexpr int64_t kMaxNormDim = 32768;
 
-size_t elem(int32_t dtype) { return dtype == SS_BF16 ? 2 : 4; }
-
-bool bad_stride(int64_t stride, int64_t dim, int64_t most) {
-  return stride != 0 && (stride < dim || stride > most);
-}
-
-// Rows read or written with a stride need their element alignment only.
-size_t row_align(int64_t stride, int32_t dtype) {
-  return stride == 0 ? kPtrAlign : elem(dtype);
-}
-
-bool all_aligned(std::initializer_list<const void*> ptrs) {
-  for (const void* p : ptrs)
-    if (p && !aligned(p, kPtrAlign)) return false;
-  return true;
-}
-
 // whether p is one of the given pointers (NULL never is)
 bool among(const void* p, std::initializer_list<const void*> ptrs) {
   if (!p) return false;

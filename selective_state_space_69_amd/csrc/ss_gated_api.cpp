@@ -1,6 +1,7 @@
 // C-ABI entry points of a gated recurrent block's operators: the gated linear
-// recurrence, the gated half of a feed-forward block, projections in 8-bit integers.  As for the scan, validation is plain host logic that runs before any
-// HIP call; then the device is checked and the kernels are launched.
+// recurrence, the gated half of a feed-forward block, projections in 8-bit integers.
+// As for the scan, validation is plain host logic that runs before any HIP call; then
+// the device is checked and the kernels are launched.
 #include <cmath>
 #include <cstdint>
 #include <initializer_list>
@@ -12,24 +13,11 @@ namespace {
 
 constexpr int64_t kMaxElems = int64_t(1) << 40;
 constexpr int64_t kMaxDim = int64_t(1) << 20;
-constexpr int64_t kMaxGroups = int64_t(1) << 21;     // of 64 channels, two workgroups of 512 threads each:
-                                                     // a grid's threads stay below 2^32
+// of 64 channels, two workgroups of 512 threads each: a grid's threads stay below 2^32
+constexpr int64_t kMaxGroups = int64_t(1) << 21;
 
-size_t elem(int32_t dtype) { return dtype == SS_BF16 ? 2 : 4; }
-
-bool bad_stride(int64_t stride, int64_t dim, int64_t most) {
-  return stride != 0 && (stride < dim || stride > most);
-}
-
-// A tensor read with a row stride needs its element alignment only.
 bool row_aligned(const void* p, int64_t stride, int32_t dtype) {
-  return !p || aligned(p, stride == 0 ? kPtrAlign : elem(dtype));
-}
-
-bool all_aligned(std::initializer_list<const void*> ptrs) {
-  for (const void* p : ptrs)
-    if (p && !aligned(p, kPtrAlign)) return false;
-  return true;
+  return !p || aligned(p, row_align(stride, dtype));
 }
 
 // whether two of the outputs, or an output and an input, are one buffer (NULL never is)
@@ -50,7 +38,8 @@ bool bad_workspace(const void* workspace, size_t ws_bytes, size_t need) {
 
 int check_rec(const ss_rec_desc_t* d) {
   if (!d) return SS_ERR_INVALID_ARG;
-  if (d->batch < 1 || d->seqlen < 1 || d->seqlen > INT32_MAX || d->dim < 1 || d->dim > kMaxDim) return SS_ERR_INVALID_ARG;
+  if (d->batch < 1 || d->seqlen < 1 || d->seqlen > INT32_MAX || d->dim < 1 || d->dim > kMaxDim)
+    return SS_ERR_INVALID_ARG;
   if (d->batch > kMaxGroups / ((d->dim + 63) / 64)) return SS_ERR_INVALID_ARG;
   for (int64_t s : {d->x_stride, d->r_stride, d->i_stride, d->z_stride}) {
     if (bad_stride(s, d->dim, kMaxDim)) return SS_ERR_INVALID_ARG;

@@ -5,6 +5,7 @@
 
 #include <cstddef>
 #include <cstdint>
+#include <initializer_list>
 
 #include "ss_ckpt.h"
 #include "ss_conv.h"
@@ -28,6 +29,18 @@ constexpr size_t kAlign = 256;     // workspace alignment
 constexpr size_t kPtrAlign = 16;   // every tensor pointer (rows are read with 16-byte loads)
 inline bool valid_dtype(int32_t t) { return t == SS_F32 || t == SS_BF16; }
 inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+inline bool all_aligned(std::initializer_list<const void*> ptrs) {      // NULL is
+  for (const void* p : ptrs)
+    if (p && !aligned(p, kPtrAlign)) return false;
+  return true;
+}
+// Rows read or written with a stride need their element alignment only.
+inline size_t row_align(int64_t stride, int32_t dtype) {
+  return stride == 0 ? kPtrAlign : dtype == SS_BF16 ? 2 : 4;
+}
+inline bool bad_stride(int64_t stride, int64_t dim, int64_t most) {
+  return stride != 0 && (stride < dim || stride > most);
+}
 
 // How a forward (or the forward recompute inside the backward) is split.
 // nsplit : waves per (b, 64-channel block), each holding 16 / nsplit states;
@@ -264,7 +277,9 @@ int launch_linear_bwd(const ss_linear_desc_t& d, const LinearPlan& pl, const voi
 
 // Gated linear recurrence (ss_rec.hip): time in nchunks chunks of `chunk` steps, one
 // workgroup each per group of channels.  Workspace, fp32 (B, nchunks, D) arrays, 256-byte
-// aligned: chunks' log decays and carries (nchunks > 1), backward partial sums of dlam.
+// aligned: chunks' log2 decays (off_log) and their end states or leaving adjoints (off_carry)
+// where nchunks > 1, and then, forward, a (B, D) copy of h0 (off_first); backward partial sums
+// of dlam (off_part).
 struct RecPlan {
   int64_t chunk = 0, nchunks = 1;
   size_t off_log = 0, off_carry = 0, off_first = 0, off_part = 0, bytes = 0;

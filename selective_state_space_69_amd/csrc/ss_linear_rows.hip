@@ -25,27 +25,6 @@ namespace {
 constexpr int kWaves = 8;
 constexpr int kUnroll = 5;      // loads of w in flight per wave
 
-enum { kMm, kGlu, kInt8 };     // what is multiplied and what comes of it
-
-template <typename T, typename Acc>
-__device__ __forceinline__ Acc mma16(u32x4 a, u32x4 b, Acc c) {
-#if defined(__HIP_DEVICE_COMPILE__)
-  if constexpr (sizeof(T) == 1) {
-    return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, a),
-                                                 __builtin_bit_cast(i32x4, b), c, 0, 0, 0);
-  } else if constexpr (sizeof(T) == 2) {
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
-                                                   __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      c = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(a[i]), __uint_as_float(b[i]), c, 0,
-                                               0, 0);
-  }
-#endif
-  return c;
-}
-
 // 16 bytes of a row from element t of n; VEC: n and the row's alignment allow
 // whole 16-byte units
 template <typename T, bool VEC>
@@ -103,7 +82,7 @@ __global__ __launch_bounds__(kWaves * kWave) void rows_kernel(MmParams p) {
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u)
 #pragma unroll
-      for (int b = 0; b < MB; ++b) acc[b] = mma16<T>(a[u], v[u][b], acc[b]);
+      for (int b = 0; b < MB; ++b) acc[b] = mfma<T>(a[u], v[u][b], acc[b]);
   }
   // lane: rows s0 + 4 g .. + 3 of w, row m of x
 #pragma unroll

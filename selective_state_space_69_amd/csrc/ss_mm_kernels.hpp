@@ -66,8 +66,6 @@ namespace {
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) void* lds_ptr;
 
-// what is multiplied and what comes of it
-enum { kMm, kGlu, kInt8 };
 template <int KIND> struct KindOf { using Elem = uint16_t; using Acc = f32x4; };
 template <> struct KindOf<kInt8> { using Elem = uint8_t; using Acc = i32x4; };
 
@@ -81,24 +79,6 @@ constexpr int kOffR = 0, kOffLo = 65536, kOffHi = 98304, kOffEpi = 131072;
 constexpr int kLds = 163840;
 
 #if defined(__HIP_DEVICE_COMPILE__)
-
-// 16 bytes of t of either operand
-template <typename T, typename V, typename Acc>
-__device__ __forceinline__ Acc mfma(V a, V b, Acc c) {
-  if constexpr (sizeof(T) == 1) {
-    return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, a),
-                                                 __builtin_bit_cast(i32x4, b), c, 0, 0, 0);
-  } else if constexpr (sizeof(T) == 2) {
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
-                                                   __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      c = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(a[i]), __uint_as_float(b[i]), c, 0,
-                                               0, 0);
-    return c;
-  }
-}
 
 template <int N>
 __device__ __forceinline__ void wait_copies() {

@@ -126,15 +126,12 @@ __device__ __forceinline__ void unpack(const Chans<uint16_t>& q, float (&v)[kV])
     v[j] = __uint_as_float(j & 1 ? q.w[j / 2] & 0xffff0000u : q.w[j / 2] << 16);
 }
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 template <typename T>
 __device__ __forceinline__ Chans<T> buf_chans(Rsrc v, uint32_t at, uint32_t row) {
   if constexpr (kWords<T> == 1)
     return __builtin_bit_cast(Chans<T>, __builtin_amdgcn_raw_buffer_load_b32(v, at, row, 0));
-  else if constexpr (kWords<T> == 2)
-    return __builtin_bit_cast(Chans<T>, __builtin_amdgcn_raw_buffer_load_b64(v, at, row, 0));
   else
-    return __builtin_bit_cast(Chans<T>, __builtin_amdgcn_raw_buffer_load_b128(v, at, row, 0));
+    return __builtin_bit_cast(Chans<T>, __builtin_amdgcn_raw_buffer_load_b64(v, at, row, 0));
 }
 template <typename T>
 __device__ __forceinline__ void buf_put(Rsrc v, uint32_t at, uint32_t row, const float (&f)[kV]) {
@@ -144,10 +141,8 @@ __device__ __forceinline__ void buf_put(Rsrc v, uint32_t at, uint32_t row, const
     q.w[j] = sizeof(T) == 2 ? cvt_bf16x2(f[2 * j % kV], f[(2 * j + 1) % kV]) : __float_as_uint(f[j]);
   if constexpr (kWords<T> == 1)
     __builtin_amdgcn_raw_buffer_store_b32(q.w[0], v, at, row, 0);
-  else if constexpr (kWords<T> == 2)
-    __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, q), v, at, row, 0);
   else
-    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, q), v, at, row, 0);
+    __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, q), v, at, row, 0);
 }
 // A lane's n channels of a (D) row of floats; others repeat the first.
 __device__ __forceinline__ void load_f32(const float* p, int n, float (&v)[kV]) {
@@ -245,8 +240,6 @@ __device__ __forceinline__ float wave_log(float l) {
   swap_halves(a + b, a, b);
   return a + b;
 }
-
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
 // Which stretch of which channels a lane has.
 struct Place {
