@@ -216,7 +216,10 @@ __global__ __launch_bounds__(kThreads) void dpre_kernel(DpreParams p) {
 
 // Both halves of a gated dpre, d = [dy up act'(gate), dy act(gate)], in rows of ld
 // elements that are zero past 2 F, and their column sums: as dpre_kernel, a lane taking V
-// columns of each half.  V is 8 where F is a whole number of 16-byte units.
+// columns of each half.  V is 8 where F is a whole number of 16-byte units.  The products of
+// bf16 operands see of d what they see of a dpre: with bf16 gradients bf16(d), half a step
+// beside their own (16384 x 2560 -> 6912: 2.4e-3 off for 1.7e-3, 2000 us), with fp32 ones d to
+// 2^-16 (2e-6; 3960 us).
 struct DgluParams {
   const void* dy;     // (M, F)
   const void* pre;    // (M, 2 F)

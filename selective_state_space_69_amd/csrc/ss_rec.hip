@@ -9,10 +9,10 @@
 // those in front of it.
 //
 // Measured (bf16): 8 x 2048 x 2560 with a gate 121 us, 3.47 TB/s of the least traffic (which
-// is what the counters see) against a copy's 5.1; the vector ALU is busy 56% of it.  What holds
+// is what the counters see) against a copy's 5.1; the vector ALU is busy 67% of it.  What holds
 // it back is how the rows lie: 335 MB as 7 x 2048 x 2336 take 79 us, as 8 x 2048 x 2048, rows
 // 4096 bytes apart, 102.  A batch row's workgroups on one XCD matter most (in plain order 155
-// us, when the kernel took 118).  1 x 262144 x 256: 252 us, of them 110 the sums' pass.
+// us, when the kernel took 118).  1 x 262144 x 256: 251 us, of them 113 the sums' pass.
 #include "ss_rec.hpp"
 
 namespace ss {
@@ -22,10 +22,10 @@ constexpr int kS = 4;                       // steps of a lane's stretch
 constexpr int kWaveSteps = kSubs * kS;
 constexpr int kWaves = 8;
 constexpr int kBlock = kWaves * kWaveSteps;
-// Steps of a lane, waves (bf16 8 x 2048 x 2560 with a gate, us; with decays joined as fp32
-// numbers, 3 us less than now): 4, 8 117; 4, 4 146; 8, 4 145
-// (more loads than the counter of those in flight holds); 4, 16 139.  Rows 5120 bytes apart
-// are the slow ones of these: 8 x 2048 x 2592 takes 110, 107, 112 and 124.
+// Steps of a lane, waves (bf16 8 x 2048 x 2560 with a gate, us; measured with decays joined as
+// fp32 numbers, which takes 3 less than now): 4, 8 117; 4, 4 146; 8, 4 145 (more loads than the
+// counter of those in flight holds); 4, 16 139.  Rows 5120 bytes apart are the slow ones of
+// these: 8 x 2048 x 2592 takes 110, 107, 112 and 124.
 static_assert(SS_REC_CHUNK % kWaveSteps == 0 && kBlock % SS_REC_CHUNK == 0,
               "states are kept at a wave's first step");
 

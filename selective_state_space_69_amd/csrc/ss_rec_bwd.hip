@@ -7,8 +7,8 @@
 // leaving adjoint; both walks are joined by one barrier per block, then every lane runs
 // its steps forward (states) and backward (adjoints, gradients) from true values.
 //
-// Measured (bf16): 8 x 2048 x 2560 with a gate 245 us, 3.1 TB/s; the vector ALU is busy 55% of
-// it (104 operations an element), and what else holds is the forward's.
+// Measured (bf16): 8 x 2048 x 2560 with a gate 245 us, 3.1 TB/s; the vector ALU is busy 57% of
+// it (114 operations an element), and what else holds is the forward's.
 #include "ss_rec.hpp"
 
 namespace ss {
